@@ -77,6 +77,43 @@ class ConvArgs(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class DlaArgs(ctypes.Structure):
+    _fields_ = [("q", Rows), ("k", Rows), ("v", Rows), ("o", Rows), ("d_o", Rows), ("dq", Rows),
+                ("dk", Rows), ("dv", Rows), ("g", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+                ("ht", ctypes.c_void_p), ("dht", ctypes.c_void_p), ("dh0", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("seq_order", ctypes.c_void_p),
+                ("dev_status", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("t_max", ctypes.c_int64),
+                ("n_max", ctypes.c_int32), ("H", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("V", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class DlaStepArgs(ctypes.Structure):
+    _fields_ = [("q", Rows), ("k", Rows), ("v", Rows), ("o", Rows), ("g", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("dev_status", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("n_slots", ctypes.c_int32), ("H", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("V", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class QkArgs(ctypes.Structure):
+    _fields_ = [("q", Rows), ("k", Rows), ("yq", Rows), ("yk", Rows), ("dyq", Rows), ("dyk", Rows),
+                ("dq", Rows), ("dk", Rows), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("dq_weight", ctypes.c_void_p),
+                ("dk_weight", ctypes.c_void_p), ("cos_table", ctypes.c_void_p),
+                ("sin_table", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("dev_status", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("t_max", ctypes.c_int64),
+                ("n_positions", ctypes.c_int64), ("HQ", ctypes.c_int32), ("HK", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("R", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("norm", ctypes.c_int32), ("pair", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 def load_library(path: str = LIB_PATH):
     """Load libgcl.so and declare its C signatures."""
     if not os.path.exists(path):
@@ -120,6 +157,20 @@ def load_library(path: str = LIB_PATH):
         getattr(lib, fn).argtypes = [ctypes.POINTER(ConvArgs), vp]
     lib.gcl_causal_conv1d_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.gcl_causal_conv1d_bwd_workspace_bytes.argtypes = [ctypes.POINTER(ConvArgs)]
+    for fn, args in (("dla_chunk_fwd", DlaArgs), ("dla_chunk_bwd", DlaArgs),
+                     ("dla_step", DlaStepArgs), ("qk_norm_rope_fwd", QkArgs),
+                     ("qk_norm_rope_bwd", QkArgs)):
+        getattr(lib, fn).restype = ctypes.c_int
+        getattr(lib, fn).argtypes = [ctypes.POINTER(args), vp]
+    for fn, args in (("gcl_dla_fwd_workspace_bytes", DlaArgs),
+                     ("gcl_dla_bwd_workspace_bytes", DlaArgs),
+                     ("gcl_qk_norm_rope_bwd_workspace_bytes", QkArgs)):
+        getattr(lib, fn).restype = ctypes.c_size_t
+        getattr(lib, fn).argtypes = [ctypes.POINTER(args)]
+    lib.gcl_dla_segment_tokens.restype = i64
+    lib.gcl_dla_segment_tokens.argtypes = [i64, i32, i32, i32]
+    lib.rope_table_build.restype = ctypes.c_int
+    lib.rope_table_build.argtypes = [vp, vp, i64, i32, ctypes.c_double, vp]
     return lib
 
 
@@ -478,3 +529,213 @@ def causal_conv1d_bwd(*args, stream=None, **kw):
     validate_conv("causal_conv1d_bwd", _named(conv_args, args, kw))
     a = conv_args(*args, **kw)
     _check("causal_conv1d_bwd", lib().causal_conv1d_bwd(ctypes.byref(a), _stream(stream)))
+
+
+# ------------------------------------------------- decayed linear attention, norm and rotation
+# These calls take strided rows and are also made for single tokens, so their checks are plain
+# comparisons on each tensor (a few microseconds a call).
+def _rows(fn, name, t, shape, dtype, device):
+    """gcl_rows of a tensor [tokens, heads, D] with contiguous D and any token and head strides."""
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor on the call's device (got {t.device})")
+    if t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{fn}: {name} must have contiguous rows (strides {t.stride()})")
+    if shape[1] == 1:                        # the stride of an extent of one is free: one that fits
+        sh = shape[2]
+    if shape[0] == 1:
+        st = shape[1] * sh
+    return Rows(t.data_ptr(), st, sh)
+
+
+def _flat(fn, name, t, shape, dtype, device):
+    """Pointer of a contiguous tensor of exactly this shape, or None."""
+    if t is None:
+        return None
+    if t.get_device() != device or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous CUDA tensor {shape} of {dtype} on the "
+                         f"call's device (got {tuple(t.shape)}, {t.dtype}, {t.device})")
+    return t.data_ptr()
+
+
+def _scratch(fn, t, device):
+    if t is None:
+        return None, 0
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor on the call's device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _dla_sizes(q, v, cu_seqlens):
+    T, H, K = q.shape
+    return DlaArgs(t_max=T, n_max=cu_seqlens.shape[0] - 1, H=H, K=K, V=v.shape[2], dtype=_dtype_of(q))
+
+
+def dla_segment_tokens(t_max: int, n_max: int, H: int, backward: bool = False) -> int:
+    """Tokens per segment of the plan for these capacities (t_max or more: sequences stay whole)."""
+    return int(lib().gcl_dla_segment_tokens(t_max, n_max, H, int(backward)))
+
+
+def dla_fwd_workspace_bytes(q, v, cu_seqlens) -> int:
+    """Workspace of dla_chunk_fwd for these sizes (0: none)."""
+    return int(lib().gcl_dla_fwd_workspace_bytes(ctypes.byref(_dla_sizes(q, v, cu_seqlens))))
+
+
+def dla_bwd_workspace_bytes(q, v, cu_seqlens) -> int:
+    """Workspace of dla_chunk_bwd for these sizes (0: none)."""
+    return int(lib().gcl_dla_bwd_workspace_bytes(ctypes.byref(_dla_sizes(q, v, cu_seqlens))))
+
+
+def _dla_common(fn, q, k, v, g, cu_seqlens, h0, seq_order, dev_status, workspace, scale):
+    import torch
+    T, H, K = q.shape
+    V, N, dt, dev = v.shape[2], cu_seqlens.shape[0] - 1, q.dtype, q.get_device()
+    f32, i32 = torch.float32, torch.int32
+    ws, wsb = _scratch(fn, workspace, dev)
+    a = DlaArgs(q=_rows(fn, "q", q, (T, H, K), dt, dev), k=_rows(fn, "k", k, (T, H, K), dt, dev),
+                v=_rows(fn, "v", v, (T, H, V), dt, dev), g=_flat(fn, "g", g, (H,), f32, dev),
+                h0=_flat(fn, "h0", h0, (N, H, K, V), f32, dev),
+                cu_seqlens=_flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev),
+                seq_order=_flat(fn, "seq_order", seq_order, (N,), i32, dev),
+                dev_status=_flat(fn, "dev_status", dev_status, (1,), i32, dev), workspace=ws,
+                workspace_bytes=wsb, t_max=T, n_max=N, H=H, K=K, V=V,
+                scale=float(K ** -0.5 if scale is None else scale), dtype=_dtype_of(q))
+    return a, (T, H, K, V, N, dt, dev)
+
+
+def dla_chunk_fwd(q, k, v, g, cu_seqlens, o, h0=None, ht=None, seq_order=None, dev_status=None,
+                  workspace=None, scale=None, stream=None):
+    """Linear attention with the fixed log decay g [H] over packed sequences (include/gcl.h, dla):
+    o [T, H, V] (None: only ht) and ht from q, k [T, H, K], v [T, H, V] and h0.  q, k, v and o may
+    have strided tokens and heads."""
+    import torch
+    fn = "dla_chunk_fwd"
+    a, (T, H, K, V, N, dt, dev) = _dla_common(fn, q, k, v, g, cu_seqlens, h0, seq_order, dev_status,
+                                              workspace, scale)
+    if o is not None:
+        a.o = _rows(fn, "o", o, (T, H, V), dt, dev)
+    a.ht = _flat(fn, "ht", ht, (N, H, K, V), torch.float32, dev)
+    _check(fn, lib().dla_chunk_fwd(ctypes.byref(a), _stream(stream)))
+
+
+def dla_chunk_bwd(q, k, v, g, d_o, cu_seqlens, dq, dk, dv, h0=None, dht=None, dh0=None,
+                  seq_order=None, dev_status=None, workspace=None, scale=None, stream=None):
+    """The backward of dla_chunk_fwd: dq, dk, dv (of q's dtype) and dh0 from d_o and dht."""
+    import torch
+    fn = "dla_chunk_bwd"
+    a, (T, H, K, V, N, dt, dev) = _dla_common(fn, q, k, v, g, cu_seqlens, h0, seq_order, dev_status,
+                                              workspace, scale)
+    a.d_o = _rows(fn, "d_o", d_o, (T, H, V), dt, dev)
+    a.dq = _rows(fn, "dq", dq, (T, H, K), dt, dev)
+    a.dk = _rows(fn, "dk", dk, (T, H, K), dt, dev)
+    a.dv = _rows(fn, "dv", dv, (T, H, V), dt, dev)
+    a.dht = _flat(fn, "dht", dht, (N, H, K, V), torch.float32, dev)
+    a.dh0 = _flat(fn, "dh0", dh0, (N, H, K, V), torch.float32, dev)
+    _check(fn, lib().dla_chunk_bwd(ctypes.byref(a), _stream(stream)))
+
+
+def dla_step(q, k, v, g, state, o, slots=None, dev_status=None, scale=None, stream=None):
+    """One token of each request: the states [n_slots, H, K, V] of the requests' slots are updated
+    in place and o [B, H, V] is written (include/gcl.h, dla_step).  slots int32 [B]; negative: idle."""
+    import torch
+    fn = "dla_step"
+    B, H, K = q.shape
+    V, dt, dev = v.shape[2], q.dtype, q.get_device()
+    n_slots = state.shape[0]
+    a = DlaStepArgs(q=_rows(fn, "q", q, (B, H, K), dt, dev), k=_rows(fn, "k", k, (B, H, K), dt, dev),
+                    v=_rows(fn, "v", v, (B, H, V), dt, dev), o=_rows(fn, "o", o, (B, H, V), dt, dev),
+                    g=_flat(fn, "g", g, (H,), torch.float32, dev),
+                    state=_flat(fn, "state", state, (n_slots, H, K, V), torch.float32, dev),
+                    slots=_flat(fn, "slots", slots, (B,), torch.int32, dev),
+                    dev_status=_flat(fn, "dev_status", dev_status, (1,), torch.int32, dev), batch=B,
+                    n_slots=n_slots, H=H, K=K, V=V,
+                    scale=float(K ** -0.5 if scale is None else scale), dtype=_dtype_of(q))
+    _check(fn, lib().dla_step(ctypes.byref(a), _stream(stream)))
+
+
+NORMS = {None: 0, "none": 0, "rms": 1, "l2": 2}
+PAIRINGS = {"half": 0, "adjacent": 1}
+
+
+def _qk_common(fn, q, k, q_weight, k_weight, cos, sin, positions, norm, eps, pairing, dev_status):
+    import torch
+    T, HQ, D = q.shape
+    HK = 0 if k is None else k.shape[1]
+    dt, dev = q.dtype, q.get_device()
+    f32, i32 = torch.float32, torch.int32
+    if norm not in NORMS or pairing not in PAIRINGS:
+        raise ValueError(f"{fn}: norm {norm!r} or pairing {pairing!r} is not one of {tuple(NORMS)}, "
+                         f"{tuple(PAIRINGS)}")
+    a = QkArgs(q=_rows(fn, "q", q, (T, HQ, D), dt, dev),
+               q_weight=_flat(fn, "q_weight", q_weight, (D,), dt, dev),
+               k_weight=_flat(fn, "k_weight", k_weight, (D,), dt, dev),
+               positions=_flat(fn, "positions", positions, (T,), i32, dev),
+               dev_status=_flat(fn, "dev_status", dev_status, (1,), i32, dev), t_max=T, HQ=HQ,
+               HK=HK, D=D, eps=float(eps), norm=NORMS[norm], pair=PAIRINGS[pairing],
+               dtype=_dtype_of(q))
+    if HK:
+        a.k = _rows(fn, "k", k, (T, HK, D), dt, dev)
+    if (cos is None) != (sin is None):
+        raise ValueError(f"{fn}: cos and sin come together")
+    if cos is not None:
+        P, half = cos.shape
+        a.cos_table = _flat(fn, "cos", cos, (P, half), f32, dev)
+        a.sin_table = _flat(fn, "sin", sin, (P, half), f32, dev)
+        a.n_positions, a.R = P, 2 * half
+    return a, (T, HQ, HK, D, dt, dev)
+
+
+def qk_norm_rope_fwd(q, k, yq, yk, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                     norm="rms", eps=1e-6, pairing="half", dev_status=None, stream=None):
+    """Norm of each head's queries [T, HQ, D] and keys [T, HK, D] (k None: queries alone) and the
+    rotation by the rows `positions` of cos, sin [P, R / 2], in one pass (include/gcl.h,
+    qk_norm_rope)."""
+    fn = "qk_norm_rope_fwd"
+    a, (T, HQ, HK, D, dt, dev) = _qk_common(fn, q, k, q_weight, k_weight, cos, sin, positions, norm,
+                                            eps, pairing, dev_status)
+    a.yq = _rows(fn, "yq", yq, (T, HQ, D), dt, dev)
+    if HK:
+        a.yk = _rows(fn, "yk", yk, (T, HK, D), dt, dev)
+    _check(fn, lib().qk_norm_rope_fwd(ctypes.byref(a), _stream(stream)))
+
+
+def qk_norm_rope_bwd_workspace_bytes(q, k) -> int:
+    """Workspace of qk_norm_rope_bwd with weight gradients."""
+    T, HQ, D = q.shape
+    a = QkArgs(t_max=T, HQ=HQ, HK=0 if k is None else k.shape[1], D=D)
+    return int(lib().gcl_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(a)))
+
+
+def qk_norm_rope_bwd(q, k, dyq, dyk, dq, dk, q_weight=None, k_weight=None, dq_weight=None,
+                     dk_weight=None, cos=None, sin=None, positions=None, norm="rms", eps=1e-6,
+                     pairing="half", workspace=None, dev_status=None, stream=None):
+    """The backward of qk_norm_rope_fwd: dq, dk from dyq, dyk, and the weights' gradients fp32 [D]."""
+    import torch
+    fn = "qk_norm_rope_bwd"
+    a, (T, HQ, HK, D, dt, dev) = _qk_common(fn, q, k, q_weight, k_weight, cos, sin, positions, norm,
+                                            eps, pairing, dev_status)
+    a.dyq, a.dq = _rows(fn, "dyq", dyq, (T, HQ, D), dt, dev), _rows(fn, "dq", dq, (T, HQ, D), dt, dev)
+    if HK:
+        a.dyk = _rows(fn, "dyk", dyk, (T, HK, D), dt, dev)
+        a.dk = _rows(fn, "dk", dk, (T, HK, D), dt, dev)
+    a.dq_weight = _flat(fn, "dq_weight", dq_weight, (D,), torch.float32, dev)
+    a.dk_weight = _flat(fn, "dk_weight", dk_weight, (D,), torch.float32, dev)
+    a.workspace, a.workspace_bytes = _scratch(fn, workspace, dev)
+    _check(fn, lib().qk_norm_rope_bwd(ctypes.byref(a), _stream(stream)))
+
+
+def rope_table_build(cos, sin, base: float = 10000.0, stream=None):
+    """Fills the tables cos, sin [P, R / 2] fp32 with the angles p base^(-2 i / R)."""
+    import torch
+    fn = "rope_table_build"
+    if cos.dim() != 2:
+        raise ValueError(f"{fn}: cos must be [positions, R / 2]")
+    shape, dev = tuple(cos.shape), cos.get_device()
+    if dev < 0:
+        raise ValueError(f"{fn}: cos must be a CUDA tensor (got {cos.device})")
+    c, s = _flat(fn, "cos", cos, shape, torch.float32, dev), _flat(fn, "sin", sin, shape, torch.float32, dev)
+    _check(fn, lib().rope_table_build(c, s, shape[0], 2 * shape[1], float(base), _stream(stream)))

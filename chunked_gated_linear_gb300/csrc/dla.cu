@@ -1,0 +1,241 @@
+// dla.cu -- decayed linear attention: the C entry points, the segment plan and the scan of the
+// segments' states.
+//
+// Plans.  With at least as many (sequence, head) units as SMs one CTA walks each sequence: every
+// input is read once.  With fewer, sequences are cut into segments: the segments' own states (a
+// launch that reads k and v once more), their scan, then the outputs from the entering states.  The
+// scan is elementwise over a [K, V] state: S(i + 1) = gamma^seg S(i) + own(i).
+#include "dla.cuh"
+
+namespace gcl {
+namespace dla {
+namespace {
+
+constexpr int kScanThreads = 256;
+
+// One thread per four state values of one (sequence, head), over the sequence's segments in
+// time order; blockIdx.z: 0 forwards, 1 backwards.  The sequence's first row is the number of
+// segments before it, summed by the block.
+__global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) {
+    if (status_blocks_cta(p.status)) return;
+    const int h = blockIdx.y % p.H, n = blockIdx.y / p.H, tid = threadIdx.x;
+    const bool rev = blockIdx.z != 0;
+    __shared__ int s_sum[kScanThreads / 32];
+    int sum = 0, bad = 0;
+    for (int m = tid; m <= n; m += kScanThreads) {
+        const int64_t b = p.cu[m], e = p.cu[m + 1];
+        if (b < 0 || e < b || e > p.t_max) bad = 1;
+        else if (m < n) sum += (int)((e - b + p.seg - 1) / p.seg);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
+        return;
+    }
+    int64_t row0 = 0;
+    for (int w = 0; w < kScanThreads / 32; ++w) row0 += s_sum[w];
+    const int64_t len = (int64_t)p.cu[n + 1] - p.cu[n];
+    const int count = (int)((len + p.seg - 1) / p.seg);
+    if (row0 + count > p.n_rows) {
+        if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
+        return;
+    }
+    const int64_t KV = (int64_t)p.K * p.V, e = ((int64_t)blockIdx.x * kScanThreads + tid) * 4;
+    if (e >= KV) return;
+    const float g = p.g[h];
+    const int64_t at = ((int64_t)n * p.H + h) * KV + e;
+    const float *first = rev ? p.dht : p.h0;
+    float4 cur = first && GCL_RANGE_IN_BOUNDS(at, at + 3, (int64_t)p.n_max * p.H * KV, p.status)
+                     ? *reinterpret_cast<const float4 *>(first + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (count == 0) {                                      // an empty sequence passes its state on
+        float *last = rev ? p.dh0 : p.ht;
+        if (last && GCL_RANGE_IN_BOUNDS(at, at + 3, (int64_t)p.n_max * p.H * KV, p.status))
+            *reinterpret_cast<float4 *>(last + at) = cur;
+        return;
+    }
+    float *seg = rev ? p.seg_rev : p.seg_fwd;
+    const float gs = decay_pow(g, p.seg);
+    const int64_t step = (int64_t)p.H * KV;
+    float *at_row = seg + row0 * step + h * KV + e;
+    for (int j0 = 0; j0 < count; j0 += 8) {                // eight loads in flight
+        float4 own[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int j = j0 + u;
+            // (the last segment in time has no own state: nothing enters from it)
+            own[u] = j + 1 < count ? *reinterpret_cast<const float4 *>(at_row + (rev ? count - 1 - j : j) * step)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int j = j0 + u;
+            if (j >= count) break;
+            *reinterpret_cast<float4 *>(at_row + (rev ? count - 1 - j : j) * step) = cur;
+            // backwards the first segment met is the sequence's last, possibly a short one
+            const float f = rev && j == 0 ? decay_pow(g, len - (int64_t)(count - 1) * p.seg) : gs;
+            cur.x = fmaf(f, cur.x, own[u].x);
+            cur.y = fmaf(f, cur.y, own[u].y);
+            cur.z = fmaf(f, cur.z, own[u].z);
+            cur.w = fmaf(f, cur.w, own[u].w);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_scan(const Params &p, bool backward, cudaStream_t s) {
+    const int64_t kv4 = (int64_t)p.K * p.V / 4;
+    dla_scan_kernel<<<dim3((unsigned)((kv4 + kScanThreads - 1) / kScanThreads), (unsigned)(p.n_max * p.H), backward ? 2 : 1),
+                      kScanThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_simt(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s) {
+    if (dtype == GCL_BF16) return launch_simt_t<__nv_bfloat16>(p, own_states, n_roles, roles, s);
+    if (dtype == GCL_F16) return launch_simt_t<__half>(p, own_states, n_roles, roles, s);
+    return launch_simt_t<float>(p, own_states, n_roles, roles, s);
+}
+
+namespace {
+
+constexpr int kSegUnit = 128;
+
+// Tokens per segment.  Cost model in chunks of 128 tokens, for n_max sequences of t_max / n_max
+// tokens: the waves of CTAs times (a segment's chunks + 2 for its start), times 1.5 for the
+// extra read of k and v (the own states' launch) and its own start once a sequence is cut.
+int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward) {
+    const int64_t sms = num_sms(), units = (int64_t)n_max * H * (backward ? 3 : 1);
+    const int64_t chunks = (t_max / n_max + kSegUnit - 1) / kSegUnit;    // of an average sequence
+    const int64_t whole = (t_max + kSegUnit - 1) / kSegUnit * kSegUnit;
+    if (units >= 8 * sms || chunks <= 2 || units > 65535) return whole;
+    double best = (double)((units + sms - 1) / sms) * (chunks + 2);
+    int64_t seg = whole;
+    for (int64_t c = 1; c < chunks; ++c) {
+        const int64_t parts = (chunks + c - 1) / c;
+        const double cost = 1.5 * (double)((units * parts + sms - 1) / sms) * (c + 2) + 2;
+        if (cost < best) {
+            best = cost;
+            seg = c * kSegUnit;
+        }
+    }
+    return seg;
+}
+
+int64_t segment_rows(int64_t t_max, int32_t n_max, int64_t seg) {
+    return seg >= t_max ? n_max : gcl_nt_max(t_max, n_max, (int32_t)seg);
+}
+
+size_t segment_bytes(const gcl_dla_args *a, bool backward) {
+    if (a->t_max < 1 || a->t_max >= (int64_t(1) << 31) || a->n_max < 1 || a->H < 1 || a->K < 1 || a->V < 1) return 0;
+    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward);
+    if (seg >= a->t_max) return 0;
+    return (size_t)segment_rows(a->t_max, a->n_max, seg) * a->H * a->K * a->V * sizeof(float) * (backward ? 2 : 1);
+}
+
+}  // namespace
+
+gcl_status_t check_rows(const char *fn, const char *name, const gcl_rows &r, int64_t tokens, int64_t heads, int32_t D,
+                        int32_t esize, bool output) {
+    if (!r.ptr) return fail(GCL_ERR_INVALID_ARG, "%s: %s is required", fn, name);
+    const int64_t unit = 16 / esize;
+    if (!aligned(r.ptr, 16)) return fail(GCL_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+    if (r.token_stride < D || r.head_stride < D || r.token_stride % unit || r.head_stride % unit ||
+        r.token_stride >= (int64_t(1) << 36) || r.head_stride >= (int64_t(1) << 36))
+        return fail(GCL_ERR_INVALID_ARG, "%s: %s strides (%lld, %lld) must be at least the row's %d values and multiples of 16 bytes",
+                    fn, name, (long long)r.token_stride, (long long)r.head_stride, D);
+    if (output && r.token_stride < (heads - 1) * r.head_stride + D && r.head_stride < (tokens - 1) * r.token_stride + D)
+        return fail(GCL_ERR_INVALID_ARG, "%s: rows of %s overlap", fn, name);
+    return GCL_OK;
+}
+
+gcl_status_t check_sizes(const char *fn, int32_t H, int32_t K, int32_t V, int32_t dtype) {
+    if (H < 1 || H > 65535) return fail(GCL_ERR_INVALID_ARG, "%s: H=%d (1 to 65535)", fn, H);
+    if ((K != 64 && K != 128) || (V != 64 && V != 128))
+        return fail(GCL_ERR_UNSUPPORTED, "%s: K=%d V=%d (supported: 64 or 128 each)", fn, K, V);
+    if (dtype != GCL_F32 && dtype != GCL_BF16 && dtype != GCL_F16)
+        return fail(GCL_ERR_UNSUPPORTED, "%s: dtype %d (supported: GCL_F32, GCL_BF16, GCL_F16)", fn, dtype);
+    return GCL_OK;
+}
+
+namespace {
+
+gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cudaStream_t s) {
+    fail(GCL_OK, "%s", "");                                // clears gcl_last_error()
+    if (!a) return fail(GCL_ERR_INVALID_ARG, "%s: args is NULL", fn);
+    if (!a->g || !a->cu_seqlens) return fail(GCL_ERR_INVALID_ARG, "%s: g and cu_seqlens are required", fn);
+    if (a->t_max < 1 || a->t_max >= (int64_t(1) << 31) || a->n_max < 1)
+        return fail(GCL_ERR_INVALID_ARG, "%s: need 1 <= t_max < 2^31 and n_max >= 1", fn);
+    gcl_status_t st = check_sizes(fn, a->H, a->K, a->V, a->dtype);
+    if (st != GCL_OK) return st;
+    if ((int64_t)a->n_max * a->H >= (int64_t(1) << 31))
+        return fail(GCL_ERR_UNSUPPORTED, "%s: n_max * H must be below 2^31", fn);
+    const int es = a->dtype == GCL_F32 ? 4 : 2;
+    struct { const char *name; const gcl_rows *r; int32_t D; bool in, out; } need[] = {
+        {"q", &a->q, a->K, true, false}, {"k", &a->k, a->K, true, false}, {"v", &a->v, a->V, true, false},
+        {"o", &a->o, a->V, false, !backward && a->o.ptr}, {"d_o", &a->d_o, a->V, backward, false},
+        {"dq", &a->dq, a->K, false, backward}, {"dk", &a->dk, a->K, false, backward},
+        {"dv", &a->dv, a->V, false, backward}};
+    for (const auto &x : need)
+        if ((x.in || x.out) && (st = check_rows(fn, x.name, *x.r, a->t_max, a->H, x.D, es, x.out)) != GCL_OK) return st;
+    for (const void *x : {(const void *)a->h0, (const void *)a->ht, (const void *)a->dht, (const void *)a->dh0})
+        if (!aligned(x, 16)) return fail(GCL_ERR_INVALID_ARG, "%s: states must be 16-byte aligned", fn);
+    const size_t bytes = segment_bytes(a, backward);
+    if (bytes && (!a->workspace || a->workspace_bytes < bytes))
+        return fail(GCL_ERR_CAPACITY, "%s: workspace of %zu bytes needed, %zu given", fn, bytes,
+                    a->workspace ? a->workspace_bytes : (size_t)0);
+    if (bytes && !aligned(a->workspace, 16)) return fail(GCL_ERR_INVALID_ARG, "%s: the workspace must be 16-byte aligned", fn);
+
+    Params p{};
+    p.q = rows(a->q); p.k = rows(a->k); p.v = rows(a->v);
+    if (backward) {
+        p.d_o = rows(a->d_o); p.dq = rows(a->dq); p.dk = rows(a->dk); p.dv = rows(a->dv);
+        p.dht = a->dht; p.dh0 = a->dh0;
+    } else {
+        p.o = rows(a->o);
+        p.ht = a->ht;
+    }
+    p.g = a->g; p.h0 = a->h0;
+    p.cu = a->cu_seqlens; p.seq_order = a->seq_order; p.status = a->dev_status;
+    p.t_max = a->t_max; p.n_max = a->n_max; p.H = a->H; p.K = a->K; p.V = a->V; p.scale = a->scale;
+    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward);
+    p.n_rows = segment_rows(a->t_max, a->n_max, seg);
+    p.seg = (int32_t)(seg < a->t_max ? seg : a->t_max);
+    const int both[2] = {kFwd, kDv}, out[3] = {kDq, kDv, kDk};
+    cudaError_t e = cudaSuccess;
+    if (bytes) {
+        p.seg_fwd = static_cast<float *>(a->workspace);
+        if (backward) p.seg_rev = p.seg_fwd + bytes / 2 / sizeof(float);
+        e = launch_simt(p, a->dtype, true, backward ? 2 : 1, both, s);
+        if (e == cudaSuccess) e = launch_scan(p, backward, s);
+    }
+    if (e == cudaSuccess) e = launch_simt(p, a->dtype, false, backward ? 3 : 1, backward ? out : both, s);
+    return cuda_check(e, fn);
+}
+
+}  // namespace
+}  // namespace dla
+}  // namespace gcl
+
+using namespace gcl;
+
+extern "C" {
+
+int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward) {
+    if (t_max < 1 || t_max >= (int64_t(1) << 31) || n_max < 1 || H < 1) return 0;
+    return dla::segment_tokens(t_max, n_max, H, backward != 0);
+}
+
+size_t gcl_dla_fwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, false) : 0; }
+size_t gcl_dla_bwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, true) : 0; }
+
+gcl_status_t dla_chunk_fwd(const gcl_dla_args *a, gcl_stream_t stream) {
+    return dla::run_chunk("dla_chunk_fwd", a, false, static_cast<cudaStream_t>(stream));
+}
+
+gcl_status_t dla_chunk_bwd(const gcl_dla_args *a, gcl_stream_t stream) {
+    return dla::run_chunk("dla_chunk_bwd", a, true, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

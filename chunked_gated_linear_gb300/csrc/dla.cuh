@@ -1,0 +1,160 @@
+// dla.cuh -- decayed linear attention (one fixed decay per head): what its kernels share.
+//
+// Forward and backward are one engine in four roles.  With gamma = exp(g_h), the recurrence
+//   M <- gamma M + b_j c_j^T,   out_i = a_i M     (inclusive of j = i)
+// over the tokens of a sequence, forwards or backwards in time, is
+//   role  a    b    c    time       M            out          M before the first token
+//   FWD   q    k    v    forwards   S   [K, V]   o / scale    h0
+//   DQ    do   v    k    forwards   S^T [V, K]   dq / scale   h0^T
+//   DV    k    q    do   backwards  G   [K, V]   dv           dht, met before a decay
+//   DK    v    do   q    backwards  G^T [V, K]   dk           dht^T, likewise
+// (G with scale q do^T as its increments.)  In chunk form, for the chunk's tokens i, j and len of
+// them, with M the state that enters the chunk:
+//   forwards   out_i = sum_{j <= i} gamma^(i-j) (a_i b_j) c_j + gamma^(i+1) a_i M
+//              M'    = gamma^len M + sum_j gamma^(len-1-j) b_j c_j^T
+//   backwards  out_i = sum_{j >= i} gamma^(j-i) (a_i b_j) c_j + gamma^(len-1-i) a_i M
+//              M'    = gamma^len M + sum_j gamma^(j+1) b_j c_j^T
+// where backwards M carries one decay more than G (it is gamma G), so that dht enters and dh0
+// leaves as they are.
+#pragma once
+
+#include "gcl_internal.cuh"
+
+namespace gcl {
+namespace dla {
+
+enum Role { kFwd = 0, kDq = 1, kDv = 2, kDk = 3 };
+
+struct Rows {                      // a gcl_rows, strides in elements
+    void *p;
+    int64_t st, sh;
+};
+
+struct Params {
+    Rows q, k, v, d_o, o, dq, dk, dv;
+    const float *g, *h0, *dht;
+    float *ht, *dh0;
+    const int32_t *cu, *seq_order;
+    int32_t *status;
+    float *seg_fwd, *seg_rev;      // [n_rows, H, K, V]: the segments' own states, after the scan the
+                                   // states that enter them; NULL for one segment per sequence
+    int64_t t_max;
+    int64_t n_rows;                // segment rows (capacity)
+    int32_t seg;                   // tokens per segment
+    int32_t n_max, H, K, V;
+    float scale;
+    uint32_t roles;                // the role of blockIdx.z, 2 bits each
+};
+
+// Row t of head h.
+template <typename T>
+__host__ __device__ __forceinline__ T *row_ptr(const Rows &r, int64_t t, int h) {
+    return static_cast<T *>(r.p) + t * r.st + h * r.sh;
+}
+
+// gamma^n (n >= 0): 1 for n = 0 whatever g is (also g = -inf).
+__device__ __forceinline__ float decay_pow(float g, int64_t n) { return n == 0 ? 1.f : expf(g * (float)n); }
+
+// The work of row j of the grid: sequence n, its tokens [bos, eos), the segment's number i in it and
+// its tokens [s0, s1), and whether it is the sequence's last.  Every thread of the block calls it (block
+// barriers); the answer is the same for all.  False: nothing to do.  One segment per sequence: row j
+// is the sequence slot (in seq_order).  Otherwise the block adds up the segments of the sequences,
+// kBlock at a time, until row j falls into one.
+struct Item {
+    int n, i;
+    int64_t bos, eos, s0, s1;
+    bool last;
+};
+
+template <int kBlock>
+__device__ __forceinline__ bool find_item(const Params &p, int64_t j, Item &it) {
+    __shared__ int s_warp[32];
+    __shared__ int s_hit[2], s_bad;
+    const int tid = threadIdx.x;
+    if (p.seg_fwd == nullptr && p.seg_rev == nullptr) {
+        const int n = p.seq_order ? p.seq_order[j] : (int)j;
+        if (n < 0 || n >= p.n_max) {
+            if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
+            return false;
+        }
+        it.n = n;
+        it.i = 0;
+        it.bos = p.cu[n];
+        it.eos = p.cu[n + 1];
+        it.s0 = it.bos;
+        it.s1 = it.eos;
+        it.last = true;
+    } else {
+        if (tid == 0) { s_hit[0] = -1; s_bad = 0; }
+        __syncthreads();
+        int64_t base = 0;
+        for (int n0 = 0; n0 < p.n_max; n0 += kBlock) {
+            const int n = n0 + tid;
+            int c = 0;
+            bool bad = false;
+            if (n < p.n_max) {
+                const int64_t b = p.cu[n], e = p.cu[n + 1];
+                bad = b < 0 || e < b || e > p.t_max;
+                if (bad) s_bad = 1;
+                else c = (int)((e - b + p.seg - 1) / p.seg);
+            }
+            int x = c;                                     // inclusive prefix over the block
+            const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 31) s_warp[warp] = x;
+            __syncthreads();
+            int before = 0, total = 0;
+            for (int w = 0; w < kBlock / 32; ++w) {
+                if (w < warp) before += s_warp[w];
+                total += s_warp[w];
+            }
+            const int64_t end = base + before + x;
+            if (c > 0 && j < end && j >= end - c) {
+                s_hit[0] = n;
+                s_hit[1] = (int)(j - (end - c));
+            }
+            base += total;
+            if (__syncthreads_or(bad || (c > 0 && j < end && j >= end - c))) break;
+        }
+        if (s_bad) {
+            if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
+            return false;
+        }
+        if (s_hit[0] < 0) return false;
+        it.n = s_hit[0];
+        it.i = s_hit[1];
+        it.bos = p.cu[it.n];
+        it.eos = p.cu[it.n + 1];
+        it.s0 = it.bos + (int64_t)it.i * p.seg;
+        it.s1 = it.s0 + p.seg < it.eos ? it.s0 + p.seg : it.eos;
+        it.last = it.s1 == it.eos;
+    }
+    if (it.bos < 0 || it.eos < it.bos || it.eos > p.t_max) {
+        if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
+        return false;
+    }
+    return true;
+}
+
+// ---- host checks shared by the entry points that take gcl_rows ---------------
+inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline Rows rows(const gcl_rows &r) { return Rows{r.ptr, r.token_stride, r.head_stride}; }
+gcl_status_t check_rows(const char *fn, const char *name, const gcl_rows &r, int64_t tokens, int64_t heads, int32_t D,
+                        int32_t esize, bool output);
+gcl_status_t check_sizes(const char *fn, int32_t H, int32_t K, int32_t V, int32_t dtype);
+
+// ---- launchers ------------------------------------------------------------
+// CUDA cores, fp32 arithmetic, every dtype.  own_states: the segments' own states only (roles kFwd
+// and kDv); otherwise the outputs of the given roles.
+template <typename T>
+cudaError_t launch_simt_t(const Params &p, bool own_states, int n_roles, const int *roles, cudaStream_t s);
+cudaError_t launch_simt(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s);
+// The states that enter the segments, in place of the segments' own; ht and dh0 of empty sequences.
+cudaError_t launch_scan(const Params &p, bool backward, cudaStream_t s);
+
+}  // namespace dla
+}  // namespace gcl

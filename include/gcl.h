@@ -455,6 +455,154 @@ gcl_status_t causal_conv1d_fwd(const gcl_conv_args *args, gcl_stream_t stream);
 size_t gcl_causal_conv1d_bwd_workspace_bytes(const gcl_conv_args *args);
 gcl_status_t causal_conv1d_bwd(const gcl_conv_args *args, gcl_stream_t stream);
 
+/*
+ * Rows of a token-major tensor [tokens, heads, D] whose tokens and heads may be strided: element
+ * (t, h, d) lies at ptr + t * token_stride + h * head_stride + d, strides in elements.  So the
+ * slices of one projection's output, and head-major tensors, are passed without a copy.  Both
+ * strides are at least D and multiples of 16 bytes, and ptr is 16-byte aligned.  Rows of an
+ * output do not overlap: one stride spans the whole extent of the other.
+ */
+typedef struct gcl_rows {
+    void *ptr;
+    int64_t token_stride, head_stride;
+} gcl_rows;
+
+/*
+ * dla -- decayed linear attention: linear attention with a fixed decay for each head.  No page
+ * of the sources has it; it is the recurrence above without the delta rule and with
+ * gamma_h = exp(g_h) constant over the tokens (g is a constant of the layer: it gets no gradient).
+ * Per sequence and head, with S_-1 = h0 (zeros without h0) and L tokens:
+ *
+ *   S_t = gamma S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   ht = S_{L-1}
+ *
+ * The backward takes d_o and dht, the gradients w.r.t. o and ht (zeros without dht), and gives
+ *   G_t = gamma G_{t+1} + scale q_t do_t^T   (gamma G_L stands for dht),
+ *   dq_t = scale S_t do_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,   dh0 = gamma G_0.
+ *
+ * A zero-length sequence passes its state through (ht = h0, dh0 = dht).  gamma = 0 (g = -inf)
+ * and gamma = 1 (g = 0) are allowed; g > 0 is computed as given as long as exp(g n) over a
+ * segment's n tokens stays finite.  Token rows at or past cu_seqlens[n_max] are never read into a
+ * result nor written.  Products are formed per chunk of tokens: a token whose v (backward: v,
+ * d_o, q or k) is not finite can make other rows of its own chunk of 128 tokens not finite.
+ *
+ * Supported: K, V in {64, 128}; dtype GCL_F32, GCL_BF16, GCL_F16 for every gcl_rows; states and
+ * their gradients [n_max, H, K, V] fp32, g [H] fp32.  Sums and states are fp32.  The
+ * gradients dq, dk, dv have the type of the inputs: the projections' backward reads them so.
+ */
+typedef struct gcl_dla_args {
+    gcl_rows q, k;                 /* [t_max, H, K] dtype                                    */
+    gcl_rows v;                    /* [t_max, H, V] dtype                                    */
+    gcl_rows o;                    /* forward: [t_max, H, V] dtype (out); ptr may be NULL    */
+    gcl_rows d_o;                  /* backward: [t_max, H, V] dtype                          */
+    gcl_rows dq, dk;               /* backward: [t_max, H, K] dtype (out)                    */
+    gcl_rows dv;                   /* backward: [t_max, H, V] dtype (out)                    */
+    const float *g;                /* [H] fp32 log decay, <= 0                               */
+    const float *h0;               /* [n_max, H, K, V] fp32 or NULL                          */
+    float *ht;                     /* forward: [n_max, H, K, V] fp32 (out) or NULL           */
+    const float *dht;              /* backward: [n_max, H, K, V] fp32 or NULL                */
+    float *dh0;                    /* backward: [n_max, H, K, V] fp32 (out) or NULL          */
+    const int32_t *cu_seqlens;     /* [n_max + 1] int32                                      */
+    const int32_t *seq_order;      /* [n_max] from chunk_meta_build, or NULL (index order)   */
+    int32_t *dev_status;           /* [1] or NULL, as in gcl_fwd_args                        */
+    void *workspace;               /* device scratch, 16-byte aligned, at least              */
+    size_t workspace_bytes;        /* gcl_dla_{fwd,bwd}_workspace_bytes() bytes              */
+    int64_t t_max;
+    int32_t n_max, H, K, V;
+    float scale;                   /* read-out scale, usually K^-1/2                         */
+    int32_t dtype;                 /* gcl_dtype_t                                            */
+} gcl_dla_args;
+
+/*
+ * Tokens per segment of the plan for these capacities (a multiple of 128, or t_max or more for
+ * one segment per sequence).  With fewer sequence-head units than SMs each sequence is cut into
+ * segments: one launch sums each segment's own state, one scans the states at the segments'
+ * starts, one computes every segment from its start state.  Segments are found from cu_seqlens on
+ * the device, so the launches depend on the capacities only.  Returns 0 for invalid sizes.
+ */
+int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward);
+
+/* Bytes of workspace (0 when one segment per sequence runs); sizes and the dtype are read. */
+size_t gcl_dla_fwd_workspace_bytes(const gcl_dla_args *args);
+size_t gcl_dla_bwd_workspace_bytes(const gcl_dla_args *args);
+
+gcl_status_t dla_chunk_fwd(const gcl_dla_args *args, gcl_stream_t stream);
+gcl_status_t dla_chunk_bwd(const gcl_dla_args *args, gcl_stream_t stream);
+
+/*
+ * dla_step -- the recurrent form for single tokens: for request b and head h, with the state of
+ * slot s = slots[b] (slots NULL: s = b) updated in place,
+ *   S <- gamma S + k_b v_b^T,   o_b = scale S^T q_b.
+ * A request with a negative slot is idle (padding of a captured batch): no state is touched and its
+ * rows of o are zeros.  A slot >= n_slots sets GCL_DEV_BAD_RANGE and is treated as idle.
+ * Two requests of one call must not share a slot.
+ */
+typedef struct gcl_dla_step_args {
+    gcl_rows q, k;                 /* [batch, H, K] dtype                                    */
+    gcl_rows v;                    /* [batch, H, V] dtype                                    */
+    gcl_rows o;                    /* [batch, H, V] dtype (out)                              */
+    const float *g;                /* [H] fp32 log decay                                     */
+    float *state;                  /* [n_slots, H, K, V] fp32 (in and out)                   */
+    const int32_t *slots;          /* [batch] or NULL                                        */
+    int32_t *dev_status;           /* [1] or NULL                                            */
+    int32_t batch, n_slots, H, K, V;
+    float scale;
+    int32_t dtype;
+} gcl_dla_step_args;
+
+gcl_status_t dla_step(const gcl_dla_step_args *args, gcl_stream_t stream);
+
+/*
+ * qk_norm_rope -- norm of the queries and keys of each head and the position rotation, in one
+ * pass.  Per token t and head, for x a row of q or k with its weight w (ones without weight):
+ *   n = x / sqrt(mean(x^2) + eps)  (GCL_NORM_RMS),  x / sqrt(sum(x^2) + eps)  (GCL_NORM_L2),  x
+ *   z = n * w,   y = z with each of its first R / 2 pairs (a, b) turned by the angle of the row's
+ *   position: (a cos - b sin, a sin + b cos), the pair i being channels (i, i + R / 2)
+ *   (GCL_PAIR_HALF) or (2i, 2i + 1) (GCL_PAIR_ADJACENT); channels R and up keep z.
+ * cos and sin are the rows positions[t] of tables [n_positions, R / 2] fp32 (rope_table_build).
+ * R = 0: no rotation; the tables are not read.  A token with a negative position is padding: its
+ * rows are neither read nor written.  A position >= n_positions sets GCL_DEV_BAD_RANGE and its
+ * rows are left alone as well.  Without positions every row is live (R must be 0).
+ *
+ * The backward takes dyq, dyk and the forward's inputs and gives dq, dk and, where a weight is
+ * given, its gradient (fp32, summed over the tokens and heads in a fixed order).
+ * Arithmetic is fp32; each output is rounded once.  The forward may run in place (yq = q, yk = k
+ * with the same strides).
+ * Supported: D in {64, 128, 256}; R a multiple of 16, 0 <= R <= D; any HQ, HK >= 1 (q alone:
+ * HK = 0 and k, yk NULL); dtype GCL_F32, GCL_BF16, GCL_F16 for the rows and the weights.
+ */
+typedef enum { GCL_NORM_NONE = 0, GCL_NORM_RMS = 1, GCL_NORM_L2 = 2 } gcl_norm_t;
+typedef enum { GCL_PAIR_HALF = 0, GCL_PAIR_ADJACENT = 1 } gcl_pair_t;
+
+typedef struct gcl_qk_args {
+    gcl_rows q, k;                 /* [t_max, HQ, D], [t_max, HK, D] dtype                   */
+    gcl_rows yq, yk;               /* forward: outputs of the same shapes                    */
+    gcl_rows dyq, dyk;             /* backward: gradients w.r.t. yq, yk                      */
+    gcl_rows dq, dk;               /* backward: outputs                                      */
+    const void *q_weight, *k_weight;   /* [D] dtype or NULL, 16-byte aligned                 */
+    float *dq_weight, *dk_weight;  /* backward: [D] fp32 (out) or NULL                       */
+    const float *cos_table, *sin_table;   /* [n_positions, R / 2] fp32                       */
+    const int32_t *positions;      /* [t_max] int32 or NULL                                  */
+    int32_t *dev_status;           /* [1] or NULL                                            */
+    void *workspace;               /* backward with weight gradients:                        */
+    size_t workspace_bytes;        /*   gcl_qk_norm_rope_bwd_workspace_bytes() bytes         */
+    int64_t t_max, n_positions;
+    int32_t HQ, HK, D, R;
+    float eps;
+    int32_t norm, pair, dtype;     /* gcl_norm_t, gcl_pair_t, gcl_dtype_t                    */
+} gcl_qk_args;
+
+gcl_status_t qk_norm_rope_fwd(const gcl_qk_args *args, gcl_stream_t stream);
+size_t gcl_qk_norm_rope_bwd_workspace_bytes(const gcl_qk_args *args);
+gcl_status_t qk_norm_rope_bwd(const gcl_qk_args *args, gcl_stream_t stream);
+
+/*
+ * rope_table_build -- cos and sin [n_positions, R / 2] fp32 of the angles p base^(-2 i / R),
+ * formed in fp64 and rounded once (in fp32 the angle of position 100,000 would be off by 4e-3).
+ * R even and positive, base > 0.
+ */
+gcl_status_t rope_table_build(float *cos_table, float *sin_table, int64_t n_positions, int32_t R,
+                              double base, gcl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
