@@ -92,8 +92,8 @@ cudaError_t launch_scan(const Params &p, bool backward, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_simt(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s) {
-    if (dtype == GCL_BF16) return launch_simt_t<__nv_bfloat16>(p, own_states, n_roles, roles, s);
+cudaError_t launch(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s) {
+    if (dtype == GCL_BF16) return launch_tc(p, own_states, n_roles, roles, s);
     if (dtype == GCL_F16) return launch_simt_t<__half>(p, own_states, n_roles, roles, s);
     return launch_simt_t<float>(p, own_states, n_roles, roles, s);
 }
@@ -169,8 +169,8 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
         return fail(GCL_ERR_INVALID_ARG, "%s: need 1 <= t_max < 2^31 and n_max >= 1", fn);
     gcl_status_t st = check_sizes(fn, a->H, a->K, a->V, a->dtype);
     if (st != GCL_OK) return st;
-    if ((int64_t)a->n_max * a->H >= (int64_t(1) << 31))
-        return fail(GCL_ERR_UNSUPPORTED, "%s: n_max * H must be below 2^31", fn);
+    if ((int64_t)a->n_max * a->H >= (int64_t(1) << 29))
+        return fail(GCL_ERR_UNSUPPORTED, "%s: n_max * H must be below 2^29", fn);
     const int es = a->dtype == GCL_F32 ? 4 : 2;
     struct { const char *name; const gcl_rows *r; int32_t D; bool in, out; } need[] = {
         {"q", &a->q, a->K, true, false}, {"k", &a->k, a->K, true, false}, {"v", &a->v, a->V, true, false},
@@ -207,10 +207,10 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
     if (bytes) {
         p.seg_fwd = static_cast<float *>(a->workspace);
         if (backward) p.seg_rev = p.seg_fwd + bytes / 2 / sizeof(float);
-        e = launch_simt(p, a->dtype, true, backward ? 2 : 1, both, s);
+        e = launch(p, a->dtype, true, backward ? 2 : 1, both, s);
         if (e == cudaSuccess) e = launch_scan(p, backward, s);
     }
-    if (e == cudaSuccess) e = launch_simt(p, a->dtype, false, backward ? 3 : 1, backward ? out : both, s);
+    if (e == cudaSuccess) e = launch(p, a->dtype, false, backward ? 3 : 1, backward ? out : both, s);
     return cuda_check(e, fn);
 }
 

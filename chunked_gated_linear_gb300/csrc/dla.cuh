@@ -43,8 +43,20 @@ struct Params {
     int32_t seg;                   // tokens per segment
     int32_t n_max, H, K, V;
     float scale;
-    uint32_t roles;                // the role of blockIdx.z, 2 bits each
+    int32_t n_roles;               // roles of this launch: block b of (row, head) u has b = u n_roles + r
+    uint32_t roles;                // role r, 2 bits each
 };
+
+// Host: the given roles whose states have shape 0 ([K, V]: kFwd, kDv; every role when K = V) or 1 ([V, K]).
+inline bool take_roles(Params &p, int n_roles, const int *roles, int shape) {
+    p.n_roles = 0;
+    p.roles = 0;
+    for (int i = 0; i < n_roles; ++i) {
+        const bool trans = roles[i] == kDq || roles[i] == kDk;
+        if (p.K != p.V ? trans == (shape == 1) : shape == 0) p.roles |= (uint32_t)roles[i] << (2 * p.n_roles++);
+    }
+    return p.n_roles > 0;
+}
 
 // Row t of head h.
 template <typename T>
@@ -148,11 +160,13 @@ gcl_status_t check_rows(const char *fn, const char *name, const gcl_rows &r, int
 gcl_status_t check_sizes(const char *fn, int32_t H, int32_t K, int32_t V, int32_t dtype);
 
 // ---- launchers ------------------------------------------------------------
-// CUDA cores, fp32 arithmetic, every dtype.  own_states: the segments' own states only (roles kFwd
+// CUDA cores, fp32 arithmetic (fp32 and fp16 rows).  own_states: the segments' own states only (roles kFwd
 // and kDv); otherwise the outputs of the given roles.
 template <typename T>
 cudaError_t launch_simt_t(const Params &p, bool own_states, int n_roles, const int *roles, cudaStream_t s);
-cudaError_t launch_simt(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s);
+cudaError_t launch(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s);
+// Tensor cores, bf16.
+cudaError_t launch_tc(const Params &p, bool own_states, int n_roles, const int *roles, cudaStream_t s);
 // The states that enter the segments, in place of the segments' own; ht and dh0 of empty sequences.
 cudaError_t launch_scan(const Params &p, bool backward, cudaStream_t s);
 

@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(kSimtThreads) dla_simt_kernel(const Params p) 
           *sP = sm + Lay::oP;
     if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int h = blockIdx.x % p.H;
-    const int64_t row = blockIdx.x / p.H;
-    const int role = (p.roles >> (2 * blockIdx.z)) & 3;
+    const int unit = blockIdx.x / p.n_roles, h = unit % p.H;
+    const int64_t row = unit / p.H;
+    const int role = (p.roles >> (2 * (blockIdx.x % p.n_roles))) & 3;
     const bool rev = role >= kDv, trans = role == kDq || role == kDk;
     Item it;
     if (!find_item<kSimtThreads>(p, row, it)) return;
@@ -298,12 +298,12 @@ __global__ void __launch_bounds__(kSimtThreads) dla_simt_kernel(const Params p) 
 }
 
 template <typename T, int NA, int NV, bool OWN>
-cudaError_t launch_simt_one(const Params &p, int n_roles, cudaStream_t s) {
+cudaError_t launch_simt_one(const Params &p, cudaStream_t s) {
     auto kern = dla_simt_kernel<T, NA, NV, OWN>;
     constexpr size_t smem = SimtLayout<NA, NV>::bytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(p.n_rows * p.H), 1, n_roles), kSimtThreads, smem, s>>>(p);
+    kern<<<(unsigned)(p.n_rows * p.H * p.n_roles), kSimtThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -312,25 +312,19 @@ template <typename T>
 cudaError_t launch_simt_t(const Params &p0, bool own_states, int n_roles, const int *roles, cudaStream_t s) {
     for (int shape = 0; shape < 2; ++shape) {
         Params p = p0;
-        int count = 0;
-        p.roles = 0;
-        for (int i = 0; i < n_roles; ++i) {
-            const bool trans = roles[i] == kDq || roles[i] == kDk;
-            if (p.K != p.V ? trans == (shape == 1) : shape == 0) p.roles |= (uint32_t)roles[i] << (2 * count++);
-        }
-        if (count == 0) continue;
+        if (!take_roles(p, n_roles, roles, shape)) continue;
         const int na = shape == 0 ? p.K : p.V, nv = shape == 0 ? p.V : p.K;
         cudaError_t e = cudaErrorInvalidValue;
         if (own_states) {
-            if (na == 64 && nv == 64) e = launch_simt_one<T, 64, 64, true>(p, count, s);
-            if (na == 64 && nv == 128) e = launch_simt_one<T, 64, 128, true>(p, count, s);
-            if (na == 128 && nv == 64) e = launch_simt_one<T, 128, 64, true>(p, count, s);
-            if (na == 128 && nv == 128) e = launch_simt_one<T, 128, 128, true>(p, count, s);
+            if (na == 64 && nv == 64) e = launch_simt_one<T, 64, 64, true>(p, s);
+            if (na == 64 && nv == 128) e = launch_simt_one<T, 64, 128, true>(p, s);
+            if (na == 128 && nv == 64) e = launch_simt_one<T, 128, 64, true>(p, s);
+            if (na == 128 && nv == 128) e = launch_simt_one<T, 128, 128, true>(p, s);
         } else {
-            if (na == 64 && nv == 64) e = launch_simt_one<T, 64, 64, false>(p, count, s);
-            if (na == 64 && nv == 128) e = launch_simt_one<T, 64, 128, false>(p, count, s);
-            if (na == 128 && nv == 64) e = launch_simt_one<T, 128, 64, false>(p, count, s);
-            if (na == 128 && nv == 128) e = launch_simt_one<T, 128, 128, false>(p, count, s);
+            if (na == 64 && nv == 64) e = launch_simt_one<T, 64, 64, false>(p, s);
+            if (na == 64 && nv == 128) e = launch_simt_one<T, 64, 128, false>(p, s);
+            if (na == 128 && nv == 64) e = launch_simt_one<T, 128, 64, false>(p, s);
+            if (na == 128 && nv == 128) e = launch_simt_one<T, 128, 128, false>(p, s);
         }
         if (e != cudaSuccess) return e;
     }
