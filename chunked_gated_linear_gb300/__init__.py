@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import inspect
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgcl.so")
@@ -532,15 +533,41 @@ def causal_conv1d_bwd(*args, stream=None, **kw):
 
 
 # ------------------------------------------------- decayed linear attention, norm and rotation
-# These calls take strided rows and are also made for single tokens, so their checks are plain
-# comparisons on each tensor (a few microseconds a call).
+# These calls take strided rows and are also made for single tokens, where the host's time counts:
+# each tensor is checked by plain comparisons, and the argument struct is packed in one go (the
+# layouts of DlaArgs, DlaStepArgs and QkArgs above, which the C structs share).
+_ROWS_FMT = "Pqq"
+_DLA_PACK = struct.Struct("@" + _ROWS_FMT * 8 + "PPPPPPPPPNqiiiifi0q")
+_STEP_PACK = struct.Struct("@" + _ROWS_FMT * 4 + "PPPPiiiiifi0q")
+_QK_PACK = struct.Struct("@" + _ROWS_FMT * 8 + "PPPPPPPPPNqqiiiifiii0q")
+_NO_ROWS = (0, 0, 0)
+
+
+def _packed_call(fn, packed, stream, device):
+    """Calls entry point `fn` of the loaded library with a packed argument struct."""
+    handle = lib()
+    entry = handle.__dict__.get("_packed_" + fn)
+    if entry is None:
+        entry = handle._FuncPtr((fn, handle))
+        entry.restype, entry.argtypes = ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]
+        handle.__dict__["_packed_" + fn] = entry
+    if stream is None:
+        import torch
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    st = entry(packed, stream)
+    if st != 0:
+        _check(fn, st)
+
+
 def _rows(fn, name, t, shape, dtype, device):
     """gcl_rows of a tensor [tokens, heads, D] with contiguous D and any token and head strides."""
     if t.get_device() != device or device < 0:
         raise ValueError(f"{fn}: {name} must be a CUDA tensor on the call's device (got {t.device})")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
     st, sh, sd = t.stride()
     if sd != 1:
@@ -549,14 +576,16 @@ def _rows(fn, name, t, shape, dtype, device):
         sh = shape[2]
     if shape[0] == 1:
         st = shape[1] * sh
-    return Rows(t.data_ptr(), st, sh)
+    if st < 0 or sh < 0:
+        raise ValueError(f"{fn}: {name} has negative strides {t.stride()}")
+    return t.data_ptr(), st, sh
 
 
 def _flat(fn, name, t, shape, dtype, device):
-    """Pointer of a contiguous tensor of exactly this shape, or None."""
+    """Pointer of a contiguous tensor of exactly this shape; 0 for None."""
     if t is None:
-        return None
-    if t.get_device() != device or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        return 0
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous CUDA tensor {shape} of {dtype} on the "
                          f"call's device (got {tuple(t.shape)}, {t.dtype}, {t.device})")
     return t.data_ptr()
@@ -564,7 +593,7 @@ def _flat(fn, name, t, shape, dtype, device):
 
 def _scratch(fn, t, device):
     if t is None:
-        return None, 0
+        return 0, 0
     if t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor on the call's device")
     return t.data_ptr(), t.numel() * t.element_size()
@@ -590,103 +619,100 @@ def dla_bwd_workspace_bytes(q, v, cu_seqlens) -> int:
     return int(lib().gcl_dla_bwd_workspace_bytes(ctypes.byref(_dla_sizes(q, v, cu_seqlens))))
 
 
-def _dla_common(fn, q, k, v, g, cu_seqlens, h0, seq_order, dev_status, workspace, scale):
-    import torch
-    T, H, K = q.shape
-    V, N, dt, dev = v.shape[2], cu_seqlens.shape[0] - 1, q.dtype, q.get_device()
-    f32, i32 = torch.float32, torch.int32
-    ws, wsb = _scratch(fn, workspace, dev)
-    a = DlaArgs(q=_rows(fn, "q", q, (T, H, K), dt, dev), k=_rows(fn, "k", k, (T, H, K), dt, dev),
-                v=_rows(fn, "v", v, (T, H, V), dt, dev), g=_flat(fn, "g", g, (H,), f32, dev),
-                h0=_flat(fn, "h0", h0, (N, H, K, V), f32, dev),
-                cu_seqlens=_flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev),
-                seq_order=_flat(fn, "seq_order", seq_order, (N,), i32, dev),
-                dev_status=_flat(fn, "dev_status", dev_status, (1,), i32, dev), workspace=ws,
-                workspace_bytes=wsb, t_max=T, n_max=N, H=H, K=K, V=V,
-                scale=float(K ** -0.5 if scale is None else scale), dtype=_dtype_of(q))
-    return a, (T, H, K, V, N, dt, dev)
-
-
 def dla_chunk_fwd(q, k, v, g, cu_seqlens, o, h0=None, ht=None, seq_order=None, dev_status=None,
                   workspace=None, scale=None, stream=None):
     """Linear attention with the fixed log decay g [H] over packed sequences (include/gcl.h, dla):
     o [T, H, V] (None: only ht) and ht from q, k [T, H, K], v [T, H, V] and h0.  q, k, v and o may
     have strided tokens and heads."""
-    import torch
+    from torch import float32 as f32, int32 as i32
     fn = "dla_chunk_fwd"
-    a, (T, H, K, V, N, dt, dev) = _dla_common(fn, q, k, v, g, cu_seqlens, h0, seq_order, dev_status,
-                                              workspace, scale)
-    if o is not None:
-        a.o = _rows(fn, "o", o, (T, H, V), dt, dev)
-    a.ht = _flat(fn, "ht", ht, (N, H, K, V), torch.float32, dev)
-    _check(fn, lib().dla_chunk_fwd(ctypes.byref(a), _stream(stream)))
+    sk = tuple(q.shape)
+    T, H, K = sk
+    V, N, dt, dev = v.shape[2], cu_seqlens.shape[0] - 1, q.dtype, q.get_device()
+    sv, ss = (T, H, V), (N, H, K, V)
+    packed = _DLA_PACK.pack(
+        *_rows(fn, "q", q, sk, dt, dev), *_rows(fn, "k", k, sk, dt, dev), *_rows(fn, "v", v, sv, dt, dev),
+        *(_NO_ROWS if o is None else _rows(fn, "o", o, sv, dt, dev)), *_NO_ROWS, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
+        _flat(fn, "g", g, (H,), f32, dev), _flat(fn, "h0", h0, ss, f32, dev), _flat(fn, "ht", ht, ss, f32, dev), 0, 0,
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "seq_order", seq_order, (N,), i32, dev),
+        _flat(fn, "dev_status", dev_status, (1,), i32, dev), *_scratch(fn, workspace, dev), T, N, H, K, V,
+        K ** -0.5 if scale is None else scale, _dtype_of(q))
+    _packed_call(fn, packed, stream, dev)
 
 
 def dla_chunk_bwd(q, k, v, g, d_o, cu_seqlens, dq, dk, dv, h0=None, dht=None, dh0=None,
                   seq_order=None, dev_status=None, workspace=None, scale=None, stream=None):
     """The backward of dla_chunk_fwd: dq, dk, dv (of q's dtype) and dh0 from d_o and dht."""
-    import torch
+    from torch import float32 as f32, int32 as i32
     fn = "dla_chunk_bwd"
-    a, (T, H, K, V, N, dt, dev) = _dla_common(fn, q, k, v, g, cu_seqlens, h0, seq_order, dev_status,
-                                              workspace, scale)
-    a.d_o = _rows(fn, "d_o", d_o, (T, H, V), dt, dev)
-    a.dq = _rows(fn, "dq", dq, (T, H, K), dt, dev)
-    a.dk = _rows(fn, "dk", dk, (T, H, K), dt, dev)
-    a.dv = _rows(fn, "dv", dv, (T, H, V), dt, dev)
-    a.dht = _flat(fn, "dht", dht, (N, H, K, V), torch.float32, dev)
-    a.dh0 = _flat(fn, "dh0", dh0, (N, H, K, V), torch.float32, dev)
-    _check(fn, lib().dla_chunk_bwd(ctypes.byref(a), _stream(stream)))
+    sk = tuple(q.shape)
+    T, H, K = sk
+    V, N, dt, dev = v.shape[2], cu_seqlens.shape[0] - 1, q.dtype, q.get_device()
+    sv, ss = (T, H, V), (N, H, K, V)
+    packed = _DLA_PACK.pack(
+        *_rows(fn, "q", q, sk, dt, dev), *_rows(fn, "k", k, sk, dt, dev), *_rows(fn, "v", v, sv, dt, dev), *_NO_ROWS,
+        *_rows(fn, "d_o", d_o, sv, dt, dev), *_rows(fn, "dq", dq, sk, dt, dev), *_rows(fn, "dk", dk, sk, dt, dev),
+        *_rows(fn, "dv", dv, sv, dt, dev), _flat(fn, "g", g, (H,), f32, dev), _flat(fn, "h0", h0, ss, f32, dev), 0,
+        _flat(fn, "dht", dht, ss, f32, dev), _flat(fn, "dh0", dh0, ss, f32, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "seq_order", seq_order, (N,), i32, dev),
+        _flat(fn, "dev_status", dev_status, (1,), i32, dev), *_scratch(fn, workspace, dev), T, N, H, K, V,
+        K ** -0.5 if scale is None else scale, _dtype_of(q))
+    _packed_call(fn, packed, stream, dev)
 
 
 def dla_step(q, k, v, g, state, o, slots=None, dev_status=None, scale=None, stream=None):
     """One token of each request: the states [n_slots, H, K, V] of the requests' slots are updated
     in place and o [B, H, V] is written (include/gcl.h, dla_step).  slots int32 [B]; negative: idle."""
-    import torch
+    from torch import float32 as f32, int32 as i32
     fn = "dla_step"
-    B, H, K = q.shape
-    V, dt, dev = v.shape[2], q.dtype, q.get_device()
-    n_slots = state.shape[0]
-    a = DlaStepArgs(q=_rows(fn, "q", q, (B, H, K), dt, dev), k=_rows(fn, "k", k, (B, H, K), dt, dev),
-                    v=_rows(fn, "v", v, (B, H, V), dt, dev), o=_rows(fn, "o", o, (B, H, V), dt, dev),
-                    g=_flat(fn, "g", g, (H,), torch.float32, dev),
-                    state=_flat(fn, "state", state, (n_slots, H, K, V), torch.float32, dev),
-                    slots=_flat(fn, "slots", slots, (B,), torch.int32, dev),
-                    dev_status=_flat(fn, "dev_status", dev_status, (1,), torch.int32, dev), batch=B,
-                    n_slots=n_slots, H=H, K=K, V=V,
-                    scale=float(K ** -0.5 if scale is None else scale), dtype=_dtype_of(q))
-    _check(fn, lib().dla_step(ctypes.byref(a), _stream(stream)))
+    sk = tuple(q.shape)
+    B, H, K = sk
+    V, dt, dev, n_slots = v.shape[2], q.dtype, q.get_device(), state.shape[0]
+    sv = (B, H, V)
+    packed = _STEP_PACK.pack(
+        *_rows(fn, "q", q, sk, dt, dev), *_rows(fn, "k", k, sk, dt, dev), *_rows(fn, "v", v, sv, dt, dev),
+        *_rows(fn, "o", o, sv, dt, dev), _flat(fn, "g", g, (H,), f32, dev),
+        _flat(fn, "state", state, (n_slots, H, K, V), f32, dev), _flat(fn, "slots", slots, (B,), i32, dev),
+        _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, H, K, V,
+        K ** -0.5 if scale is None else scale, _dtype_of(q))
+    _packed_call(fn, packed, stream, dev)
 
 
 NORMS = {None: 0, "none": 0, "rms": 1, "l2": 2}
 PAIRINGS = {"half": 0, "adjacent": 1}
 
 
-def _qk_common(fn, q, k, q_weight, k_weight, cos, sin, positions, norm, eps, pairing, dev_status):
-    import torch
-    T, HQ, D = q.shape
+def _qk_call(fn, q, k, yq, yk, dyq, dyk, dq, dk, q_weight, k_weight, dq_weight, dk_weight, cos, sin, positions, norm,
+             eps, pairing, workspace, dev_status, stream, backward):
+    from torch import float32 as f32, int32 as i32
+    sq = tuple(q.shape)
+    T, HQ, D = sq
     HK = 0 if k is None else k.shape[1]
-    dt, dev = q.dtype, q.get_device()
-    f32, i32 = torch.float32, torch.int32
+    sk, dt, dev = (T, HK, D), q.dtype, q.get_device()
     if norm not in NORMS or pairing not in PAIRINGS:
         raise ValueError(f"{fn}: norm {norm!r} or pairing {pairing!r} is not one of {tuple(NORMS)}, "
                          f"{tuple(PAIRINGS)}")
-    a = QkArgs(q=_rows(fn, "q", q, (T, HQ, D), dt, dev),
-               q_weight=_flat(fn, "q_weight", q_weight, (D,), dt, dev),
-               k_weight=_flat(fn, "k_weight", k_weight, (D,), dt, dev),
-               positions=_flat(fn, "positions", positions, (T,), i32, dev),
-               dev_status=_flat(fn, "dev_status", dev_status, (1,), i32, dev), t_max=T, HQ=HQ,
-               HK=HK, D=D, eps=float(eps), norm=NORMS[norm], pair=PAIRINGS[pairing],
-               dtype=_dtype_of(q))
-    if HK:
-        a.k = _rows(fn, "k", k, (T, HK, D), dt, dev)
+    P = half = c = s = 0
     if (cos is None) != (sin is None):
         raise ValueError(f"{fn}: cos and sin come together")
     if cos is not None:
         P, half = cos.shape
-        a.cos_table = _flat(fn, "cos", cos, (P, half), f32, dev)
-        a.sin_table = _flat(fn, "sin", sin, (P, half), f32, dev)
-        a.n_positions, a.R = P, 2 * half
-    return a, (T, HQ, HK, D, dt, dev)
+        c, s = _flat(fn, "cos", cos, (P, half), f32, dev), _flat(fn, "sin", sin, (P, half), f32, dev)
+    rq = _rows(fn, "q", q, sq, dt, dev)
+    rk = _rows(fn, "k", k, sk, dt, dev) if HK else _NO_ROWS
+    if backward:
+        out = (*_NO_ROWS, *_NO_ROWS, *_rows(fn, "dyq", dyq, sq, dt, dev),
+               *(_rows(fn, "dyk", dyk, sk, dt, dev) if HK else _NO_ROWS), *_rows(fn, "dq", dq, sq, dt, dev),
+               *(_rows(fn, "dk", dk, sk, dt, dev) if HK else _NO_ROWS))
+    else:
+        out = (*_rows(fn, "yq", yq, sq, dt, dev), *(_rows(fn, "yk", yk, sk, dt, dev) if HK else _NO_ROWS),
+               *_NO_ROWS, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS)
+    packed = _QK_PACK.pack(
+        *rq, *rk, *out, _flat(fn, "q_weight", q_weight, (D,), dt, dev), _flat(fn, "k_weight", k_weight, (D,), dt, dev),
+        _flat(fn, "dq_weight", dq_weight, (D,), f32, dev), _flat(fn, "dk_weight", dk_weight, (D,), f32, dev), c, s,
+        _flat(fn, "positions", positions, (T,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        *_scratch(fn, workspace, dev), T, P, HQ, HK, D, 2 * half, eps, NORMS[norm], PAIRINGS[pairing], _dtype_of(q))
+    _packed_call(fn, packed, stream, dev)
 
 
 def qk_norm_rope_fwd(q, k, yq, yk, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
@@ -694,13 +720,8 @@ def qk_norm_rope_fwd(q, k, yq, yk, q_weight=None, k_weight=None, cos=None, sin=N
     """Norm of each head's queries [T, HQ, D] and keys [T, HK, D] (k None: queries alone) and the
     rotation by the rows `positions` of cos, sin [P, R / 2], in one pass (include/gcl.h,
     qk_norm_rope)."""
-    fn = "qk_norm_rope_fwd"
-    a, (T, HQ, HK, D, dt, dev) = _qk_common(fn, q, k, q_weight, k_weight, cos, sin, positions, norm,
-                                            eps, pairing, dev_status)
-    a.yq = _rows(fn, "yq", yq, (T, HQ, D), dt, dev)
-    if HK:
-        a.yk = _rows(fn, "yk", yk, (T, HK, D), dt, dev)
-    _check(fn, lib().qk_norm_rope_fwd(ctypes.byref(a), _stream(stream)))
+    _qk_call("qk_norm_rope_fwd", q, k, yq, yk, None, None, None, None, q_weight, k_weight, None, None, cos, sin,
+             positions, norm, eps, pairing, None, dev_status, stream, False)
 
 
 def qk_norm_rope_bwd_workspace_bytes(q, k) -> int:
@@ -714,28 +735,18 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, dq, dk, q_weight=None, k_weight=None, dq_we
                      dk_weight=None, cos=None, sin=None, positions=None, norm="rms", eps=1e-6,
                      pairing="half", workspace=None, dev_status=None, stream=None):
     """The backward of qk_norm_rope_fwd: dq, dk from dyq, dyk, and the weights' gradients fp32 [D]."""
-    import torch
-    fn = "qk_norm_rope_bwd"
-    a, (T, HQ, HK, D, dt, dev) = _qk_common(fn, q, k, q_weight, k_weight, cos, sin, positions, norm,
-                                            eps, pairing, dev_status)
-    a.dyq, a.dq = _rows(fn, "dyq", dyq, (T, HQ, D), dt, dev), _rows(fn, "dq", dq, (T, HQ, D), dt, dev)
-    if HK:
-        a.dyk = _rows(fn, "dyk", dyk, (T, HK, D), dt, dev)
-        a.dk = _rows(fn, "dk", dk, (T, HK, D), dt, dev)
-    a.dq_weight = _flat(fn, "dq_weight", dq_weight, (D,), torch.float32, dev)
-    a.dk_weight = _flat(fn, "dk_weight", dk_weight, (D,), torch.float32, dev)
-    a.workspace, a.workspace_bytes = _scratch(fn, workspace, dev)
-    _check(fn, lib().qk_norm_rope_bwd(ctypes.byref(a), _stream(stream)))
+    _qk_call("qk_norm_rope_bwd", q, k, None, None, dyq, dyk, dq, dk, q_weight, k_weight, dq_weight, dk_weight, cos, sin,
+             positions, norm, eps, pairing, workspace, dev_status, stream, True)
 
 
 def rope_table_build(cos, sin, base: float = 10000.0, stream=None):
     """Fills the tables cos, sin [P, R / 2] fp32 with the angles p base^(-2 i / R)."""
-    import torch
+    from torch import float32 as f32
     fn = "rope_table_build"
     if cos.dim() != 2:
         raise ValueError(f"{fn}: cos must be [positions, R / 2]")
     shape, dev = tuple(cos.shape), cos.get_device()
     if dev < 0:
         raise ValueError(f"{fn}: cos must be a CUDA tensor (got {cos.device})")
-    c, s = _flat(fn, "cos", cos, shape, torch.float32, dev), _flat(fn, "sin", sin, shape, torch.float32, dev)
+    c, s = _flat(fn, "cos", cos, shape, f32, dev), _flat(fn, "sin", sin, shape, f32, dev)
     _check(fn, lib().rope_table_build(c, s, shape[0], 2 * shape[1], float(base), _stream(stream)))

@@ -7,8 +7,9 @@
 //   dx = r (u - x r^2 sum(u x) / D)   (RMS; L2 without / D),   dw = sum over rows of dz n.
 // HBM-bound: rows are read and written once (the backward reads x and dy, writes dx).  D / 8 lanes
 // hold one row, 16 bytes (fp32: 32) each; sums over a row are shuffles inside those lanes, and the
-// partner of a half-split pair sits R / 16 lanes away.  Lanes keep one token for several heads, so
-// that its cos and sin rows and the weights are loaded once for them.
+// partner of a half-split pair sits R / 16 lanes away.  Lanes keep one token for up to four heads: its
+// cos and sin rows and the weights are loaded once for them, and the rows of all four are in flight
+// together (one row at a time left HBM at half its rate).
 #include "dla.cuh"
 #include "dla_simt.cuh"
 
@@ -35,7 +36,6 @@ struct QkParams {
     int64_t t_max, n_pos;
     int32_t R, norm, pair;
     float eps;
-    int32_t per;                   // heads per lane group and step
     int32_t groups[2];             // head groups of q and of k for each token
 };
 
@@ -104,48 +104,78 @@ __device__ __forceinline__ void angles(const QkParams &p, int64_t pos, int l, fl
     }
 }
 
-// One lane group (D / 8 lanes) takes heads [h0, h0 + per) of one token of q or k at a time; groups
-// walk the (token, head group) pairs with the grid's stride.  Lanes without work stay for the
-// shuffles.  BWD: y gets dx, and the weights' gradients are summed per block.
-template <typename T, int D, bool BWD>
+// Eight consecutive values of a row as loaded.
+template <typename T>
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = reinterpret_cast<const uint4 *>(p)[e];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float *x) const { dla::load8f(reinterpret_cast<const T *>(v), x); }
+};
+
+// One lane group (D / 8 lanes) takes PER heads of one token of q or k at a time; groups walk the (token,
+// head group) pairs with the grid's stride.  Lanes without work stay for the shuffles.  BWD: y gets
+// dx, and the weights' gradients are summed per block.
+template <typename T, int D, bool BWD, int PER>
 __global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p) {
     constexpr int L = D / 8, G = kThreads / L;             // lanes per row, lane groups per block
     __shared__ float s_dw[BWD ? 2 : 1][BWD ? G : 1][BWD ? D : 1];
     if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, l = tid % L, grp = tid / L;
-    const int per_token = p.groups[0] + p.groups[1];
+    const uint32_t per_token = p.groups[0] + p.groups[1];
     const int64_t work = p.t_max * per_token;
     float dw[BWD ? 2 : 1][8] = {};
     for (int64_t i0 = (int64_t)blockIdx.x * G; i0 < work; i0 += (int64_t)gridDim.x * G) {
         const int64_t i = i0 + grp;
         bool live = i < work;
-        const int64_t t = live ? i / per_token : 0;
-        int hg = live ? (int)(i % per_token) : 0;
+        int64_t t = 0;
+        int hg = 0;
+        if (live) {
+            t = i >> 32 ? i / per_token : (uint32_t)i / per_token;
+            hg = (int)(i - t * per_token);
+        }
         const int which = hg < p.groups[0] ? 0 : 1;
-        hg -= which ? p.groups[0] : 0;
         const Side &sd = p.side[which];
+        const int h0 = (hg - (which ? p.groups[0] : 0)) * PER;
         float c[8] = {}, s[8] = {};
+        int64_t pos = 0;
         if (live && p.pos) {
-            const int64_t pos = p.pos[t];
+            pos = p.pos[t];
             live = pos >= 0;
             if (p.R > 0 && pos >= p.n_pos) {
                 live = false;
                 status_set(p.status, GCL_DEV_BAD_RANGE);
             }
-            if (live && p.R > 0) angles(p, pos, l, c, s);
         }
+        Raw<T> xr[PER], dr[BWD ? PER : 1];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const bool on = live && h0 + j < sd.H;
+            if (on) xr[j].load(row_ptr<const T>(sd.x, t, h0 + j) + l * 8);
+            else xr[j].zero();
+            if (BWD) {
+                if (on) dr[j].load(row_ptr<const T>(sd.dy, t, h0 + j) + l * 8);
+                else dr[j].zero();
+            }
+        }
+        if (live && p.R > 0) angles(p, pos, l, c, s);
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = 1.f;
         if (sd.w) dla::load8f(static_cast<const T *>(sd.w) + l * 8, w);
-        const int h0 = hg * p.per, h1 = h0 + p.per < sd.H ? h0 + p.per : sd.H;
-        for (int h = h0; h < h0 + p.per; ++h) {            // (the same count for every lane of the warp)
-            const bool on = live && h < h1;
-            float x[8] = {}, y[8] = {};
-            if (on) {
-                dla::load8f(row_ptr<const T>(sd.x, t, h) + l * 8, x);
-                if (BWD) dla::load8f(row_ptr<const T>(sd.dy, t, h) + l * 8, y);
-            }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int h = h0 + j;
+            const bool on = live && h < sd.H;
+            float x[8], y[8];
+            xr[j].get(x);
+            if (BWD) dr[j].get(y);
             float r = 1.f;
             if (p.norm != GCL_NORM_NONE) {
                 float ss = 0.f;
@@ -235,29 +265,33 @@ int bwd_blocks(int64_t t_max, int32_t HQ, int32_t HK, int D) {
     return (int)(most < want ? most : want);
 }
 
-template <typename T, int D>
-cudaError_t launch_qk(QkParams &p, bool backward, cudaStream_t s) {
+template <typename T, int D, int PER>
+cudaError_t launch_qk_per(QkParams &p, bool backward, cudaStream_t s) {
     const int64_t G = kThreads / (D / 8), sms = num_sms();
-    const int64_t rows = p.t_max * ((int64_t)p.side[0].H + p.side[1].H);
-    // heads per lane group: four share a token's angles and weights once there are rows for two
-    // full waves; few rows are spread one by one, for latency
-    p.per = rows >= 4 * 16 * sms * G ? 4 : 1;
-    for (int i = 0; i < 2; ++i) p.groups[i] = (p.side[i].H + p.per - 1) / p.per;
+    for (int i = 0; i < 2; ++i) p.groups[i] = (p.side[i].H + PER - 1) / PER;
     const int64_t work = p.t_max * (p.groups[0] + p.groups[1]);
     const int64_t most = (work + G - 1) / G;
     if (!backward) {
-        qk_kernel<T, D, false><<<(unsigned)(most < 8 * sms ? most : 8 * sms), kThreads, 0, s>>>(p);
+        qk_kernel<T, D, false, PER><<<(unsigned)(most < 16 * sms ? most : 16 * sms), kThreads, 0, s>>>(p);
         return cudaGetLastError();
     }
     const int cap = bwd_blocks(p.t_max, p.side[0].H, p.side[1].H, D);
     const int blocks = (int)(most < cap ? most : cap);
-    qk_kernel<T, D, true><<<blocks, kThreads, 0, s>>>(p);
+    qk_kernel<T, D, true, PER><<<blocks, kThreads, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && (p.side[0].partial || p.side[1].partial)) {
         qk_dw_kernel<<<dim3(D / 32, 2), 256, 0, s>>>(p, blocks, D);
         e = cudaGetLastError();
     }
     return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_qk(QkParams &p, bool backward, cudaStream_t s) {
+    // four heads per lane group once there are rows for two full waves; few rows are spread one by one,
+    // for latency
+    const int64_t G = kThreads / (D / 8), rows = p.t_max * ((int64_t)p.side[0].H + p.side[1].H);
+    return rows >= 4 * 16 * (int64_t)num_sms() * G ? launch_qk_per<T, D, 4>(p, backward, s) : launch_qk_per<T, D, 1>(p, backward, s);
 }
 
 template <typename T>

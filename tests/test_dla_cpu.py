@@ -185,3 +185,19 @@ def test_binding_refuses_host_tensors_and_shapes(gcl):
             call()
     with pytest.raises(ValueError, match="norm"):
         gcl.qk_norm_rope_fwd(q, q, q, q, norm="layer")
+
+
+def test_packed_structs_match_the_declared_ones(gcl):
+    """The packed argument layouts have the size and the field offsets of the ctypes structs."""
+    for pack, cls in ((gcl._DLA_PACK, gcl.DlaArgs), (gcl._STEP_PACK, gcl.DlaStepArgs), (gcl._QK_PACK, gcl.QkArgs)):
+        assert pack.size == ctypes.sizeof(cls)
+        kinds = []
+        for _, t in cls._fields_:
+            kinds += [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64] if t is gcl.Rows else [t]
+        values = [float(i) if t is ctypes.c_float else i for i, t in enumerate(kinds, start=1)]
+        a = cls.from_buffer_copy(pack.pack(*values))
+        got = []
+        for name, t in cls._fields_:
+            x = getattr(a, name)
+            got += [x.ptr, x.token_stride, x.head_stride] if t is gcl.Rows else [x]
+        assert got == values
