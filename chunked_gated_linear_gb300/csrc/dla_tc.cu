@@ -37,6 +37,7 @@
 #include <cudaTypedefs.h>
 
 #include "dla.cuh"
+#include "f32x2.cuh"
 #include "op16.cuh"
 #include "tc_ptx.cuh"
 
@@ -171,27 +172,7 @@ struct Ctx {                       // what every warp of a CTA needs of its work
     }
 };
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t r) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
-    return f;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
+// Two fp32 values (f32x2.cuh) to and from two bf16 ones.
 __device__ __forceinline__ uint32_t pack(uint64_t a) {
     const float2 f = unpair(a);
     return Op16<BF>::pack2(f.x, f.y);

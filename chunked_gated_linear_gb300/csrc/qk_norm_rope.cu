@@ -7,11 +7,14 @@
 //   dx = r (u - x r^2 sum(u x) / D)   (RMS; L2 without / D),   dw = sum over rows of dz n.
 // HBM-bound: rows are read and written once (the backward reads x and dy, writes dx).  D / 8 lanes
 // hold one row, 16 bytes (fp32: 32) each; sums over a row are shuffles inside those lanes, and the
-// partner of a half-split pair sits R / 16 lanes away.  Lanes keep one token for up to four heads: its
-// cos and sin rows and the weights are loaded once for them, and the rows of all four are in flight
-// together (one row at a time left HBM at half its rate).
+// partner of a half-split pair sits R / 16 lanes away (shuffled as loaded, two values to a word).  A lane
+// group keeps a token for its heads: the cos and sin rows are loaded once and joined with the weights
+// (forward: y = r (x c w + x' s w'), four fp32 pairs of products a lane), and the rows of four heads are in
+// flight together.  32,768 tokens of 16 + 16 heads of 128, bf16: 100 us, 5.4 TB/s; backward, 16,384
+// tokens of 16 + 2 heads: 67 us, 3.8 TB/s (two blocks of 126 registers an SM keep fewer rows in flight).
 #include "dla.cuh"
 #include "dla_simt.cuh"
+#include "f32x2.cuh"
 
 namespace gcl {
 namespace qk {
@@ -36,20 +39,9 @@ struct QkParams {
     int64_t t_max, n_pos;
     int32_t R, norm, pair;
     float eps;
-    int32_t groups[2];             // head groups of q and of k for each token
+    int32_t heads[2], groups[2];   // heads per item (a multiple of PER) and items per token, of q and of k
+    int32_t blocks_q;              // blocks of q; the others take k
 };
-
-__device__ __forceinline__ void store8f(float *p, const float *v) {
-    dla::store4f(p, v);
-    dla::store4f(p + 4, v + 4);
-}
-template <typename T>
-__device__ __forceinline__ void store8f(T *p, const float *v) {
-    uint4 u;
-    dla::store4f(reinterpret_cast<T *>(&u), v);
-    dla::store4f(reinterpret_cast<T *>(&u) + 4, v + 4);
-    *reinterpret_cast<uint4 *>(p) = u;
-}
 
 // Sum over the D / 8 lanes of a row.
 template <int L>
@@ -59,48 +51,25 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// Turns the eight channels 8 l .. 8 l + 7 of a row by the token's angles (sign -1: back).  c, s: the
-// lane's cosines and sines.  Every lane of the warp calls it.
-template <int L>
-__device__ __forceinline__ void rotate(float *z, const float *c, const float *s, int l, int R, int pair, float sign) {
-    if (R == 0) return;
-    const bool in = l < R / 8;
-    if (pair == GCL_PAIR_ADJACENT) {
-        if (in) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = z[2 * e], b = z[2 * e + 1], sn = sign * s[e];
-                z[2 * e] = a * c[e] - b * sn;
-                z[2 * e + 1] = fmaf(a, sn, b * c[e]);
-            }
-        }
-        return;
-    }
-    const int half = R / 16;                               // lanes of half the rotated channels
-    const bool first = l < half;
-    const int lane = threadIdx.x & 31;
-    const int src = in ? (first ? lane + half : lane - half) : lane;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(0xffffffffu, z[e], src);
-        const float sn = sign * s[e];
-        if (in) z[e] = first ? z[e] * c[e] - o * sn : fmaf(o, sn, z[e] * c[e]);
-    }
-}
-
-// The lane's cosines and sines of position `pos`.
-__device__ __forceinline__ void angles(const QkParams &p, int64_t pos, int l, float *c, float *s) {
+// The lane's factors of the rotation of one token, y_e = z_e c_e + z_partner(e) s_e: with the signs of the two
+// halves of a pair in s (turned back: `sign` -1), and c = 1, s = 0 past the rotated channels.
+__device__ __forceinline__ void angles(const QkParams &p, int64_t pos, int l, float sign, float *c, float *s) {
     if (l >= p.R / 8) return;
     const int64_t row = pos * (p.R / 2);
     if (p.pair == GCL_PAIR_ADJACENT) {
         const float4 a = *reinterpret_cast<const float4 *>(p.cos_t + row + l * 4);
         const float4 b = *reinterpret_cast<const float4 *>(p.sin_t + row + l * 4);
-        c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
-        s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
+        c[0] = c[1] = a.x; c[2] = c[3] = a.y; c[4] = c[5] = a.z; c[6] = c[7] = a.w;
+        s[1] = sign * b.x; s[3] = sign * b.y; s[5] = sign * b.z; s[7] = sign * b.w;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) s[e] = -s[e + 1];
     } else {
-        const int at = (l % (p.R / 16)) * 8;
+        const int half = p.R / 16, at = (l % half) * 8;
         dla::load8f(p.cos_t + row + at, c);
         dla::load8f(p.sin_t + row + at, s);
+        const float sg = l < half ? -sign : sign;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] *= sg;
     }
 }
 
@@ -116,125 +85,237 @@ struct Raw {
 #pragma unroll
         for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void get(float *x) const { dla::load8f(reinterpret_cast<const T *>(v), x); }
+    __device__ __forceinline__ void get(uint64_t *x) const {
+        float f[8];
+        dla::load8f(reinterpret_cast<const T *>(v), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = pair(f[2 * e], f[2 * e + 1]);
+    }
+    // The values' partners: another lane's eight (lane src; zeros where `in` is false), or the neighbours
+    // within the lane's pairs.
+    __device__ __forceinline__ void partners(uint64_t *x, bool adjacent, int src, bool in) const {
+        Raw o;
+        if (adjacent) {
+            get(x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpair(x[e]);
+                x[e] = in ? pair(f.y, f.x) : 0;
+            }
+            return;
+        }
+        const uint32_t *a = reinterpret_cast<const uint32_t *>(v);
+        uint32_t *b = reinterpret_cast<uint32_t *>(o.v);
+#pragma unroll
+        for (int e = 0; e < 2 * (int)sizeof(T); ++e) {
+            const uint32_t y = __shfl_sync(0xffffffffu, a[e], src);
+            b[e] = in ? y : 0;
+        }
+        o.get(x);
+    }
+    __device__ __forceinline__ void put(const uint64_t *x) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 t = unpair(x[e]);
+            f[2 * e] = t.x;
+            f[2 * e + 1] = t.y;
+        }
+        dla::store4f(reinterpret_cast<T *>(v), f);
+        dla::store4f(reinterpret_cast<T *>(v) + 4, f + 4);
+    }
+    __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(T) / 2; ++e) reinterpret_cast<uint4 *>(p)[e] = v[e];
+    }
 };
 
-// One lane group (D / 8 lanes) takes PER heads of one token of q or k at a time; groups walk the (token,
-// head group) pairs with the grid's stride.  Lanes without work stay for the shuffles.  BWD: y gets
-// dx, and the weights' gradients are summed per block.
+// An item is some of the heads of one token, of q or of k by the block; a lane group (D / 8 lanes) takes its
+// heads PER at a time, with their rows in flight together, and keeps the token's rotation factors.  Lane
+// groups walk the items with the stride of the side's blocks.  Lanes without work stay for the
+// shuffles.  BWD: y gets dx, and the weight's gradient is summed per block.
 template <typename T, int D, bool BWD, int PER>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParams p) {
     constexpr int L = D / 8, G = kThreads / L;             // lanes per row, lane groups per block
-    __shared__ float s_dw[BWD ? 2 : 1][BWD ? G : 1][BWD ? D : 1];
+    __shared__ __align__(8) float s_dw[BWD ? G : 1][BWD ? D : 1];
     if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, l = tid % L, grp = tid / L;
-    const uint32_t per_token = p.groups[0] + p.groups[1];
+    const int which = blockIdx.x < p.blocks_q ? 0 : 1;
+    const int block = which ? blockIdx.x - p.blocks_q : blockIdx.x, blocks = which ? gridDim.x - p.blocks_q : p.blocks_q;
+    const Side &sd = p.side[which];
+    const uint32_t per_token = p.groups[which];
     const int64_t work = p.t_max * per_token;
-    float dw[BWD ? 2 : 1][8] = {};
-    for (int64_t i0 = (int64_t)blockIdx.x * G; i0 < work; i0 += (int64_t)gridDim.x * G) {
-        const int64_t i = i0 + grp;
-        bool live = i < work;
-        int64_t t = 0;
-        int hg = 0;
-        if (live) {
-            t = i >> 32 ? i / per_token : (uint32_t)i / per_token;
-            hg = (int)(i - t * per_token);
-        }
-        const int which = hg < p.groups[0] ? 0 : 1;
-        const Side &sd = p.side[which];
-        const int h0 = (hg - (which ? p.groups[0] : 0)) * PER;
-        float c[8] = {}, s[8] = {};
-        int64_t pos = 0;
+    uint64_t dw[4] = {};
+    const bool adjacent = p.pair == GCL_PAIR_ADJACENT, rot = p.R > 0;
+    const bool in = l < p.R / 8;                           // the lane's channels are rotated
+    const int lane = tid & 31, half = p.R / 16;
+    const int src = !in ? lane : l < half ? lane + half : lane - half;
+    uint64_t w2[4];
+    if (sd.w) {
+        Raw<T> w;
+        w.load(static_cast<const T *>(sd.w) + l * 8);
+        w.get(w2);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w2[e] = pair(1.f, 1.f);
+    }
+    const int heads = p.heads[which];
+    // item i: heads h0 .. of token t
+    auto item = [&](int64_t i, int64_t &t, int &h0) {
+        t = i >> 32 ? i / per_token : (uint32_t)i / per_token;
+        h0 = (int)(i - t * per_token) * heads;
+    };
+    const int64_t step = (int64_t)blocks * G;
+    int64_t i = (int64_t)block * G + grp, t_next = 0, pos_next = 0;
+    int h_next = 0;
+    if (i < work) {
+        item(i, t_next, h_next);
+        if (p.pos) pos_next = p.pos[t_next];
+    }
+    for (int64_t i0 = (int64_t)block * G; i0 < work; i0 += step, i += step) {
+        const bool exists = i < work;
+        bool live = exists;
+        const int64_t pos = pos_next, t = t_next;
+        const int h0 = h_next, h1 = h0 + heads < sd.H ? h0 + heads : sd.H;
+        // the first rows (of padding too: its values are not used), before anything that waits for the position
+        Raw<T> xr[PER], dr[BWD ? PER : 1];
+        const T *px = row_ptr<const T>(sd.x, t, h0) + l * 8, *pd = BWD ? row_ptr<const T>(sd.dy, t, h0) + l * 8 : nullptr;
+        T *py = row_ptr<T>(sd.y, t, h0) + l * 8;
+        int left = exists ? h1 - h0 : 0;                   // heads of the item not yet loaded
+        auto load = [&]() {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (j < left) xr[j].load(px);
+                else xr[j].zero();
+                px += sd.x.sh;
+                if (BWD) {
+                    if (j < left) dr[j].load(pd);
+                    else dr[j].zero();
+                    pd += sd.dy.sh;
+                }
+            }
+        };
+        load();
         if (live && p.pos) {
-            pos = p.pos[t];
             live = pos >= 0;
-            if (p.R > 0 && pos >= p.n_pos) {
+            if (rot && pos >= p.n_pos) {
                 live = false;
                 status_set(p.status, GCL_DEV_BAD_RANGE);
             }
         }
-        Raw<T> xr[PER], dr[BWD ? PER : 1];
+        float c[8], s[8];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const bool on = live && h0 + j < sd.H;
-            if (on) xr[j].load(row_ptr<const T>(sd.x, t, h0 + j) + l * 8);
-            else xr[j].zero();
-            if (BWD) {
-                if (on) dr[j].load(row_ptr<const T>(sd.dy, t, h0 + j) + l * 8);
-                else dr[j].zero();
-            }
+        for (int e = 0; e < 8; ++e) { c[e] = 1.f; s[e] = 0.f; }
+        if (live && rot) angles(p, pos, l, BWD ? -1.f : 1.f, c, s);
+        if (i + step < work) {                             // the next item's position is under way meanwhile
+            item(i + step, t_next, h_next);
+            if (p.pos) pos_next = p.pos[t_next];
         }
-        if (live && p.R > 0) angles(p, pos, l, c, s);
-        float w[8];
+        uint64_t c2[4], s2[4];
+        // forward: y = r (x c w + x' s w') with ' the partner; the weights join the factors once per token.
+        // Backward: dz = dy c + dy' s.
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.f;
-        if (sd.w) dla::load8f(static_cast<const T *>(sd.w) + l * 8, w);
+        for (int e = 0; e < 4; ++e) {
+            c2[e] = pair(c[2 * e], c[2 * e + 1]);
+            s2[e] = pair(s[2 * e], s[2 * e + 1]);
+            if (!BWD) c2[e] = mul2(c2[e], w2[e]);
+        }
+        if (!BWD && rot) {
+            uint64_t wp[4];
+            if (adjacent) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int h = h0 + j;
-            const bool on = live && h < sd.H;
-            float x[8], y[8];
-            xr[j].get(x);
-            if (BWD) dr[j].get(y);
-            float r = 1.f;
-            if (p.norm != GCL_NORM_NONE) {
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                ss = row_sum<L>(ss);
-                r = rsqrtf((p.norm == GCL_NORM_RMS ? ss * (1.f / D) : ss) + p.eps);
-            }
-            if (!BWD) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[e] * r * w[e];
-                rotate<L>(y, c, s, l, p.R, p.pair, 1.f);
-                if (on) store8f(row_ptr<T>(sd.y, t, h) + l * 8, y);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpair(w2[e]);
+                    wp[e] = pair(f.y, f.x);
+                }
             } else {
-                rotate<L>(y, c, s, l, p.R, p.pair, -1.f);  // dz
-                float ux = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = x[e] * r;
-                    if (on) {                              // (constant indexes: dw stays in registers)
-                        if (which == 0) dw[0][e] = fmaf(y[e], n, dw[0][e]);
-                        else dw[BWD][e] = fmaf(y[e], n, dw[BWD][e]);
-                    }
-                    y[e] *= w[e];                          // u
-                    ux = fmaf(y[e], n, ux);
-                    x[e] = n;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpair(w2[e]);
+                    wp[e] = pair(__shfl_sync(0xffffffffu, f.x, src), __shfl_sync(0xffffffffu, f.y, src));
                 }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s2[e] = in ? mul2(s2[e], wp[e]) : 0;
+        }
+        for (int hb = 0; hb < heads; hb += PER, left -= PER) {     // (the same count for every lane of the warp)
+            if (hb > 0) load();
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const bool on = live && j < left;
+                uint64_t x[4], y[4];
+                xr[j].get(x);
+                float r = 1.f;
                 if (p.norm != GCL_NORM_NONE) {
-                    ux = row_sum<L>(ux) * (p.norm == GCL_NORM_RMS ? 1.f / D : 1.f);
+                    uint64_t q = mul2(x[0], x[0]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = r * fmaf(-x[e], ux, y[e]);
+                    for (int e = 1; e < 4; ++e) q = fma2(x[e], x[e], q);
+                    const float2 f = unpair(q);
+                    const float ss = row_sum<L>(f.x + f.y);
+                    r = rsqrtf((p.norm == GCL_NORM_RMS ? ss * (1.f / D) : ss) + p.eps);
                 }
-                if (on) store8f(row_ptr<T>(sd.y, t, h) + l * 8, y);
+                const uint64_t r2 = pair(r, r);
+                Raw<T> out;
+                if (!BWD) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = mul2(x[e], c2[e]);
+                    if (rot) {
+                        uint64_t xp[4];
+                        xr[j].partners(xp, adjacent, src, in);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = fma2(xp[e], s2[e], y[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], r2);
+                } else {
+                    uint64_t z[4], m2 = 0;
+                    dr[j].get(z);
+                    if (rot) {
+                        uint64_t zp[4];
+                        dr[j].partners(zp, adjacent, src, in);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[e] = fma2(zp[e], s2[e], mul2(z[e], c2[e]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = mul2(x[e], r2);                 // n
+                        if (on) dw[e] = fma2(z[e], x[e], dw[e]);
+                        y[e] = mul2(z[e], w2[e]);              // u
+                        m2 = fma2(y[e], x[e], m2);
+                    }
+                    if (p.norm != GCL_NORM_NONE) {
+                        const float2 f = unpair(m2);
+                        const float m = row_sum<L>(f.x + f.y) * (p.norm == GCL_NORM_RMS ? -1.f / D : -1.f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = mul2(fma2(x[e], pair(m, m), y[e]), r2);
+                    }
+                }
+                out.put(y);
+                if (on) out.store(py);
+                py += sd.y.sh;
             }
         }
     }
-    if (BWD && (p.side[0].partial || p.side[1].partial)) {
+    if (BWD && sd.partial) {
 #pragma unroll
-        for (int which = 0; which < 2; ++which)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s_dw[which][grp][l * 8 + e] = dw[which][e];
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(&s_dw[grp][l * 8 + 2 * e]) = unpair(dw[e]);
         __syncthreads();
-        for (int e = tid; e < 2 * D; e += kThreads) {
-            const int which = e / D, ch = e % D;
+        for (int ch = tid; ch < D; ch += kThreads) {
             float sum = 0.f;
-            for (int g = 0; g < G; ++g) sum += s_dw[which][g][ch];
-            if (p.side[which].partial) p.side[which].partial[(int64_t)blockIdx.x * D + ch] = sum;
+            for (int g = 0; g < G; ++g) sum += s_dw[g][ch];
+            sd.partial[(int64_t)block * D + ch] = sum;
         }
     }
 }
 
 // The weights' gradients from the blocks' sums, in a fixed order: one block per 32 channels, eight
 // rows of threads over the sums.
-__global__ void __launch_bounds__(256) qk_dw_kernel(const QkParams p, int blocks, int D) {
+__global__ void __launch_bounds__(256) qk_dw_kernel(const QkParams p, int blocks_k, int D) {
     __shared__ float s[8][32];
     if (status_blocks_cta(p.status)) return;
     const Side &sd = p.side[blockIdx.y];
     if (!sd.partial) return;
-    const int ch = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+    const int ch = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5, blocks = blockIdx.y ? blocks_k : p.blocks_q;
     float sum = 0.f;
     for (int b = r; b < blocks; b += 8) sum += sd.partial[(int64_t)b * D + ch];
     s[r][threadIdx.x & 31] = sum;
@@ -256,31 +337,35 @@ __global__ void rope_table_kernel(float *cos_t, float *sin_t, int64_t n, int hal
     sin_t[e] = (float)sn;
 }
 
-// Blocks of the backward: a fixed number per SM, each walking many tokens, so that the partial
-// sums of the weights' gradients stay few.
-int bwd_blocks(int64_t t_max, int32_t HQ, int32_t HK, int D) {
-    const int64_t groups = kThreads / (D / 8);
-    const int64_t most = (t_max * ((int64_t)HQ + HK) + groups - 1) / groups;
-    const int64_t want = 4 * (int64_t)num_sms();
-    return (int)(most < want ? most : want);
-}
+// Most blocks of the backward: a fixed number per SM, each walking many tokens, so that the partial sums
+// of the weights' gradients stay few.
+int bwd_blocks() { return 4 * num_sms(); }
 
-template <typename T, int D, int PER>
-cudaError_t launch_qk_per(QkParams &p, bool backward, cudaStream_t s) {
-    const int64_t G = kThreads / (D / 8), sms = num_sms();
-    for (int i = 0; i < 2; ++i) p.groups[i] = (p.side[i].H + PER - 1) / PER;
-    const int64_t work = p.t_max * (p.groups[0] + p.groups[1]);
-    const int64_t most = (work + G - 1) / G;
-    if (!backward) {
-        qk_kernel<T, D, false, PER><<<(unsigned)(most < 16 * sms ? most : 16 * sms), kThreads, 0, s>>>(p);
-        return cudaGetLastError();
+template <typename T, int D, bool BWD, int PER>
+cudaError_t launch_qk_per(QkParams &p, cudaStream_t s) {
+    const int64_t G = kThreads / (D / 8);
+    int64_t need[2];                                       // blocks that give every lane group one item
+    for (int i = 0; i < 2; ++i) {
+        // a whole token per item while that gives every lane group of the GPU two; else fewer heads
+        int32_t heads = (p.side[i].H + PER - 1) / PER * PER;
+        const int64_t fill = 2 * (int64_t)num_sms() * (BWD ? 2 : 3) * G;
+        while (heads > PER && p.t_max * ((p.side[i].H + heads - 1) / heads) < fill) heads = (heads / PER + 1) / 2 * PER;
+        p.heads[i] = heads > 0 ? heads : PER;
+        p.groups[i] = (p.side[i].H + p.heads[i] - 1) / p.heads[i];
+        need[i] = (p.t_max * p.groups[i] + G - 1) / G;
     }
-    const int cap = bwd_blocks(p.t_max, p.side[0].H, p.side[1].H, D);
-    const int blocks = (int)(most < cap ? most : cap);
-    qk_kernel<T, D, true, PER><<<blocks, kThreads, 0, s>>>(p);
+    // at most so many blocks, shared by the sides' rows (the backward's number bounds its partial sums)
+    const int64_t most = BWD ? bwd_blocks() : 6 * (int64_t)num_sms();
+    if (need[0] + need[1] > most) {
+        const double all = (double)(need[0] + need[1]);
+        for (int i = 0; i < 2; ++i)
+            if (need[i] > 0) need[i] = (int64_t)(need[i] / all * (most - 1)) + 1;
+    }
+    p.blocks_q = (int32_t)need[0];
+    qk_kernel<T, D, BWD, PER><<<(unsigned)(need[0] + need[1]), kThreads, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && (p.side[0].partial || p.side[1].partial)) {
-        qk_dw_kernel<<<dim3(D / 32, 2), 256, 0, s>>>(p, blocks, D);
+    if (BWD && e == cudaSuccess && (p.side[0].partial || p.side[1].partial)) {
+        qk_dw_kernel<<<dim3(D / 32, 2), 256, 0, s>>>(p, (int)need[1], D);
         e = cudaGetLastError();
     }
     return e;
@@ -288,10 +373,13 @@ cudaError_t launch_qk_per(QkParams &p, bool backward, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_qk(QkParams &p, bool backward, cudaStream_t s) {
-    // four heads per lane group once there are rows for two full waves; few rows are spread one by one,
+    // four heads per lane group and step once there are rows for two full waves (32,768 tokens of 16 + 16
+    // heads of 128, bf16: 100 us with four, 131 with two, 168 with one); few rows are spread one by one,
     // for latency
     const int64_t G = kThreads / (D / 8), rows = p.t_max * ((int64_t)p.side[0].H + p.side[1].H);
-    return rows >= 4 * 16 * (int64_t)num_sms() * G ? launch_qk_per<T, D, 4>(p, backward, s) : launch_qk_per<T, D, 1>(p, backward, s);
+    const bool many = rows >= 4 * 16 * (int64_t)num_sms() * G;
+    if (backward) return many ? launch_qk_per<T, D, true, 4>(p, s) : launch_qk_per<T, D, true, 1>(p, s);
+    return many ? launch_qk_per<T, D, false, 4>(p, s) : launch_qk_per<T, D, false, 1>(p, s);
 }
 
 template <typename T>
@@ -305,7 +393,7 @@ size_t bwd_workspace(const gcl_qk_args *a) {
     if (!a || a->t_max < 1 || a->t_max >= (int64_t(1) << 31) || a->HQ < 1 || a->HK < 0 ||
         (a->D != 64 && a->D != 128 && a->D != 256) || (int64_t)a->HQ + a->HK > 65535)
         return 0;
-    return (size_t)bwd_blocks(a->t_max, a->HQ, a->HK, a->D) * 2 * a->D * sizeof(float);
+    return (size_t)(bwd_blocks() + 2) * 2 * a->D * sizeof(float);
 }
 
 gcl_status_t run(const char *fn, const gcl_qk_args *a, bool backward, cudaStream_t s) {

@@ -560,7 +560,7 @@ gcl_status_t dla_step(const gcl_dla_step_args *args, gcl_stream_t stream);
  *   (GCL_PAIR_HALF) or (2i, 2i + 1) (GCL_PAIR_ADJACENT); channels R and up keep z.
  * cos and sin are the rows positions[t] of tables [n_positions, R / 2] fp32 (rope_table_build).
  * R = 0: no rotation; the tables are not read.  A token with a negative position is padding: its
- * rows are neither read nor written.  A position >= n_positions sets GCL_DEV_BAD_RANGE and its
+ * rows are not used and not written.  A position >= n_positions sets GCL_DEV_BAD_RANGE and its
  * rows are left alone as well.  Without positions every row is live (R must be 0).
  *
  * The backward takes dyq, dyk and the forward's inputs and gives dq, dk and, where a weight is
