@@ -13,7 +13,7 @@ namespace {
 
 constexpr int kScanThreads = 256;
 
-// One thread per four state values of one (sequence, head), over the sequence's segments in
+// Threads take four state values of one (sequence, head) each, over the sequence's segments in
 // time order; blockIdx.z: 0 forwards, 1 backwards.  The sequence's first row is the number of
 // segments before it, summed by the block.
 __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) {
@@ -42,43 +42,43 @@ __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) 
         if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
         return;
     }
-    const int64_t KV = (int64_t)p.K * p.V, e = ((int64_t)blockIdx.x * kScanThreads + tid) * 4;
-    if (e >= KV) return;
-    const float g = p.g[h];
-    const int64_t at = ((int64_t)n * p.H + h) * KV + e;
+    if (count == 1) return;                                // its one segment enters from h0 (dht) itself
+    const int64_t KV = (int64_t)p.K * p.V, n_state = (int64_t)p.n_max * p.H * KV, base = ((int64_t)n * p.H + h) * KV;
+    const float g = p.g[h], gs = decay_pow(g, p.seg);
     const float *first = rev ? p.dht : p.h0;
-    float4 cur = first && GCL_RANGE_IN_BOUNDS(at, at + 3, (int64_t)p.n_max * p.H * KV, p.status)
-                     ? *reinterpret_cast<const float4 *>(first + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (count == 0) {                                      // an empty sequence passes its state on
-        float *last = rev ? p.dh0 : p.ht;
-        if (last && GCL_RANGE_IN_BOUNDS(at, at + 3, (int64_t)p.n_max * p.H * KV, p.status))
-            *reinterpret_cast<float4 *>(last + at) = cur;
-        return;
-    }
-    float *seg = rev ? p.seg_rev : p.seg_fwd;
-    const float gs = decay_pow(g, p.seg);
+    float *last = rev ? p.dh0 : p.ht, *seg = rev ? p.seg_rev : p.seg_fwd;
     const int64_t step = (int64_t)p.H * KV;
-    float *at_row = seg + row0 * step + h * KV + e;
-    for (int j0 = 0; j0 < count; j0 += 8) {                // eight loads in flight
-        float4 own[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int j = j0 + u;
-            // (the last segment in time has no own state: nothing enters from it)
-            own[u] = j + 1 < count ? *reinterpret_cast<const float4 *>(at_row + (rev ? count - 1 - j : j) * step)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t e = ((int64_t)blockIdx.x * kScanThreads + tid) * 4; e < KV; e += (int64_t)gridDim.x * kScanThreads * 4) {
+        const int64_t at = base + e;
+        float4 cur = first && GCL_RANGE_IN_BOUNDS(at, at + 3, n_state, p.status) ? *reinterpret_cast<const float4 *>(first + at)
+                                                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (count == 0) {                                  // an empty sequence passes its state on
+            if (last && GCL_RANGE_IN_BOUNDS(at, at + 3, n_state, p.status)) *reinterpret_cast<float4 *>(last + at) = cur;
+            continue;
         }
+        float *at_row = seg + row0 * step + h * KV + e;
+        for (int j0 = 0; j0 < count; j0 += 8) {            // eight loads in flight
+            float4 own[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int j = j0 + u;
-            if (j >= count) break;
-            *reinterpret_cast<float4 *>(at_row + (rev ? count - 1 - j : j) * step) = cur;
-            // backwards the first segment met is the sequence's last, possibly a short one
-            const float f = rev && j == 0 ? decay_pow(g, len - (int64_t)(count - 1) * p.seg) : gs;
-            cur.x = fmaf(f, cur.x, own[u].x);
-            cur.y = fmaf(f, cur.y, own[u].y);
-            cur.z = fmaf(f, cur.z, own[u].z);
-            cur.w = fmaf(f, cur.w, own[u].w);
+            for (int u = 0; u < 8; ++u) {
+                const int j = j0 + u;
+                // (the last segment in time has no own state: nothing enters from it)
+                own[u] = j + 1 < count ? *reinterpret_cast<const float4 *>(at_row + (rev ? count - 1 - j : j) * step)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = j0 + u;
+                if (j >= count) break;
+                // (the first segment in time enters from h0 or dht itself)
+                if (j > 0) *reinterpret_cast<float4 *>(at_row + (rev ? count - 1 - j : j) * step) = cur;
+                // backwards the first segment met is the sequence's last, possibly a short one
+                const float f = rev && j == 0 ? decay_pow(g, len - (int64_t)(count - 1) * p.seg) : gs;
+                cur.x = fmaf(f, cur.x, own[u].x);
+                cur.y = fmaf(f, cur.y, own[u].y);
+                cur.z = fmaf(f, cur.z, own[u].z);
+                cur.w = fmaf(f, cur.w, own[u].w);
+            }
         }
     }
 }
@@ -86,9 +86,11 @@ __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) 
 }  // namespace
 
 cudaError_t launch_scan(const Params &p, bool backward, cudaStream_t s) {
-    const int64_t kv4 = (int64_t)p.K * p.V / 4;
-    dla_scan_kernel<<<dim3((unsigned)((kv4 + kScanThreads - 1) / kScanThreads), (unsigned)(p.n_max * p.H), backward ? 2 : 1),
-                      kScanThreads, 0, s>>>(p);
+    // blocks per state: as many as fill the GPU twice, at most one per 1,024 values
+    const int64_t most = (int64_t)p.K * p.V / 4 / kScanThreads, units = (int64_t)p.n_max * p.H;
+    int64_t per = 4 * (int64_t)num_sms() / units;
+    per = per < 1 ? 1 : per > most ? most : per;
+    dla_scan_kernel<<<dim3((unsigned)per, (unsigned)units, backward ? 2 : 1), kScanThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -100,27 +102,48 @@ cudaError_t launch(const Params &p, int dtype, bool own_states, int n_roles, con
 
 namespace {
 
-constexpr int kSegUnit = 128;
-
-// Tokens per segment.  Cost model in chunks of 128 tokens, for n_max sequences of t_max / n_max
-// tokens: the waves of CTAs times (a segment's chunks + 2 for its start), times 1.5 for the
-// extra read of k and v (the own states' launch) and its own start once a sequence is cut.
-int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward) {
-    const int64_t sms = num_sms(), units = (int64_t)n_max * H * (backward ? 3 : 1);
-    const int64_t chunks = (t_max / n_max + kSegUnit - 1) / kSegUnit;    // of an average sequence
-    const int64_t whole = (t_max + kSegUnit - 1) / kSegUnit * kSegUnit;
-    if (units >= 8 * sms || chunks <= 2 || units > 65535) return whole;
-    double best = (double)((units + sms - 1) / sms) * (chunks + 2);
+// Tokens per segment, from the capacities.  Time is counted in chunks (128 tokens on the tensor cores, 64 on
+// the CUDA cores) of one CTA: an output CTA takes its chunks and kStart, an own-state CTA kOwn of its
+// chunks and kStart, the scan and the two further launches kLaunch.
+//  - Every candidate length is costed for n_max sequences of t_max / n_max tokens.  (One sequence of
+//    65,536 tokens, 4 heads: whole 1,620 us, segments of 1,792 105 us.  4 sequences of 8,192, 16 heads,
+//    backward: whole 470 us, segments of 2,816 434 us.)
+//  - With several sequences their lengths differ, and where units are few (less than two per SM) the
+//    longest one's CTA would be the last to finish: no segment is longer than half of each SM's share of
+//    all tokens (7 ragged sequences of 5,003 tokens in all, 6 heads, backward: 70 us, without this 105).
+//    More units are balanced by their order instead (32 prompts of 1 to 4,716 tokens in 64 slots, 16 heads:
+//    whole in seq_order 165 us, cut at 1,792 tokens 242).
+//  - Sequences of one or two chunks on average, and units that fill every SM eight times, stay whole.
+int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, int32_t dtype) {
+    const bool tc = dtype == GCL_BF16;
+    const int64_t unit = tc ? 128 : 64, sms = num_sms(), roles = backward ? 3 : 1;
+    const int64_t units = (int64_t)n_max * H * roles, chunks = (t_max / n_max + unit - 1) / unit;
+    const int64_t whole = (t_max + unit - 1) / unit * unit;
+    if (units >= 8 * sms || chunks <= (tc ? 2 : 1) || units > 65535) return whole;
+    const double kStart = tc ? 2.2 : 0.3, kOwn = tc ? 0.58 : 0.5, kLaunch = tc ? 4.0 : 0.6;
+    int64_t most = chunks;                                 // longest candidate, in chunks
+    if (n_max > 1 && units < 2 * sms) {
+        const int64_t half = (t_max * H * roles / (2 * sms) + unit - 1) / unit;
+        most = half < 4 ? 4 : half;
+    }
+    double best = 1e300;
     int64_t seg = whole;
-    for (int64_t c = 1; c < chunks; ++c) {
-        const int64_t parts = (chunks + c - 1) / c;
-        const double cost = 1.5 * (double)((units * parts + sms - 1) / sms) * (c + 2) + 2;
+    for (int64_t c = 1; c <= (most < chunks ? most : chunks); ++c) {
+        const int64_t full = chunks / c, rest = chunks % c, parts = full + (rest > 0);
+        const double item = c + kStart, work = (double)units * (chunks + parts * kStart) / sms;
+        const double waves = (double)((units * full + sms - 1) / sms) * item;
+        const double spread = work + (rest > 0 ? 0.5 * (rest + kStart) : 0.0);
+        double cost = waves > spread ? waves : spread;
+        if (parts > 1) {
+            const int64_t own = (int64_t)n_max * H * (backward ? 2 : 1) * (parts - 1);
+            cost += (double)((own + sms - 1) / sms) * (kOwn * c + kStart) + kLaunch;
+        }
         if (cost < best) {
             best = cost;
-            seg = c * kSegUnit;
+            seg = c * unit;
         }
     }
-    return seg;
+    return seg >= chunks * unit ? whole : seg;
 }
 
 int64_t segment_rows(int64_t t_max, int32_t n_max, int64_t seg) {
@@ -129,7 +152,7 @@ int64_t segment_rows(int64_t t_max, int32_t n_max, int64_t seg) {
 
 size_t segment_bytes(const gcl_dla_args *a, bool backward) {
     if (a->t_max < 1 || a->t_max >= (int64_t(1) << 31) || a->n_max < 1 || a->H < 1 || a->K < 1 || a->V < 1) return 0;
-    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward);
+    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype);
     if (seg >= a->t_max) return 0;
     return (size_t)segment_rows(a->t_max, a->n_max, seg) * a->H * a->K * a->V * sizeof(float) * (backward ? 2 : 1);
 }
@@ -199,7 +222,7 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
     p.g = a->g; p.h0 = a->h0;
     p.cu = a->cu_seqlens; p.seq_order = a->seq_order; p.status = a->dev_status;
     p.t_max = a->t_max; p.n_max = a->n_max; p.H = a->H; p.K = a->K; p.V = a->V; p.scale = a->scale;
-    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward);
+    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype);
     p.n_rows = segment_rows(a->t_max, a->n_max, seg);
     p.seg = (int32_t)(seg < a->t_max ? seg : a->t_max);
     const int both[2] = {kFwd, kDv}, out[3] = {kDq, kDv, kDk};
@@ -222,9 +245,9 @@ using namespace gcl;
 
 extern "C" {
 
-int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward) {
+int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward, int32_t dtype) {
     if (t_max < 1 || t_max >= (int64_t(1) << 31) || n_max < 1 || H < 1) return 0;
-    return dla::segment_tokens(t_max, n_max, H, backward != 0);
+    return dla::segment_tokens(t_max, n_max, H, backward != 0, dtype);
 }
 
 size_t gcl_dla_fwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, false) : 0; }

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kSimtThreads) dla_simt_kernel(const Params p) 
 
     for (int e = tid; e <= C; e += kSimtThreads) sP[e] = decay_pow(g, e);
     {   // the entering state; element (r, c) of M is at r * NV + c, transposed roles: c * NA + r
-        const float *seg = rev ? p.seg_rev : p.seg_fwd;
+        const float *seg = (rev ? it.last : it.i == 0) ? nullptr : rev ? p.seg_rev : p.seg_fwd;
         const float *src = OWN ? nullptr : seg ? seg + row_state : rev ? p.dht : p.h0;
         if (!OWN && !seg && src) src += seq_state;
         if (src && !GCL_RANGE_IN_BOUNDS(seg ? row_state : seq_state, (seg ? row_state : seq_state) + KV - 1,

@@ -21,7 +21,7 @@
 //   warps 0-3    score and output epilogues (a token per lane)
 //   warps 4-11   the split of b, 32 tokens at a time into two TMEM buffers, and the state (a row per
 //                lane, half of the columns per warp)
-//   warp 12      MMA issue: MMA2, the four quarters of MMA4, MMA3, the next chunk's MMA1
+//   warp 12      MMA issue: MMA2, three quarters of MMA4, MMA3, the last quarter, the next chunk's MMA1
 //   warp 13      TMA loads, one chunk ahead: five tiles, three of the chunk and two of the next;
 //                the third of the next goes where a was once MMA2 has read it
 // (128 registers a thread: what spills misses the little L1 that 224 KiB of shared memory leave, and
@@ -159,8 +159,8 @@ struct Ctx {                       // what every warp of a CTA needs of its work
         b /= p.n_roles;
         h = b % p.H;
         row = b / p.H;
-        Item it;
-        if (!find_item<kBlock>(p, row, it)) return false;
+        Item it = {};
+        const bool ok = find_item<kBlock>(p, row, it);
         n = uniform(it.n);
         i = uniform(it.i);
         s0 = uniform((int)it.s0);
@@ -168,7 +168,7 @@ struct Ctx {                       // what every warp of a CTA needs of its work
         last = uniform((int)it.last) != 0;
         rev = role >= kDv;
         nch = (s1 - s0 + C - 1) / C;
-        return true;
+        return ok;
     }
 };
 
@@ -295,19 +295,21 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
         bar_go, bar_end;
     __shared__ uint32_t s_tmem, s_rows[2];
     __shared__ int s_err;
-    if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    // the status word is loaded beside the item, not before it: each is a chain of loads
+    const bool blocked = status_blocks(p.status);
     Ctx x;
     int64_t row;
     bool last;
-    if (!x.find<kEngineThreads>(p, blockIdx.x, row, last)) return;
+    const bool found = x.find<kEngineThreads>(p, blockIdx.x, row, last);
+    if (__syncthreads_or(blocked) || !found) return;
     const bool rev = x.rev;
     const int nch = x.nch, h = x.h;
     const float s_state = rev ? 1.f : p.scale, s_inc = rev ? p.scale : 1.f;
     // the entering state (NULL: zeros) and where the leaving one goes (NULL: nowhere)
     auto entering = [&]() -> const float * {
         const int64_t KV = (int64_t)NA * NV;
-        const float *seg = rev ? p.seg_rev : p.seg_fwd, *first = rev ? p.dht : p.h0;
+        const float *seg = (rev ? last : x.i == 0) ? nullptr : rev ? p.seg_rev : p.seg_fwd, *first = rev ? p.dht : p.h0;
         return seg ? seg + (row * p.H + h) * KV : first ? first + ((int64_t)x.n * p.H + h) * KV : nullptr;
     };
     auto leaving = [&]() -> float * {
@@ -316,10 +318,20 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
     };
     x.leaves = leaving() != nullptr;
     if (nch == 0) {                                        // an empty sequence passes its state on
-        const float *src = entering();
-        float *dst = leaving();
-        if (dst)
-            for (int e = tid; e < NA * NV; e += kEngineThreads) dst[e] = src ? src[e] : 0.f;
+        const float4 *src = reinterpret_cast<const float4 *>(entering());
+        float4 *dst = reinterpret_cast<float4 *>(leaving());
+        if (dst) {
+            constexpr int N4 = NA * NV / 4, PT = (N4 + kEngineThreads - 1) / kEngineThreads;
+            float4 v[PT];                                  // (all in flight: one at a time took 20 us a state)
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const int e = tid + i * kEngineThreads;
+                v[i] = src && e < N4 ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < PT; ++i)
+                if (tid + i * kEngineThreads < N4) dst[tid + i * kEngineThreads] = v[i];
+        }
         return;
     }
 
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
             for (; ic + 1 < nch; ++ic) {                   // the next chunk's tiles
                 const int b = (ic + 1) & 1;
                 half = false;
-                if (ic > 0) ok = wait_bar(&bar_o, (ic - 1) & 1, &s_err, 1);        // b and c of chunk ic - 1 are read
+                if (ic > 0) ok = wait_bar(&bar_d, (ic - 1) & 1, &s_err, 1);        // b and c of chunk ic - 1 are read
                 if (!ok) break;
                 load(mb, sl.s[3], NA, ic + 1, &full_b[b]);
                 load(ma, sl.s[4], NA, ic + 1, &full_a[b]);
@@ -429,7 +441,6 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
                     // (what is ready before M is waited for first, while MMA1 runs: the MMAs then follow each other)
                     const bool upd = updates(ic);
                     ok = wait_warp(&full_c[ph], (ic >> 1) & 1, &s_err, 8) && wait_warp(&bar_split[0], 0, &s_err, 9) &&
-                         (!upd || wait_warp(&bar_split[1], 0, &s_err, 19)) &&
                          wait_warp(&bar_go, ph, &s_err, 6);                        // M in shared memory; D and O read
                     if (!ok) break;
                     tc_fence_after();
@@ -439,10 +450,23 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
                     for (int s = 0; s < NA / 16; ++s)
                         mma_ss(tmem + cO, da + (s >> 2) * (C * 8) + (s & 3) * 2, dm + s * 128, idesc_bf16(128, NV, 0, 1), s > 0);
                     commit_warp(&bar_m2);
+                    // MMA3 goes before the last quarter of MMA4: its scores are ready by then, and the outputs and
+                    // the next chunk's scores no longer wait for the state's chain
 #pragma unroll 1
-                    for (int q = 0; upd && q < C / kRows; ++q) {                   // (step 4 ic + q: buffer q & 1,
-                        if (q > 1) {                                               // its use 2 ic + (q >> 1))
-                            ok = wait_warp(&bar_split[q & 1], 1, &s_err, 20);
+                    for (int q = 0; q < C / kRows; ++q) {  // (step 4 ic + q: buffer q & 1, its use 2 ic + (q >> 1))
+                        if (q == C / kRows - 1) {
+                            ok = wait_warp(&bar_p, ph, &s_err, 10);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t dc = smem_desc(tcc, C * 128, 1024, kSwizzle128B);
+#pragma unroll
+                            for (int s = 0; s < 8; ++s)
+                                mma_ts(tmem + cO, tmem + cX + s * 8, dc + s * 128, idesc_bf16(128, NV, 0, 1), 1);
+                            commit_warp(&bar_o);
+                        }
+                        if (!upd) continue;
+                        if (q > 0) {
+                            ok = wait_warp(&bar_split[q & 1], q >> 1, &s_err, 20);
                             if (!ok) break;
                             tc_fence_after();
                         }
@@ -451,14 +475,6 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
                     }
                     if (!ok) break;
                     if (upd) commit_warp(&bar_d);
-                    ok = wait_warp(&bar_p, ph, &s_err, 10);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dc = smem_desc(tcc, C * 128, 1024, kSwizzle128B);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_ts(tmem + cO, tmem + cX + s * 8, dc + s * 128, idesc_bf16(128, NV, 0, 1), 1);
-                    commit_warp(&bar_o);
                     if (ic + 1 == nch) break;
                     sl.next();
                 }
@@ -713,9 +729,9 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
 
 // ---------------------------------------------------------------- the segments' own states
 // sum_j gamma^(distance to the segment's end) b_j c_j^T over one segment: MMA4 alone, with the decay
-// taken to the segment's end, so that the sum stays in TMEM until the last chunk.  Warps 0-7 split b
-// (32 tokens at a time, four TMEM buffers), warp 8 loads, warp 9 issues.  b, c: three tiles each.
-constexpr int kOwnWarps = 8, kOwnTma = 8, kOwnMma = 9, kOwnThreads = 10 * 32, kBufs = C / kRows, kOwnTiles = 3;
+// taken to the segment's end, so that the sum stays in TMEM until the last chunk.  Warps 0-15 split b
+// (eight take 32 tokens at a time, four TMEM buffers), warp 16 loads, warp 17 issues.  b, c: three tiles each.
+constexpr int kOwnWarps = 16, kOwnTma = 16, kOwnMma = 17, kOwnThreads = 18 * 32, kBufs = C / kRows, kOwnTiles = 3;
 
 template <int NA, int NV>
 struct OwnLayout {
@@ -733,19 +749,20 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
     __shared__ uint64_t full[kOwnTiles], bar_split[kBufs], bar_free[kBufs], bar_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
-    if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    const bool blocked = status_blocks(p.status);
     Ctx x;
     int64_t row;
     bool last;
-    if (!x.find<kOwnThreads>(p, blockIdx.x, row, last)) return;
+    const bool found = x.find<kOwnThreads>(p, blockIdx.x, row, last);
+    if (__syncthreads_or(blocked) || !found) return;
     const bool rev = x.rev;
     if (rev ? x.i == 0 : last) return;                     // no later (earlier) segment reads it
     const int h = x.h, nch = x.nch;
     if (tid == 0) {
         for (int i = 0; i < kOwnTiles; ++i) mbar_init(&full[i], 1);
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&bar_split[i], kOwnWarps);
+            mbar_init(&bar_split[i], kOwnWarps / 2);
             mbar_init(&bar_free[i], 1);
         }
         mbar_init(&bar_end, 1);
@@ -797,19 +814,19 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
         __syncwarp();
     } else {
         const float g = p.g[h], s_inc = rev ? p.scale : 1.f;
-        const int m = (warp & 3) * 32 + lane, half = warp >> 2;
+        const int m = (warp & 3) * 32 + lane, half = (warp >> 2) & 1, odd = warp >> 3;   // odd: takes steps 1, 3
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         float *w = reinterpret_cast<float *>(smem + Lay::oW) + warp * 16;
         bool ok = true;
         for (int ic = 0; ic < nch && ok; ++ic) {
             const int s = ic % kOwnTiles, len = x.len(ic), t0 = x.t0(ic);
             ok = wait_warp(&full[s], (ic / kOwnTiles) & 1, &s_err, 4);
-            if (ok && len < C) {
-                zero_tail<NV, kOwnWarps * 32>(smem + Lay::oC + s * Lay::sc, len, tid);
+            if (ok && len < C) {                           // (each group of eight the whole tail, before its first step)
+                zero_tail<NV, kOwnWarps / 2 * 32>(smem + Lay::oC + s * Lay::sc, len, tid & (kOwnWarps / 2 * 32 - 1));
                 fence_async_smem();
             }
 #pragma unroll 1
-            for (int q = 0; q < kBufs && ok; ++q) {
+            for (int q = odd; q < kBufs && ok; q += 2) {
                 if (ic > 0 && !(ok = wait_warp(&bar_free[q], (ic - 1) & 1, &s_err, 5))) break;
                 tc_fence_after();
                 const int r0 = q * kRows + half * 16, t = t0 + r0 + lane;          // the warp's 16 weights
@@ -830,7 +847,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
             constexpr int RC = NV / 4;
             if (NA == 128 || m < NA) {
 #pragma unroll 1
-                for (int u = half * 16; u < NV; u += 32) {
+                for (int u = (warp >> 2) * 16; u < NV; u += 64) {
                     float d[16];
                     tmem_ld16(tmem + lane_off + u, d);
                     tmem_ld_wait();
