@@ -169,7 +169,7 @@ def load_library(path: str = LIB_PATH):
         getattr(lib, fn).restype = ctypes.c_size_t
         getattr(lib, fn).argtypes = [ctypes.POINTER(args)]
     lib.gcl_dla_segment_tokens.restype = i64
-    lib.gcl_dla_segment_tokens.argtypes = [i64, i32, i32, i32, i32]
+    lib.gcl_dla_segment_tokens.argtypes = [i64, i32, i32, i32, i32, i32, i32]
     lib.rope_table_build.restype = ctypes.c_int
     lib.rope_table_build.argtypes = [vp, vp, i64, i32, ctypes.c_double, vp]
     return lib
@@ -604,9 +604,10 @@ def _dla_sizes(q, v, cu_seqlens):
     return DlaArgs(t_max=T, n_max=cu_seqlens.shape[0] - 1, H=H, K=K, V=v.shape[2], dtype=_dtype_of(q))
 
 
-def dla_segment_tokens(t_max: int, n_max: int, H: int, backward: bool = False, dtype: int = GCL_BF16) -> int:
+def dla_segment_tokens(t_max: int, n_max: int, H: int, backward: bool = False, dtype: int = GCL_BF16,
+                       K: int = 128, V: int = 128) -> int:
     """Tokens per segment of the plan for these capacities (t_max or more: sequences stay whole)."""
-    return int(lib().gcl_dla_segment_tokens(t_max, n_max, H, int(backward), dtype))
+    return int(lib().gcl_dla_segment_tokens(t_max, n_max, H, int(backward), dtype, K, V))
 
 
 def dla_fwd_workspace_bytes(q, v, cu_seqlens) -> int:

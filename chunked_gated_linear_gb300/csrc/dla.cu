@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) 
     const int64_t step = (int64_t)p.H * KV;
     for (int64_t e = ((int64_t)blockIdx.x * kScanThreads + tid) * 4; e < KV; e += (int64_t)gridDim.x * kScanThreads * 4) {
         const int64_t at = base + e;
+        (void)n_state;                                     // (checked in the debug build)
         float4 cur = first && GCL_RANGE_IN_BOUNDS(at, at + 3, n_state, p.status) ? *reinterpret_cast<const float4 *>(first + at)
                                                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
         if (count == 0) {                                  // an empty sequence passes its state on
@@ -57,17 +58,17 @@ __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) 
             continue;
         }
         float *at_row = seg + row0 * step + h * KV + e;
-        for (int j0 = 0; j0 < count; j0 += 8) {            // eight loads in flight
-            float4 own[8];
+        for (int j0 = 0; j0 < count; j0 += 16) {           // sixteen loads in flight
+            float4 own[16];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < 16; ++u) {
                 const int j = j0 + u;
                 // (the last segment in time has no own state: nothing enters from it)
                 own[u] = j + 1 < count ? *reinterpret_cast<const float4 *>(at_row + (rev ? count - 1 - j : j) * step)
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < 16; ++u) {
                 const int j = j0 + u;
                 if (j >= count) break;
                 // (the first segment in time enters from h0 or dht itself)
@@ -114,17 +115,18 @@ namespace {
 //    More units are balanced by their order instead (32 prompts of 1 to 4,716 tokens in 64 slots, 16 heads:
 //    whole in seq_order 165 us, cut at 1,792 tokens 242).
 //  - Sequences of one or two chunks on average, and units that fill every SM eight times, stay whole.
-int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, int32_t dtype) {
+int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, int32_t dtype, int32_t K, int32_t V) {
     const bool tc = dtype == GCL_BF16;
-    const int64_t unit = tc ? 128 : 64, sms = num_sms(), roles = backward ? 3 : 1;
+    const int64_t unit = tc ? 128 : 64, sms = num_sms() * (tc ? 1 : simt_ctas(K, V)), roles = backward ? 3 : 1;
     const int64_t units = (int64_t)n_max * H * roles, chunks = (t_max / n_max + unit - 1) / unit;
     const int64_t whole = (t_max + unit - 1) / unit * unit;
     if (units >= 8 * sms || chunks <= (tc ? 2 : 1) || units > 65535) return whole;
-    const double kStart = tc ? 2.2 : 0.3, kOwn = tc ? 0.58 : 0.5, kLaunch = tc ? 4.0 : 0.6;
+    const double kStart = tc ? 2.2 : 0.3, kOwn = tc ? 0.58 : 0.4, kLaunch = tc ? 4.0 : 0.6;
     int64_t most = chunks;                                 // longest candidate, in chunks
     if (n_max > 1 && units < 2 * sms) {
         const int64_t half = (t_max * H * roles / (2 * sms) + unit - 1) / unit;
-        most = half < 4 ? 4 : half;
+        const int64_t least = tc ? 4 : 1;
+        most = half < least ? least : half;
     }
     double best = 1e300;
     int64_t seg = whole;
@@ -152,7 +154,7 @@ int64_t segment_rows(int64_t t_max, int32_t n_max, int64_t seg) {
 
 size_t segment_bytes(const gcl_dla_args *a, bool backward) {
     if (a->t_max < 1 || a->t_max >= (int64_t(1) << 31) || a->n_max < 1 || a->H < 1 || a->K < 1 || a->V < 1) return 0;
-    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype);
+    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype, a->K, a->V);
     if (seg >= a->t_max) return 0;
     return (size_t)segment_rows(a->t_max, a->n_max, seg) * a->H * a->K * a->V * sizeof(float) * (backward ? 2 : 1);
 }
@@ -222,7 +224,7 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
     p.g = a->g; p.h0 = a->h0;
     p.cu = a->cu_seqlens; p.seq_order = a->seq_order; p.status = a->dev_status;
     p.t_max = a->t_max; p.n_max = a->n_max; p.H = a->H; p.K = a->K; p.V = a->V; p.scale = a->scale;
-    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype);
+    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype, a->K, a->V);
     p.n_rows = segment_rows(a->t_max, a->n_max, seg);
     p.seg = (int32_t)(seg < a->t_max ? seg : a->t_max);
     const int both[2] = {kFwd, kDv}, out[3] = {kDq, kDv, kDk};
@@ -245,9 +247,9 @@ using namespace gcl;
 
 extern "C" {
 
-int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward, int32_t dtype) {
+int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward, int32_t dtype, int32_t K, int32_t V) {
     if (t_max < 1 || t_max >= (int64_t(1) << 31) || n_max < 1 || H < 1) return 0;
-    return dla::segment_tokens(t_max, n_max, H, backward != 0, dtype);
+    return dla::segment_tokens(t_max, n_max, H, backward != 0, dtype, K, V);
 }
 
 size_t gcl_dla_fwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, false) : 0; }

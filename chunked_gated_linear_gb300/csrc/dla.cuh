@@ -159,6 +159,9 @@ gcl_status_t check_rows(const char *fn, const char *name, const gcl_rows &r, int
                         int32_t esize, bool output);
 gcl_status_t check_sizes(const char *fn, int32_t H, int32_t K, int32_t V, int32_t dtype);
 
+// CTAs per SM that the CUDA-core engine is built for: two where shared memory and registers allow.
+__host__ __device__ constexpr int simt_ctas(int na, int nv) { return na == 64 && nv == 64 ? 2 : 1; }
+
 // ---- launchers ------------------------------------------------------------
 // CUDA cores, fp32 arithmetic (fp32 and fp16 rows).  own_states: the segments' own states only (roles kFwd
 // and kDv); otherwise the outputs of the given roles.

@@ -513,14 +513,15 @@ typedef struct gcl_dla_args {
 } gcl_dla_args;
 
 /*
- * Tokens per segment of the plan for these capacities and dtype (a multiple of the engine's chunk, 128
+ * Tokens per segment of the plan for these capacities, dtype and dims (a multiple of the engine's chunk, 128
  * tokens for bf16 and 64 else; t_max or more: one segment per sequence).  Where whole sequences would
  * leave SMs idle, they are cut into segments: one launch sums each segment's own state, one
  * scans the states at the segments' starts, one computes every segment from its start state; a
  * sequence no longer than a segment takes part in the last alone.  Segments are found from cu_seqlens on
  * the device, so the launches depend on the capacities only.  Returns 0 for invalid sizes.
  */
-int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward, int32_t dtype);
+int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t backward, int32_t dtype,
+                               int32_t K, int32_t V);
 
 /* Bytes of workspace (0 when one segment per sequence runs); sizes and the dtype are read. */
 size_t gcl_dla_fwd_workspace_bytes(const gcl_dla_args *args);
