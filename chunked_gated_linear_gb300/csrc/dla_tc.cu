@@ -120,9 +120,11 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *er
     return mbar_test(bar, parity) || wait_more(at, parity, err, code);
 }
 // The same for a whole warp, which then takes one way: a wait that gave up in some lanes only would
-// leave the others at the warp's next barrier.
+// leave the others at the warp's next barrier.  (A phase that is complete already costs one probe and one
+// vote; the polling loop is out of the way of the code that follows.)
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int *err, int code) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, err, code));
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_test(bar, parity)), 1)) return true;
+    return __all_sync(0xffffffffu, wait_more(smem_u32(bar), parity, err, code));
 }
 
 // Barrier N of the block over `threads` threads.
@@ -154,7 +156,7 @@ struct Ctx {                       // what every warp of a CTA needs of its work
     // The role, head and segment of block b; false: nothing to do.
     // (Its values are made uniform, so that code on them stays convergent.)
     template <int kBlock>
-    __device__ __forceinline__ bool find(const Params &p, int b, int64_t &row, bool &last) {
+    __device__ __forceinline__ bool find(const Params &p, int b, int &row, bool &last) {
         role = (p.roles >> (2 * (b % p.n_roles))) & 3;
         b /= p.n_roles;
         h = b % p.H;
@@ -198,35 +200,37 @@ __device__ __forceinline__ void split16(uint32_t b, int m0, int r0, int len, con
     const int lane = threadIdx.x & 31, ch = ((m0 & 63) >> 3) + (lane >> 3);
     const uint32_t row = b + (m0 >> 6) * (C * 128) + (r0 + (lane & 7)) * 128 + ((ch ^ (lane & 7)) << 4);
     const uint64_t minus = pair(-1.f, -1.f);
-    uint32_t hi[8], mid[8], lo[8];                         // [channels 0-15: 4, 16-31: 4][token group][8 channels]
+    uint32_t x8[2][4];                                     // [8 tokens][8 channels]
+    uint64_t w2[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {                          // 8 tokens
-        uint32_t x4[4];
+    for (int t = 0; t < 2; ++t) {
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x4[0]), "=r"(x4[1]), "=r"(x4[2]), "=r"(x4[3]) : "r"(row + t * 1024) : "memory");
+                     : "=r"(x8[t][0]), "=r"(x8[t][1]), "=r"(x8[t][2]), "=r"(x8[t][3]) : "r"(row + t * 1024) : "memory");
         const int r = t * 8 + (lane & 3) * 2;
         const float2 wv = *reinterpret_cast<const float2 *>(w + r);
-        const uint64_t w2 = pair(wv.x, wv.y);
-        const uint32_t keep = r0 + 16 <= len ? 0xffffffffu : (r0 + r < len ? 0xffffu : 0u) | (r0 + r + 1 < len ? 0xffff0000u : 0u);
+        w2[t] = pair(wv.x, wv.y);
+        if (r0 + 16 > len) {
+            const uint32_t keep = (r0 + r < len ? 0xffffu : 0u) | (r0 + r + 1 < len ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int e = (c >> 1) * 4 + t * 2 + (c & 1);
-            uint64_t x = mul2(unpack(x4[c] & keep), w2);
+            for (int c = 0; c < 4; ++c) x8[t][c] &= keep;
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {                          // channels 0-15, 16-31
+        uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {                      // (token group e / 2, channels 8 (2 g + e % 2) ..)
+            uint64_t x = mul2(unpack(x8[e >> 1][2 * g + (e & 1)]), w2[e >> 1]);
             hi[e] = pack(x);
             x = fma2(unpack(hi[e]), minus, x);
             mid[e] = pack(x);
             x = fma2(unpack(mid[e]), minus, x);
             lo[e] = pack(x);
         }
-    }
-    const uint32_t high = 16u << 16;
-    tmem_st_frag(taddr, hi);
-    tmem_st_frag(taddr + high, hi + 4);
-    tmem_st_frag(taddr + kTermCols, mid);
-    tmem_st_frag(taddr + kTermCols + high, mid + 4);
-    if (three) {
-        tmem_st_frag(taddr + 2 * kTermCols, lo);
-        tmem_st_frag(taddr + 2 * kTermCols + high, lo + 4);
+        const uint32_t at = taddr + (uint32_t)(g * 16 << 16);
+        tmem_st_frag(at, hi);
+        tmem_st_frag(at + kTermCols, mid);
+        if (three) tmem_st_frag(at + 2 * kTermCols, lo);
     }
 }
 
@@ -291,26 +295,44 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
     constexpr int HV = NV / 2;                             // columns per warp of a pair
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full_b[2], full_a[2], full_c[2], bar_m1, bar_m2, bar_split[2], bar_free[2], bar_d, bar_p, bar_o,
+    __shared__ uint64_t full_ab[2], full_c[2], bar_m1, bar_m2, bar_split[2], bar_free[2], bar_d, bar_p, bar_o,
         bar_go, bar_end;
     __shared__ uint32_t s_tmem, s_rows[2];
     __shared__ int s_err;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    // the status word is loaded beside the item, not before it: each is a chain of loads
+    // the status word is loaded beside the item, not before it: each is a chain of loads, and what needs neither
+    // is done meanwhile
     const bool blocked = status_blocks(p.status);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&full_ab[i], 1);
+            mbar_init(&full_c[i], 1);
+            mbar_init(&bar_split[i], kWarpsB);
+            mbar_init(&bar_free[i], 1);
+        }
+        mbar_init(&bar_d, 1);
+        mbar_init(&bar_m1, 1);
+        mbar_init(&bar_m2, 1);
+        mbar_init(&bar_p, kWarpsA);
+        mbar_init(&bar_o, 1);
+        mbar_init(&bar_go, kWarpsA + kWarpsB);
+        mbar_init(&bar_end, 1);
+        s_err = 0;
+        fence_barrier_init();
+    }
+    if (warp == kTmaWarp && lane < (p.d_o.p ? 4 : 3)) prefetch_tmap(&maps.m[lane]);
     Ctx x;
-    int64_t row;
+    int row;
     bool last;
     const bool found = x.find<kEngineThreads>(p, blockIdx.x, row, last);
     if (__syncthreads_or(blocked) || !found) return;
     const bool rev = x.rev;
     const int nch = x.nch, h = x.h;
-    const float s_state = rev ? 1.f : p.scale, s_inc = rev ? p.scale : 1.f;
     // the entering state (NULL: zeros) and where the leaving one goes (NULL: nowhere)
     auto entering = [&]() -> const float * {
         const int64_t KV = (int64_t)NA * NV;
         const float *seg = (rev ? last : x.i == 0) ? nullptr : rev ? p.seg_rev : p.seg_fwd, *first = rev ? p.dht : p.h0;
-        return seg ? seg + (row * p.H + h) * KV : first ? first + ((int64_t)x.n * p.H + h) * KV : nullptr;
+        return seg ? seg + ((int64_t)row * p.H + h) * KV : first ? first + ((int64_t)x.n * p.H + h) * KV : nullptr;
     };
     auto leaving = [&]() -> float * {
         float *d = x.role == kFwd && last ? p.ht : x.role == kDv && x.i == 0 ? p.dh0 : nullptr;
@@ -335,7 +357,30 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
         return;
     }
 
-    const float g = p.g[h];
+    // tile loads (one thread); those of the first chunk go out at once
+    auto load = [&](int operand, int slot, int D, int ic, uint64_t *bar) {
+        const CUtensorMap *m = &maps.m[map_of(x.role, operand)];
+        for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_3d(smem + slot * Lay::slot + cb * C * 128, m, cb * 64, h, x.t0(ic), bar);
+    };
+    auto load_ab = [&](int slot_b, int slot_a, int ic) {
+        mbar_arrive_expect_tx(&full_ab[ic & 1], 2 * C * NA * 2);
+        load(1, slot_b, NA, ic, &full_ab[ic & 1]);
+        load(0, slot_a, NA, ic, &full_ab[ic & 1]);
+    };
+    auto load_c = [&](int slot, int ic) {
+        mbar_arrive_expect_tx(&full_c[ic & 1], C * NV * 2);
+        load(2, slot, NV, ic, &full_c[ic & 1]);
+    };
+    if (warp == kTmaWarp && lane == 0) {
+        load_ab(0, 1, 0);
+        load_c(2, 0);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&s_tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    const float g = p.g[h], s_inc = rev ? p.scale : 1.f;   // (s_inc: of the increments, s_state: of a M)
     float *sP = reinterpret_cast<float *>(smem + Lay::oP), *sNear = sP + 132, *sW = sNear + 32;
     for (int e = tid; e <= C; e += kEngineThreads) {
         const float w = decay_pow(g, e);
@@ -347,28 +392,6 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
         if (rev ? e > 0 : e < tail) sW[C + (rev ? e - 1 : tail - 1 - e)] = s_inc * w;
         if (!rev && e >= tail && e < C) sW[C + e] = 0.f;
     }
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full_b[i], 1);
-            mbar_init(&full_a[i], 1);
-            mbar_init(&full_c[i], 1);
-            mbar_init(&bar_split[i], kWarpsB);
-            mbar_init(&bar_free[i], 1);
-        }
-        mbar_init(&bar_d, 1);
-        mbar_init(&bar_m1, 1);
-        mbar_init(&bar_m2, 1);
-        mbar_init(&bar_p, kWarpsA);
-        mbar_init(&bar_o, 1);
-        mbar_init(&bar_go, kWarpsA + kWarpsB);
-        mbar_init(&bar_end, 1);
-        s_err = 0;
-        fence_barrier_init();
-    }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&s_tmem, kTmemCols);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -378,41 +401,26 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
 
     if (warp >= kMmaWarp) {
         if (warp == kTmaWarp && lane == 0) {
-            const CUtensorMap *ma = &maps.m[map_of(x.role, 0)], *mb = &maps.m[map_of(x.role, 1)], *mc = &maps.m[map_of(x.role, 2)];
-            auto load = [&](const CUtensorMap *m, int slot, int D, int ic, uint64_t *bar) {
-                mbar_arrive_expect_tx(bar, C * D * 2);
-                for (int cb = 0; cb < D / 64; ++cb)
-                    tma_load_3d(smem + slot * Lay::slot + cb * C * 128, m, cb * 64, h, x.t0(ic), bar);
-            };
             Slots sl;
-            load(mb, sl.s[0], NA, 0, &full_b[0]);
-            load(ma, sl.s[1], NA, 0, &full_a[0]);
-            load(mc, sl.s[2], NV, 0, &full_c[0]);
             bool ok = true, half = false;                  // half: b and a of chunk ic + 1 are under way
             int ic = 0;
             for (; ic + 1 < nch; ++ic) {                   // the next chunk's tiles
-                const int b = (ic + 1) & 1;
                 half = false;
                 if (ic > 0) ok = wait_bar(&bar_d, (ic - 1) & 1, &s_err, 1);        // b and c of chunk ic - 1 are read
                 if (!ok) break;
-                load(mb, sl.s[3], NA, ic + 1, &full_b[b]);
-                load(ma, sl.s[4], NA, ic + 1, &full_a[b]);
+                load_ab(sl.s[3], sl.s[4], ic + 1);
                 half = true;
                 ok = wait_bar(&bar_m2, ic & 1, &s_err, 2);                         // a of chunk ic is read
                 if (!ok) break;
-                load(mc, sl.s[1], NV, ic + 1, &full_c[b]);
+                load_c(sl.s[1], ic + 1);
                 sl.next();
             }
             if (!ok) {                                     // no copy may land after the CTA is gone
                 for (int c = ic > 0 ? ic - 1 : 0; c <= ic; ++c) {
-                    drain(&full_b[c & 1], (c >> 1) & 1);
-                    drain(&full_a[c & 1], (c >> 1) & 1);
+                    drain(&full_ab[c & 1], (c >> 1) & 1);
                     drain(&full_c[c & 1], (c >> 1) & 1);
                 }
-                if (half) {
-                    drain(&full_b[(ic + 1) & 1], ((ic + 1) >> 1) & 1);
-                    drain(&full_a[(ic + 1) & 1], ((ic + 1) >> 1) & 1);
-                }
+                if (half) drain(&full_ab[(ic + 1) & 1], ((ic + 1) >> 1) & 1);
             }
         } else if (warp == kMmaWarp) {
             const uint32_t sbase = smem_u32(smem);
@@ -420,8 +428,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
             // (descriptor addresses count 16 bytes: 2 per 16 channels, C * 8 per 64-channel block, 128 per
             // 16 rows)
             auto scores = [&](int ic, int slot_b, int slot_a) {                    // MMA1 of chunk ic
-                if (!wait_warp(&full_b[ic & 1], (ic >> 1) & 1, &s_err, 3) || !wait_warp(&full_a[ic & 1], (ic >> 1) & 1, &s_err, 4))
-                    return false;
+                if (!wait_warp(&full_ab[ic & 1], (ic >> 1) & 1, &s_err, 3)) return false;
                 if (ic > 0 && !wait_warp(&bar_o, (ic - 1) & 1, &s_err, 5)) return false;    // X~ is read
                 tc_fence_after();
                 const uint64_t da = smem_desc(sbase + slot_a * Lay::slot, 16, 1024, kSwizzle128B);
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
             if (!wait_warp(&bar_m2, ph, &s_err, 11)) break;
             tc_fence_after();
             {
-                const float f = s_state * sP[i < len ? (rev ? len - 1 - i : i + 1) : 0];
+                const float s_state = rev ? 1.f : p.scale, f = s_state * sP[i < len ? (rev ? len - 1 - i : i + 1) : 0];
                 const uint64_t f2 = pair(f, f);
 #pragma unroll 1
                 for (int u = 0; u < NV / 32; ++u) {
@@ -620,8 +627,16 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
 #pragma unroll
                 for (int j = 0; j < HV; ++j) S[j] = mine ? src[(int64_t)(half * HV + j) * NA + m] : 0.f;
             } else if (src) {
-                for (int e = bt; e < NA * RC; e += kWarpsB * 32)
-                    rows[(e / RC) * RC + ((e % RC) ^ ((e / RC) & (RC - 1)))] = reinterpret_cast<const float4 *>(src)[e];
+                // (every load before the first store: one after the other they took 10,000 cycles)
+                constexpr int PT = NA * RC / (kWarpsB * 32);
+                float4 v[PT];
+#pragma unroll
+                for (int i = 0; i < PT; ++i) v[i] = reinterpret_cast<const float4 *>(src)[bt + i * (kWarpsB * 32)];
+#pragma unroll
+                for (int i = 0; i < PT; ++i) {
+                    const int e = bt + i * (kWarpsB * 32);
+                    rows[(e / RC) * RC + ((e % RC) ^ ((e / RC) & (RC - 1)))] = v[i];
+                }
                 named_sync<1>(kWarpsB * 32);
 #pragma unroll
                 for (int j = 0; j < HV; j += 4) {
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
                 zero_tail<NV, kWarpsB * 32>(smem + sl.s[2] * Lay::slot, len, tid - kWarpsA * 32);
                 fence_async_smem();
             }
-            if (upd && !(ok = wait_warp(&full_b[ic & 1], (ic >> 1) & 1, &s_err, 15))) break;
+            if (upd && !(ok = wait_warp(&full_ab[ic & 1], (ic >> 1) & 1, &s_err, 15))) break;
 #pragma unroll 1
             for (int q = 0; q < C / kRows; ++q) {
                 // step q of chunk ic: buffer q & 1, its use 2 ic + (q >> 1)
@@ -752,7 +767,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const bool blocked = status_blocks(p.status);
     Ctx x;
-    int64_t row;
+    int row;
     bool last;
     const bool found = x.find<kOwnThreads>(p, blockIdx.x, row, last);
     if (__syncthreads_or(blocked) || !found) return;
@@ -865,7 +880,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
     if (tid == 0 && s_err != 0) status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
     if (s_err == 0) {
         const float4 *rows = reinterpret_cast<const float4 *>(smem);
-        float4 *dst = reinterpret_cast<float4 *>((rev ? p.seg_rev : p.seg_fwd) + (row * p.H + h) * (int64_t)(NA * NV));
+        float4 *dst = reinterpret_cast<float4 *>((rev ? p.seg_rev : p.seg_fwd) + ((int64_t)row * p.H + h) * (NA * NV));
         constexpr int RC = NV / 4;
         for (int e = tid; e < NA * RC; e += kOwnThreads) dst[e] = rows[(e / RC) * RC + ((e % RC) ^ ((e / RC) & (RC - 1)))];
     }
