@@ -17,6 +17,8 @@ constexpr int kScanThreads = 256;
 // time order; blockIdx.z: 0 forwards, 1 backwards.  The sequence's first row is the number of
 // segments before it, summed by the block.
 __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) {
+    launch_dependents();                                   // (the outputs' launch waits for this grid's end)
+    grid_dependency_wait();                                // the segments' own states
     if (status_blocks_cta(p.status)) return;
     const int h = blockIdx.y % p.H, n = blockIdx.y / p.H, tid = threadIdx.x;
     const bool rev = blockIdx.z != 0;
@@ -91,8 +93,7 @@ cudaError_t launch_scan(const Params &p, bool backward, cudaStream_t s) {
     const int64_t most = (int64_t)p.K * p.V / 4 / kScanThreads, units = (int64_t)p.n_max * p.H;
     int64_t per = 4 * (int64_t)num_sms() / units;
     per = per < 1 ? 1 : per > most ? most : per;
-    dla_scan_kernel<<<dim3((unsigned)per, (unsigned)units, backward ? 2 : 1), kScanThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(dla_scan_kernel, dim3((unsigned)per, (unsigned)units, backward ? 2 : 1), dim3(kScanThreads), 0, s, p);
 }
 
 cudaError_t launch(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s) {

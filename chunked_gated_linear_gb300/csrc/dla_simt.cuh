@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(NA, NV)) dla_simt_kern
     extern __shared__ __align__(16) float sm[];
     float *sA = sm + Lay::oA, *sB = sm + Lay::oB, *sC = sm + Lay::oC, *sX = sm + Lay::oX, *sM = sm + Lay::oM,
           *sP = sm + Lay::oP;
+    if (OWN) launch_dependents();                          // (the scan waits for this grid's end)
+    else grid_dependency_wait();                           // (after the scan: the entering states)
     if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int unit = blockIdx.x / p.n_roles, h = unit % p.H;
@@ -321,7 +323,9 @@ cudaError_t launch_simt_one(const Params &p, cudaStream_t s) {
     constexpr size_t smem = SimtLayout<NA, NV>::bytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(p.n_rows * p.H * p.n_roles), kSimtThreads, smem, s>>>(p);
+    const unsigned grid = (unsigned)(p.n_rows * p.H * p.n_roles);
+    if (!OWN && (p.seg_fwd || p.seg_rev)) return launch_dependent(kern, dim3(grid), dim3(kSimtThreads), smem, s, p);
+    kern<<<grid, kSimtThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
     __shared__ uint32_t s_tmem, s_rows[2];
     __shared__ int s_err;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    grid_dependency_wait();                                // (after the scan: the entering states)
     // the status word is loaded beside the item, not before it: each is a chain of loads, and what needs neither
     // is done meanwhile
     const bool blocked = status_blocks(p.status);
@@ -765,6 +766,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    launch_dependents();                                   // (the scan waits for this grid's end)
     const bool blocked = status_blocks(p.status);
     Ctx x;
     int row;
@@ -905,6 +907,8 @@ cudaError_t launch_one(const Maps &maps, const Params &p, bool own_states, cudaS
         cudaError_t e = cudaFuncSetAttribute(dla_tc_kernel<NA, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)TcLayout<NA, NV>::bytes);
         if (e != cudaSuccess) return e;
+        if (p.seg_fwd || p.seg_rev)                        // (its set-up overlaps the scan's end)
+            return launch_dependent(dla_tc_kernel<NA, NV>, dim3(grid), dim3(kEngineThreads), TcLayout<NA, NV>::bytes, s, maps, p);
         dla_tc_kernel<NA, NV><<<grid, kEngineThreads, TcLayout<NA, NV>::bytes, s>>>(maps, p);
     }
     return cudaGetLastError();
