@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
     constexpr int HV = NV / 2;                             // columns per warp of a pair
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full_ab[2], full_c[2], bar_m1, bar_m2, bar_split[2], bar_free[2], bar_d, bar_p, bar_o,
+    __shared__ uint64_t full_ab[2], full_c[2], bar_m1, bar_m2, bar_split[2], bar_free[2], bar_d[2], bar_p, bar_o,
         bar_go, bar_end;
     __shared__ uint32_t s_tmem, s_rows[2];
     __shared__ int s_err;
@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
             mbar_init(&full_c[i], 1);
             mbar_init(&bar_split[i], kWarpsB);
             mbar_init(&bar_free[i], 1);
+            mbar_init(&bar_d[i], 1);
         }
-        mbar_init(&bar_d, 1);
         mbar_init(&bar_m1, 1);
         mbar_init(&bar_m2, 1);
         mbar_init(&bar_p, kWarpsA);
@@ -407,7 +407,9 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
             int ic = 0;
             for (; ic + 1 < nch; ++ic) {                   // the next chunk's tiles
                 half = false;
-                if (ic > 0) ok = wait_bar(&bar_d, (ic - 1) & 1, &s_err, 1);        // b and c of chunk ic - 1 are read
+                // b and c of chunk ic - 1 are read.  (A barrier for odd and one for even chunks: neither can pass its
+                // next phase before these loads, so a wait that comes late does not miss one.)
+                if (ic > 0) ok = wait_bar(&bar_d[(ic - 1) & 1], ((ic - 1) >> 1) & 1, &s_err, 1);
                 if (!ok) break;
                 load_ab(sl.s[3], sl.s[4], ic + 1);
                 half = true;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
                     const uint32_t ph = ic & 1, tcc = sbase + sl.s[2] * Lay::slot;
                     // (what is ready before M is waited for first, while MMA1 runs: the MMAs then follow each other)
                     const bool upd = updates(ic);
-                    ok = wait_warp(&full_c[ph], (ic >> 1) & 1, &s_err, 8) && wait_warp(&bar_split[0], 0, &s_err, 9) &&
+                    ok = wait_warp(&full_c[ph], (ic >> 1) & 1, &s_err, 8) && (!upd || wait_warp(&bar_split[0], 0, &s_err, 9)) &&
                          wait_warp(&bar_go, ph, &s_err, 6);                        // M in shared memory; D and O read
                     if (!ok) break;
                     tc_fence_after();
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
                         commit_warp(&bar_free[q & 1]);
                     }
                     if (!ok) break;
-                    if (upd) commit_warp(&bar_d);
+                    if (upd) commit_warp(&bar_d[ph]);
                     if (ic + 1 == nch) break;
                     sl.next();
                 }
@@ -681,12 +683,12 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (more && lane == 0 && (upd || q == 0)) mbar_arrive(&bar_split[q & 1]);
+                if (upd && lane == 0) mbar_arrive(&bar_split[q & 1]);
                 if (q > 0) continue;
                 // the state that enters chunk ic (after the chunk's first step, which needs no state and fills the
                 // time until MMA4 of the last chunk is done)
                 if (ic > 0) {
-                    if (!(ok = wait_warp(&bar_d, (ic - 1) & 1, &s_err, 18))) break;
+                    if (!(ok = wait_warp(&bar_d[(ic - 1) & 1], ((ic - 1) >> 1) & 1, &s_err, 18))) break;
                     tc_fence_after();
                     const float gl = sP[x.len(ic - 1)];
 #pragma unroll
