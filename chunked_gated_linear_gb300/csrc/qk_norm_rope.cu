@@ -10,8 +10,8 @@
 // partner of a half-split pair sits R / 16 lanes away (shuffled as loaded, two values to a word).  A lane
 // group keeps a token for its heads: the cos and sin rows are loaded once and joined with the weights
 // (forward: y = r (x c w + x' s w'), four fp32 pairs of products a lane), and the rows of four heads are in
-// flight together.  32,768 tokens of 16 + 16 heads of 128, bf16: 100 us, 5.4 TB/s; backward, 16,384
-// tokens of 16 + 2 heads: 67 us, 3.8 TB/s (two blocks of 126 registers an SM keep fewer rows in flight).
+// flight together.  32,768 tokens of 16 + 16 heads of 128, bf16: 97 us, 5.5 TB/s; backward, 16,384
+// tokens of 16 + 2 heads: 63 us, 3.6 TB/s (two blocks of 126 registers an SM keep fewer rows in flight).
 #include "dla.cuh"
 #include "dla_simt.cuh"
 #include "f32x2.cuh"
@@ -130,14 +130,17 @@ struct Raw {
     }
 };
 
+constexpr int qk_ctas(bool bwd) { return bwd ? 2 : 3; }    // resident blocks per SM
+
 // An item is some of the heads of one token, of q or of k by the block; a lane group (D / 8 lanes) takes its
 // heads PER at a time, with their rows in flight together, and keeps the token's rotation factors.  Lane
 // groups walk the items with the stride of the side's blocks.  Lanes without work stay for the
 // shuffles.  BWD: y gets dx, and the weight's gradient is summed per block.
 template <typename T, int D, bool BWD, int PER>
-__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kThreads, qk_ctas(BWD)) qk_kernel(const QkParams p) {
     constexpr int L = D / 8, G = kThreads / L;             // lanes per row, lane groups per block
     __shared__ __align__(8) float s_dw[BWD ? G : 1][BWD ? D : 1];
+    if (BWD) launch_dependents();                          // (the sums of the weights' gradients wait for this grid's end)
     if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, l = tid % L, grp = tid / L;
     const int which = blockIdx.x < p.blocks_q ? 0 : 1;
@@ -308,23 +311,31 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
     }
 }
 
-// The weights' gradients from the blocks' sums, in a fixed order: one block per 32 channels, eight
-// rows of threads over the sums.
-__global__ void __launch_bounds__(256) qk_dw_kernel(const QkParams p, int blocks_k, int D) {
-    __shared__ float s[8][32];
+// The weights' gradients from the blocks' sums, in a fixed order: one block per 32 channels, 32 rows of
+// threads over the sums, eight loads of each in flight.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const QkParams p, int blocks_k, int D) {
+    __shared__ float s[32][33];
+    grid_dependency_wait();
     if (status_blocks_cta(p.status)) return;
     const Side &sd = p.side[blockIdx.y];
     if (!sd.partial) return;
-    const int ch = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5, blocks = blockIdx.y ? blocks_k : p.blocks_q;
+    const int lane = threadIdx.x & 31, ch = blockIdx.x * 32 + lane, r = threadIdx.x >> 5;
+    const int blocks = blockIdx.y ? blocks_k : p.blocks_q;
     float sum = 0.f;
-    for (int b = r; b < blocks; b += 8) sum += sd.partial[(int64_t)b * D + ch];
-    s[r][threadIdx.x & 31] = sum;
-    __syncthreads();
-    if (r == 0) {
+    for (int b0 = r; b0 < blocks; b0 += 8 * 32) {
+        float v[8];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) sum += s[i][threadIdx.x];
-        sd.dw[ch] = sum;
+        for (int i = 0; i < 8; ++i) v[i] = b0 + i * 32 < blocks ? sd.partial[(int64_t)(b0 + i * 32) * D + ch] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += v[i];
     }
+    s[r][lane] = sum;
+    __syncthreads();
+    // thread (r, lane): the sum over the rows of channel r of the block's 32
+    float t = s[lane][r];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+    if (lane == 0) sd.dw[blockIdx.x * 32 + r] = t;
 }
 
 __global__ void rope_table_kernel(float *cos_t, float *sin_t, int64_t n, int half, double base) {
@@ -337,9 +348,9 @@ __global__ void rope_table_kernel(float *cos_t, float *sin_t, int64_t n, int hal
     sin_t[e] = (float)sn;
 }
 
-// Most blocks of the backward: a fixed number per SM, each walking many tokens, so that the partial sums
-// of the weights' gradients stay few.
-int bwd_blocks() { return 4 * num_sms(); }
+// Most blocks of the backward: those that are resident, each walking many tokens, so that the partial sums of
+// the weights' gradients stay few.
+int bwd_blocks() { return qk_ctas(true) * num_sms(); }
 
 template <typename T, int D, bool BWD, int PER>
 cudaError_t launch_qk_per(QkParams &p, cudaStream_t s) {
@@ -348,25 +359,30 @@ cudaError_t launch_qk_per(QkParams &p, cudaStream_t s) {
     for (int i = 0; i < 2; ++i) {
         // a whole token per item while that gives every lane group of the GPU two; else fewer heads
         int32_t heads = (p.side[i].H + PER - 1) / PER * PER;
-        const int64_t fill = 2 * (int64_t)num_sms() * (BWD ? 2 : 3) * G;
+        const int64_t fill = 2 * (int64_t)num_sms() * qk_ctas(BWD) * G;
         while (heads > PER && p.t_max * ((p.side[i].H + heads - 1) / heads) < fill) heads = (heads / PER + 1) / 2 * PER;
         p.heads[i] = heads > 0 ? heads : PER;
         p.groups[i] = (p.side[i].H + p.heads[i] - 1) / p.heads[i];
         need[i] = (p.t_max * p.groups[i] + G - 1) / G;
     }
-    // at most so many blocks, shared by the sides' rows (the backward's number bounds its partial sums)
-    const int64_t most = BWD ? bwd_blocks() : 6 * (int64_t)num_sms();
+    // at most one wave (32,768 tokens of 16 + 16 heads forwards: 97 us, two waves 99; 16,384 backwards: 89 and
+    // 97), shared by the sides' rows, and by their items for the angles (16 + 2 heads backwards: 63 us; an equal
+    // share 82, by rows alone 63, but forwards 72 against 64)
+    const int64_t most = qk_ctas(BWD) * (int64_t)num_sms();
     if (need[0] + need[1] > most) {
-        const double all = (double)(need[0] + need[1]);
+        double w[2];
+        for (int i = 0; i < 2; ++i) w[i] = p.side[i].H > 0 ? (double)p.groups[i] * (p.heads[i] + 1) : 0.;
         for (int i = 0; i < 2; ++i)
-            if (need[i] > 0) need[i] = (int64_t)(need[i] / all * (most - 1)) + 1;
+            if (need[i] > 0) {
+                const int64_t part = (int64_t)(w[i] / (w[0] + w[1]) * most + 0.5);
+                need[i] = part < 1 ? 1 : part < need[i] ? part : need[i];
+            }
     }
     p.blocks_q = (int32_t)need[0];
     qk_kernel<T, D, BWD, PER><<<(unsigned)(need[0] + need[1]), kThreads, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (BWD && e == cudaSuccess && (p.side[0].partial || p.side[1].partial)) {
-        qk_dw_kernel<<<dim3(D / 32, 2), 256, 0, s>>>(p, (int)need[1], D);
-        e = cudaGetLastError();
+        e = launch_dependent(qk_dw_kernel, dim3(D / 32, 2), dim3(1024), 0, s, p, (int)need[1], D);
     }
     return e;
 }
@@ -374,7 +390,7 @@ cudaError_t launch_qk_per(QkParams &p, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t launch_qk(QkParams &p, bool backward, cudaStream_t s) {
     // four heads per lane group and step once there are rows for two full waves (32,768 tokens of 16 + 16
-    // heads of 128, bf16: 100 us with four, 131 with two, 168 with one); few rows are spread one by one,
+    // heads of 128, bf16: 97 us with four, 131 with two, 168 with one); few rows are spread one by one,
     // for latency
     const int64_t G = kThreads / (D / 8), rows = p.t_max * ((int64_t)p.side[0].H + p.side[1].H);
     const bool many = rows >= 4 * 16 * (int64_t)num_sms() * G;
