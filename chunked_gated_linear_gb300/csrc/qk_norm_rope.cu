@@ -5,13 +5,15 @@
 // or 1; z = n w; y = rotation of z.  The rotation's transpose turns by the opposite angle, so with
 // dz = rotation^T dy and u = dz w:
 //   dx = r (u - x r^2 sum(u x) / D)   (RMS; L2 without / D),   dw = sum over rows of dz n.
+// (Neither sum(x^2) nor sum(u x) waits for the other: they cross the row's lanes together.)
 // HBM-bound: rows are read and written once (the backward reads x and dy, writes dx).  D / 8 lanes
 // hold one row, 16 bytes (fp32: 32) each; sums over a row are shuffles inside those lanes, and the
 // partner of a half-split pair sits R / 16 lanes away (shuffled as loaded, two values to a word).  A lane
 // group keeps a token for its heads: the cos and sin rows are loaded once and joined with the weights
 // (forward: y = r (x c w + x' s w'), four fp32 pairs of products a lane), and the rows of four heads are in
 // flight together.  32,768 tokens of 16 + 16 heads of 128, bf16: 97 us, 5.5 TB/s; backward, 16,384
-// tokens of 16 + 2 heads: 63 us, 3.6 TB/s (two blocks of 126 registers an SM keep fewer rows in flight).
+// tokens of 16 + 2 heads: 60 us, 3.8 TB/s (bound by issue and the shuffles' latency: two blocks of 126 registers
+// an SM; three spill, 79 us, and rows brought ahead through shared memory take as long, 60).
 #include "dla.cuh"
 #include "dla_simt.cuh"
 #include "f32x2.cuh"
@@ -49,6 +51,17 @@ __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
     for (int d = L / 2; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
+}
+
+// Two sums over the row's lanes at once.
+template <int L>
+__device__ __forceinline__ void row_sums(float &a, float &b) {
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, a, d), v = __shfl_xor_sync(0xffffffffu, b, d);
+        a += u;
+        b += v;
+    }
 }
 
 // The lane's factors of the rotation of one token, y_e = z_e c_e + z_partner(e) s_e: with the signs of the two
@@ -248,18 +261,18 @@ __global__ void __launch_bounds__(kThreads, qk_ctas(BWD)) qk_kernel(const QkPara
                 const bool on = live && j < left;
                 uint64_t x[4], y[4];
                 xr[j].get(x);
-                float r = 1.f;
-                if (p.norm != GCL_NORM_NONE) {
-                    uint64_t q = mul2(x[0], x[0]);
-#pragma unroll
-                    for (int e = 1; e < 4; ++e) q = fma2(x[e], x[e], q);
-                    const float2 f = unpair(q);
-                    const float ss = row_sum<L>(f.x + f.y);
-                    r = rsqrtf((p.norm == GCL_NORM_RMS ? ss * (1.f / D) : ss) + p.eps);
-                }
-                const uint64_t r2 = pair(r, r);
                 Raw<T> out;
                 if (!BWD) {
+                    float r = 1.f;
+                    if (p.norm != GCL_NORM_NONE) {
+                        uint64_t q = mul2(x[0], x[0]);
+#pragma unroll
+                        for (int e = 1; e < 4; ++e) q = fma2(x[e], x[e], q);
+                        const float2 f = unpair(q);
+                        const float ss = row_sum<L>(f.x + f.y);
+                        r = rsqrtf((p.norm == GCL_NORM_RMS ? ss * (1.f / D) : ss) + p.eps);
+                    }
+                    const uint64_t r2 = pair(r, r);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) y[e] = mul2(x[e], c2[e]);
                     if (rot) {
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, qk_ctas(BWD)) qk_kernel(const QkPara
 #pragma unroll
                     for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], r2);
                 } else {
-                    uint64_t z[4], m2 = 0;
+                    uint64_t z[4];
                     dr[j].get(z);
                     if (rot) {
                         uint64_t zp[4];
@@ -279,18 +292,28 @@ __global__ void __launch_bounds__(kThreads, qk_ctas(BWD)) qk_kernel(const QkPara
 #pragma unroll
                         for (int e = 0; e < 4; ++e) z[e] = fma2(zp[e], s2[e], mul2(z[e], c2[e]));
                     }
+                    // u = z w; the sums of x^2 and of u x together
+                    uint64_t q = mul2(x[0], x[0]), m2;
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) q = fma2(x[e], x[e], q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = mul2(z[e], w2[e]);
+                    m2 = mul2(y[0], x[0]);
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) m2 = fma2(y[e], x[e], m2);
+                    const float2 fq = unpair(q), fm = unpair(m2);
+                    float ss = fq.x + fq.y, su = fm.x + fm.y;
+                    float r = 1.f, m = 0.f;
+                    if (p.norm != GCL_NORM_NONE) {
+                        row_sums<L>(ss, su);
+                        r = rsqrtf((p.norm == GCL_NORM_RMS ? ss * (1.f / D) : ss) + p.eps);
+                        m = su * r * r * (p.norm == GCL_NORM_RMS ? -1.f / D : -1.f);
+                    }
+                    const uint64_t r2 = pair(r, r), mm = pair(m, m);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[e] = mul2(x[e], r2);                 // n
-                        if (on) dw[e] = fma2(z[e], x[e], dw[e]);
-                        y[e] = mul2(z[e], w2[e]);              // u
-                        m2 = fma2(y[e], x[e], m2);
-                    }
-                    if (p.norm != GCL_NORM_NONE) {
-                        const float2 f = unpair(m2);
-                        const float m = row_sum<L>(f.x + f.y) * (p.norm == GCL_NORM_RMS ? -1.f / D : -1.f);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = mul2(fma2(x[e], pair(m, m), y[e]), r2);
+                        if (on) dw[e] = fma2(mul2(z[e], x[e]), r2, dw[e]);
+                        y[e] = mul2(fma2(x[e], mm, y[e]), r2);
                     }
                 }
                 out.put(y);
@@ -365,9 +388,9 @@ cudaError_t launch_qk_per(QkParams &p, cudaStream_t s) {
         p.groups[i] = (p.side[i].H + p.heads[i] - 1) / p.heads[i];
         need[i] = (p.t_max * p.groups[i] + G - 1) / G;
     }
-    // at most one wave (32,768 tokens of 16 + 16 heads forwards: 97 us, two waves 99; 16,384 backwards: 89 and
-    // 97), shared by the sides' rows, and by their items for the angles (16 + 2 heads backwards: 63 us; an equal
-    // share 82, by rows alone 63, but forwards 72 against 64)
+    // at most one wave (32,768 tokens of 16 + 16 heads forwards: 97 us, two waves 99; backwards a
+    // tenth less), shared by the sides' rows, and by their items for the angles (16 + 2 heads forwards: 64 us; by
+    // rows alone 72)
     const int64_t most = qk_ctas(BWD) * (int64_t)num_sms();
     if (need[0] + need[1] > most) {
         double w[2];
