@@ -108,13 +108,15 @@ namespace {
 // the CUDA cores) of one CTA: an output CTA takes its chunks and kStart, an own-state CTA kOwn of its
 // chunks and kStart, the scan and the two further launches kLaunch.
 //  - Every candidate length is costed for n_max sequences of t_max / n_max tokens.  (One sequence of
-//    65,536 tokens, 4 heads: whole 1,620 us, segments of 1,792 105 us.  4 sequences of 8,192, 16 heads,
-//    backward: whole 470 us, segments of 2,816 434 us.)
+//    65,536 tokens, 4 heads: whole 1,540 us, segments of 1,792 or 1,920 101 to 104, of 4,096 163.  4 sequences of
+//    8,192, 16 heads, backward: whole 454 us, segments of 2,816 or 4,096 422, of 1,792 452.  fp32, 2 sequences,
+//    4,096 tokens, 8 heads of 64: whole 659 us, segments of 64 74, of 128 68, of 256 107.)
 //  - With several sequences their lengths differ, and where units are few (less than two per SM) the
 //    longest one's CTA would be the last to finish: no segment is longer than half of each SM's share of
-//    all tokens (7 ragged sequences of 5,003 tokens in all, 6 heads, backward: 70 us, without this 105).
+//    all tokens, but four chunks (two on the CUDA cores) are allowed (7 ragged sequences of 5,003 tokens in
+//    all, 6 heads, backward: 64 us, without this 105).
 //    More units are balanced by their order instead (32 prompts of 1 to 4,716 tokens in 64 slots, 16 heads:
-//    whole in seq_order 165 us, cut at 1,792 tokens 242).
+//    whole in seq_order 147 us, cut at 1,792 tokens 225).
 //  - Sequences of one or two chunks on average, and units that fill every SM eight times, stay whole.
 int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, int32_t dtype, int32_t K, int32_t V) {
     const bool tc = dtype == GCL_BF16;
@@ -126,7 +128,7 @@ int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, i
     int64_t most = chunks;                                 // longest candidate, in chunks
     if (n_max > 1 && units < 2 * sms) {
         const int64_t half = (t_max * H * roles / (2 * sms) + unit - 1) / unit;
-        const int64_t least = tc ? 4 : 1;
+        const int64_t least = tc ? 4 : 2;
         most = half < least ? least : half;
     }
     double best = 1e300;
