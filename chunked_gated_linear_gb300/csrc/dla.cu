@@ -1,10 +1,10 @@
 // dla.cu -- decayed linear attention: the C entry points, the segment plan and the scan of the
 // segments' states.
 //
-// Plans.  With at least as many (sequence, head) units as SMs one CTA walks each sequence: every
-// input is read once.  With fewer, sequences are cut into segments: the segments' own states (a
-// launch that reads k and v once more), their scan, then the outputs from the entering states.  The
-// scan is elementwise over a [K, V] state: S(i + 1) = gamma^seg S(i) + own(i).
+// Plans.  Where whole sequences keep the SMs evenly busy one CTA walks each: every input is read once.  Else
+// sequences are cut into segments: the segments' own states (a launch that reads k and v once more), their
+// scan, then the outputs from the entering states; a sequence's first segment (in the role's time) waits for
+// neither and runs beside them.  The scan is elementwise over a [K, V] state: S(i + 1) = gamma^seg S(i) + own(i).
 #include "dla.cuh"
 
 namespace gcl {
@@ -13,9 +13,9 @@ namespace {
 
 constexpr int kScanThreads = 256;
 
-// Threads take four state values of one (sequence, head) each, over the sequence's segments in
-// time order; blockIdx.z: 0 forwards, 1 backwards.  The sequence's first row is the number of
-// segments before it, summed by the block.
+// Threads take four state values of one (sequence, head) each, over the borders of the sequence's segments in
+// time order; blockIdx.z: 0 forwards, 1 backwards.  The sequence's first row is the number of borders
+// before it, summed by the block.
 __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) {
     launch_dependents();                                   // (the outputs' launch waits for this grid's end)
     grid_dependency_wait();                                // the segments' own states
@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) 
     for (int m = tid; m <= n; m += kScanThreads) {
         const int64_t b = p.cu[m], e = p.cu[m + 1];
         if (b < 0 || e < b || e > p.t_max) bad = 1;
-        else if (m < n) sum += (int)((e - b + p.seg - 1) / p.seg);
+        else if (m < n) sum += borders(e - b, p.seg);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -39,48 +39,42 @@ __global__ void __launch_bounds__(kScanThreads) dla_scan_kernel(const Params p) 
     int64_t row0 = 0;
     for (int w = 0; w < kScanThreads / 32; ++w) row0 += s_sum[w];
     const int64_t len = (int64_t)p.cu[n + 1] - p.cu[n];
-    const int count = (int)((len + p.seg - 1) / p.seg);
+    const int count = borders(len, p.seg);
     if (row0 + count > p.n_rows) {
         if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
         return;
     }
-    if (count == 1) return;                                // its one segment enters from h0 (dht) itself
+    if (count == 0) return;
     const int64_t KV = (int64_t)p.K * p.V, n_state = (int64_t)p.n_max * p.H * KV, base = ((int64_t)n * p.H + h) * KV;
     const float g = p.g[h], gs = decay_pow(g, p.seg);
     const float *first = rev ? p.dht : p.h0;
-    float *last = rev ? p.dh0 : p.ht, *seg = rev ? p.seg_rev : p.seg_fwd;
+    float *seg = rev ? p.seg_rev : p.seg_fwd;
     const int64_t step = (int64_t)p.H * KV;
     for (int64_t e = ((int64_t)blockIdx.x * kScanThreads + tid) * 4; e < KV; e += (int64_t)gridDim.x * kScanThreads * 4) {
         const int64_t at = base + e;
         (void)n_state;                                     // (checked in the debug build)
         float4 cur = first && GCL_RANGE_IN_BOUNDS(at, at + 3, n_state, p.status) ? *reinterpret_cast<const float4 *>(first + at)
                                                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (count == 0) {                                  // an empty sequence passes its state on
-            if (last && GCL_RANGE_IN_BOUNDS(at, at + 3, n_state, p.status)) *reinterpret_cast<float4 *>(last + at) = cur;
-            continue;
-        }
         float *at_row = seg + row0 * step + h * KV + e;
         for (int j0 = 0; j0 < count; j0 += 16) {           // sixteen loads in flight
             float4 own[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
                 const int j = j0 + u;
-                // (the last segment in time has no own state: nothing enters from it)
-                own[u] = j + 1 < count ? *reinterpret_cast<const float4 *>(at_row + (rev ? count - 1 - j : j) * step)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                own[u] = j < count ? *reinterpret_cast<const float4 *>(at_row + (rev ? count - 1 - j : j) * step)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
                 const int j = j0 + u;
                 if (j >= count) break;
-                // (the first segment in time enters from h0 or dht itself)
-                if (j > 0) *reinterpret_cast<float4 *>(at_row + (rev ? count - 1 - j : j) * step) = cur;
                 // backwards the first segment met is the sequence's last, possibly a short one
-                const float f = rev && j == 0 ? decay_pow(g, len - (int64_t)(count - 1) * p.seg) : gs;
+                const float f = rev && j == 0 ? decay_pow(g, len - (int64_t)count * p.seg) : gs;
                 cur.x = fmaf(f, cur.x, own[u].x);
                 cur.y = fmaf(f, cur.y, own[u].y);
                 cur.z = fmaf(f, cur.z, own[u].z);
                 cur.w = fmaf(f, cur.w, own[u].w);
+                *reinterpret_cast<float4 *>(at_row + (rev ? count - 1 - j : j) * step) = cur;
             }
         }
     }
@@ -109,14 +103,15 @@ namespace {
 // chunks and kStart, the scan and the two further launches kLaunch.
 //  - Every candidate length is costed for n_max sequences of t_max / n_max tokens.  (One sequence of
 //    65,536 tokens, 4 heads: whole 1,540 us, segments of 1,792 or 1,920 101 to 104, of 4,096 163.  4 sequences of
-//    8,192, 16 heads, backward: whole 454 us, segments of 2,816 or 4,096 422, of 1,792 452.  fp32, 2 sequences,
+//    8,192, 16 heads, backward: whole 454 us, segments of 2,816 or 4,096 413 to 422, of 1,792 452.  fp32, 2 sequences,
 //    4,096 tokens, 8 heads of 64: whole 659 us, segments of 64 74, of 128 68, of 256 107.)
 //  - With several sequences their lengths differ, and where units are few (less than two per SM) the
 //    longest one's CTA would be the last to finish: no segment is longer than half of each SM's share of
 //    all tokens, but four chunks (two on the CUDA cores) are allowed (7 ragged sequences of 5,003 tokens in
-//    all, 6 heads, backward: 64 us, without this 105).
+//    all, 6 heads, backward: 62 us, without this 105).
 //    More units are balanced by their order instead (32 prompts of 1 to 4,716 tokens in 64 slots, 16 heads:
-//    whole in seq_order 147 us, cut at 1,792 tokens 225).
+//    whole in seq_order 147 us, cut at 1,792 tokens 225, at 2,432 to 4,096 190 to 203: own states and scan come
+//    first).  The price: one prompt of 33,000 tokens alone in the 64 slots takes 806 us, in one slot 161.
 //  - Sequences of one or two chunks on average, and units that fill every SM eight times, stay whole.
 int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, int32_t dtype, int32_t K, int32_t V) {
     const bool tc = dtype == GCL_BF16;
@@ -151,15 +146,15 @@ int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, i
     return seg >= chunks * unit ? whole : seg;
 }
 
-int64_t segment_rows(int64_t t_max, int32_t n_max, int64_t seg) {
-    return seg >= t_max ? n_max : gcl_nt_max(t_max, n_max, (int32_t)seg);
-}
+// Borders between segments, at most: a sequence has (length - 1) / seg of them.
+int64_t border_rows(int64_t t_max, int64_t seg) { return seg >= t_max ? 0 : (t_max - 1) / seg; }
 
 size_t segment_bytes(const gcl_dla_args *a, bool backward) {
     if (a->t_max < 1 || a->t_max >= (int64_t(1) << 31) || a->n_max < 1 || a->H < 1 || a->K < 1 || a->V < 1) return 0;
     const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype, a->K, a->V);
     if (seg >= a->t_max) return 0;
-    return (size_t)segment_rows(a->t_max, a->n_max, seg) * a->H * a->K * a->V * sizeof(float) * (backward ? 2 : 1);
+    // a state per segment (a border's states need one less a sequence)
+    return (size_t)gcl_nt_max(a->t_max, a->n_max, (int32_t)seg) * a->H * a->K * a->V * sizeof(float) * (backward ? 2 : 1);
 }
 
 }  // namespace
@@ -228,7 +223,7 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
     p.cu = a->cu_seqlens; p.seq_order = a->seq_order; p.status = a->dev_status;
     p.t_max = a->t_max; p.n_max = a->n_max; p.H = a->H; p.K = a->K; p.V = a->V; p.scale = a->scale;
     const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype, a->K, a->V);
-    p.n_rows = segment_rows(a->t_max, a->n_max, seg);
+    p.n_rows = border_rows(a->t_max, seg);
     p.seg = (int32_t)(seg < a->t_max ? seg : a->t_max);
     const int both[2] = {kFwd, kDv}, out[3] = {kDq, kDv, kDk};
     cudaError_t e = cudaSuccess;

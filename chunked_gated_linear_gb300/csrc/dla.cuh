@@ -36,10 +36,11 @@ struct Params {
     float *ht, *dh0;
     const int32_t *cu, *seq_order;
     int32_t *status;
-    float *seg_fwd, *seg_rev;      // [n_rows, H, K, V]: the segments' own states, after the scan the
-                                   // states that enter them; NULL for one segment per sequence
+    float *seg_fwd, *seg_rev;      // [n_rows, H, K, V], a row per border between segments: the own state of the
+                                   // segment that it ends (in the role's time), after the scan the state there;
+                                   // NULL for one segment per sequence
     int64_t t_max;
-    int64_t n_rows;                // segment rows (capacity)
+    int64_t n_rows;                // borders (capacity; 0: one segment per sequence)
     int32_t seg;                   // tokens per segment
     int32_t n_max, H, K, V;
     float scale;
@@ -67,36 +68,41 @@ __host__ __device__ __forceinline__ T *row_ptr(const Rows &r, int64_t t, int h) 
 // gamma^n (n >= 0): 1 for n = 0 whatever g is (also g = -inf).
 __device__ __forceinline__ float decay_pow(float g, int64_t n) { return n == 0 ? 1.f : expf(g * (float)n); }
 
-// The work of row j of the grid: sequence n, its tokens [bos, eos), the segment's number i in it and
-// its tokens [s0, s1), and whether it is the sequence's last.  Every thread of the block calls it (block
-// barriers); the answer is the same for all.  False: nothing to do.  One segment per sequence: row j
-// is the sequence slot (in seq_order).  Otherwise the block adds up the segments of the sequences,
-// kBlock at a time, until row j falls into one.
+// The work of row j of the grid: sequence n, the segment's number i in it, its tokens [s0, s1), whether it is the
+// sequence's last, and the row of its state among the segments' (-1: none).  Every thread of the block calls it
+// (block barriers); the answer is the same for all.  False: nothing to do.
+// The output kernels' first n_max rows are the sequence slots (in seq_order): each sequence's first segment in
+// the role's time, which enters from h0 (dht) and needs nothing of the launches before.  The rows after
+// them are the borders between two segments, sequence by sequence; the block adds up the sequences' borders,
+// kBlock at a time, until row j falls into one.  Such a row's segment is the one that the border's state
+// enters; of the own-state kernels (whose rows are the borders alone) the one that it leaves.
 struct Item {
     int n, i;
-    int64_t bos, eos, s0, s1;
+    int64_t bos, eos, s0, s1, row;
     bool last;
 };
 
-template <int kBlock>
-__device__ __forceinline__ bool find_item(const Params &p, int64_t j, Item &it) {
+__device__ __forceinline__ int borders(int64_t len, int32_t seg) { return len > seg ? (int)((len - 1) / seg) : 0; }
+
+template <int kBlock, bool kOwn>
+__device__ __forceinline__ bool find_item(const Params &p, int64_t j, bool rev, Item &it) {
     __shared__ int s_warp[32];
     __shared__ int s_hit[2], s_bad;
     const int tid = threadIdx.x;
-    if (p.seg_fwd == nullptr && p.seg_rev == nullptr) {
+    const bool cut = p.seg_fwd != nullptr || p.seg_rev != nullptr;
+    if (!kOwn && j < p.n_max) {
         const int n = p.seq_order ? p.seq_order[j] : (int)j;
         if (n < 0 || n >= p.n_max) {
             if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
             return false;
         }
         it.n = n;
-        it.i = 0;
+        it.row = -1;
         it.bos = p.cu[n];
         it.eos = p.cu[n + 1];
-        it.s0 = it.bos;
-        it.s1 = it.eos;
-        it.last = true;
+        it.i = rev && cut ? borders(it.eos - it.bos, p.seg) : 0;
     } else {
+        if (!kOwn) j -= p.n_max;
         if (tid == 0) { s_hit[0] = -1; s_bad = 0; }
         __syncthreads();
         int64_t base = 0;
@@ -108,7 +114,7 @@ __device__ __forceinline__ bool find_item(const Params &p, int64_t j, Item &it) 
                 const int64_t b = p.cu[n], e = p.cu[n + 1];
                 bad = b < 0 || e < b || e > p.t_max;
                 if (bad) s_bad = 1;
-                else c = (int)((e - b + p.seg - 1) / p.seg);
+                else c = borders(e - b, p.seg);
             }
             int x = c;                                     // inclusive prefix over the block
             const int lane = tid & 31, warp = tid >> 5;
@@ -138,17 +144,18 @@ __device__ __forceinline__ bool find_item(const Params &p, int64_t j, Item &it) 
         }
         if (s_hit[0] < 0) return false;
         it.n = s_hit[0];
-        it.i = s_hit[1];
+        it.row = j;
         it.bos = p.cu[it.n];
         it.eos = p.cu[it.n + 1];
-        it.s0 = it.bos + (int64_t)it.i * p.seg;
-        it.s1 = it.s0 + p.seg < it.eos ? it.s0 + p.seg : it.eos;
-        it.last = it.s1 == it.eos;
+        it.i = s_hit[1] + (kOwn == rev ? 1 : 0);           // border k lies between segments k and k + 1
     }
     if (it.bos < 0 || it.eos < it.bos || it.eos > p.t_max) {
         if (tid == 0) status_set(p.status, GCL_DEV_BAD_RANGE);
         return false;
     }
+    it.s0 = it.bos + (cut ? (int64_t)it.i * p.seg : 0);
+    it.s1 = cut && it.s0 + p.seg < it.eos ? it.s0 + p.seg : it.eos;
+    it.last = it.s1 == it.eos;
     return true;
 }
 

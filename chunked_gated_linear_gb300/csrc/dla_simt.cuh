@@ -81,16 +81,14 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(NA, NV)) dla_simt_kern
     float *sA = sm + Lay::oA, *sB = sm + Lay::oB, *sC = sm + Lay::oC, *sX = sm + Lay::oX, *sM = sm + Lay::oM,
           *sP = sm + Lay::oP;
     if (OWN) launch_dependents();                          // (the scan waits for this grid's end)
-    else grid_dependency_wait();                           // (after the scan: the entering states)
+    else if (blockIdx.x / p.n_roles / p.H >= p.n_max) grid_dependency_wait();    // (not a first segment: after the scan)
     if (status_blocks_cta(p.status)) return;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int unit = blockIdx.x / p.n_roles, h = unit % p.H;
-    const int64_t row = unit / p.H;
     const int role = (p.roles >> (2 * (blockIdx.x % p.n_roles))) & 3;
     const bool rev = role >= kDv, trans = role == kDq || role == kDk;
     Item it;
-    if (!find_item<kSimtThreads>(p, row, it)) return;
-    if (OWN && (rev ? it.i == 0 : it.last)) return;       // no later (earlier) segment reads it
+    if (!find_item<kSimtThreads, OWN>(p, unit / p.H, rev, it)) return;
     const Rows ra = role == kFwd ? p.q : role == kDq ? p.d_o : role == kDv ? p.k : p.v;
     const Rows rb = role == kFwd ? p.k : role == kDq ? p.v : role == kDv ? p.q : p.d_o;
     const Rows rc = role == kFwd ? p.v : role == kDq ? p.k : role == kDv ? p.d_o : p.q;
@@ -100,12 +98,12 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(NA, NV)) dla_simt_kern
     // the increments
     const float s_inner = p.scale, s_state = rev ? 1.f : p.scale, s_inc = rev ? p.scale : 1.f;
     const int64_t KV = (int64_t)NA * NV;
-    const int64_t seq_state = ((int64_t)it.n * p.H + h) * KV, row_state = (row * p.H + h) * KV;
+    const int64_t seq_state = ((int64_t)it.n * p.H + h) * KV, row_state = (it.row * p.H + h) * KV;
     const int64_t n_seq = (int64_t)p.n_max * p.H * KV, n_row = p.n_rows * p.H * KV;
 
     for (int e = tid; e <= C; e += kSimtThreads) sP[e] = decay_pow(g, e);
     {   // the entering state; element (r, c) of M is at r * NV + c, transposed roles: c * NA + r
-        const float *seg = (rev ? it.last : it.i == 0) ? nullptr : rev ? p.seg_rev : p.seg_fwd;
+        const float *seg = it.row < 0 ? nullptr : rev ? p.seg_rev : p.seg_fwd;
         const float *src = OWN ? nullptr : seg ? seg + row_state : rev ? p.dht : p.h0;
         if (!OWN && !seg && src) src += seq_state;
         if (src && !GCL_RANGE_IN_BOUNDS(seg ? row_state : seq_state, (seg ? row_state : seq_state) + KV - 1,
@@ -323,7 +321,7 @@ cudaError_t launch_simt_one(const Params &p, cudaStream_t s) {
     constexpr size_t smem = SimtLayout<NA, NV>::bytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)(p.n_rows * p.H * p.n_roles);
+    const unsigned grid = (unsigned)(((OWN ? 0 : p.n_max) + p.n_rows) * p.H * p.n_roles);
     if (!OWN && (p.seg_fwd || p.seg_rev)) return launch_dependent(kern, dim3(grid), dim3(kSimtThreads), smem, s, p);
     kern<<<grid, kSimtThreads, smem, s>>>(p);
     return cudaGetLastError();

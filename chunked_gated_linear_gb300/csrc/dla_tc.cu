@@ -159,20 +159,20 @@ struct Ctx {                       // what every warp of a CTA needs of its work
     __device__ __forceinline__ bool three() const { return role == kFwd || role == kDv; }
     // The role, head and segment of block b; false: nothing to do.
     // (Its values are made uniform, so that code on them stays convergent.)
-    template <int kBlock>
+    template <int kBlock, bool kOwn>
     __device__ __forceinline__ bool find(const Params &p, int b, int &row, bool &last) {
         role = (p.roles >> (2 * (b % p.n_roles))) & 3;
         b /= p.n_roles;
         h = b % p.H;
-        row = b / p.H;
+        rev = role >= kDv;
         Item it = {};
-        const bool ok = find_item<kBlock>(p, row, it);
+        const bool ok = find_item<kBlock, kOwn>(p, b / p.H, rev, it);
+        row = uniform((int)it.row);
         n = uniform(it.n);
         i = uniform(it.i);
         s0 = uniform((int)it.s0);
         s1 = uniform((int)it.s1);
         last = uniform((int)it.last) != 0;
-        rev = role >= kDv;
         nch = (s1 - s0 + C - 1) / C;
         return ok;
     }
@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
     __shared__ uint32_t s_tmem, s_rows[2];
     __shared__ int s_err;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    grid_dependency_wait();                                // (after the scan: the entering states)
+    // a row past the sequences' first segments needs the scan's states; the others start before it
+    if (blockIdx.x / p.n_roles / p.H >= p.n_max) grid_dependency_wait();
     // the status word is loaded beside the item, not before it: each is a chain of loads, and what needs neither
     // is done meanwhile
     const bool blocked = status_blocks(p.status);
@@ -329,14 +330,14 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
     Ctx x;
     int row;
     bool last;
-    const bool found = x.find<kEngineThreads>(p, blockIdx.x, row, last);
+    const bool found = x.find<kEngineThreads, false>(p, blockIdx.x, row, last);
     if (__syncthreads_or(blocked) || !found) return;
     const bool rev = x.rev;
     const int nch = x.nch, h = x.h;
     // the entering state (NULL: zeros) and where the leaving one goes (NULL: nowhere)
     auto entering = [&]() -> const float * {
         const int64_t KV = (int64_t)NA * NV;
-        const float *seg = (rev ? last : x.i == 0) ? nullptr : rev ? p.seg_rev : p.seg_fwd, *first = rev ? p.dht : p.h0;
+        const float *seg = row < 0 ? nullptr : rev ? p.seg_rev : p.seg_fwd, *first = rev ? p.dht : p.h0;
         return seg ? seg + ((int64_t)row * p.H + h) * KV : first ? first + ((int64_t)x.n * p.H + h) * KV : nullptr;
     };
     auto leaving = [&]() -> float * {
@@ -778,10 +779,9 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
     Ctx x;
     int row;
     bool last;
-    const bool found = x.find<kOwnThreads>(p, blockIdx.x, row, last);
+    const bool found = x.find<kOwnThreads, true>(p, blockIdx.x, row, last);
     if (__syncthreads_or(blocked) || !found) return;
     const bool rev = x.rev;
-    if (rev ? x.i == 0 : last) return;                     // no later (earlier) segment reads it
     const int h = x.h, nch = x.nch;
     if (tid == 0) {
         for (int i = 0; i < kOwnTiles; ++i) mbar_init(&full[i], 1);
@@ -904,7 +904,7 @@ bool make_map(CUtensorMap *m, const Rows &r, int D, int H, int64_t t_max, int bo
 
 template <int NA, int NV>
 cudaError_t launch_one(const Maps &maps, const Params &p, bool own_states, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.n_rows * p.H * p.n_roles);
+    const unsigned grid = (unsigned)(((own_states ? 0 : p.n_max) + p.n_rows) * p.H * p.n_roles);
     if (own_states) {
         cudaError_t e = cudaFuncSetAttribute(dla_own_kernel<NA, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)OwnLayout<NA, NV>::bytes);
@@ -914,7 +914,7 @@ cudaError_t launch_one(const Maps &maps, const Params &p, bool own_states, cudaS
         cudaError_t e = cudaFuncSetAttribute(dla_tc_kernel<NA, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)TcLayout<NA, NV>::bytes);
         if (e != cudaSuccess) return e;
-        if (p.seg_fwd || p.seg_rev)                        // (its set-up overlaps the scan's end)
+        if (p.seg_fwd || p.seg_rev)                        // (first segments run beside the launches before)
             return launch_dependent(dla_tc_kernel<NA, NV>, dim3(grid), dim3(kEngineThreads), TcLayout<NA, NV>::bytes, s, maps, p);
         dla_tc_kernel<NA, NV><<<grid, kEngineThreads, TcLayout<NA, NV>::bytes, s>>>(maps, p);
     }
