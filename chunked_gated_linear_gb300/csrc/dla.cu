@@ -204,6 +204,11 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
         if ((x.in || x.out) && (st = check_rows(fn, x.name, *x.r, a->t_max, a->H, x.D, es, x.out)) != GCL_OK) return st;
     for (const void *x : {(const void *)a->h0, (const void *)a->ht, (const void *)a->dht, (const void *)a->dh0})
         if (!aligned(x, 16)) return fail(GCL_ERR_INVALID_ARG, "%s: states must be 16-byte aligned", fn);
+    // (a sequence's segments run side by side: one may write the state before another has read it)
+    const float *out_state = backward ? a->dh0 : a->ht;
+    if (out_state && (out_state == a->h0 || (backward && out_state == a->dht)))
+        return fail(GCL_ERR_INVALID_ARG, "%s: %s must not be %s", fn, backward ? "dh0" : "ht",
+                    out_state == a->h0 ? "h0" : "dht");
     const size_t bytes = segment_bytes(a, backward);
     if (bytes && (!a->workspace || a->workspace_bytes < bytes))
         return fail(GCL_ERR_CAPACITY, "%s: workspace of %zu bytes needed, %zu given", fn, bytes,
