@@ -754,6 +754,8 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
 // sum_j gamma^(distance to the segment's end) b_j c_j^T over one segment: MMA4 alone, with the decay
 // taken to the segment's end, so that the sum stays in TMEM until the last chunk.  Warps 0-15 split b
 // (eight take 32 tokens at a time, four TMEM buffers), warp 16 loads, warp 17 issues.  b, c: three tiles each.
+// Every wait is for a barrier whose next phase its waiter has to allow first (a parity says nothing about the phase
+// after): a buffer's by the warps that fill it next, a tile's by the loader, the sum's by a barrier that completes once.
 // 65,536 tokens of 4 heads, 128 x 128: 32 us, 4.1 TB/s, with the split's instructions (52% of issue) before HBM.
 constexpr int kOwnWarps = 16, kOwnTma = 16, kOwnMma = 17, kOwnThreads = 18 * 32, kBufs = C / kRows, kOwnTiles = 3;
 
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
     using Lay = OwnLayout<NA, NV>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[kOwnTiles], bar_split[kBufs], bar_free[kBufs], bar_end;
+    __shared__ uint64_t full[kOwnTiles], empty[kOwnTiles], bar_split[kBufs], bar_free[kBufs], bar_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -784,7 +786,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
     const bool rev = x.rev;
     const int h = x.h, nch = x.nch;
     if (tid == 0) {
-        for (int i = 0; i < kOwnTiles; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < kOwnTiles; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&bar_split[i], kOwnWarps / 2);
             mbar_init(&bar_free[i], 1);
@@ -808,7 +813,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
             for (; ic < nch; ++ic) {
                 const int s = ic % kOwnTiles;
                 // (MMA4 of chunk ic - kOwnTiles has read c; its split has read b before)
-                if (ic >= kOwnTiles && !wait_bar(&bar_free[kBufs - 1], (ic - kOwnTiles) & 1, &s_err, 1)) break;
+                if (ic >= kOwnTiles && !wait_bar(&empty[s], (ic / kOwnTiles - 1) & 1, &s_err, 1)) break;
                 mbar_arrive_expect_tx(&full[s], C * (NA + NV) * 2);
                 for (int cb = 0; cb < NA / 64; ++cb)
                     tma_load_3d(smem + Lay::oB + s * Lay::sb + cb * C * 128, mb, cb * 64, h, x.t0(ic), &full[s]);
@@ -832,8 +837,9 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
                 mma_state<NV>(tmem, tmem + 128 + q * 64, sbase + Lay::oC + s * Lay::sc, q, ic + q, true);
                 commit_warp(&bar_free[q]);
             }
+            if (ok) commit_warp(&empty[s]);
         }
-        commit_warp(&bar_end);
+        commit_warp(&bar_end);                              // every MMA issued has finished
         if (lane == 0) drain(&bar_end, 0);
         __syncwarp();
     } else {
@@ -865,7 +871,9 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
                 if (lane == 0) mbar_arrive(&bar_split[q]);
             }
         }
-        if (ok && wait_warp(&bar_free[kBufs - 1], (nch - 1) & 1, &s_err, 6)) {
+        // (Not bar_free of the last step: the warps that take the even steps have not waited for it before, so that
+        // its phase may still be the one before the last chunk's, whose parity passes.)
+        if (ok && wait_warp(&bar_end, 0, &s_err, 6)) {
             tc_fence_after();
             float4 *rows = reinterpret_cast<float4 *>(smem);       // through the tiles, to whole lines
             constexpr int RC = NV / 4;
