@@ -159,6 +159,22 @@ __device__ __forceinline__ bool find_item(const Params &p, int64_t j, bool rev, 
     return true;
 }
 
+// Whether the block does nothing, the status word having been set before the call; for the calls that go on past an index
+// of their own out of range (bad(i) of i < n), whose blocks start before and after it is found and the word is set.  A word
+// that holds GCL_DEV_BAD_RANGE stops the block only if the call has no such index: each block then takes
+// the same way.  (Looked up in that case alone.)  Every thread of the block calls it (block barriers).
+template <typename Bad>
+__device__ __forceinline__ bool call_blocked(const int32_t *status, int64_t n, Bad bad) {
+    __shared__ int s_word;
+    if (threadIdx.x == 0) s_word = status ? *reinterpret_cast<const volatile int32_t *>(status) : 0;
+    __syncthreads();
+    if (s_word == 0) return false;
+    if (s_word != GCL_DEV_BAD_RANGE) return true;
+    bool own = false;
+    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) own |= bad(i);
+    return !__syncthreads_or(own);
+}
+
 // ---- host checks shared by the entry points that take gcl_rows ---------------
 inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline Rows rows(const gcl_rows &r) { return Rows{r.ptr, r.token_stride, r.head_stride}; }

@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kStepThreads) dla_step_kernel(const StepParams
     constexpr int RPT = K / RG > 0 ? K / RG : 1;           // key rows per thread
     __shared__ float sq[K], sk[K];
     __shared__ __align__(16) float so[RG][VS];
-    if (status_blocks_cta(p.status)) return;
+    if (call_blocked(p.status, p.slots ? p.batch : 0, [&](int64_t i) { return p.slots[i] >= p.n_slots; })) return;
     const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
     const int h = (blockIdx.x / (V / VS)) % p.H, v0 = (blockIdx.x % (V / VS)) * VS;
     const int b = blockIdx.x / (V / VS) / p.H;

@@ -536,8 +536,11 @@ gcl_status_t dla_chunk_bwd(const gcl_dla_args *args, gcl_stream_t stream);
  * slot s = slots[b] (slots NULL: s = b) updated in place,
  *   S <- gamma S + k_b v_b^T,   o_b = scale S^T q_b.
  * A request with a negative slot is idle (padding of a captured batch): no state is touched and its
- * rows of o are zeros.  A slot >= n_slots sets GCL_DEV_BAD_RANGE and is treated as idle.
- * Two requests of one call must not share a slot.
+ * rows of o are zeros.  A slot >= n_slots sets GCL_DEV_BAD_RANGE and is treated as idle; every
+ * other request of the call is served.  (A word that already holds GCL_DEV_BAD_RANGE stops the call
+ * like any other, except one with such a slot, which cannot tell the word from its own: it
+ * serves the other requests.)  Two requests of one call must not share a slot, and o overlaps
+ * neither q, k, v nor the states.
  */
 typedef struct gcl_dla_step_args {
     gcl_rows q, k;                 /* [batch, H, K] dtype                                    */
