@@ -145,6 +145,11 @@ struct Raw {
 
 constexpr int qk_ctas(bool bwd) { return bwd ? 2 : 3; }    // resident blocks per SM
 
+// The call does nothing.  (A position of its own past the tables leaves that token's rows alone, not the others.)
+__device__ __forceinline__ bool blocked(const QkParams &p) {
+    return dla::call_blocked(p.status, p.R > 0 ? p.t_max : 0, [&](int64_t t) { return p.pos[t] >= p.n_pos; });
+}
+
 // An item is some of the heads of one token, of q or of k by the block; a lane group (D / 8 lanes) takes its
 // heads PER at a time, with their rows in flight together, and keeps the token's rotation factors.  Lane
 // groups walk the items with the stride of the side's blocks.  Lanes without work stay for the
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, qk_ctas(BWD)) qk_kernel(const QkPara
     constexpr int L = D / 8, G = kThreads / L;             // lanes per row, lane groups per block
     __shared__ __align__(8) float s_dw[BWD ? G : 1][BWD ? D : 1];
     if (BWD) launch_dependents();                          // (the sums of the weights' gradients wait for this grid's end)
-    if (status_blocks_cta(p.status)) return;
+    if (blocked(p)) return;
     const int tid = threadIdx.x, l = tid % L, grp = tid / L;
     const int which = blockIdx.x < p.blocks_q ? 0 : 1;
     const int block = which ? blockIdx.x - p.blocks_q : blockIdx.x, blocks = which ? gridDim.x - p.blocks_q : p.blocks_q;
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, qk_ctas(BWD)) qk_kernel(const QkPara
 __global__ void __launch_bounds__(1024) qk_dw_kernel(const QkParams p, int blocks_k, int D) {
     __shared__ float s[32][33];
     grid_dependency_wait();
-    if (status_blocks_cta(p.status)) return;
+    if (blocked(p)) return;
     const Side &sd = p.side[blockIdx.y];
     if (!sd.partial) return;
     const int lane = threadIdx.x & 31, ch = blockIdx.x * 32 + lane, r = threadIdx.x >> 5;

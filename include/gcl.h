@@ -566,8 +566,10 @@ gcl_status_t dla_step(const gcl_dla_step_args *args, gcl_stream_t stream);
  *   (GCL_PAIR_HALF) or (2i, 2i + 1) (GCL_PAIR_ADJACENT); channels R and up keep z.
  * cos and sin are the rows positions[t] of tables [n_positions, R / 2] fp32 (rope_table_build).
  * R = 0: no rotation; the tables are not read.  A token with a negative position is padding: its
- * rows are not used and not written.  A position >= n_positions sets GCL_DEV_BAD_RANGE and its
- * rows are left alone as well.  Without positions every row is live (R must be 0).
+ * rows are not used and not written.  With R > 0 a position >= n_positions sets GCL_DEV_BAD_RANGE and
+ * its rows are left alone as well; every other row is written and the weights' gradients are those of the
+ * others.  (A word that already holds GCL_DEV_BAD_RANGE stops the call like any other, except one with such a
+ * position, which cannot tell the word from its own.)  Without positions every row is live (R must be 0).
  *
  * The backward takes dyq, dyk and the forward's inputs and gives dq, dk and, where a weight is
  * given, its gradient (fp32, summed over the tokens and heads in a fixed order).
