@@ -543,8 +543,22 @@ _QK_PACK = struct.Struct("@" + _ROWS_FMT * 8 + "PPPPPPPPPNqqiiiifiii0q")
 _NO_ROWS = (0, 0, 0)
 
 
+def _current_device():
+    import torch
+    return torch._C._cuda_getDevice()
+
+
+def _on_device(fn, device):
+    """The library launches on the current device and plans for it, so the tensors have to live there.  (A pointer of
+    another device would be used on this one.)"""
+    if device != _current_device():
+        raise ValueError(f"{fn}: the tensors are on cuda:{device}, the current device is cuda:{_current_device()}; make "
+                         f"theirs current (torch.cuda.device)")
+
+
 def _packed_call(fn, packed, stream, device):
     """Calls entry point `fn` of the loaded library with a packed argument struct."""
+    _on_device(fn, device)
     handle = lib()
     entry = handle.__dict__.get("_packed_" + fn)
     if entry is None:
@@ -599,25 +613,29 @@ def _scratch(fn, t, device):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _dla_sizes(q, v, cu_seqlens):
+def _dla_sizes(fn, q, v, cu_seqlens):
+    if q.get_device() >= 0:                                # (the plan is for the current device's SMs)
+        _on_device(fn, q.get_device())
     T, H, K = q.shape
     return DlaArgs(t_max=T, n_max=cu_seqlens.shape[0] - 1, H=H, K=K, V=v.shape[2], dtype=_dtype_of(q))
 
 
 def dla_segment_tokens(t_max: int, n_max: int, H: int, backward: bool = False, dtype: int = GCL_BF16,
                        K: int = 128, V: int = 128) -> int:
-    """Tokens per segment of the plan for these capacities (t_max or more: sequences stay whole)."""
+    """Tokens per segment of the plan for these capacities on the current device (t_max or more: sequences stay whole)."""
     return int(lib().gcl_dla_segment_tokens(t_max, n_max, H, int(backward), dtype, K, V))
 
 
 def dla_fwd_workspace_bytes(q, v, cu_seqlens) -> int:
     """Workspace of dla_chunk_fwd for these sizes (0: none)."""
-    return int(lib().gcl_dla_fwd_workspace_bytes(ctypes.byref(_dla_sizes(q, v, cu_seqlens))))
+    a = _dla_sizes("dla_fwd_workspace_bytes", q, v, cu_seqlens)
+    return int(lib().gcl_dla_fwd_workspace_bytes(ctypes.byref(a)))
 
 
 def dla_bwd_workspace_bytes(q, v, cu_seqlens) -> int:
     """Workspace of dla_chunk_bwd for these sizes (0: none)."""
-    return int(lib().gcl_dla_bwd_workspace_bytes(ctypes.byref(_dla_sizes(q, v, cu_seqlens))))
+    a = _dla_sizes("dla_bwd_workspace_bytes", q, v, cu_seqlens)
+    return int(lib().gcl_dla_bwd_workspace_bytes(ctypes.byref(a)))
 
 
 def dla_chunk_fwd(q, k, v, g, cu_seqlens, o, h0=None, ht=None, seq_order=None, dev_status=None,
@@ -727,6 +745,8 @@ def qk_norm_rope_fwd(q, k, yq, yk, q_weight=None, k_weight=None, cos=None, sin=N
 
 def qk_norm_rope_bwd_workspace_bytes(q, k) -> int:
     """Workspace of qk_norm_rope_bwd with weight gradients."""
+    if q.get_device() >= 0:
+        _on_device("qk_norm_rope_bwd_workspace_bytes", q.get_device())
     T, HQ, D = q.shape
     a = QkArgs(t_max=T, HQ=HQ, HK=0 if k is None else k.shape[1], D=D)
     return int(lib().gcl_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(a)))
@@ -750,4 +770,5 @@ def rope_table_build(cos, sin, base: float = 10000.0, stream=None):
     if dev < 0:
         raise ValueError(f"{fn}: cos must be a CUDA tensor (got {cos.device})")
     c, s = _flat(fn, "cos", cos, shape, f32, dev), _flat(fn, "sin", sin, shape, f32, dev)
+    _on_device(fn, dev)
     _check(fn, lib().rope_table_build(c, s, shape[0], 2 * shape[1], float(base), _stream(stream)))
