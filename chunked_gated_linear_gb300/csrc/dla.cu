@@ -206,9 +206,13 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
         if (!aligned(x, 16)) return fail(GCL_ERR_INVALID_ARG, "%s: states must be 16-byte aligned", fn);
     // (a sequence's segments run side by side: one may write the state before another has read it)
     const float *out_state = backward ? a->dh0 : a->ht;
-    if (out_state && (out_state == a->h0 || (backward && out_state == a->dht)))
-        return fail(GCL_ERR_INVALID_ARG, "%s: %s must not be %s", fn, backward ? "dh0" : "ht",
-                    out_state == a->h0 ? "h0" : "dht");
+    const uintptr_t state_bytes = sizeof(float) * (uintptr_t)a->n_max * a->H * a->K * a->V;
+    struct { const char *name; const float *p; } in_state[] = {{"h0", a->h0}, {"dht", backward ? a->dht : nullptr}};
+    for (const auto &x : in_state) {
+        const uintptr_t i = reinterpret_cast<uintptr_t>(x.p), o = reinterpret_cast<uintptr_t>(out_state);
+        if (i && o && (i < o ? o - i : i - o) < state_bytes)
+            return fail(GCL_ERR_INVALID_ARG, "%s: %s must not be %s (their states overlap)", fn, backward ? "dh0" : "ht", x.name);
+    }
     const size_t bytes = segment_bytes(a, backward);
     if (bytes && (!a->workspace || a->workspace_bytes < bytes))
         return fail(GCL_ERR_CAPACITY, "%s: workspace of %zu bytes needed, %zu given", fn, bytes,

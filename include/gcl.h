@@ -488,7 +488,8 @@ typedef struct gcl_rows {
  * Supported: K, V in {64, 128}; dtype GCL_F32, GCL_BF16, GCL_F16 for every gcl_rows; states and
  * their gradients [n_max, H, K, V] fp32, g [H] fp32.  Sums and states are fp32.  The
  * gradients dq, dk, dv have the type of the inputs: the projections' backward reads them so.
- * Outputs overlap no input: a sequence's segments run side by side (ht = h0, dh0 = dht or h0 are refused).
+ * Outputs overlap no input: a sequence's segments run side by side (an ht that shares memory with h0, a dh0
+ * that does with dht or h0, are refused).
  */
 typedef struct gcl_dla_args {
     gcl_rows q, k;                 /* [t_max, H, K] dtype                                    */
