@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(NA, NV)) dla_simt_kern
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    // (zeros past the end as well: gamma^d may be infinite there if g > 0)
                     const int r = ty + 16 * i, c = tx + 16 * j, d = rev ? c - r : r - c;
-                    sX[r * LX + c] = d >= 0 ? s_inner * sP[d] * x[i][j] : 0.f;
+                    sX[r * LX + c] = d >= 0 && (rev ? c : r) < len ? s_inner * sP[d] * x[i][j] : 0.f;
                 }
             __syncthreads();
             // ---- out = X c + gamma^e a M

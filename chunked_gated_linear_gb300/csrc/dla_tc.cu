@@ -392,11 +392,12 @@ __global__ void __launch_bounds__(kEngineThreads, 1) dla_tc_kernel(const __grid_
         const float w = decay_pow(g, e);
         sP[e] = w;
         if (e < 32) sNear[rev ? e : 31 - e] = w;           // gamma^(block's near end to column)
-        // w of a whole chunk's tokens, and of the short chunk at the segment's end (backwards the same)
+        // w of a whole chunk's tokens, and of the short chunk at the segment's end (zero past it, where w may be
+        // infinite if g > 0 and the split has zeros for b)
         if (rev ? e > 0 : e < C) sW[rev ? e - 1 : C - 1 - e] = s_inc * w;
         const int tail = (x.s1 - x.s0) % C;
-        if (rev ? e > 0 : e < tail) sW[C + (rev ? e - 1 : tail - 1 - e)] = s_inc * w;
-        if (!rev && e >= tail && e < C) sW[C + e] = 0.f;
+        if (rev ? e > 0 && e <= tail : e < tail) sW[C + (rev ? e - 1 : tail - 1 - e)] = s_inc * w;
+        if (e >= tail && e < C) sW[C + e] = 0.f;
     }
     tc_fence_before();
     __syncthreads();
@@ -860,7 +861,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) dla_own_kernel(const __grid_co
                 if (ic > 0 && !(ok = wait_warp(&bar_free[q], (ic - 1) & 1, &s_err, 5))) break;
                 tc_fence_after();
                 const int r0 = q * kRows + half * 16, t = t0 + r0 + lane;          // the warp's 16 weights
-                if (lane < 16) w[lane] = s_inc * decay_pow(g, rev ? t - x.s0 + 1 : x.s1 - 1 - t > 0 ? x.s1 - 1 - t : 0);
+                if (lane < 16) w[lane] = t < x.s1 ? s_inc * decay_pow(g, rev ? t - x.s0 + 1 : x.s1 - 1 - t) : 0.f;
                 __syncwarp();
                 if (NA == 128 || m < NA)
                     split16<NA>(smem_u32(smem) + Lay::oB + s * Lay::sb, (warp & 3) * 32, r0, len, w,

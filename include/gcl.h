@@ -480,8 +480,8 @@ typedef struct gcl_rows {
  *   dq_t = scale S_t do_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,   dh0 = gamma G_0.
  *
  * A zero-length sequence passes its state through (ht = h0, dh0 = dht).  gamma = 0 (g = -inf)
- * and gamma = 1 (g = 0) are allowed; g > 0 is computed as given as long as exp(g n) over a
- * segment's n tokens stays finite.  Token rows at or past cu_seqlens[n_max] are never read into a
+ * and gamma = 1 (g = 0) are allowed; g > 0 is computed as given as long as exp(g n) is
+ * finite for the n tokens of every sequence.  Token rows at or past cu_seqlens[n_max] are never read into a
  * result nor written.  Products are formed per chunk of tokens: a token whose v (backward: v,
  * d_o, q or k) is not finite can make other rows of its own chunk of 128 tokens not finite.
  *
