@@ -101,7 +101,8 @@ namespace {
 // Tokens per segment, from the capacities.  Time is counted in chunks (128 tokens on the tensor cores, 64 on
 // the CUDA cores) of one CTA: an output CTA takes its chunks and kStart, an own-state CTA kOwn of its
 // chunks and kStart, the scan and the two further launches kLaunch.
-//  - Every candidate length is costed for n_max sequences of t_max / n_max tokens.  (One sequence of
+//  - Candidate lengths, every one up to 128 chunks and then a 64th apart (a plan is made on every call; a million
+//    tokens are 8,192 chunks, 400 candidates), are costed for n_max sequences of t_max / n_max tokens.  (One sequence of
 //    65,536 tokens, 4 heads: whole 1,540 us, segments of 1,792 or 1,920 101 to 104, of 4,096 163.  4 sequences of
 //    8,192, 16 heads, backward: whole 454 us, segments of 2,816 or 4,096 413 to 422, of 1,792 452.  fp32, 2 sequences,
 //    4,096 tokens, 8 heads of 64: whole 659 us, segments of 64 74, of 128 68, of 256 107.)
@@ -128,7 +129,10 @@ int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, i
     }
     double best = 1e300;
     int64_t seg = whole;
-    for (int64_t c = 1; c <= (most < chunks ? most : chunks); ++c) {
+    if (most > chunks) most = chunks;
+    for (int64_t c = 1, next; c <= most; c = next) {
+        next = c < 128 ? c + 1 : c + c / 64;
+        if (next > most && c < most) next = most;          // (the longest, for a whole sequence, always)
         const int64_t full = chunks / c, rest = chunks % c, parts = full + (rest > 0);
         const double item = c + kStart, work = (double)units * (chunks + parts * kStart) / sms;
         const double waves = (double)((units * full + sms - 1) / sms) * item;
@@ -149,10 +153,15 @@ int64_t segment_tokens(int64_t t_max, int32_t n_max, int32_t H, bool backward, i
 // Borders between segments, at most: a sequence has (length - 1) / seg of them.
 int64_t border_rows(int64_t t_max, int64_t seg) { return seg >= t_max ? 0 : (t_max - 1) / seg; }
 
-size_t segment_bytes(const gcl_dla_args *a, bool backward) {
+// The plan of a call, 0 for sizes that have none.
+int64_t plan(const gcl_dla_args *a, bool backward) {
     if (a->t_max < 1 || a->t_max >= (int64_t(1) << 31) || a->n_max < 1 || a->H < 1 || a->K < 1 || a->V < 1) return 0;
-    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype, a->K, a->V);
-    if (seg >= a->t_max) return 0;
+    return segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype, a->K, a->V);
+}
+
+// Workspace of the plan with segments of seg tokens.
+size_t segment_bytes(const gcl_dla_args *a, bool backward, int64_t seg) {
+    if (seg < 1 || seg >= a->t_max) return 0;
     // a state per segment (a border's states need one less a sequence)
     return (size_t)gcl_nt_max(a->t_max, a->n_max, (int32_t)seg) * a->H * a->K * a->V * sizeof(float) * (backward ? 2 : 1);
 }
@@ -213,7 +222,8 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
         if (i && o && (i < o ? o - i : i - o) < state_bytes)
             return fail(GCL_ERR_INVALID_ARG, "%s: %s must not be %s (their states overlap)", fn, backward ? "dh0" : "ht", x.name);
     }
-    const size_t bytes = segment_bytes(a, backward);
+    const int64_t seg = plan(a, backward);
+    const size_t bytes = segment_bytes(a, backward, seg);
     if (bytes && (!a->workspace || a->workspace_bytes < bytes))
         return fail(GCL_ERR_CAPACITY, "%s: workspace of %zu bytes needed, %zu given", fn, bytes,
                     a->workspace ? a->workspace_bytes : (size_t)0);
@@ -231,7 +241,6 @@ gcl_status_t run_chunk(const char *fn, const gcl_dla_args *a, bool backward, cud
     p.g = a->g; p.h0 = a->h0;
     p.cu = a->cu_seqlens; p.seq_order = a->seq_order; p.status = a->dev_status;
     p.t_max = a->t_max; p.n_max = a->n_max; p.H = a->H; p.K = a->K; p.V = a->V; p.scale = a->scale;
-    const int64_t seg = segment_tokens(a->t_max, a->n_max, a->H, backward, a->dtype, a->K, a->V);
     p.n_rows = border_rows(a->t_max, seg);
     p.seg = (int32_t)(seg < a->t_max ? seg : a->t_max);
     const int both[2] = {kFwd, kDv}, out[3] = {kDq, kDv, kDk};
@@ -259,8 +268,8 @@ int64_t gcl_dla_segment_tokens(int64_t t_max, int32_t n_max, int32_t H, int32_t 
     return dla::segment_tokens(t_max, n_max, H, backward != 0, dtype, K, V);
 }
 
-size_t gcl_dla_fwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, false) : 0; }
-size_t gcl_dla_bwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, true) : 0; }
+size_t gcl_dla_fwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, false, dla::plan(a, false)) : 0; }
+size_t gcl_dla_bwd_workspace_bytes(const gcl_dla_args *a) { return a ? dla::segment_bytes(a, true, dla::plan(a, true)) : 0; }
 
 gcl_status_t dla_chunk_fwd(const gcl_dla_args *a, gcl_stream_t stream) {
     return dla::run_chunk("dla_chunk_fwd", a, false, static_cast<cudaStream_t>(stream));

@@ -193,7 +193,7 @@ cudaError_t launch_simt_t(const Params &p, bool own_states, int n_roles, const i
 cudaError_t launch(const Params &p, int dtype, bool own_states, int n_roles, const int *roles, cudaStream_t s);
 // Tensor cores, bf16.
 cudaError_t launch_tc(const Params &p, bool own_states, int n_roles, const int *roles, cudaStream_t s);
-// The states that enter the segments, in place of the segments' own; ht and dh0 of empty sequences.
+// The states at the segments' borders, in place of the segments' own.
 cudaError_t launch_scan(const Params &p, bool backward, cudaStream_t s);
 
 }  // namespace dla
