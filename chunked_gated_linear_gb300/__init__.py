@@ -543,8 +543,13 @@ _QK_PACK = struct.Struct("@" + _ROWS_FMT * 8 + "PPPPPPPPPNqqiiiifiii0q")
 _NO_ROWS = (0, 0, 0)
 
 
+_devices = 0                             # visible devices, counted at the first call
+
+
 def _current_device():
+    global _devices
     import torch
+    _devices = torch.cuda.device_count()
     return torch._C._cuda_getDevice()
 
 
@@ -558,7 +563,8 @@ def _on_device(fn, device):
 
 def _packed_call(fn, packed, stream, device):
     """Calls entry point `fn` of the loaded library with a packed argument struct."""
-    _on_device(fn, device)
+    if _devices != 1:                    # (with one device there is no other; the look at it takes 0.4 us a call)
+        _on_device(fn, device)
     handle = lib()
     entry = handle.__dict__.get("_packed_" + fn)
     if entry is None:

@@ -47,6 +47,7 @@ def cuda0(gcl, monkeypatch):  # noqa: F811
             raise AssertionError(f"{name} was called")
 
     monkeypatch.setattr(gcl, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(gcl, "_devices", 2, raising=False)
     monkeypatch.setattr(gcl, "_lib", Unreached())
     return gcl
 
