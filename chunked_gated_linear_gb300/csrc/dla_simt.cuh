@@ -1,6 +1,7 @@
 // dla_simt.cuh -- decayed linear attention on the CUDA cores, all arithmetic in fp32: the engine of
-// dla.cuh for fp32 inputs (whose results leave no room for 16-bit operands) and for fp16 ones (whose
-// states and scores can pass fp16's largest value).
+// dla.cuh for fp32 and fp16 inputs.  (One 16-bit operand a value holds neither: fp32 results leave no room for its
+// rounding, and states and scores can pass fp16's largest value.  Sums of bf16 terms would, two for an fp16 value and
+// three for an fp32 one, at as many more products on the tensor cores; that form is not built.)
 //
 // One CTA of 256 threads owns one segment of one (sequence, head) in one role and walks its chunks
 // of C = 64 tokens with the state M [NA x NV] in shared memory.  Per chunk:

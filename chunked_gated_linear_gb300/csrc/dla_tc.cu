@@ -25,7 +25,8 @@
 //   warp 13      TMA loads, one chunk ahead: five tiles, three of the chunk and two of the next;
 //                the third of the next goes where a was once MMA2 has read it
 // (128 registers a thread: what spills misses the little L1 that 224 KiB of shared memory leave, and
-// with 96 registers those misses took more time than the arithmetic.)
+// with 96 registers those misses took more time than the arithmetic.  At NV = 128 12 registers a thread still
+// spill, 48 to 52 bytes; at NV = 64 none.)
 // What an MMA of this shape reads from shared memory (A and B, 8 KiB in 64 cycles) fills its port, so
 // everything else that goes through it waits: the split terms therefore go to TMEM, and outputs and
 // states cross a staging tile to leave and enter in whole lines (a lane per row touches 32 lines with
@@ -37,7 +38,8 @@
 // Shared memory at NA = NV = 128: 5 tiles, the staging tile and M, 32 KiB each.  TMEM: X, O, D and
 // the two split buffers, 128 columns each.
 // Rows past the end are selected to zero in w o b and zeroed in c, so no other sequence's rows
-// (or NaN padding) reach a sum.
+// (or NaN padding) reach a sum.  Within a sequence masked scores are zeros, which a row of c that is not finite
+// turns into NaN for its whole chunk; an infinite b gives NaN in the state (its terms are inf and inf - inf).
 #include <cudaTypedefs.h>
 
 #include "dla.cuh"

@@ -13,7 +13,10 @@
 // (forward: y = r (x c w + x' s w'), four fp32 pairs of products a lane), and the rows of four heads are in
 // flight together.  32,768 tokens of 16 + 16 heads of 128, bf16: 97 us, 5.5 TB/s; backward, 16,384
 // tokens of 16 + 2 heads: 60 us, 3.8 TB/s (bound by issue and the shuffles' latency: two blocks of 126 registers
-// an SM; three spill, 79 us, and rows brought ahead through shared memory take as long, 60).
+// an SM; three spill, 79 us, and rows brought ahead through shared memory take as long, 60).  The shuffles are this
+// layout's, twelve for a lane's eight values: lanes that held both halves of a pair would need none for the partners and
+// half of those for the sums (not tried).  fp32 rows, twice the registers, spill 156 bytes a thread with four in flight
+// (204 backwards at D = 256); they were not timed at a size that fills the GPU.
 #include "dla.cuh"
 #include "dla_simt.cuh"
 #include "f32x2.cuh"
@@ -418,8 +421,8 @@ cudaError_t launch_qk_per(QkParams &p, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t launch_qk(QkParams &p, bool backward, cudaStream_t s) {
     // four heads per lane group and step once there are rows for two full waves (32,768 tokens of 16 + 16
-    // heads of 128, bf16: 97 us with four, 131 with two, 168 with one); few rows are spread one by one,
-    // for latency
+    // heads of 128, bf16: 97 us with four, 131 with two, 168 with one; the other types follow bf16); few rows are
+    // spread one by one, for latency
     const int64_t G = kThreads / (D / 8), rows = p.t_max * ((int64_t)p.side[0].H + p.side[1].H);
     const bool many = rows >= 4 * 16 * (int64_t)num_sms() * G;
     if (backward) return many ? launch_qk_per<T, D, true, 4>(p, s) : launch_qk_per<T, D, true, 1>(p, s);

@@ -482,11 +482,15 @@ typedef struct gcl_rows {
  * A zero-length sequence passes its state through (ht = h0, dh0 = dht).  gamma = 0 (g = -inf)
  * and gamma = 1 (g = 0) are allowed; g > 0 is computed as given as long as exp(g n) is
  * finite for the n tokens of every sequence.  Token rows at or past cu_seqlens[n_max] are never read into a
- * result nor written.  Products are formed per chunk of tokens: a token whose v (backward: v,
- * d_o, q or k) is not finite can make other rows of its own chunk of 128 tokens not finite.
+ * result nor written.  Products are formed per chunk of tokens (128 for bf16, 64 else): a token whose v
+ * (backward: v, d_o, q or k) is not finite can make other rows of its own chunk not finite, earlier ones
+ * too, and for bf16 an infinite k (dh0: q) gives NaN in the state where the recurrence has infinity.
  *
  * Supported: K, V in {64, 128}; dtype GCL_F32, GCL_BF16, GCL_F16 for every gcl_rows; states and
- * their gradients [n_max, H, K, V] fp32, g [H] fp32.  Sums and states are fp32.  The
+ * their gradients [n_max, H, K, V] fp32, g [H] fp32.  Sums and states are fp32.  fp32 and fp16 rows
+ * are computed in fp32.  bf16 rows run on the tensor cores, where a chunk's scores and the state that enters it are
+ * rounded to bf16 once more as operands: o, dq, dk, dv carry 2.3e-3 in the norm, of which the rounding of the
+ * result is 1.7e-3; states that leave do not (three bf16 terms hold each increment to fp32).  The
  * gradients dq, dk, dv have the type of the inputs: the projections' backward reads them so.
  * Outputs overlap no input: a sequence's segments run side by side (an ht that shares memory with h0, a dh0
  * that does with dht or h0, are refused).
