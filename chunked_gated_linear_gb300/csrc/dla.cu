@@ -110,7 +110,7 @@ namespace {
 //    longest one's CTA would be the last to finish: no segment is longer than half of each SM's share of
 //    all tokens, but four chunks (two on the CUDA cores) are allowed (7 ragged sequences of 5,003 tokens in
 //    all, 6 heads, backward: 62 us, without this 105).
-//    More units are balanced by their order instead (32 prompts of 1 to 4,716 tokens in 64 slots, 16 heads:
+//    More units are balanced by their order instead (32 prompts of 73 to 4,716 tokens in 64 slots, 16 heads:
 //    whole in seq_order 147 us, cut at 1,792 tokens 225, at 2,432 to 4,096 190 to 203: own states and scan come
 //    first).  The price: one prompt of 33,000 tokens alone in the 64 slots takes 806 us, in one slot 161.
 //  - Sequences of one or two chunks on average, and units that fill every SM eight times, stay whole.
