@@ -287,7 +287,7 @@ def _plain_bwd(s):
     first, last, some = _ranges(s)
     nxt = torch.cat([a[1:], a.new_zeros(1, a.shape[1])])     # G_t = do_t + a_{t+1} G_{t+1} within a sequence
     nxt[last] = 0
-    g = s["do"].float()
+    g = s["do"].float().clone()                              # (fp32 rows would be changed in place)
     g[last] += s["dht"][some]
     G = _scan(nxt.flip(0), g.flip(0)).flip(0)
     dh0 = s["dht"].clone()
