@@ -115,6 +115,25 @@ class QkArgs(ctypes.Structure):
                 ("norm", ctypes.c_int32), ("pair", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class GlrArgs(ctypes.Structure):
+    _fields_ = [("x", Rows), ("r", Rows), ("i", Rows), ("o", Rows), ("d_o", Rows), ("dx", Rows),
+                ("dr", Rows), ("di", Rows), ("rate", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+                ("ht", ctypes.c_void_p), ("dht", ctypes.c_void_p), ("dh0", ctypes.c_void_p),
+                ("drate", ctypes.c_void_p), ("h_save", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("dev_status", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("t_max", ctypes.c_int64), ("n_max", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("decay", ctypes.c_int32), ("mix", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class GlrStepArgs(ctypes.Structure):
+    _fields_ = [("x", Rows), ("r", Rows), ("i", Rows), ("o", Rows), ("rate", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("dev_status", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("n_slots", ctypes.c_int32), ("D", ctypes.c_int32), ("decay", ctypes.c_int32),
+                ("mix", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 def load_library(path: str = LIB_PATH):
     """Load libgcl.so and declare its C signatures."""
     if not os.path.exists(path):
@@ -160,12 +179,15 @@ def load_library(path: str = LIB_PATH):
     lib.gcl_causal_conv1d_bwd_workspace_bytes.argtypes = [ctypes.POINTER(ConvArgs)]
     for fn, args in (("dla_chunk_fwd", DlaArgs), ("dla_chunk_bwd", DlaArgs),
                      ("dla_step", DlaStepArgs), ("qk_norm_rope_fwd", QkArgs),
-                     ("qk_norm_rope_bwd", QkArgs)):
+                     ("qk_norm_rope_bwd", QkArgs), ("glr_fwd", GlrArgs), ("glr_bwd", GlrArgs),
+                     ("glr_step", GlrStepArgs)):
         getattr(lib, fn).restype = ctypes.c_int
         getattr(lib, fn).argtypes = [ctypes.POINTER(args), vp]
     for fn, args in (("gcl_dla_fwd_workspace_bytes", DlaArgs),
                      ("gcl_dla_bwd_workspace_bytes", DlaArgs),
-                     ("gcl_qk_norm_rope_bwd_workspace_bytes", QkArgs)):
+                     ("gcl_qk_norm_rope_bwd_workspace_bytes", QkArgs),
+                     ("gcl_glr_fwd_workspace_bytes", GlrArgs),
+                     ("gcl_glr_bwd_workspace_bytes", GlrArgs)):
         getattr(lib, fn).restype = ctypes.c_size_t
         getattr(lib, fn).argtypes = [ctypes.POINTER(args)]
     lib.gcl_dla_segment_tokens.restype = i64
@@ -778,3 +800,121 @@ def rope_table_build(cos, sin, base: float = 10000.0, stream=None):
     c, s = _flat(fn, "cos", cos, shape, f32, dev), _flat(fn, "sin", sin, shape, f32, dev)
     _on_device(fn, dev)
     _check(fn, lib().rope_table_build(c, s, shape[0], 2 * shape[1], float(base), _stream(stream)))
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+DECAYS = {"log": 0, "sigmoid": 1, "power": 2}
+MIXES = {"one": 0, "complement": 1, "root": 2}
+_GLR_PACK = struct.Struct("@" + _ROWS_FMT * 8 + "PPPPPPPPPPNqiiiii0q")
+_GLR_STEP_PACK = struct.Struct("@" + _ROWS_FMT * 4 + "PPPPiiiiii0q")
+
+
+def _rows2(fn, name, t, shape, dtype, device):
+    """gcl_rows of a tensor [tokens, D] with contiguous D and any token stride."""
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor on the call's device (got {t.device})")
+    if t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    st, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{fn}: {name} must have contiguous rows (strides {t.stride()})")
+    if shape[0] == 1:                        # the stride of an extent of one is free: one that fits
+        st = shape[1]
+    if st < 0:
+        raise ValueError(f"{fn}: {name} has negative strides {t.stride()}")
+    return t.data_ptr(), st, shape[1]
+
+
+def _kind(fn, decay, mix):
+    if decay not in DECAYS or mix not in MIXES:
+        raise ValueError(f"{fn}: decay {decay!r} or mix {mix!r} is not one of {tuple(DECAYS)}, {tuple(MIXES)}")
+    return DECAYS[decay], MIXES[mix]
+
+
+def _save_rows(T):
+    return -(-T // CHUNK)
+
+
+def glr_fwd_workspace_bytes(x, cu_seqlens) -> int:
+    """Workspace of glr_fwd for these sizes."""
+    if x.get_device() >= 0:
+        _on_device("glr_fwd_workspace_bytes", x.get_device())
+    a = GlrArgs(t_max=x.shape[0], n_max=cu_seqlens.shape[0] - 1, D=x.shape[1], dtype=_dtype_of(x))
+    return int(lib().gcl_glr_fwd_workspace_bytes(ctypes.byref(a)))
+
+
+def glr_bwd_workspace_bytes(x, cu_seqlens, h_save=None, drate=True) -> int:
+    """Workspace of glr_bwd for these sizes, with the states h_save of the forward or without (None), and with
+    the gradient of the rates (drate) or without."""
+    if x.get_device() >= 0:
+        _on_device("glr_bwd_workspace_bytes", x.get_device())
+    a = GlrArgs(t_max=x.shape[0], n_max=cu_seqlens.shape[0] - 1, D=x.shape[1], dtype=_dtype_of(x),
+                h_save=None if h_save is None else 16, drate=16 if drate is not None and drate is not False else None)
+    return int(lib().gcl_glr_bwd_workspace_bytes(ctypes.byref(a)))
+
+
+def glr_fwd(x, r, cu_seqlens, o, i=None, rate=None, h0=None, ht=None, h_save=None, decay="power", mix="root",
+            dev_status=None, workspace=None, stream=None):
+    """The gated linear recurrence over packed sequences (include/gcl.h, glr): o [T, D] (None: only the states) and
+    ht [N, D] from x, the decay gate r, the input gate i (or None) [T, D] and h0.  x, r, i and o may have strided
+    tokens.  h_save [ceil(T / 64), D] fp32 keeps the states that the backward reads."""
+    from torch import float32 as f32, int32 as i32
+    fn = "glr_fwd"
+    sx = tuple(x.shape)
+    T, D = sx
+    N, dt, dev = cu_seqlens.shape[0] - 1, x.dtype, x.get_device()
+    kd, km = _kind(fn, decay, mix)
+    packed = _GLR_PACK.pack(
+        *_rows2(fn, "x", x, sx, dt, dev), *_rows2(fn, "r", r, sx, dt, dev),
+        *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)),
+        *(_NO_ROWS if o is None else _rows2(fn, "o", o, sx, dt, dev)), *_NO_ROWS, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
+        _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "h0", h0, (N, D), f32, dev), _flat(fn, "ht", ht, (N, D), f32, dev),
+        0, 0, 0, _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        *_scratch(fn, workspace, dev), T, N, D, kd, km, _dtype_of(x))
+    _packed_call(fn, packed, stream, dev)
+
+
+def glr_bwd(x, r, d_o, cu_seqlens, dx, dr, i=None, di=None, rate=None, drate=None, h0=None, dht=None, dh0=None,
+            h_save=None, decay="power", mix="root", dev_status=None, workspace=None, stream=None):
+    """The backward of glr_fwd: dx, dr, di (with i) of x's dtype, drate [D] and dh0 [N, D] from d_o and dht.  With the
+    forward's h_save the states are not formed again."""
+    from torch import float32 as f32, int32 as i32
+    fn = "glr_bwd"
+    sx = tuple(x.shape)
+    T, D = sx
+    N, dt, dev = cu_seqlens.shape[0] - 1, x.dtype, x.get_device()
+    kd, km = _kind(fn, decay, mix)
+    if (i is None) != (di is None):
+        raise ValueError(f"{fn}: i and di come together")
+    packed = _GLR_PACK.pack(
+        *_rows2(fn, "x", x, sx, dt, dev), *_rows2(fn, "r", r, sx, dt, dev),
+        *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)), *_NO_ROWS, *_rows2(fn, "d_o", d_o, sx, dt, dev),
+        *_rows2(fn, "dx", dx, sx, dt, dev), *_rows2(fn, "dr", dr, sx, dt, dev),
+        *(_NO_ROWS if di is None else _rows2(fn, "di", di, sx, dt, dev)),
+        _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "h0", h0, (N, D), f32, dev), 0,
+        _flat(fn, "dht", dht, (N, D), f32, dev), _flat(fn, "dh0", dh0, (N, D), f32, dev),
+        _flat(fn, "drate", drate, (D,), f32, dev), _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        *_scratch(fn, workspace, dev), T, N, D, kd, km, _dtype_of(x))
+    _packed_call(fn, packed, stream, dev)
+
+
+def glr_step(x, r, state, o, i=None, rate=None, slots=None, decay="power", mix="root", dev_status=None, stream=None):
+    """One token of each request: the states [n_slots, D] of the requests' slots are updated in place and
+    o [B, D] is written (include/gcl.h, glr_step).  slots int32 [B]; negative: idle."""
+    from torch import float32 as f32, int32 as i32
+    fn = "glr_step"
+    sx = tuple(x.shape)
+    B, D = sx
+    dt, dev, n_slots = x.dtype, x.get_device(), state.shape[0]
+    kd, km = _kind(fn, decay, mix)
+    packed = _GLR_STEP_PACK.pack(
+        *_rows2(fn, "x", x, sx, dt, dev), *_rows2(fn, "r", r, sx, dt, dev),
+        *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)), *_rows2(fn, "o", o, sx, dt, dev),
+        _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "state", state, (n_slots, D), f32, dev),
+        _flat(fn, "slots", slots, (B,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, D, kd, km,
+        _dtype_of(x))
+    _packed_call(fn, packed, stream, dev)

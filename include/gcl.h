@@ -616,6 +616,90 @@ gcl_status_t qk_norm_rope_bwd(const gcl_qk_args *args, gcl_stream_t stream);
 gcl_status_t rope_table_build(float *cos_table, float *sin_table, int64_t n_positions, int32_t R,
                               double base, gcl_stream_t stream);
 
+/*
+ * glr -- gated linear recurrence: a state of one value per channel with a decay of its own at every
+ * token, the recurrent mixer that stands beside the linear attention in hybrid layers (behind the same
+ * short convolution).  No page of the sources has it.  Per sequence and channel d, with h_-1 = h0
+ * (zeros without h0) and L tokens:
+ *
+ *   h_t = a_t h_{t-1} + m(a_t) u_t,   o_t = h_t,   ht = h_{L-1},   u_t = x_t sigmoid(i_t)  (x_t without i)
+ *   a = exp(r)                    (GCL_DECAY_LOG: r holds log decays, <= 0)
+ *       sigmoid(r)                (GCL_DECAY_SIGMOID)
+ *       exp(-rate_d sigmoid(r))   (GCL_DECAY_POWER, rate [D] fp32 >= 0)
+ *   m = 1 (GCL_MIX_ONE),  1 - a (GCL_MIX_COMPLEMENT),  sqrt(1 - a^2) (GCL_MIX_ROOT)
+ *
+ * The backward takes d_o and dht, the gradients w.r.t. o and ht (zeros without dht), and gives, with
+ * G_t = d_o_t + a_{t+1} G_{t+1} (the last token's G = d_o + dht) and l = log a:
+ *   dx = G m sigmoid(i),  di = G m x sigmoid'(i),  dh0 = a_0 G_0,  dl = a G h_{t-1} + G u dm/dl,
+ *   dr = dl | dl (1 - a) | dl l (1 - sigmoid(r)),  drate = -sum over tokens of dl sigmoid(r).
+ * dm/dl = -a^2 / m of GCL_MIX_ROOT is taken as 0 where m = 0 (a = 1).
+ *
+ * A zero-length sequence passes its state through (ht = h0, dh0 = dht).  a = 0 (r = -inf) and a = 1 are
+ * allowed; r > 0 of GCL_DECAY_LOG is computed as given (m(a) = 0 with GCL_MIX_ROOT) as long as the product of a over
+ * 128 consecutive tokens is finite.  Rows at or past cu_seqlens[n_max] are neither used nor written.  A value
+ * that is not finite reaches later tokens of its own sequence and channel alone (a d_o: earlier ones).
+ *
+ * h_save (forward, optional) receives the state before tokens 0, 64, 128, ... of the packed axis (a
+ * sequence's first token: h0); a backward that gets it does not form the states again.
+ *
+ * Rows x, r, i, o, d_o, dx, dr, di are [t_max, D] with any token stride (gcl_rows; head_stride is not
+ * read).  States and their gradients are [n_max, D] fp32.  Supported: D a multiple of 8; dtype GCL_F32, GCL_BF16,
+ * GCL_F16.  Arithmetic, states and sums are fp32, each output is rounded once; the results do not depend
+ * on the schedule.  Outputs overlap no input (an ht or dh0 that shares memory with h0 or dht is refused).
+ */
+typedef enum { GCL_DECAY_LOG = 0, GCL_DECAY_SIGMOID = 1, GCL_DECAY_POWER = 2 } gcl_decay_t;
+typedef enum { GCL_MIX_ONE = 0, GCL_MIX_COMPLEMENT = 1, GCL_MIX_ROOT = 2 } gcl_mix_t;
+
+typedef struct gcl_glr_args {
+    gcl_rows x, r;                 /* [t_max, D] dtype                                       */
+    gcl_rows i;                    /* [t_max, D] dtype; ptr NULL: no input gate              */
+    gcl_rows o;                    /* forward: [t_max, D] dtype (out); ptr may be NULL       */
+    gcl_rows d_o;                  /* backward: [t_max, D] dtype                             */
+    gcl_rows dx, dr;               /* backward: [t_max, D] dtype (out)                       */
+    gcl_rows di;                   /* backward with i: [t_max, D] dtype (out)                */
+    const float *rate;             /* [D] fp32, GCL_DECAY_POWER; else not read               */
+    const float *h0;               /* [n_max, D] fp32 or NULL                                */
+    float *ht;                     /* forward: [n_max, D] fp32 (out) or NULL                 */
+    const float *dht;              /* backward: [n_max, D] fp32 or NULL                      */
+    float *dh0;                    /* backward: [n_max, D] fp32 (out) or NULL                */
+    float *drate;                  /* backward, GCL_DECAY_POWER: [D] fp32 (out) or NULL      */
+    float *h_save;                 /* [ceil(t_max / 64), D] fp32 or NULL; forward: out       */
+    const int32_t *cu_seqlens;     /* [n_max + 1] int32                                      */
+    int32_t *dev_status;           /* [1] or NULL, as in gcl_fwd_args                        */
+    void *workspace;               /* device scratch, 16-byte aligned, at least              */
+    size_t workspace_bytes;        /* gcl_glr_{fwd,bwd}_workspace_bytes() bytes              */
+    int64_t t_max;
+    int32_t n_max, D;
+    int32_t decay, mix, dtype;     /* gcl_decay_t, gcl_mix_t, gcl_dtype_t                    */
+} gcl_glr_args;
+
+/* Bytes of workspace (0 for invalid sizes); sizes and the dtype are read, and h_save and drate of the backward
+ * for whether they are NULL. */
+size_t gcl_glr_fwd_workspace_bytes(const gcl_glr_args *args);
+size_t gcl_glr_bwd_workspace_bytes(const gcl_glr_args *args);
+
+gcl_status_t glr_fwd(const gcl_glr_args *args, gcl_stream_t stream);
+gcl_status_t glr_bwd(const gcl_glr_args *args, gcl_stream_t stream);
+
+/*
+ * glr_step -- the recurrence for single tokens: for request b, with the state of slot s = slots[b]
+ * (slots NULL: s = b) updated in place, h <- a h + m(a) u, o_b = h.  Negative slots (idle: no state is
+ * touched, the row of o is zeros), slots past the pool and the status word as in dla_step.  Two requests of one
+ * call must not share a slot, and o overlaps neither x, r, i nor the states.
+ */
+typedef struct gcl_glr_step_args {
+    gcl_rows x, r, i;              /* [batch, D] dtype; i.ptr NULL: no input gate            */
+    gcl_rows o;                    /* [batch, D] dtype (out)                                 */
+    const float *rate;             /* [D] fp32, GCL_DECAY_POWER                              */
+    float *state;                  /* [n_slots, D] fp32 (in and out)                         */
+    const int32_t *slots;          /* [batch] or NULL                                        */
+    int32_t *dev_status;           /* [1] or NULL                                            */
+    int32_t batch, n_slots, D;
+    int32_t decay, mix, dtype;
+} gcl_glr_step_args;
+
+gcl_status_t glr_step(const gcl_glr_step_args *args, gcl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
