@@ -134,6 +134,21 @@ class GlrStepArgs(ctypes.Structure):
                 ("mix", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class BlockArgs(ctypes.Structure):
+    _fields_ = [("y", Rows), ("gate", Rows), ("x", Rows), ("xo", Rows), ("z", Rows), ("dxo", Rows),
+                ("dz", Rows), ("dy", Rows), ("dgate", Rows), ("dx", Rows),
+                ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("dpost_weight", ctypes.c_void_p), ("dpre_weight", ctypes.c_void_p),
+                ("rng", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p),
+                ("dev_status", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("t_max", ctypes.c_int64),
+                ("n_max", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("dropout", ctypes.c_float),
+                ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32)]
+
+
 def load_library(path: str = LIB_PATH):
     """Load libgcl.so and declare its C signatures."""
     if not os.path.exists(path):
@@ -180,14 +195,16 @@ def load_library(path: str = LIB_PATH):
     for fn, args in (("dla_chunk_fwd", DlaArgs), ("dla_chunk_bwd", DlaArgs),
                      ("dla_step", DlaStepArgs), ("qk_norm_rope_fwd", QkArgs),
                      ("qk_norm_rope_bwd", QkArgs), ("glr_fwd", GlrArgs), ("glr_bwd", GlrArgs),
-                     ("glr_step", GlrStepArgs)):
+                     ("glr_step", GlrStepArgs), ("block_norm_fwd", BlockArgs),
+                     ("block_norm_bwd", BlockArgs)):
         getattr(lib, fn).restype = ctypes.c_int
         getattr(lib, fn).argtypes = [ctypes.POINTER(args), vp]
     for fn, args in (("gcl_dla_fwd_workspace_bytes", DlaArgs),
                      ("gcl_dla_bwd_workspace_bytes", DlaArgs),
                      ("gcl_qk_norm_rope_bwd_workspace_bytes", QkArgs),
                      ("gcl_glr_fwd_workspace_bytes", GlrArgs),
-                     ("gcl_glr_bwd_workspace_bytes", GlrArgs)):
+                     ("gcl_glr_bwd_workspace_bytes", GlrArgs),
+                     ("gcl_block_norm_bwd_workspace_bytes", BlockArgs)):
         getattr(lib, fn).restype = ctypes.c_size_t
         getattr(lib, fn).argtypes = [ctypes.POINTER(args)]
     lib.gcl_dla_segment_tokens.restype = i64
@@ -918,3 +935,71 @@ def glr_step(x, r, state, o, i=None, rate=None, slots=None, decay="power", mix="
         _flat(fn, "slots", slots, (B,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, D, kd, km,
         _dtype_of(x))
     _packed_call(fn, packed, stream, dev)
+
+
+# ------------------------------------------------------------------ norms around a block
+GATE_ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+_BLOCK_PACK = struct.Struct("@" + _ROWS_FMT * 10 + "PPPPPPPPNqiiifffiiiii0q")
+
+
+def _rows3(fn, name, t, shape, dtype, device):
+    """gcl_rows of a tensor [tokens, heads, D], or [tokens, D] where the call's rows have one head; None: no rows."""
+    if t is None:
+        return _NO_ROWS
+    return (_rows2 if len(shape) == 2 else _rows)(fn, name, t, shape, dtype, device)
+
+
+def _block_call(fn, y, gate, x, xo, z, dxo, dz, dy, dgate, dx, post_weight, pre_weight, dpost_weight, dpre_weight,
+                post_norm, pre_norm, activation, scale, eps, dropout, rng, cu_seqlens, dev_status, workspace, stream):
+    from torch import float32 as f32, int32 as i32, int64 as i64
+    sy = tuple(y.shape)
+    T, H, D = sy if len(sy) == 3 else (sy[0], 1, sy[1])
+    dt, dev = y.dtype, y.get_device()
+    if post_norm not in NORMS or pre_norm not in NORMS or activation not in GATE_ACTIVATIONS:
+        raise ValueError(f"{fn}: post_norm {post_norm!r}, pre_norm {pre_norm!r} or activation {activation!r} is not one of "
+                         f"{tuple(NORMS)}, {tuple(GATE_ACTIVATIONS)}")
+    flow = x if x is not None else xo if xo is not None else dxo            # its type is the residual stream's
+    st = dt if flow is None else flow.dtype
+    if st is not dt and st is not f32:
+        raise ValueError(f"{fn}: x, xo and their gradients have dtype {st}, expected {dt} or {f32}")
+    n = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    packed = _BLOCK_PACK.pack(
+        *_rows3(fn, "y", y, sy, dt, dev), *_rows3(fn, "gate", gate, sy, dt, dev), *_rows3(fn, "x", x, sy, st, dev),
+        *_rows3(fn, "xo", xo, sy, st, dev), *_rows3(fn, "z", z, sy, dt, dev), *_rows3(fn, "dxo", dxo, sy, st, dev),
+        *_rows3(fn, "dz", dz, sy, dt, dev), *_rows3(fn, "dy", dy, sy, dt, dev), *_rows3(fn, "dgate", dgate, sy, dt, dev),
+        *_rows3(fn, "dx", dx, sy, st, dev), _flat(fn, "post_weight", post_weight, (D,), dt, dev),
+        _flat(fn, "pre_weight", pre_weight, (D,), dt, dev), _flat(fn, "dpost_weight", dpost_weight, (D,), f32, dev),
+        _flat(fn, "dpre_weight", dpre_weight, (D,), f32, dev), _flat(fn, "rng", rng, (2,), i64, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (n + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        *_scratch(fn, workspace, dev), T, n, H, D, scale, eps, dropout, NORMS[post_norm], NORMS[pre_norm],
+        GATE_ACTIVATIONS[activation], _dtype_of(y), GCL_F32 if st is f32 else _dtype_of(y))
+    _packed_call(fn, packed, stream, dev)
+
+
+def block_norm_fwd(y, xo, x=None, z=None, gate=None, post_weight=None, pre_weight=None, post_norm="rms", pre_norm="rms",
+                   activation=None, scale=1.0, eps=1e-6, dropout=0.0, rng=None, cu_seqlens=None, dev_status=None, stream=None):
+    """What lies between two blocks, in one pass (include/gcl.h, block_norm): xo = x + scale drop(act(gate) norm(y) w_post)
+    and z = norm(xo) w_pre, for rows [T, H, D] or [T, D] with any token and head strides.  Every part but y may be left out
+    (None), xo where z is given.  x and xo have y's dtype or fp32."""
+    _block_call("block_norm_fwd", y, gate, x, xo, z, None, None, None, None, None, post_weight, pre_weight, None, None,
+                post_norm, pre_norm, activation, scale, eps, dropout, rng, cu_seqlens, dev_status, None, stream)
+
+
+def block_norm_bwd_workspace_bytes(y) -> int:
+    """Workspace of block_norm_bwd with weight gradients."""
+    if y.get_device() >= 0:
+        _on_device("block_norm_bwd_workspace_bytes", y.get_device())
+    T, H, D = y.shape if y.dim() == 3 else (y.shape[0], 1, y.shape[1])
+    a = BlockArgs(t_max=T, H=H, D=D, dtype=_dtype_of(y))
+    return int(lib().gcl_block_norm_bwd_workspace_bytes(ctypes.byref(a)))
+
+
+def block_norm_bwd(y, dxo, dy, x=None, dx=None, dz=None, gate=None, dgate=None, post_weight=None, pre_weight=None,
+                   dpost_weight=None, dpre_weight=None, post_norm="rms", pre_norm="rms", activation=None, scale=1.0, eps=1e-6,
+                   dropout=0.0, rng=None, cu_seqlens=None, dev_status=None, workspace=None, stream=None):
+    """The backward of block_norm_fwd: dy, dgate, dx and the weights' gradients fp32 [D] from dxo and dz (one of them may
+    be None) and the forward's inputs; dropout's mask is formed again from rng."""
+    if (gate is None) != (dgate is None):
+        raise ValueError("block_norm_bwd: gate and dgate come together")
+    _block_call("block_norm_bwd", y, gate, x, None, None, dxo, dz, dy, dgate, dx, post_weight, pre_weight, dpost_weight,
+                dpre_weight, post_norm, pre_norm, activation, scale, eps, dropout, rng, cu_seqlens, dev_status, workspace, stream)

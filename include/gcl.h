@@ -424,7 +424,8 @@ gcl_status_t kda_chunk_bwd(const gcl_bwd_args *args, gcl_stream_t stream);
  * graph-capturable.  Errors: INVALID_ARG / UNSUPPORTED on the host before anything is
  * enqueued, data errors through dev_status as for the chunk attention.
  */
-typedef enum { GCL_ACT_NONE = 0, GCL_ACT_SILU = 1 } gcl_activation_t;
+/* (GCL_ACT_SIGMOID: block_norm alone) */
+typedef enum { GCL_ACT_NONE = 0, GCL_ACT_SILU = 1, GCL_ACT_SIGMOID = 2 } gcl_activation_t;
 
 typedef struct gcl_conv_args {
     const void *x;                 /* [t_max, D] dtype                                       */
@@ -699,6 +700,62 @@ typedef struct gcl_glr_step_args {
 } gcl_glr_step_args;
 
 gcl_status_t glr_step(const gcl_glr_step_args *args, gcl_stream_t stream);
+
+/*
+ * block_norm -- the norms after and before a block of a layer with what lies between two blocks, in one pass
+ * over the rows: the norm of the block's output with a weight (or the weight alone, a scale for each channel), its
+ * gate, dropout, the residual scale and sum, and the norm before the next block.  Per row (token t, head h):
+ *
+ *   v = scale drop(act(gate) n w_post),  n = y / |y|_post,   xo = x + v  (v without x),   z = xo / |xo|_pre w_pre
+ *
+ * with |.| of qk_norm_rope over the row's D values (GCL_NORM_RMS, GCL_NORM_L2 or none) and act(gate) the gate itself,
+ * its SiLU or its sigmoid (1 without gate).  Parts: gate, x, z and the weights (then ones) may be NULL, and xo where z is given.
+ * So it is also the gated norm of each head's output (y and gate [t_max, H, D], no x, no z), a
+ * residual sum with the next norm (post_norm none), and a norm alone.  z is formed from the unrounded xo.
+ *
+ * Dropout.  With dropout = p > 0 each value of v is kept with probability 1 - c / 65536, c = round(65536 p), times
+ * 65536 / (65536 - c).  The mask is a function of rng = {seed, offset} (device int64 [2]) and of the value's index
+ * e = (t H + h) D + d alone, so the backward forms it again and nothing is stored: e takes half-word e mod 8
+ * (low half of word 0 first) of the block Philox4x32-10(key = seed, counter = (e / 8, offset)) (Salmon,
+ * Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011; 64-bit key and counter halves, low word
+ * first), and is kept where that is at least c.  A captured call reads rng when it is replayed.
+ *
+ * The backward takes dxo and dz, the gradients w.r.t. xo and z (either may be NULL: zeros), and the forward's
+ * inputs, and gives dy, dgate, dx (may be NULL) and the weights' gradients (fp32, summed over the tokens and heads in a fixed
+ * order), with d = dxo + back(dz w_pre; xo), back(u; a) = (u - n_a mean(u n_a)) / |a|, n_a = a / |a| (mean: the sum for GCL_NORM_L2):
+ *   dx = d,  dgate = scale drop(d n w_post) act'(gate),  dy = back(scale drop(d act) w_post; y).
+ *
+ * Rows y, gate, z and theirs have dtype; x, xo and theirs stream_dtype: the same, or GCL_F32.  With cu_seqlens rows
+ * at or past cu_seqlens[n_max] are neither used nor written; without, every row is live.  Arithmetic is fp32; each output is
+ * rounded once.  The forward may run in place (xo = x with the same strides), the backward likewise (dx = dxo); other
+ * outputs overlap no input.
+ * Supported: D a multiple of 8 up to 16,384; any H >= 1; dtype GCL_F32, GCL_BF16, GCL_F16.
+ */
+typedef struct gcl_block_args {
+    gcl_rows y, gate;              /* [t_max, H, D] dtype; gate.ptr may be NULL              */
+    gcl_rows x;                    /* [t_max, H, D] stream_dtype or NULL                     */
+    gcl_rows xo;                   /* forward: [t_max, H, D] stream_dtype (out)              */
+    gcl_rows z;                    /* forward: [t_max, H, D] dtype (out) or NULL             */
+    gcl_rows dxo, dz;              /* backward: gradients w.r.t. xo and z                    */
+    gcl_rows dy, dgate, dx;        /* backward: outputs                                      */
+    const void *post_weight, *pre_weight;   /* [D] dtype or NULL                             */
+    float *dpost_weight, *dpre_weight;      /* backward: [D] fp32 (out) or NULL              */
+    const int64_t *rng;            /* [2] seed and offset; dropout > 0 only                  */
+    const int32_t *cu_seqlens;     /* [n_max + 1] int32 or NULL                              */
+    int32_t *dev_status;           /* [1] or NULL, as in gcl_fwd_args                        */
+    void *workspace;               /* backward with weight gradients:                        */
+    size_t workspace_bytes;        /*   gcl_block_norm_bwd_workspace_bytes() bytes           */
+    int64_t t_max;
+    int32_t n_max, H, D;
+    float scale, eps, dropout;     /* residual scale; under the norms' roots; 0 <= p < 1     */
+    int32_t post_norm, pre_norm;   /* gcl_norm_t                                             */
+    int32_t activation;            /* gcl_activation_t                                       */
+    int32_t dtype, stream_dtype;   /* gcl_dtype_t                                            */
+} gcl_block_args;
+
+gcl_status_t block_norm_fwd(const gcl_block_args *args, gcl_stream_t stream);
+size_t gcl_block_norm_bwd_workspace_bytes(const gcl_block_args *args);
+gcl_status_t block_norm_bwd(const gcl_block_args *args, gcl_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -106,3 +106,86 @@ def check(name, got, ref, dtype, e32, scale=None):
     assert np.isfinite(got).all(), f"{name}: values that are not finite"
     worst = (err - bound).max()
     assert worst <= 0, f"{name}: off by {err.flat[(err - bound).argmax()]:.3e}, allowed {np.asarray(bound + 0 * err).flat[(err - bound).argmax()]:.3e}"
+
+
+# ---------------------------------------------------------------- norms around a block
+# Tolerances: each result is rounded once (U); before that fp32, some twenty roundings a value and sums of a row's D
+# values, serial over at most 32 of them and a tree over the rest: 64 2^-24 of the largest value covers both.  The weights' gradients
+# add up rows: as much of the sum of their terms' magnitudes.
+E_NORM = 64 * E32
+
+
+def philox(counter, key):
+    """Philox4x32-10 (Salmon, Moraes, Dror, Shaw 2011): counter [..., 4] and key [2] of 32-bit words."""
+    c, k = [counter[..., j].astype(np.uint64) for j in range(4)], [np.uint64(key[0]), np.uint64(key[1])]
+    low, s32 = np.uint64(0xFFFFFFFF), np.uint64(32)
+    for _ in range(10):
+        p, q = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(q >> s32) ^ c[1] ^ k[0], q & low, (p >> s32) ^ c[3] ^ k[1], p & low]
+        k = [(k[0] + np.uint64(0x9E3779B9)) & low, (k[1] + np.uint64(0xBB67AE85)) & low]
+    return np.stack(c, -1)
+
+
+def keep(shape, p, seed, offset):
+    """Dropout's factors: 0, or 65536 / (65536 - c) for kept values."""
+    cut = int(np.floor(np.float64(np.float32(p)) * 65536 + 0.5))
+    if cut == 0:
+        return np.ones(shape)
+    n = int(np.prod(shape))
+    at = np.arange(-(-n // 8), dtype=np.uint64)
+    seed, offset = np.uint64(seed % (1 << 64)), np.uint64(offset % (1 << 64))
+    low, s32 = np.uint64(0xFFFFFFFF), np.uint64(32)
+    ctr = np.stack([at & low, at >> s32, np.full_like(at, offset & low), np.full_like(at, offset >> s32)], -1)
+    w = philox(ctr, (seed & low, seed >> s32))
+    halves = np.stack([w & np.uint64(0xFFFF), w >> np.uint64(16)], -1).reshape(-1)[:n]
+    return (halves >= cut).reshape(shape) * (65536.0 / (65536 - cut))
+
+
+def length(x, norm, eps):
+    if norm in (None, "none"):
+        return np.ones(x.shape[:-1] + (1,))
+    s = (x * x).sum(-1, keepdims=True)
+    return np.sqrt((s / x.shape[-1] if norm == "rms" else s) + eps)
+
+
+def back(u, x, norm, eps):
+    if norm in (None, "none"):
+        return u
+    l = length(x, norm, eps)
+    n = x / l
+    m = (u * n).sum(-1, keepdims=True) / (x.shape[-1] if norm == "rms" else 1)
+    return (u - n * m) / l
+
+
+def act(g, kind):
+    """act(gate) and its derivative; 1 and 0 without gate."""
+    if g is None:
+        return 1.0, 0.0
+    s = sigmoid(g)
+    return {None: (g, np.ones_like(g)), "sigmoid": (s, s * (1 - s)), "silu": (g * s, s * (1 + g * (1 - s)))}[kind]
+
+
+def block_fwd(y, gate, x, w_post, w_pre, f, post, pre, kind, eps):
+    """xo, z; f: residual scale times dropout's factors."""
+    w = 1.0 if w_post is None else w_post
+    v = y / length(y, post, eps) * w * act(gate, kind)[0] * f
+    xo = v if x is None else x + v
+    return xo, xo / length(xo, pre, eps) * (1.0 if w_pre is None else w_pre)
+
+
+def block_bwd(y, gate, x, dxo, dz, w_post, w_pre, f, post, pre, kind, eps):
+    """dy, dgate, dx, dw_post, dw_pre and the sums of the weights' terms' magnitudes."""
+    w1, w2 = (1.0 if w is None else w for w in (w_post, w_pre))
+    a, da = act(gate, kind)
+    n = y / length(y, post, eps)
+    xo, _ = block_fwd(y, gate, x, w_post, w_pre, f, post, pre, kind, eps)
+    d = np.zeros_like(xo) if dxo is None else dxo
+    t2 = np.zeros_like(xo)
+    if dz is not None:
+        d = d + back(dz * w2, xo, pre, eps)
+        t2 = dz * xo / length(xo, pre, eps)
+    dn = d * f * a
+    t1 = dn * n
+    axes = tuple(range(xo.ndim - 1))
+    return (back(dn * w1, y, post, eps), d * f * n * w1 * da, d, t1.sum(axes), t2.sum(axes), np.abs(t1).sum(axes).max(),
+            np.abs(t2).sum(axes).max())
