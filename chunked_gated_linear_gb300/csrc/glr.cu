@@ -1,24 +1,33 @@
 // glr.cu -- gated linear recurrence over packed sequences: forward and backward.
 //
-// A tile is kTile tokens of the packed axis by one warp's width of channels; a warp of it walks kRun tokens.  The
-// sequences need no plan of their own: a token that starts one takes its state from h0, whatever was before.
-// Three launches: each tile's product of decays and own state; the states that enter the tiles, along the packed
-// axis; the outputs.  Backwards likewise, from the states before each 64 tokens (saved by the forward, or formed
-// again): with c_t = a_t G_t the gradient that token t passes on,
+// A tile is kTile tokens of the packed axis by the 128 bytes of a warp's width of channels; each of its warps walks kRun
+// tokens.  The sequences need no plan of their own: a token that starts one takes its state from h0, whatever
+// was before.  One pass: blocks take tiles in the order of the recurrence (a counter), form a tile's product of decays and its
+// state from zero, publish both, and take the state that enters from the tile before, or from an earlier one and the products and
+// own states between; the sum is folded from the oldest on, so the result is the same whichever tile had its state
+// ready.  A block waits for tiles with lower tickets alone, whose blocks run already, so the first of them
+// never waits: the launch ends whatever else runs on the GPU.  (Three launches -- own states, their scan, outputs -- read
+// x, r and i twice: 65,536 tokens of 2,048 channels 1,424 us.)
+// Backwards from the states before each 64 tokens (saved by the forward, or formed again): with c_t = a_t G_t the gradient that
+// token t passes on,
 //   G_t = d_o_t + c_{t+1},   c_t = a_t G_t,
-// the same recurrence with the same decays, cut where a sequence ends.
+// the same recurrence with the same decays, cut where a sequence ends, over the tiles from last to first.
 #include "glr.cuh"
+#include "tc_ptx.cuh"
 
 namespace gcl {
 namespace glr {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRunF = 16, kRunB = 8;                   // tokens of a warp
-constexpr int kTileF = kWarps * kRunF, kTileB = kWarps * kRunB;
+// Forward: 128 tokens, 16 warps of 8.  Backward: 64 tokens, 8 warps of 8.
+constexpr int kRun = 8;
+constexpr int kWarpsF = 16, kWarpsB = 8, kTileF = kWarpsF * kRun, kTileB = kWarpsB * kRun;
+constexpr int kCtasF = 2, kCtasB = 3;                  // resident blocks an SM
 
-// ---- set-up: checks cu_seqlens, finds each tile's first sequence, passes states of empty sequences through ----
+// ---- set-up: checks cu_seqlens, finds each tile's first sequence, passes states of empty sequences through, clears the
+// flags between tiles ----
 __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const float *in_state, float *out_state, int tile) {
+    launch_dependents();
     const int tid = threadIdx.x;
     int bad = 0;
     for (int n = tid; n < p.n_max; n += blockDim.x) {
@@ -30,14 +39,16 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const f
     if (blockIdx.x == 0 && tid == 0) {
         p.head->blocked = blocked || bad;
         p.head->live = blocked || bad ? 0 : p.cu[p.n_max];
+        p.head->ticket = 0;
         if (bad) status_set(p.status, GCL_DEV_BAD_RANGE);
     }
     if (blocked || bad) return;
-    for (int64_t j = blockIdx.x * (int64_t)blockDim.x + tid; j <= p.tiles; j += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t at = blockIdx.x * (int64_t)blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t e = at; e < p.tiles * p.n_cb; e += step) p.chain.flag[e] = 0;
+    for (int64_t j = at; j < p.tiles; j += step) {
         const int64_t t0 = j * tile;
-        int lo = 0, hi = p.n_max;                          // first n with cu[n] >= t0 (n_max + 1 if none)
-        if (p.cu[p.n_max] < t0) lo = p.n_max + 1;
-        else while (lo < hi) {
+        int lo = 0, hi = p.n_max;                          // first n with cu[n] >= t0 (n_max if none)
+        while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (p.cu[mid] >= t0) hi = mid;
             else lo = mid + 1;
@@ -48,43 +59,33 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const f
     for (int n = blockIdx.x; n < p.n_max; n += gridDim.x) {
         if (p.cu[n + 1] != p.cu[n]) continue;
         for (int d = tid; d < p.D; d += blockDim.x) {
-            const int64_t at = (int64_t)n * p.D + d;
-            out_state[at] = in_state ? in_state[at] : 0.f;
+            const int64_t e = (int64_t)n * p.D + d;
+            out_state[e] = in_state ? in_state[e] : 0.f;
         }
     }
 }
 
-// Sequences that start and end within the tile's tokens, by token; -1: none.  (Block barriers.)
+// Sequences that start and end within the tile's tokens, by token; -1: none.  One warp.
 template <int TILE>
-__device__ __forceinline__ void borders(const Params &p, int64_t j, int64_t t0, int *s_start, int *s_end) {
-    for (int k = threadIdx.x; k < TILE; k += kThreads) s_start[k] = s_end[k] = -1;
-    __syncthreads();
+__device__ __forceinline__ void borders(const Params &p, int64_t j, int *s_start, int *s_end) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t0 = j * TILE;
     const int f = p.first[j];
-    for (int n = (f > 0 ? f - 1 : 0) + (int)threadIdx.x; n < p.n_max; n += kThreads) {
+#pragma unroll
+    for (int k = lane; k < TILE; k += 32) s_start[k] = s_end[k] = -1;
+    __syncwarp();
+    for (int n = (f > 0 ? f - 1 : 0) + lane; n < p.n_max; n += 32) {
         const int64_t b = p.cu[n] - t0, e = p.cu[n + 1] - t0;
         if (b >= TILE) break;
         if (e <= b) continue;
         if (b >= 0) s_start[b] = n;
         if (e >= 1 && e <= TILE) s_end[e - 1] = n;
     }
-    __syncthreads();
 }
 
 template <typename T>
-__device__ __forceinline__ const uint32_t *word(const Rows &r, int64_t t, int ch) {
-    return reinterpret_cast<const uint32_t *>(static_cast<const T *>(r.p) + t * r.st + ch);
-}
-
-// The lane's values of N / V tokens from t on; zeros past `live`.
-template <typename T, int RUN>
-__device__ __forceinline__ void load_run(const Params &p, const Rows &r, int64_t t, int64_t live, int ch, bool on, float *v) {
-    constexpr int V = Lane<T>::V;
-    uint32_t w[RUN];
-#pragma unroll
-    for (int k = 0; k < RUN; ++k)
-        w[k] = on && t + k < live && GCL_IN_BOUNDS(t + k, p.t_max, p.status) ? *word<T>(r, t + k, ch) : 0;
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) Lane<T>::get(w[k], v + k * V);
+__device__ __forceinline__ uint32_t *word(const Rows &r, int64_t t, int ch) {
+    return reinterpret_cast<uint32_t *>(static_cast<T *>(r.p) + t * r.st + ch);
 }
 
 // states [n, D]
@@ -100,289 +101,488 @@ __device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, 
     for (int v = 0; v < V; ++v) s[n * D + ch + v] = h[v];
 }
 
-// ---- forward -------------------------------------------------------------
-template <typename T, bool OUT>
-__global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const Params p) {
-    constexpr int V = Lane<T>::V, CB = Lane<T>::CB, RUN = kRunF, N = RUN * V;
-    __shared__ float s_a[kWarps][CB], s_b[kWarps][CB];
-    __shared__ int s_start[kTileF], s_end[kTileF], s_cut[kWarps];
-    if (p.head->blocked) return;
-    const int64_t live = p.head->live, j = blockIdx.x / p.n_cb, t0 = j * kTileF;
-    if (t0 >= live) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ch = (blockIdx.x % p.n_cb) * CB + lane * V;
-    const bool on = ch < p.D;
-    const int64_t t = t0 + warp * RUN;
-    float rate[V];
-    load_state<V>(p.kind.rate, 0, p.D, ch, on && p.kind.decay == GCL_DECAY_POWER, rate);
-    float a[N], b[N];
-    {
-        float r[N];
-        load_run<T, RUN>(p, p.r, t, live, ch, on, r);
-        decays<T, N>(p.kind, rate, r, a, b);
-        mixes<T, N>(p.kind, a, b);
-        load_run<T, RUN>(p, p.x, t, live, ch, on, r);
+// The tile's rows (tokens from t0 to live, channels of block cb) into shared memory, asynchronously; zeros elsewhere.
+template <typename T, int TILE, int THREADS>
+__device__ __forceinline__ void stage_rows(const Params &p, const Rows &r, int64_t t0, int64_t live, int cb, uint8_t *dst) {
+    constexpr int E = 16 / sizeof(T);
 #pragma unroll
-        for (int e = 0; e < N; ++e) b[e] *= r[e];
-        if (p.i.p) {
-            load_run<T, RUN>(p, p.i, t, live, ch, on, r);
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                float s, c;
-                sigmoids<T>(r[e], s, c);
-                b[e] *= s;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < RUN; ++k)
-            if (t + k >= live)
-#pragma unroll
-                for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; b[k * V + v] = 0.f; }
+    for (int c = threadIdx.x; c < TILE * 8; c += THREADS) {
+        const int row = c >> 3, ch = cb * Lane<T>::CB + (c & 7) * E;
+        const bool on = t0 + row < live && ch < p.D && GCL_IN_BOUNDS(t0 + row, p.t_max, p.status);
+        const T *src = static_cast<const T *>(r.p) + (on ? (t0 + row) * r.st + ch : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + c * 16)), "l"(src), "r"(on ? 16 : 0)
+                     : "memory");
     }
-    borders<kTileF>(p, j, t0, s_start, s_end);
-    const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && s_start[(warp * RUN + lane) % kTileF] >= 0);
-    const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && s_end[(warp * RUN + lane) % kTileF] >= 0);
-    // the warp's own state and product of decays (from its last start on, if it has one)
-    {
-        float A[V], h[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = 0.f; }
-#pragma unroll
-        for (int k = 0; k < RUN; ++k) {
-            if (starts >> k & 1) load_state<V>(p.h0, s_start[warp * RUN + k], p.D, ch, on, h);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
-                A[v] *= a[k * V + v];
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) { s_a[warp][lane * V + v] = A[v]; s_b[warp][lane * V + v] = h[v]; }
-        if (lane == 0) s_cut[warp] = starts != 0;
-    }
-    __syncthreads();
-    if (!OUT) {
-        if (warp == 0 && on) {
-            float A[V], h[V];
-            bool cut = false;
-#pragma unroll
-            for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = 0.f; }
-            for (int w = 0; w < kWarps; ++w) {
-                cut |= s_cut[w] != 0;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    h[v] = s_cut[w] ? s_b[w][lane * V + v] : fmaf(s_a[w][lane * V + v], h[v], s_b[w][lane * V + v]);
-                    A[v] *= s_a[w][lane * V + v];
-                }
-            }
-            store_state<V>(p.agg_a, j, p.D, ch, on, A);
-            store_state<V>(p.agg_b, j, p.D, ch, on, h);
-            if (lane == 0) p.cut[j] = cut;                 // (every block of channels writes the same)
-        }
-        return;
-    }
-    float h[V];
-    load_state<V>(p.agg_b, j, p.D, ch, on, h);
-    for (int w = 0; w < warp; ++w)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            h[v] = s_cut[w] ? s_b[w][lane * V + v] : fmaf(s_a[w][lane * V + v], h[v], s_b[w][lane * V + v]);
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-        if (starts >> k & 1) load_state<V>(p.h0, s_start[warp * RUN + k], p.D, ch, on, h);
-        if ((warp * RUN + k) % kSave == 0 && t + k < live) store_state<V>(p.h_save, (t + k) / kSave, p.D, ch, on, h);
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
-        if (p.o.p && on && t + k < live && GCL_IN_BOUNDS(t + k, p.t_max, p.status))
-            *const_cast<uint32_t *>(word<T>(p.o, t + k, ch)) = Lane<T>::put(h);
-        if (ends >> k & 1) store_state<V>(p.ht, s_end[warp * RUN + k], p.D, ch, on, h);
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ int32_t load_flag(const int32_t *f) {
+    int32_t v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(f) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_flag(int32_t *f, int32_t v) {
+    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(f), "r"(v) : "memory");
+}
+
+// One warp: the warp's states of row `at` of a chain array, past the L1.
+template <int V>
+__device__ __forceinline__ void chain_load(const float *s, int64_t at, bool on, float *h) {
+    if (V == 2) {
+        const float2 f = on ? __ldcg(reinterpret_cast<const float2 *>(s + at)) : make_float2(0.f, 0.f);
+        h[0] = f.x;
+        h[V - 1] = f.y;
+    } else {
+        h[0] = on ? __ldcg(s + at) : 0.f;
     }
 }
 
-// The states that enter the tiles, in place of their own states; REV: from the last tile to the first.
-template <bool REV>
-__global__ void glr_scan_kernel(const Params p, int tile) {
-    if (p.head->blocked) return;
-    const int d = blockIdx.x * blockDim.x + threadIdx.x;
-    if (d >= p.D) return;
-    const int64_t n = (p.head->live + tile - 1) / tile;
-    float h = 0.f;
-    for (int64_t i = 0; i < n; ++i) {
-        const int64_t j = REV ? n - 1 - i : i, at = j * p.D + d;
-        const float a = p.agg_a[at], b = p.agg_b[at];
-        p.agg_b[at] = h;
-        h = p.cut[j] ? b : fmaf(a, h, b);
+// One warp: the state that enters tile `seq` (its number in the order of the recurrence, > 0), from the nearest tile
+// before it whose state is out and the own states between, folded from the oldest on.
+template <int V>
+__device__ __forceinline__ void chain_enter(const Params &p, int64_t seq, int cb, int ch, bool on, float *h) {
+    const int lane = threadIdx.x & 31;
+    const int32_t *flag = p.chain.flag + (int64_t)cb * p.tiles;
+    const int64_t mine = seq - 1 - lane;
+    const uint64_t t0 = tc::globaltimer();
+    int near;
+    while (true) {
+        const int32_t f = mine >= 0 ? load_flag(flag + mine) : 0;
+        const uint32_t done = __ballot_sync(0xffffffffu, f == kDone), own = __ballot_sync(0xffffffffu, f != 0);
+        near = __ffs(done) - 1;
+        if (near >= 0 && !(~own & ((1u << near) - 1))) break;
+        if (__shfl_sync(0xffffffffu, tc::globaltimer() - t0 > tc::kWaitLimitNs, 0)) {
+            if (lane == 0) status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = 0.f;
+            return;
+        }
     }
+    __syncwarp();
+    int64_t at = (seq - 1 - near) * p.D + ch;
+    chain_load<V>(p.chain.out, at, on, h);
+    for (int m = near; m > 0; m -= 4) {                    // four tiles' loads in flight
+        float a[4][V], b[4][V];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            chain_load<V>(p.chain.a, at + (u + 1) * (int64_t)p.D, on && u < m, a[u]);
+            chain_load<V>(p.chain.own, at + (u + 1) * (int64_t)p.D, on && u < m, b[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (u < m)
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = fmaf(a[u][v], h[v], b[u][v]);
+        at += 4 * (int64_t)p.D;
+    }
+}
+
+// One warp: publishes its channels of a tile: own states (kOwn) or the state that leaves (kDone).
+template <int V>
+__device__ __forceinline__ void chain_publish(const Params &p, int64_t seq, int cb, int ch, bool on, const float *a, const float *h, int32_t what) {
+    const int64_t at = seq * p.D + ch;
+    if (on) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (what == kOwn) {
+                __stcg(p.chain.a + at + v, a[v]);
+                __stcg(p.chain.own + at + v, h[v]);
+            } else {
+                __stcg(p.chain.out + at + v, h[v]);
+            }
+        }
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence();
+        store_flag(p.chain.flag + (int64_t)cb * p.tiles + seq, what);
+    }
+}
+
+// One warp: from the warps' products and own states (rows of s_a and s_b, in the order of the recurrence where REV is
+// false, from last to first else; s_cut: the row does not depend on the one before), publishes the tile and puts the
+// state that enters each row into s_b.
+template <int V, int WARPS, int CB, bool REV>
+__device__ __forceinline__ void chain_tile(const Params &p, int64_t seq, int cb, int ch, bool on, float (*s_a)[CB], float (*s_b)[CB], const int *s_cut) {
+    const int l = (threadIdx.x & 31) * V;
+    float A[V], h[V], c[V];
+    bool cut = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = 0.f; c[v] = 0.f; }
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        const int w = REV ? WARPS - 1 - i : i;
+        const bool k = s_cut[w] != 0;
+        cut |= k;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = k ? s_b[w][l + v] : fmaf(s_a[w][l + v], h[v], s_b[w][l + v]);
+            A[v] *= s_a[w][l + v];
+        }
+    }
+    chain_publish<V>(p, seq, cb, ch, on, A, h, cut ? kDone : kOwn);
+    if (seq > 0) chain_enter<V>(p, seq, cb, ch, on, c);    // (the first tile is cut at its first token)
+    if (!cut) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fmaf(A[v], c[v], h[v]);
+        chain_publish<V>(p, seq, cb, ch, on, A, h, kDone);
+    }
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        const int w = REV ? WARPS - 1 - i : i;
+        const bool k = s_cut[w] != 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float b = s_b[w][l + v], a = s_a[w][l + v];
+            s_b[w][l + v] = c[v];
+            c[v] = k ? b : fmaf(a, c[v], b);
+        }
+    }
+}
+
+template <int CB, int WARPS>
+struct Shared {
+    float a[WARPS][CB], b[WARPS][CB];
+    int start[2][WARPS * kRun], end[2][WARPS * kRun];
+    int cut[WARPS];
+    uint32_t ticket[2];
+};
+
+// ---- forward -------------------------------------------------------------
+// Per block: two tiles staged, so that the next one's rows are under way while this one is computed.  Bound by HBM and issue together.
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Params p) {
+    constexpr int V = Lane<T>::V, CB = Lane<T>::CB, RUN = kRun, N = RUN * V, THREADS = 32 * kWarpsF, BYTES = kTileF * 128;
+    __shared__ Shared<CB, kWarpsF> s;
+    extern __shared__ __align__(16) uint8_t s_rows[];      // [2][r, x, i][kTileF][128]
+    grid_dependency_wait();
+    if (p.head->blocked) return;
+    const int64_t live = p.head->live;
+    const uint32_t units = (uint32_t)((live + kTileF - 1) / kTileF * p.n_cb);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 3 : 2;
+    auto stage = [&](uint32_t unit, int buf) {
+        if (unit < units) {
+            const int64_t t0 = (int64_t)(unit / p.n_cb) * kTileF;
+            const int cb = unit % p.n_cb;
+            uint8_t *dst = s_rows + buf * narr * BYTES;
+            stage_rows<T, kTileF, THREADS>(p, p.r, t0, live, cb, dst);
+            stage_rows<T, kTileF, THREADS>(p, p.x, t0, live, cb, dst + BYTES);
+            if (narr == 3) stage_rows<T, kTileF, THREADS>(p, p.i, t0, live, cb, dst + 2 * BYTES);
+        }
+        stage_commit();
+    };
+    if (threadIdx.x == 0) s.ticket[0] = atomicAdd(&p.head->ticket, 1u);
+    __syncthreads();
+    uint32_t unit = s.ticket[0], next = 0;
+    if (unit >= units) return;
+    stage(unit, 0);
+    if (warp == 1) borders<kTileF>(p, unit / p.n_cb, s.start[0], s.end[0]);
+    bool first = true;
+    for (int buf = 0; unit < units; buf ^= 1) {
+        if (first) stage_wait<0>();
+        else stage_wait<1>();
+        __syncthreads();
+        // (a second tile is taken only when the first has arrived, so that few tiles spread over all blocks)
+        uint32_t taken = 0;
+        if (threadIdx.x == 32) taken = atomicAdd(&p.head->ticket, first ? 2u : 1u);
+        const int64_t j = unit / p.n_cb, t = j * kTileF + warp * RUN;
+        const int cb = unit % p.n_cb, ch = cb * CB + lane * V;
+        const bool on = ch < p.D;
+        const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
+        float a[N], b[N];
+        {
+            float rate[V];
+            load_state<V>(p.kind.rate, 0, p.D, ch, on && p.kind.decay == GCL_DECAY_POWER, rate);
+            float r[N];
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + k * 128), r + k * V);
+            decays<T, N>(p.kind, rate, r, a, b);
+            mixes<T, N>(p.kind, a, b);
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+                float x[V];
+                Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + BYTES + k * 128), x);
+#pragma unroll
+                for (int v = 0; v < V; ++v) b[k * V + v] *= x[v];
+            }
+            if (narr == 3) {
+#pragma unroll
+                for (int k = 0; k < RUN; ++k) {
+                    float g[V];
+                    Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + 2 * BYTES + k * 128), g);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) b[k * V + v] *= sigmoid<T>(g[v]);
+                }
+            }
+        }
+        if (t + RUN > live)
+#pragma unroll
+            for (int k = 0; k < RUN; ++k)
+                if (t + k >= live)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; b[k * V + v] = 0.f; }
+        const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
+        const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && start[lane % RUN] >= 0);
+        const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && end[lane % RUN] >= 0);
+        {
+            float A[V], h[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = 0.f; }
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+                if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
+                    A[v] *= a[k * V + v];
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) { s.a[warp][lane * V + v] = A[v]; s.b[warp][lane * V + v] = h[v]; }
+            if (lane == 0) s.cut[warp] = starts != 0;
+        }
+        if (threadIdx.x == 32) {
+            s.ticket[0] = first ? taken : next;
+            s.ticket[1] = first ? taken + 1 : taken;
+        }
+        __syncthreads();                                   // the rows are read, the warps' own states there
+        if (first) stage(s.ticket[0], buf ^ 1);
+        stage(s.ticket[1], buf);
+        const uint32_t unit1 = s.ticket[0];
+        next = s.ticket[1];
+        if (warp == 0) chain_tile<V, kWarpsF, CB, false>(p, j, cb, ch, on, s.a, s.b, s.cut);
+        if (warp == 1 && unit1 < units) borders<kTileF>(p, unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
+        __syncthreads();
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = s.b[warp][lane * V + v];
+        if (warp * RUN % kSave == 0 && p.h_save && t < live) {
+            if (starts & 1) load_state<V>(p.h0, start[0], p.D, ch, on, h);
+            store_state<V>(p.h_save, t / kSave, p.D, ch, on, h);
+        }
+#pragma unroll
+        for (int k = 0; k < RUN; ++k) {
+            if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
+            if (p.o.p && on && t + k < live && GCL_IN_BOUNDS(t + k, p.t_max, p.status)) *word<T>(p.o, t + k, ch) = Lane<T>::put(h);
+            if (ends >> k & 1) store_state<V>(p.ht, end[k], p.D, ch, on, h);
+        }
+        unit = unit1;
+        first = false;
+    }
+    stage_wait<0>();
 }
 
 // ---- backward ------------------------------------------------------------
-template <typename T, bool OUT>
-__global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const Params p) {
-    constexpr int V = Lane<T>::V, CB = Lane<T>::CB, RUN = kRunB, N = RUN * V;
+// As the forward, over the tiles from last to first; a tile's rows stay staged until its gradients are out, and sigmoids are
+// formed again for them (registers).  The states inside the tile come from the one saved before it.
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const Params p) {
+    constexpr int V = Lane<T>::V, CB = Lane<T>::CB, RUN = kRun, N = RUN * V, THREADS = 32 * kWarpsB, BYTES = kTileB * 128;
     static_assert(kTileB == kSave, "one saved state a tile");
-    __shared__ float s_a[kWarps][CB], s_b[kWarps][CB], s_c[kWarps][CB];
-    __shared__ int s_start[kTileB], s_end[kTileB], s_cut[kWarps], s_cute[kWarps];
+    __shared__ Shared<CB, kWarpsB> s;
+    __shared__ float s_h[kWarpsB][CB], s_d[kWarpsB][CB];
+    __shared__ int s_cuth[kWarpsB];
+    extern __shared__ __align__(16) uint8_t s_rows[];      // [2][r, x, d_o, i][kTileB][128]
+    launch_dependents();                                   // (the sum of the rates' gradients waits for this grid's end)
+    grid_dependency_wait();
     if (p.head->blocked) return;
-    const int64_t live = p.head->live, j = blockIdx.x / p.n_cb, t0 = j * kTileB;
-    if (t0 >= live) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ch = (blockIdx.x % p.n_cb) * CB + lane * V;
-    const bool on = ch < p.D;
-    const int64_t t = t0 + warp * RUN;
-    float rate[V];
-    load_state<V>(p.kind.rate, 0, p.D, ch, on && p.kind.decay == GCL_DECAY_POWER, rate);
-    float r[N], a[N], m[N], x[N], g[N], go[N];
-    load_run<T, RUN>(p, p.r, t, live, ch, on, r);
-    load_run<T, RUN>(p, p.d_o, t, live, ch, on, go);
-    decays<T, N>(p.kind, rate, r, a, m);
-    if (OUT) {
-        mixes<T, N>(p.kind, a, m);
-        load_run<T, RUN>(p, p.x, t, live, ch, on, x);
-        if (p.i.p) load_run<T, RUN>(p, p.i, t, live, ch, on, g);
-    }
-#pragma unroll
-    for (int k = 0; k < RUN; ++k)
-        if (t + k >= live)
-#pragma unroll
-            for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; m[k * V + v] = 0.f; go[k * V + v] = 0.f; }
-    borders<kTileB>(p, j, t0, s_start, s_end);
-    const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && s_start[(warp * RUN + lane) % kTileB] >= 0);
-    const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && s_end[(warp * RUN + lane) % kTileB] >= 0);
-    float A[V], h[V], c[V], u[OUT ? N : 1];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = c[v] = 0.f; }
-    if (OUT) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            float s = 1.f, q;
-            if (p.i.p) sigmoids<T>(g[e], s, q);
-            u[e] = x[e] * s;
+    const int64_t live = p.head->live, n_live = (live + kTileB - 1) / kTileB;
+    const uint32_t units = (uint32_t)(n_live * p.n_cb);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 4 : 3;
+    auto stage = [&](uint32_t unit, int buf) {
+        if (unit < units) {
+            const int64_t t0 = (n_live - 1 - unit / p.n_cb) * kTileB;
+            const int cb = unit % p.n_cb;
+            uint8_t *dst = s_rows + buf * narr * BYTES;
+            stage_rows<T, kTileB, THREADS>(p, p.r, t0, live, cb, dst);
+            stage_rows<T, kTileB, THREADS>(p, p.x, t0, live, cb, dst + BYTES);
+            stage_rows<T, kTileB, THREADS>(p, p.d_o, t0, live, cb, dst + 2 * BYTES);
+            if (narr == 4) stage_rows<T, kTileB, THREADS>(p, p.i, t0, live, cb, dst + 3 * BYTES);
         }
-#pragma unroll
-        for (int k = 0; k < RUN; ++k) {
-            if (starts >> k & 1) load_state<V>(p.h0, s_start[warp * RUN + k], p.D, ch, on, h);
-#pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = fmaf(a[k * V + v], h[v], m[k * V + v] * u[k * V + v]);
-        }
-    }
-#pragma unroll
-    for (int k = RUN - 1; k >= 0; --k) {
-        if (ends >> k & 1) load_state<V>(p.dht, s_end[warp * RUN + k], p.D, ch, on, c);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            c[v] = a[k * V + v] * (go[k * V + v] + c[v]);
-            A[v] *= a[k * V + v];
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        s_a[warp][lane * V + v] = A[v];
-        s_b[warp][lane * V + v] = h[v];
-        s_c[warp][lane * V + v] = c[v];
-    }
-    if (lane == 0) { s_cut[warp] = starts != 0; s_cute[warp] = ends != 0; }
+        stage_commit();
+    };
+    if (threadIdx.x == 0) s.ticket[0] = atomicAdd(&p.head->ticket, 1u);
     __syncthreads();
-    if (!OUT) {
-        if (warp == 0 && on) {
-            bool cut = false;
+    uint32_t unit = s.ticket[0];
+    if (unit >= units) return;
+    stage(unit, 0);
+    if (warp == 1) borders<kTileB>(p, n_live - 1 - unit / p.n_cb, s.start[0], s.end[0]);
+    for (int buf = 0; unit < units; buf ^= 1) {
+        stage_wait<0>();
+        __syncthreads();
+        uint32_t taken = 0;
+        if (threadIdx.x == 32) taken = atomicAdd(&p.head->ticket, 1u);
+        const uint32_t seq = unit / p.n_cb;
+        const int64_t j = n_live - 1 - seq, t = j * kTileB + warp * RUN;
+        const int cb = unit % p.n_cb, ch = cb * CB + lane * V;
+        const bool on = ch < p.D;
+        const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
+        auto row = [&](int arr, int k, float *v) { Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128), v); };
+        float rate[V], a[N], m[N], before[V];
+        load_state<V>(p.kind.rate, 0, p.D, ch, on && p.kind.decay == GCL_DECAY_POWER, rate);
+        if (warp == 1) load_state<V>(p.h_save, j, p.D, ch, on, before);
+        {
+            float r[N];
 #pragma unroll
-            for (int v = 0; v < V; ++v) { A[v] = 1.f; c[v] = 0.f; }
-            for (int w = kWarps - 1; w >= 0; --w) {
-                cut |= s_cute[w] != 0;
+            for (int k = 0; k < RUN; ++k) row(0, k, r + k * V);
+            decays<T, N>(p.kind, rate, r, a, m);
+            mixes<T, N>(p.kind, a, m);
+        }
+        if (t + RUN > live)
+#pragma unroll
+            for (int k = 0; k < RUN; ++k)
+                if (t + k >= live)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; m[k * V + v] = 0.f; }
+        const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
+        const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && start[lane % RUN] >= 0);
+        const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && end[lane % RUN] >= 0);
+        float prev[N];                                     // b = m u, then the state before each token
+        {
+            float A[V], h[V], c[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = c[v] = 0.f; }
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+                float x[V], g[V];
+                row(1, k, x);
+                if (narr == 4) row(3, k, g);
+                if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    c[v] = s_cute[w] ? s_c[w][lane * V + v] : fmaf(s_a[w][lane * V + v], c[v], s_c[w][lane * V + v]);
-                    A[v] *= s_a[w][lane * V + v];
+                    prev[k * V + v] = m[k * V + v] * (narr == 4 ? x[v] * sigmoid<T>(g[v]) : x[v]);
+                    h[v] = fmaf(a[k * V + v], h[v], prev[k * V + v]);
+                    A[v] *= a[k * V + v];
                 }
             }
-            store_state<V>(p.agg_a, j, p.D, ch, on, A);
-            store_state<V>(p.agg_b, j, p.D, ch, on, c);
-            if (lane == 0) p.cut[j] = cut;
-        }
-        return;
-    }
-    load_state<V>(p.h_save, j, p.D, ch, on, h);
-    for (int w = 0; w < warp; ++w)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            h[v] = s_cut[w] ? s_b[w][lane * V + v] : fmaf(s_a[w][lane * V + v], h[v], s_b[w][lane * V + v]);
-    load_state<V>(p.agg_b, j, p.D, ch, on, c);
-    for (int w = kWarps - 1; w > warp; --w)
+            for (int k = RUN - 1; k >= 0; --k) {
+                float go[V];
+                row(2, k, go);
+                if (ends >> k & 1) load_state<V>(p.dht, end[k], p.D, ch, on, c);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            c[v] = s_cute[w] ? s_c[w][lane * V + v] : fmaf(s_a[w][lane * V + v], c[v], s_c[w][lane * V + v]);
-    float prev[N];                                         // the state before each token
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-        if (starts >> k & 1) load_state<V>(p.h0, s_start[warp * RUN + k], p.D, ch, on, h);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            prev[k * V + v] = h[v];
-            h[v] = fmaf(a[k * V + v], h[v], m[k * V + v] * u[k * V + v]);
-        }
-    }
-    float dsum[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) dsum[v] = 0.f;
-#pragma unroll
-    for (int k = RUN - 1; k >= 0; --k) {
-        if (ends >> k & 1) load_state<V>(p.dht, s_end[warp * RUN + k], p.D, ch, on, c);
-        float dx[V], dr[V], di[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = k * V + v;
-            const float G = go[e] + c[v];
-            c[v] = a[e] * G;
-            float dl = c[v] * prev[e];
-            if (p.kind.mix == GCL_MIX_COMPLEMENT) dl = fmaf(-a[e] * G, u[e], dl);
-            else if (p.kind.mix == GCL_MIX_ROOT && m[e] > 0.f) dl = fmaf(-a[e] * a[e] * frcp<T>(m[e]) * G, u[e], dl);
-            float s = 1.f, q = 0.f;
-            if (p.i.p) sigmoids<T>(g[e], s, q);
-            dx[v] = G * m[e] * s;
-            di[v] = dx[v] * x[e] * q;
-            if (p.kind.decay != GCL_DECAY_LOG) {
-                sigmoids<T>(r[e], s, q);
-                if (p.kind.decay == GCL_DECAY_SIGMOID) dl *= q;
-                else {
-                    if (t + k < live) dsum[v] = fmaf(-dl, s, dsum[v]);
-                    dl *= -rate[v] * s * q;
-                }
+                for (int v = 0; v < V; ++v) c[v] = a[k * V + v] * (go[v] + c[v]);
             }
-            dr[v] = dl;
-        }
-        if (on && t + k < live && GCL_IN_BOUNDS(t + k, p.t_max, p.status)) {
-            *const_cast<uint32_t *>(word<T>(p.dx, t + k, ch)) = Lane<T>::put(dx);
-            *const_cast<uint32_t *>(word<T>(p.dr, t + k, ch)) = Lane<T>::put(dr);
-            if (p.i.p) *const_cast<uint32_t *>(word<T>(p.di, t + k, ch)) = Lane<T>::put(di);
-        }
-        if (starts >> k & 1) store_state<V>(p.dh0, s_start[warp * RUN + k], p.D, ch, on, c);
-    }
-    if (p.drate_part) {
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; ++v) s_a[warp][lane * V + v] = dsum[v];
-        __syncthreads();
-        if (warp == 0) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float sum = 0.f;
-                for (int w = 0; w < kWarps; ++w) sum += s_a[w][lane * V + v];
-                dsum[v] = sum;
+                s.a[warp][lane * V + v] = A[v];
+                s.b[warp][lane * V + v] = c[v];
+                s_h[warp][lane * V + v] = h[v];
             }
-            store_state<V>(p.drate_part, j, p.D, ch, on, dsum);
+            if (lane == 0) { s.cut[warp] = ends != 0; s_cuth[warp] = starts != 0; }
         }
+        if (threadIdx.x == 32) s.ticket[0] = taken;
+        __syncthreads();
+        const uint32_t unit1 = s.ticket[0];
+        stage(unit1, buf ^ 1);
+        if (warp == 0) {
+            chain_tile<V, kWarpsB, CB, true>(p, seq, cb, ch, on, s.a, s.b, s.cut);
+        } else if (warp == 1) {                            // the states that enter the warps' tokens
+#pragma unroll
+            for (int w = 0; w < kWarpsB; ++w)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float b = s_h[w][lane * V + v], A = s.a[w][lane * V + v];
+                    s_h[w][lane * V + v] = before[v];
+                    before[v] = s_cuth[w] ? b : fmaf(A, before[v], b);
+                }
+            if (unit1 < units) borders<kTileB>(p, n_live - 1 - unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
+        }
+        __syncthreads();
+        float h[V], c[V], dsum[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) { h[v] = s_h[warp][lane * V + v]; c[v] = s.b[warp][lane * V + v]; dsum[v] = 0.f; }
+#pragma unroll
+        for (int k = 0; k < RUN; ++k) {
+            if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float b = prev[k * V + v];
+                prev[k * V + v] = h[v];
+                h[v] = fmaf(a[k * V + v], h[v], b);
+            }
+        }
+#pragma unroll
+        for (int k = RUN - 1; k >= 0; --k) {
+            if (ends >> k & 1) load_state<V>(p.dht, end[k], p.D, ch, on, c);
+            float dx[V], dr[V], di[V], x[V], g[V], go[V], r[V];
+            row(0, k, r);
+            row(1, k, x);
+            row(2, k, go);
+            if (narr == 4) row(3, k, g);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = k * V + v;
+                const float G = go[v] + c[v];
+                c[v] = a[e] * G;
+                float sg = 1.f, ng = 0.f;
+                if (narr == 4) sigmoids<T>(g[v], sg, ng);
+                const float u = x[v] * sg;
+                dx[v] = G * m[e] * sg;
+                di[v] = dx[v] * x[v] * ng;
+                float dl = c[v] * prev[e];
+                if (p.kind.mix == GCL_MIX_COMPLEMENT) dl = fmaf(-c[v], u, dl);
+                else if (p.kind.mix == GCL_MIX_ROOT && m[e] > 0.f) dl = fmaf(-a[e] * frcp<T>(m[e]) * c[v], u, dl);
+                if (p.kind.decay != GCL_DECAY_LOG) {
+                    float sr, nr;
+                    sigmoids<T>(r[v], sr, nr);
+                    if (p.kind.decay == GCL_DECAY_SIGMOID) {
+                        dl *= nr;
+                    } else {
+                        if (t + k < live) dsum[v] = fmaf(-dl, sr, dsum[v]);
+                        dl *= -rate[v] * sr * nr;
+                    }
+                }
+                dr[v] = dl;
+            }
+            if (on && t + k < live && GCL_IN_BOUNDS(t + k, p.t_max, p.status)) {
+                *word<T>(p.dx, t + k, ch) = Lane<T>::put(dx);
+                *word<T>(p.dr, t + k, ch) = Lane<T>::put(dr);
+                if (narr == 4) *word<T>(p.di, t + k, ch) = Lane<T>::put(di);
+            }
+            if (starts >> k & 1) store_state<V>(p.dh0, start[k], p.D, ch, on, c);
+        }
+        if (p.drate_part) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s_d[warp][lane * V + v] = dsum[v];
+            __syncthreads();
+            if (warp == 2) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarpsB; ++w) sum += s_d[w][lane * V + v];
+                    dsum[v] = sum;
+                }
+                store_state<V>(p.drate_part, j, p.D, ch, on, dsum);
+            }
+        }
+        unit = unit1;
     }
+    stage_wait<0>();
 }
 
-// drate from the tiles' sums, in a fixed order: 32 channels a block, 32 rows of threads over the tiles.
+// drate from the tiles' sums, in a fixed order: 32 channels a block, 32 rows of threads over the tiles, eight loads of
+// each in flight.
 __global__ void __launch_bounds__(1024) glr_drate_kernel(const Params p, int tile) {
     __shared__ float s[32][33];
+    grid_dependency_wait();
     if (p.head->blocked) return;
     const int64_t n = (p.head->live + tile - 1) / tile;
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
     float sum = 0.f;
     if (d < p.D)
-        for (int64_t j = r; j < n; j += 32) sum += p.drate_part[j * p.D + d];
+        for (int64_t j0 = r; j0 < n; j0 += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = j0 + i * 32 < n ? p.drate_part[(j0 + i * 32) * p.D + d] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += v[i];
+        }
     s[r][lane] = sum;
     __syncthreads();
     float t = s[lane][r];
@@ -415,10 +615,12 @@ size_t layout(const gcl_glr_args *a, bool backward, Params *p) {
     const int64_t tiles = backward ? tb : tf;
     const size_t row = sizeof(float) * (size_t)a->D;
     set(o.head, sizeof(Header));
-    set(o.first, sizeof(int32_t) * (size_t)(tiles + 1));
-    set(o.cut, sizeof(int32_t) * (size_t)tiles);
-    set(o.agg_a, row * tiles);
-    set(o.agg_b, row * tiles);
+    const int64_t n_cb = (a->D * (a->dtype == GCL_F32 ? 4 : 2) + 127) / 128;
+    set(o.first, sizeof(int32_t) * (size_t)tiles);
+    set(o.chain.flag, sizeof(int32_t) * (size_t)(tiles * n_cb));
+    set(o.chain.a, row * tiles);
+    set(o.chain.own, row * tiles);
+    set(o.chain.out, row * tiles);
     if (backward) {
         if (a->drate) set(o.drate_part, row * tiles);
         if (!a->h_save) set(o.h_save, row * tb);
@@ -426,27 +628,30 @@ size_t layout(const gcl_glr_args *a, bool backward, Params *p) {
     return at;
 }
 
-template <typename T>
-cudaError_t launch_fwd(Params p, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.tiles * p.n_cb);
-    const int64_t setup = (p.tiles + 1024) / 1024 > p.n_max ? (p.tiles + 1024) / 1024 : p.n_max;
-    glr_setup_kernel<<<(unsigned)(setup < 2 * num_sms() ? setup : 2 * num_sms()), 1024, 0, s>>>(p, p.h0, p.ht, kTileF);
-    glr_fwd_kernel<T, false><<<grid, kThreads, 0, s>>>(p);
-    glr_scan_kernel<false><<<(p.D + 63) / 64, 64, 0, s>>>(p, kTileF);
-    glr_fwd_kernel<T, true><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+// Launches the set-up and, as its dependent, `kernel` with at most `ctas` blocks an SM.
+template <typename K>
+cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float *out_state, int tile, int threads, int ctas, size_t smem,
+                         cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t units = p.tiles * p.n_cb, most = (int64_t)ctas * num_sms();
+    int64_t setup = (units + 4095) / 4096;
+    if (out_state && setup < (p.n_max + 7) / 8) setup = (p.n_max + 7) / 8;
+    if (setup > num_sms()) setup = num_sms();
+    glr_setup_kernel<<<(unsigned)setup, 1024, 0, s>>>(p, in_state, out_state, tile);
+    return launch_dependent(kernel, dim3((unsigned)(units < most ? units : most)), dim3(threads), smem, s, p);
 }
 
 template <typename T>
-cudaError_t launch_bwd(Params p, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.tiles * p.n_cb);
-    const int64_t setup = (p.tiles + 1024) / 1024 > p.n_max ? (p.tiles + 1024) / 1024 : p.n_max;
-    glr_setup_kernel<<<(unsigned)(setup < 2 * num_sms() ? setup : 2 * num_sms()), 1024, 0, s>>>(p, p.dht, p.dh0, kTileB);
-    glr_bwd_kernel<T, false><<<grid, kThreads, 0, s>>>(p);
-    glr_scan_kernel<true><<<(p.D + 63) / 64, 64, 0, s>>>(p, kTileB);
-    glr_bwd_kernel<T, true><<<grid, kThreads, 0, s>>>(p);
-    if (p.drate) glr_drate_kernel<<<(p.D + 31) / 32, 1024, 0, s>>>(p, kTileB);
-    return cudaGetLastError();
+cudaError_t launch_fwd(const Params &p, cudaStream_t s) {
+    return launch_tiles(glr_fwd_kernel<T>, p, p.h0, p.ht, kTileF, 32 * kWarpsF, kCtasF, (size_t)2 * (p.i.p ? 3 : 2) * kTileF * 128, s);
+}
+
+template <typename T>
+cudaError_t launch_bwd(const Params &p, cudaStream_t s) {
+    const cudaError_t e = launch_tiles(glr_bwd_kernel<T>, p, p.dht, p.dh0, kTileB, 32 * kWarpsB, kCtasB, (size_t)2 * (p.i.p ? 4 : 3) * kTileB * 128, s);
+    if (e != cudaSuccess || !p.drate) return e;
+    return launch_dependent(glr_drate_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, p, kTileB);
 }
 
 template <typename T>

@@ -54,9 +54,14 @@ __device__ __forceinline__ void sigmoids(float x, float &s, float &c) {
     c = x >= 0.f ? lo : hi;
 }
 
+// sigmoid(x) alone.  (exp(-x) = infinity gives 0.)
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x) { return frcp<T>(1.f + fexp<T>(-x)); }
+
 // a = exp(l) and q = 1 - a.  Near l = 0 the difference loses q's digits and the fast exp's error, some units of
-// 2^-24 with one sign, would add up over all the tokens that a close to 1 remembers: there q is the series in nested
-// form y (1 - y/2 (1 - y/3 (...))), y = -l, off by less than y^7 / 8! of its value, and a = 1 - q, rounded once.
+// 2^-24 with one sign, would add up over all the tokens that a close to 1 remembers: for 0 <= y = -l < 0.7 q is
+// y P(y), P the polynomial of degree 5 that meets (1 - exp(-y)) / y at the Chebyshev points of [0, 0.7] (off by 1.2e-8 of
+// its value), and a = 1 - q, rounded once.
 template <typename T>
 __device__ __forceinline__ void exps(float l, float &a, float &q) {
     a = fexp<T>(l);
@@ -65,13 +70,12 @@ __device__ __forceinline__ void exps(float l, float &a, float &q) {
         return;
     }
     const float y = -l;
-    float s = fmaf(y, -1.f / 7.f, 1.f);
-    s = fmaf(y * (-1.f / 6.f), s, 1.f);
-    s = fmaf(y * (-1.f / 5.f), s, 1.f);
-    s = fmaf(y * (-1.f / 4.f), s, 1.f);
-    s = fmaf(y * (-1.f / 3.f), s, 1.f);
-    s = fmaf(y * -0.5f, s, 1.f);
-    const bool near = fabsf(y) < 0.35f;
+    float s = fmaf(y, -1.0332434e-3f, 8.0679525e-3f);
+    s = fmaf(y, s, -4.1572765e-2f);
+    s = fmaf(y, s, 1.6665146e-1f);
+    s = fmaf(y, s, -4.9999911e-1f);
+    s = fmaf(y, s, 1.f);
+    const bool near = __float_as_uint(y) < __float_as_uint(0.7f);          // (y < 0 and NaN have larger bits)
     q = near ? y * s : 1.f - a;
     a = near ? 1.f - q : a;
 }
@@ -95,10 +99,7 @@ __device__ __forceinline__ void decays(const Kind &k, const float *rate, const f
     } else if (k.decay == GCL_DECAY_POWER) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            float s, c;
-            sigmoids<T>(r[e], s, c);
-            const float l = -rate[e % V] * s;
-            exps<T>(l, a[e], q[e]);
+            exps<T>(-rate[e % V] * sigmoid<T>(r[e]), a[e], q[e]);
         }
     } else {
 #pragma unroll
@@ -124,8 +125,17 @@ __device__ __forceinline__ void mixes(const Kind &k, const float *a, float *q) {
 struct Header {
     int32_t blocked;               // the call does nothing (status word set, or cu_seqlens invalid)
     int32_t live;                  // cu_seqlens[n_max]
-    int32_t pad[2];
+    uint32_t ticket;               // tiles taken
+    int32_t pad;
 };
+
+// The states between tiles, by tile in the order of the recurrence and block of channels.
+struct Chain {
+    int32_t *flag;                 // [n_cb, tiles]: 0, kOwn (a and own are there), kDone (out is there)
+    float *a, *own;                // [tiles, D]: product of the tile's decays, its state from zero
+    float *out;                    // [tiles, D]: the state that leaves the tile
+};
+constexpr int32_t kOwn = 1, kDone = 2;
 
 struct Params {
     Rows x, r, i, o, d_o, dx, dr, di;
@@ -135,9 +145,8 @@ struct Params {
     const int32_t *cu;
     int32_t *status;
     Header *head;
-    int32_t *first;                // [tiles + 1]: the first sequence that starts at or behind the tile's first token
-    float *agg_a, *agg_b;          // [tiles, D]: products of a and own states of the tiles; then the states that enter
-    int32_t *cut;                  // [tiles]: a sequence starts (backward: ends) in the tile
+    int32_t *first;                // [tiles]: the first sequence that starts at or behind the tile's first token
+    Chain chain;
     float *drate_part;             // [tiles, D]
     int64_t t_max, tiles;
     int32_t n_max, D, n_cb;        // n_cb: blocks of channels
