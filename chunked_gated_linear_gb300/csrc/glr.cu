@@ -12,6 +12,8 @@
 // token t passes on,
 //   G_t = d_o_t + c_{t+1},   c_t = a_t G_t,
 // the same recurrence with the same decays, cut where a sequence ends, over the tiles from last to first.
+#include <type_traits>
+
 #include "glr.cuh"
 #include "tc_ptx.cuh"
 
@@ -101,16 +103,19 @@ __device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, 
     for (int v = 0; v < V; ++v) s[n * D + ch + v] = h[v];
 }
 
-// The tile's rows (tokens from t0 to live, channels of block cb) into shared memory, asynchronously; zeros elsewhere.
+// The tile's rows (n_live tokens from t0 on, channels of block cb) into shared memory, asynchronously; zeros elsewhere.
 template <typename T, int TILE, int THREADS>
-__device__ __forceinline__ void stage_rows(const Params &p, const Rows &r, int64_t t0, int64_t live, int cb, uint8_t *dst) {
-    constexpr int E = 16 / sizeof(T);
+__device__ __forceinline__ void stage_rows(const Params &p, const Rows &r, int64_t t0, int n_live, int cb, uint8_t *dst) {
+    constexpr int E = 16 / sizeof(T), ROWS = THREADS / 8;
+    const int row = threadIdx.x >> 3, ch = cb * Lane<T>::CB + (threadIdx.x & 7) * E;
+    const int n = ch < p.D ? n_live : 0;
+    const T *src = static_cast<const T *>(r.p) + (t0 + row) * r.st + ch;
+    const uint32_t to = tc::smem_u32(dst) + threadIdx.x * 16;
 #pragma unroll
-    for (int c = threadIdx.x; c < TILE * 8; c += THREADS) {
-        const int row = c >> 3, ch = cb * Lane<T>::CB + (c & 7) * E;
-        const bool on = t0 + row < live && ch < p.D && GCL_IN_BOUNDS(t0 + row, p.t_max, p.status);
-        const T *src = static_cast<const T *>(r.p) + (on ? (t0 + row) * r.st + ch : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + c * 16)), "l"(src), "r"(on ? 16 : 0)
+    for (int i = 0; i < TILE / ROWS; ++i) {
+        const bool on = row + i * ROWS < n && GCL_IN_BOUNDS(t0 + row + i * ROWS, p.t_max, p.status);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * THREADS * 16),
+                     "l"(on ? src + i * ROWS * r.st : static_cast<const T *>(r.p)), "r"(on ? 16 : 0)
                      : "memory");
     }
 }
@@ -264,12 +269,13 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Par
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 3 : 2;
     auto stage = [&](uint32_t unit, int buf) {
         if (unit < units) {
-            const int64_t t0 = (int64_t)(unit / p.n_cb) * kTileF;
-            const int cb = unit % p.n_cb;
+            const uint32_t j = unit / p.n_cb;
+            const int64_t t0 = (int64_t)j * kTileF;
+            const int cb = unit - j * p.n_cb, n = live - t0 < kTileF ? (int)(live - t0) : kTileF;
             uint8_t *dst = s_rows + buf * narr * BYTES;
-            stage_rows<T, kTileF, THREADS>(p, p.r, t0, live, cb, dst);
-            stage_rows<T, kTileF, THREADS>(p, p.x, t0, live, cb, dst + BYTES);
-            if (narr == 3) stage_rows<T, kTileF, THREADS>(p, p.i, t0, live, cb, dst + 2 * BYTES);
+            stage_rows<T, kTileF, THREADS>(p, p.r, t0, n, cb, dst);
+            stage_rows<T, kTileF, THREADS>(p, p.x, t0, n, cb, dst + BYTES);
+            if (narr == 3) stage_rows<T, kTileF, THREADS>(p, p.i, t0, n, cb, dst + 2 * BYTES);
         }
         stage_commit();
     };
@@ -287,8 +293,10 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Par
         // (a second tile is taken only when the first has arrived, so that few tiles spread over all blocks)
         uint32_t taken = 0;
         if (threadIdx.x == 32) taken = atomicAdd(&p.head->ticket, first ? 2u : 1u);
-        const int64_t j = unit / p.n_cb, t = j * kTileF + warp * RUN;
-        const int cb = unit % p.n_cb, ch = cb * CB + lane * V;
+        const uint32_t j = unit / p.n_cb;
+        const int64_t t = (int64_t)j * kTileF + warp * RUN;
+        const int cb = unit - j * p.n_cb, ch = cb * CB + lane * V;
+        const int n = live - t < RUN ? (int)(live - t) : RUN;            // live tokens of the warp (none: <= 0)
         const bool on = ch < p.D;
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
         float a[N], b[N];
@@ -317,10 +325,10 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Par
                 }
             }
         }
-        if (t + RUN > live)
+        if (n < RUN)
 #pragma unroll
             for (int k = 0; k < RUN; ++k)
-                if (t + k >= live)
+                if (k >= n)
 #pragma unroll
                     for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; b[k * V + v] = 0.f; }
         const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
@@ -330,15 +338,19 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Par
             float A[V], h[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = 0.f; }
+            auto walk = [&](auto cut) {
 #pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-                if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
+                for (int k = 0; k < RUN; ++k) {
+                    if (decltype(cut)::value && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
-                    A[v] *= a[k * V + v];
+                    for (int v = 0; v < V; ++v) {
+                        h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
+                        A[v] *= a[k * V + v];
+                    }
                 }
-            }
+            };
+            if (starts) walk(std::true_type());
+            else walk(std::false_type());
 #pragma unroll
             for (int v = 0; v < V; ++v) { s.a[warp][lane * V + v] = A[v]; s.b[warp][lane * V + v] = h[v]; }
             if (lane == 0) s.cut[warp] = starts != 0;
@@ -358,18 +370,25 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Par
         float h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = s.b[warp][lane * V + v];
-        if (warp * RUN % kSave == 0 && p.h_save && t < live) {
+        if (warp * RUN % kSave == 0 && p.h_save && n > 0) {
             if (starts & 1) load_state<V>(p.h0, start[0], p.D, ch, on, h);
             store_state<V>(p.h_save, t / kSave, p.D, ch, on, h);
         }
+        uint32_t *to = word<T>(p.o, t, ch);
+        const int n_out = p.o.p && on && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
+        auto walk = [&](auto plain) {                      // plain: no borders, all tokens live
 #pragma unroll
-        for (int k = 0; k < RUN; ++k) {
-            if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
+            for (int k = 0; k < RUN; ++k) {
+                if (!decltype(plain)::value && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
-            if (p.o.p && on && t + k < live && GCL_IN_BOUNDS(t + k, p.t_max, p.status)) *word<T>(p.o, t + k, ch) = Lane<T>::put(h);
-            if (ends >> k & 1) store_state<V>(p.ht, end[k], p.D, ch, on, h);
-        }
+                for (int v = 0; v < V; ++v) h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
+                if (decltype(plain)::value ? n_out > 0 : k < n_out) *to = Lane<T>::put(h);
+                to += p.o.st / V;
+                if (!decltype(plain)::value && (ends >> k & 1)) store_state<V>(p.ht, end[k], p.D, ch, on, h);
+            }
+        };
+        if (!(starts | ends) && n == RUN) walk(std::true_type());
+        else walk(std::false_type());
         unit = unit1;
         first = false;
     }
@@ -395,13 +414,14 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const Par
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 4 : 3;
     auto stage = [&](uint32_t unit, int buf) {
         if (unit < units) {
-            const int64_t t0 = (n_live - 1 - unit / p.n_cb) * kTileB;
-            const int cb = unit % p.n_cb;
+            const uint32_t seq = unit / p.n_cb;
+            const int64_t t0 = (n_live - 1 - seq) * kTileB;
+            const int cb = unit - seq * p.n_cb, n = live - t0 < kTileB ? (int)(live - t0) : kTileB;
             uint8_t *dst = s_rows + buf * narr * BYTES;
-            stage_rows<T, kTileB, THREADS>(p, p.r, t0, live, cb, dst);
-            stage_rows<T, kTileB, THREADS>(p, p.x, t0, live, cb, dst + BYTES);
-            stage_rows<T, kTileB, THREADS>(p, p.d_o, t0, live, cb, dst + 2 * BYTES);
-            if (narr == 4) stage_rows<T, kTileB, THREADS>(p, p.i, t0, live, cb, dst + 3 * BYTES);
+            stage_rows<T, kTileB, THREADS>(p, p.r, t0, n, cb, dst);
+            stage_rows<T, kTileB, THREADS>(p, p.x, t0, n, cb, dst + BYTES);
+            stage_rows<T, kTileB, THREADS>(p, p.d_o, t0, n, cb, dst + 2 * BYTES);
+            if (narr == 4) stage_rows<T, kTileB, THREADS>(p, p.i, t0, n, cb, dst + 3 * BYTES);
         }
         stage_commit();
     };
@@ -418,7 +438,8 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const Par
         if (threadIdx.x == 32) taken = atomicAdd(&p.head->ticket, 1u);
         const uint32_t seq = unit / p.n_cb;
         const int64_t j = n_live - 1 - seq, t = j * kTileB + warp * RUN;
-        const int cb = unit % p.n_cb, ch = cb * CB + lane * V;
+        const int cb = unit - seq * p.n_cb, ch = cb * CB + lane * V;
+        const int n = live - t < RUN ? (int)(live - t) : RUN;            // live tokens of the warp (none: <= 0)
         const bool on = ch < p.D;
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
         auto row = [&](int arr, int k, float *v) { Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128), v); };
@@ -432,10 +453,10 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const Par
             decays<T, N>(p.kind, rate, r, a, m);
             mixes<T, N>(p.kind, a, m);
         }
-        if (t + RUN > live)
+        if (n < RUN)
 #pragma unroll
             for (int k = 0; k < RUN; ++k)
-                if (t + k >= live)
+                if (k >= n)
 #pragma unroll
                     for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; m[k * V + v] = 0.f; }
         const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
@@ -446,27 +467,31 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const Par
             float A[V], h[V], c[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = c[v] = 0.f; }
+            auto walk = [&](auto cut) {
 #pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-                float x[V], g[V];
-                row(1, k, x);
-                if (narr == 4) row(3, k, g);
-                if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
+                for (int k = 0; k < RUN; ++k) {
+                    float x[V], g[V];
+                    row(1, k, x);
+                    if (narr == 4) row(3, k, g);
+                    if (decltype(cut)::value && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    prev[k * V + v] = m[k * V + v] * (narr == 4 ? x[v] * sigmoid<T>(g[v]) : x[v]);
-                    h[v] = fmaf(a[k * V + v], h[v], prev[k * V + v]);
-                    A[v] *= a[k * V + v];
+                    for (int v = 0; v < V; ++v) {
+                        prev[k * V + v] = m[k * V + v] * (narr == 4 ? x[v] * sigmoid<T>(g[v]) : x[v]);
+                        h[v] = fmaf(a[k * V + v], h[v], prev[k * V + v]);
+                        A[v] *= a[k * V + v];
+                    }
                 }
-            }
 #pragma unroll
-            for (int k = RUN - 1; k >= 0; --k) {
-                float go[V];
-                row(2, k, go);
-                if (ends >> k & 1) load_state<V>(p.dht, end[k], p.D, ch, on, c);
+                for (int k = RUN - 1; k >= 0; --k) {
+                    float go[V];
+                    row(2, k, go);
+                    if (decltype(cut)::value && (ends >> k & 1)) load_state<V>(p.dht, end[k], p.D, ch, on, c);
 #pragma unroll
-                for (int v = 0; v < V; ++v) c[v] = a[k * V + v] * (go[v] + c[v]);
-            }
+                    for (int v = 0; v < V; ++v) c[v] = a[k * V + v] * (go[v] + c[v]);
+                }
+            };
+            if (starts | ends) walk(std::true_type());
+            else walk(std::false_type());
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 s.a[warp][lane * V + v] = A[v];
@@ -496,56 +521,67 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const Par
         float h[V], c[V], dsum[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) { h[v] = s_h[warp][lane * V + v]; c[v] = s.b[warp][lane * V + v]; dsum[v] = 0.f; }
+        const int64_t last = t + RUN - 1;
+        uint32_t *to_x = word<T>(p.dx, last, ch), *to_r = word<T>(p.dr, last, ch), *to_i = word<T>(p.di, last, ch);
+        const int n_out = on && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
+        auto walk = [&](auto plain) {                      // plain: no borders, all tokens live
+            constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-        for (int k = 0; k < RUN; ++k) {
-            if (starts >> k & 1) load_state<V>(p.h0, start[k], p.D, ch, on, h);
+            for (int k = 0; k < RUN; ++k) {
+                if (!PLAIN && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float b = prev[k * V + v];
-                prev[k * V + v] = h[v];
-                h[v] = fmaf(a[k * V + v], h[v], b);
-            }
-        }
-#pragma unroll
-        for (int k = RUN - 1; k >= 0; --k) {
-            if (ends >> k & 1) load_state<V>(p.dht, end[k], p.D, ch, on, c);
-            float dx[V], dr[V], di[V], x[V], g[V], go[V], r[V];
-            row(0, k, r);
-            row(1, k, x);
-            row(2, k, go);
-            if (narr == 4) row(3, k, g);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = k * V + v;
-                const float G = go[v] + c[v];
-                c[v] = a[e] * G;
-                float sg = 1.f, ng = 0.f;
-                if (narr == 4) sigmoids<T>(g[v], sg, ng);
-                const float u = x[v] * sg;
-                dx[v] = G * m[e] * sg;
-                di[v] = dx[v] * x[v] * ng;
-                float dl = c[v] * prev[e];
-                if (p.kind.mix == GCL_MIX_COMPLEMENT) dl = fmaf(-c[v], u, dl);
-                else if (p.kind.mix == GCL_MIX_ROOT && m[e] > 0.f) dl = fmaf(-a[e] * frcp<T>(m[e]) * c[v], u, dl);
-                if (p.kind.decay != GCL_DECAY_LOG) {
-                    float sr, nr;
-                    sigmoids<T>(r[v], sr, nr);
-                    if (p.kind.decay == GCL_DECAY_SIGMOID) {
-                        dl *= nr;
-                    } else {
-                        if (t + k < live) dsum[v] = fmaf(-dl, sr, dsum[v]);
-                        dl *= -rate[v] * sr * nr;
-                    }
+                for (int v = 0; v < V; ++v) {
+                    const float b = prev[k * V + v];
+                    prev[k * V + v] = h[v];
+                    h[v] = fmaf(a[k * V + v], h[v], b);
                 }
-                dr[v] = dl;
             }
-            if (on && t + k < live && GCL_IN_BOUNDS(t + k, p.t_max, p.status)) {
-                *word<T>(p.dx, t + k, ch) = Lane<T>::put(dx);
-                *word<T>(p.dr, t + k, ch) = Lane<T>::put(dr);
-                if (narr == 4) *word<T>(p.di, t + k, ch) = Lane<T>::put(di);
+#pragma unroll
+            for (int k = RUN - 1; k >= 0; --k) {
+                if (!PLAIN && (ends >> k & 1)) load_state<V>(p.dht, end[k], p.D, ch, on, c);
+                float dx[V], dr[V], di[V], x[V], g[V], go[V], r[V];
+                row(0, k, r);
+                row(1, k, x);
+                row(2, k, go);
+                if (narr == 4) row(3, k, g);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int e = k * V + v;
+                    const float G = go[v] + c[v];
+                    c[v] = a[e] * G;
+                    float sg = 1.f, ng = 0.f;
+                    if (narr == 4) sigmoids<T>(g[v], sg, ng);
+                    const float u = x[v] * sg;
+                    dx[v] = G * m[e] * sg;
+                    di[v] = dx[v] * x[v] * ng;
+                    float dl = c[v] * prev[e];
+                    if (p.kind.mix == GCL_MIX_COMPLEMENT) dl = fmaf(-c[v], u, dl);
+                    else if (p.kind.mix == GCL_MIX_ROOT) dl = fmaf(m[e] > 0.f ? -a[e] * frcp<T>(m[e]) * c[v] : 0.f, u, dl);
+                    if (p.kind.decay != GCL_DECAY_LOG) {
+                        float sr, nr;
+                        sigmoids<T>(r[v], sr, nr);
+                        if (p.kind.decay == GCL_DECAY_SIGMOID) {
+                            dl *= nr;
+                        } else {
+                            if (PLAIN || k < n) dsum[v] = fmaf(-dl, sr, dsum[v]);
+                            dl *= -rate[v] * sr * nr;
+                        }
+                    }
+                    dr[v] = dl;
+                }
+                if (PLAIN ? n_out > 0 : k < n_out) {
+                    *to_x = Lane<T>::put(dx);
+                    *to_r = Lane<T>::put(dr);
+                    if (narr == 4) *to_i = Lane<T>::put(di);
+                }
+                to_x -= p.dx.st / V;
+                to_r -= p.dr.st / V;
+                to_i -= p.di.st / V;
+                if (!PLAIN && (starts >> k & 1)) store_state<V>(p.dh0, start[k], p.D, ch, on, c);
             }
-            if (starts >> k & 1) store_state<V>(p.dh0, start[k], p.D, ch, on, c);
-        }
+        };
+        if (!(starts | ends) && n == RUN) walk(std::true_type());
+        else walk(std::false_type());
         if (p.drate_part) {
 #pragma unroll
             for (int v = 0; v < V; ++v) s_d[warp][lane * V + v] = dsum[v];

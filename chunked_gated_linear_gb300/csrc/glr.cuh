@@ -42,9 +42,31 @@ struct Lane {
     }
 };
 
-// exp and 1 / x: the accurate ones for fp32 rows; a few ulp for 16-bit rows, whose own rounding is 2^13 ulp.
-template <typename T> __device__ __forceinline__ float fexp(float x) { return sizeof(T) == 4 ? expf(x) : __expf(x); }
-template <typename T> __device__ __forceinline__ float frcp(float x) { return sizeof(T) == 4 ? 1.f / x : __fdividef(1.f, x); }
+// exp, 1 / x and the square root: the accurate ones for fp32 rows; for 16-bit rows, whose own rounding is 2^13 ulp, the
+// special-function unit's, off by a few ulp.  (Flushing subnormals: without it each takes three instructions more, 40 of
+// the forward's 108 a value.)
+template <typename T>
+__device__ __forceinline__ float fexp(float x) {
+    if (sizeof(T) == 4) return expf(x);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+template <typename T>
+__device__ __forceinline__ float frcp(float x) {
+    if (sizeof(T) == 4) return 1.f / x;
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <typename T>
+__device__ __forceinline__ float root(float x) {
+    x = fmaxf(x, 0.f);
+    if (sizeof(T) == 4) return sqrtf(x);
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // sigmoid(x) and sigmoid(-x), neither by a difference.
 template <typename T>
@@ -78,15 +100,6 @@ __device__ __forceinline__ void exps(float l, float &a, float &q) {
     const bool near = __float_as_uint(y) < __float_as_uint(0.7f);          // (y < 0 and NaN have larger bits)
     q = near ? y * s : 1.f - a;
     a = near ? 1.f - q : a;
-}
-
-template <typename T>
-__device__ __forceinline__ float root(float x) {
-    x = fmaxf(x, 0.f);
-    if (sizeof(T) == 4) return sqrtf(x);
-    float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // a and q = 1 - a of N values of r (N / V tokens of the lane's V channels); the kind is the same for the grid.
