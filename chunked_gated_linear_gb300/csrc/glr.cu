@@ -8,6 +8,8 @@
 // ready.  A block waits for tiles with lower tickets alone, whose blocks run already, so the first of them
 // never waits: the launch ends whatever else runs on the GPU.  (Three launches -- own states, their scan, outputs -- read
 // x, r and i twice: 65,536 tokens of 2,048 channels 1,424 us.)
+// The wait for the state before is what a tile spends longest on, so the tiles meet in packets of 16 bytes, values and tag in one
+// access (flags with a fence before and loads behind them: 514 us at that size).
 // Backwards from the states before each 64 tokens (saved by the forward, or formed again): with c_t = a_t G_t the gradient that
 // token t passes on,
 //   G_t = d_o_t + c_{t+1},   c_t = a_t G_t,
@@ -27,7 +29,7 @@ constexpr int kWarpsF = 16, kWarpsB = 8, kTileF = kWarpsF * kRun, kTileB = kWarp
 constexpr int kCtasF = 2, kCtasB = 3;                  // resident blocks an SM
 
 // ---- set-up: checks cu_seqlens, finds each tile's first sequence, passes states of empty sequences through, clears the
-// flags between tiles ----
+// packets of the tiles that will be taken ----
 __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const float *in_state, float *out_state, int tile) {
     launch_dependents();
     const int tid = threadIdx.x;
@@ -46,7 +48,8 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const f
     }
     if (blocked || bad) return;
     const int64_t at = blockIdx.x * (int64_t)blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t e = at; e < p.tiles * p.n_cb; e += step) p.chain.flag[e] = 0;
+    const int64_t packets = ((int64_t)p.cu[p.n_max] + tile - 1) / tile * p.D;
+    for (int64_t e = at; e < packets; e += step) reinterpret_cast<uint4 *>(p.chain)[e] = make_uint4(0, 0, 0, 0);
     for (int64_t j = at; j < p.tiles; j += step) {
         const int64_t t0 = j * tile;
         int lo = 0, hi = p.n_max;                          // first n with cu[n] >= t0 (n_max if none)
@@ -90,160 +93,76 @@ __device__ __forceinline__ uint32_t *word(const Rows &r, int64_t t, int ch) {
     return reinterpret_cast<uint32_t *>(static_cast<T *>(r.p) + t * r.st + ch);
 }
 
-// states [n, D]
-template <int V>
-__device__ __forceinline__ void load_state(const float *s, int64_t n, int D, int ch, bool on, float *h) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = s && on ? s[n * D + ch + v] : 0.f;
+// A lane's values of row n of [n, D]; zeros without the array or past the channels.
+template <typename T>
+__device__ __forceinline__ typename Lane<T>::P load_state(const float *s, int64_t n, int D, int ch) {
+    return s && ch < D ? Lane<T>::load(s + n * D + ch) : Lane<T>::all(0.f);
 }
-template <int V>
-__device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, bool on, const float *h) {
-    if (!s || !on) return;
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[n * D + ch + v] = h[v];
+template <typename T>
+__device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, typename Lane<T>::P h) {
+    if (s && ch < D) Lane<T>::store(s + n * D + ch, h);
 }
 
-// The tile's rows (n_live tokens from t0 on, channels of block cb) into shared memory, asynchronously; zeros elsewhere.
-template <typename T, int TILE, int THREADS>
-__device__ __forceinline__ void stage_rows(const Params &p, const Rows &r, int64_t t0, int n_live, int cb, uint8_t *dst) {
-    constexpr int E = 16 / sizeof(T), ROWS = THREADS / 8;
-    const int row = threadIdx.x >> 3, ch = cb * Lane<T>::CB + (threadIdx.x & 7) * E;
-    const int n = ch < p.D ? n_live : 0;
-    const T *src = static_cast<const T *>(r.p) + (t0 + row) * r.st + ch;
-    const uint32_t to = tc::smem_u32(dst) + threadIdx.x * 16;
-#pragma unroll
-    for (int i = 0; i < TILE / ROWS; ++i) {
-        const bool on = row + i * ROWS < n && GCL_IN_BOUNDS(t0 + row + i * ROWS, p.t_max, p.status);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * THREADS * 16),
-                     "l"(on ? src + i * ROWS * r.st : static_cast<const T *>(r.p)), "r"(on ? 16 : 0)
-                     : "memory");
-    }
+// ---- what tiles leave each other ----
+__device__ __forceinline__ Packet load_packet(const Packet *p) {
+    unsigned __int128 v;
+    asm volatile("ld.relaxed.gpu.global.b128 %0, [%1];" : "=q"(v) : "l"(p) : "memory");
+    Packet k;
+    k.a = __uint_as_float((uint32_t)v);
+    k.own = __uint_as_float((uint32_t)(v >> 32));
+    k.out = __uint_as_float((uint32_t)(v >> 64));
+    k.tag = (uint32_t)(v >> 96);
+    return k;
 }
-__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ int32_t load_flag(const int32_t *f) {
-    int32_t v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(f) : "memory");
-    return v;
-}
-__device__ __forceinline__ void store_flag(int32_t *f, int32_t v) {
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(f), "r"(v) : "memory");
+__device__ __forceinline__ void store_packet(Packet *p, float a, float own, float out, uint32_t tag) {
+    const unsigned __int128 v = (unsigned __int128)__float_as_uint(a) | (unsigned __int128)__float_as_uint(own) << 32 |
+                                (unsigned __int128)__float_as_uint(out) << 64 | (unsigned __int128)tag << 96;
+    asm volatile("st.relaxed.gpu.global.b128 [%0], %1;" ::"l"(p), "q"(v) : "memory");
 }
 
-// One warp: the warp's states of row `at` of a chain array, past the L1.
-template <int V>
-__device__ __forceinline__ void chain_load(const float *s, int64_t at, bool on, float *h) {
-    if (V == 2) {
-        const float2 f = on ? __ldcg(reinterpret_cast<const float2 *>(s + at)) : make_float2(0.f, 0.f);
-        h[0] = f.x;
-        h[V - 1] = f.y;
-    } else {
-        h[0] = on ? __ldcg(s + at) : 0.f;
-    }
-}
-
-// One warp: the state that enters tile `seq` (its number in the order of the recurrence, > 0), from the nearest tile
-// before it whose state is out and the own states between, folded from the oldest on.
-template <int V>
-__device__ __forceinline__ void chain_enter(const Params &p, int64_t seq, int cb, int ch, bool on, float *h) {
-    const int lane = threadIdx.x & 31;
-    const int32_t *flag = p.chain.flag + (int64_t)cb * p.tiles;
-    const int64_t mine = seq - 1 - lane;
-    const uint64_t t0 = tc::globaltimer();
-    int near;
+// One warp, a channel a lane: the state that enters tile `seq` (its number in the order of the recurrence, > 0): from the nearest
+// tile before it whose state is out for all the warp's channels, and the own states of the tiles between, folded from the oldest on.
+// False: it did not come in time.
+__device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch, bool on, float &h) {
+    constexpr int W = 4;                                   // packets in flight
+    const int64_t base = seq - 1;
+    int depth = 0;
+    uint64_t t0 = 0;
     while (true) {
-        const int32_t f = mine >= 0 ? load_flag(flag + mine) : 0;
-        const uint32_t done = __ballot_sync(0xffffffffu, f == kDone), own = __ballot_sync(0xffffffffu, f != 0);
-        near = __ffs(done) - 1;
-        if (near >= 0 && !(~own & ((1u << near) - 1))) break;
-        if (__shfl_sync(0xffffffffu, tc::globaltimer() - t0 > tc::kWaitLimitNs, 0)) {
-            if (lane == 0) status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
+        Packet k[W];
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = 0.f;
-            return;
+        for (int u = 0; u < W; ++u) {
+            const int64_t at = base - depth - u;
+            k[u].a = k[u].own = k[u].out = 0.f;
+            k[u].tag = on ? 0 : kDone;
+            if (on && at >= 0) k[u] = load_packet(p.chain + at * p.D + ch);
         }
-    }
-    __syncwarp();
-    int64_t at = (seq - 1 - near) * p.D + ch;
-    chain_load<V>(p.chain.out, at, on, h);
-    for (int m = near; m > 0; m -= 4) {                    // four tiles' loads in flight
-        float a[4][V], b[4][V];
+        int found = W;
+        bool gap = false;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            chain_load<V>(p.chain.a, at + (u + 1) * (int64_t)p.D, on && u < m, a[u]);
-            chain_load<V>(p.chain.own, at + (u + 1) * (int64_t)p.D, on && u < m, b[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (u < m)
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = fmaf(a[u][v], h[v], b[u][v]);
-        at += 4 * (int64_t)p.D;
-    }
-}
-
-// One warp: publishes its channels of a tile: own states (kOwn) or the state that leaves (kDone).
-template <int V>
-__device__ __forceinline__ void chain_publish(const Params &p, int64_t seq, int cb, int ch, bool on, const float *a, const float *h, int32_t what) {
-    const int64_t at = seq * p.D + ch;
-    if (on) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (what == kOwn) {
-                __stcg(p.chain.a + at + v, a[v]);
-                __stcg(p.chain.own + at + v, h[v]);
-            } else {
-                __stcg(p.chain.out + at + v, h[v]);
+        for (int u = 0; u < W; ++u)
+            if (found == W && !gap) {
+                if (__all_sync(0xffffffffu, k[u].tag == kDone)) found = u;
+                else gap = !__all_sync(0xffffffffu, k[u].tag != 0);
             }
+        if (found < W) {
+#pragma unroll
+            for (int u = W - 1; u >= 0; --u) h = u == found ? k[u].out : u < found ? fmaf(k[u].a, h, k[u].own) : h;
+            for (int d = depth - 1; d >= 0; d -= W) {      // the tiles nearer than these (a multiple of W)
+                Packet n[W];
+#pragma unroll
+                for (int u = 0; u < W; ++u) {
+                    n[u].a = n[u].own = 0.f;
+                    if (on) n[u] = load_packet(p.chain + (base - d + u) * p.D + ch);
+                }
+#pragma unroll
+                for (int u = 0; u < W; ++u) h = fmaf(n[u].a, h, n[u].own);
+            }
+            return true;
         }
-    }
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-        __threadfence();
-        store_flag(p.chain.flag + (int64_t)cb * p.tiles + seq, what);
-    }
-}
-
-// One warp: from the warps' products and own states (rows of s_a and s_b, in the order of the recurrence where REV is
-// false, from last to first else; s_cut: the row does not depend on the one before), publishes the tile and puts the
-// state that enters each row into s_b.
-template <int V, int WARPS, int CB, bool REV>
-__device__ __forceinline__ void chain_tile(const Params &p, int64_t seq, int cb, int ch, bool on, float (*s_a)[CB], float (*s_b)[CB], const int *s_cut) {
-    const int l = (threadIdx.x & 31) * V;
-    float A[V], h[V], c[V];
-    bool cut = false;
-#pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = 0.f; c[v] = 0.f; }
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-        const int w = REV ? WARPS - 1 - i : i;
-        const bool k = s_cut[w] != 0;
-        cut |= k;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            h[v] = k ? s_b[w][l + v] : fmaf(s_a[w][l + v], h[v], s_b[w][l + v]);
-            A[v] *= s_a[w][l + v];
-        }
-    }
-    chain_publish<V>(p, seq, cb, ch, on, A, h, cut ? kDone : kOwn);
-    if (seq > 0) chain_enter<V>(p, seq, cb, ch, on, c);    // (the first tile is cut at its first token)
-    if (!cut) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(A[v], c[v], h[v]);
-        chain_publish<V>(p, seq, cb, ch, on, A, h, kDone);
-    }
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-        const int w = REV ? WARPS - 1 - i : i;
-        const bool k = s_cut[w] != 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float b = s_b[w][l + v], a = s_a[w][l + v];
-            s_b[w][l + v] = c[v];
-            c[v] = k ? b : fmaf(a, c[v], b);
-        }
+        depth = gap || depth >= 7 * W ? 0 : depth + W;
+        if (t0 == 0) t0 = tc::globaltimer();
+        if (__shfl_sync(0xffffffffu, tc::globaltimer() - t0 > tc::kWaitLimitNs, 0)) return false;
     }
 }
 
@@ -252,139 +171,172 @@ struct Shared {
     float a[WARPS][CB], b[WARPS][CB];
     int start[2][WARPS * kRun], end[2][WARPS * kRun];
     int cut[WARPS];
-    uint32_t ticket[2];
+    uint32_t ticket[3];
+    int err;
+    uint64_t full[2];
 };
 
+// One warp, a channel a lane (column c of s.a, s.b): from the warps' products and own states (in the order of the recurrence: from
+// the first row, REV from the last; s.cut: the row does not depend on the one before), publishes the tile and puts the state
+// that enters each row into s.b.  False: the state before did not come in time.
+template <bool REV, int CB, int WARPS>
+__device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch, int c, Shared<CB, WARPS> &s) {
+    const bool on = ch < p.D;
+    Packet *mine = p.chain + seq * p.D + ch;
+    float A = 1.f, h = 0.f, in = 0.f;
+    bool cut = false, ok = true;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        const int w = REV ? WARPS - 1 - i : i;
+        const bool k = s.cut[w] != 0;
+        cut |= k;
+        h = k ? s.b[w][c] : fmaf(s.a[w][c], h, s.b[w][c]);
+        A *= s.a[w][c];
+    }
+    if (on) store_packet(mine, A, h, h, cut ? kDone : kOwn);
+    if (seq > 0) ok = chain_enter(p, seq, ch, on, in);     // (the first tile is cut at its first token)
+    if (on && !cut) store_packet(mine, A, h, fmaf(A, in, h), kDone);
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        const int w = REV ? WARPS - 1 - i : i;
+        const float a = s.a[w][c], b = s.b[w][c];
+        s.b[w][c] = in;
+        in = s.cut[w] ? b : fmaf(a, in, b);
+    }
+    return ok;
+}
+
+struct Maps {                      // the staged rows: r, x, d_o (backward), i
+    CUtensorMap m[4];
+};
+
+// Waits (with a limit) until the copies into both buffers that are under way have landed; `bits`: buffers with one, and the
+// parity each ends at.
+__device__ __forceinline__ void drain(uint64_t *full, uint32_t busy, uint32_t parity) {
+    const uint64_t t0 = tc::globaltimer();
+    for (int b = 0; b < 2; ++b)
+        if (busy >> b & 1)
+            while (!tc::mbar_try_wait(&full[b], parity >> b & 1) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
+}
+
+constexpr int kIssuer = 96;        // the thread that takes tickets and issues the copies
+
 // ---- forward -------------------------------------------------------------
-// Per block: two tiles staged, so that the next one's rows are under way while this one is computed.  Bound by HBM and issue together.
+// Per block: two tiles staged, so that the next one's rows are under way while this one is computed.
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Params p) {
-    constexpr int V = Lane<T>::V, CB = Lane<T>::CB, RUN = kRun, N = RUN * V, THREADS = 32 * kWarpsF, BYTES = kTileF * 128;
+__global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const __grid_constant__ Maps maps, const Params p) {
+    using L = Lane<T>;
+    using P = typename L::P;
+    constexpr int V = L::V, CB = L::CB, RUN = kRun, BYTES = kTileF * 128;
     __shared__ Shared<CB, kWarpsF> s;
-    extern __shared__ __align__(16) uint8_t s_rows[];      // [2][r, x, i][kTileF][128]
+    extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, i][kTileF][128]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, narr = p.i.p ? 3 : 2;
+    if (tid == kIssuer) {
+        tc::mbar_init(&s.full[0], 1);
+        tc::mbar_init(&s.full[1], 1);
+        tc::fence_barrier_init();
+        s.err = 0;
+    }
     grid_dependency_wait();
     if (p.head->blocked) return;
     const int64_t live = p.head->live;
     const uint32_t units = (uint32_t)((live + kTileF - 1) / kTileF * p.n_cb);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 3 : 2;
-    auto stage = [&](uint32_t unit, int buf) {
-        if (unit < units) {
-            const uint32_t j = unit / p.n_cb;
-            const int64_t t0 = (int64_t)j * kTileF;
-            const int cb = unit - j * p.n_cb, n = live - t0 < kTileF ? (int)(live - t0) : kTileF;
-            uint8_t *dst = s_rows + buf * narr * BYTES;
-            stage_rows<T, kTileF, THREADS>(p, p.r, t0, n, cb, dst);
-            stage_rows<T, kTileF, THREADS>(p, p.x, t0, n, cb, dst + BYTES);
-            if (narr == 3) stage_rows<T, kTileF, THREADS>(p, p.i, t0, n, cb, dst + 2 * BYTES);
-        }
-        stage_commit();
+    uint32_t busy = 0, parity = 0;                         // buffers with a copy under way, the parity that they end at
+    auto issue = [&](uint32_t unit, int buf) {             // (every thread keeps the two words, the issuer copies)
+        if (unit >= units) return;
+        busy |= 1u << buf;
+        if (tid != kIssuer) return;
+        const uint32_t j = unit / p.n_cb;
+        tc::mbar_arrive_expect_tx(&s.full[buf], narr * BYTES);
+        for (int k = 0; k < narr; ++k)
+            tc::tma_load_2d(s_rows + (buf * narr + k) * BYTES, &maps.m[k < 2 ? k : 3], (unit - j * p.n_cb) * CB, j * kTileF, &s.full[buf]);
     };
-    if (threadIdx.x == 0) s.ticket[0] = atomicAdd(&p.head->ticket, 1u);
+    if (tid == kIssuer) s.ticket[2] = atomicAdd(&p.head->ticket, 1u);
     __syncthreads();
-    uint32_t unit = s.ticket[0], next = 0;
+    uint32_t unit = s.ticket[2], next = 0;
     if (unit >= units) return;
-    stage(unit, 0);
-    if (warp == 1) borders<kTileF>(p, unit / p.n_cb, s.start[0], s.end[0]);
+    issue(unit, 0);
+    if (warp == 2) borders<kTileF>(p, unit / p.n_cb, s.start[0], s.end[0]);
+    __syncthreads();
     bool first = true;
     for (int buf = 0; unit < units; buf ^= 1) {
-        if (first) stage_wait<0>();
-        else stage_wait<1>();
-        __syncthreads();
-        // (a second tile is taken only when the first has arrived, so that few tiles spread over all blocks)
-        uint32_t taken = 0;
-        if (threadIdx.x == 32) taken = atomicAdd(&p.head->ticket, first ? 2u : 1u);
         const uint32_t j = unit / p.n_cb;
         const int64_t t = (int64_t)j * kTileF + warp * RUN;
         const int cb = unit - j * p.n_cb, ch = cb * CB + lane * V;
         const int n = live - t < RUN ? (int)(live - t) : RUN;            // live tokens of the warp (none: <= 0)
-        const bool on = ch < p.D;
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
-        float a[N], b[N];
-        {
-            float rate[V];
-            load_state<V>(p.kind.rate, 0, p.D, ch, on && p.kind.decay == GCL_DECAY_POWER, rate);
-            float r[N];
+        auto row = [&](int arr, int k) { return L::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128)); };
+        const P rate = load_state<T>(p.kind.decay == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, p.D, ch);
+        const bool near = __all_sync(0xffffffffu, L::every(rate, [](float v) { return v >= 0.f && v <= kNear; }));
+        bool bad = !tc::mbar_wait(&s.full[buf], parity >> buf & 1, &s.err, GCL_DEV_WAIT_TIMEOUT);
+        busy &= ~(1u << buf);
+        parity ^= 1u << buf;
+        // (a second tile is taken only when the first has arrived, so that few tiles spread over all blocks)
+        uint32_t taken = 0;
+        if (tid == kIssuer) taken = atomicAdd(&p.head->ticket, first ? 2u : 1u);
+        P a[RUN], b[RUN];
 #pragma unroll
-            for (int k = 0; k < RUN; ++k) Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + k * 128), r + k * V);
-            decays<T, N>(p.kind, rate, r, a, b);
-            mixes<T, N>(p.kind, a, b);
+        for (int k = 0; k < RUN; ++k) b[k] = row(0, k);
+        decays<T, RUN>(p.kind, rate, near, a, b);
 #pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-                float x[V];
-                Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + BYTES + k * 128), x);
+        for (int k = 0; k < RUN; ++k) b[k] = L::mul(b[k], row(1, k));
+        if (narr == 3)
 #pragma unroll
-                for (int v = 0; v < V; ++v) b[k * V + v] *= x[v];
-            }
-            if (narr == 3) {
-#pragma unroll
-                for (int k = 0; k < RUN; ++k) {
-                    float g[V];
-                    Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + 2 * BYTES + k * 128), g);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) b[k * V + v] *= sigmoid<T>(g[v]);
-                }
-            }
-        }
+            for (int k = 0; k < RUN; ++k) b[k] = L::mul(b[k], sigmoid<T>(row(2, k)));
         if (n < RUN)
 #pragma unroll
             for (int k = 0; k < RUN; ++k)
-                if (k >= n)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; b[k * V + v] = 0.f; }
+                if (k >= n) { a[k] = L::all(1.f); b[k] = L::all(0.f); }
         const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
         const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && start[lane % RUN] >= 0);
         const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && end[lane % RUN] >= 0);
         {
-            float A[V], h[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = 0.f; }
+            P A = L::all(1.f), h = L::all(0.f);
             auto walk = [&](auto cut) {
 #pragma unroll
                 for (int k = 0; k < RUN; ++k) {
-                    if (decltype(cut)::value && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
-                        A[v] *= a[k * V + v];
-                    }
+                    if (decltype(cut)::value && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                    h = L::fma(a[k], h, b[k]);
+                    A = L::mul(A, a[k]);
                 }
             };
             if (starts) walk(std::true_type());
             else walk(std::false_type());
-#pragma unroll
-            for (int v = 0; v < V; ++v) { s.a[warp][lane * V + v] = A[v]; s.b[warp][lane * V + v] = h[v]; }
+            L::store(&s.a[warp][lane * V], A);
+            L::store(&s.b[warp][lane * V], h);
             if (lane == 0) s.cut[warp] = starts != 0;
         }
-        if (threadIdx.x == 32) {
+        if (tid == kIssuer) {
             s.ticket[0] = first ? taken : next;
             s.ticket[1] = first ? taken + 1 : taken;
         }
         __syncthreads();                                   // the rows are read, the warps' own states there
-        if (first) stage(s.ticket[0], buf ^ 1);
-        stage(s.ticket[1], buf);
         const uint32_t unit1 = s.ticket[0];
         next = s.ticket[1];
-        if (warp == 0) chain_tile<V, kWarpsF, CB, false>(p, j, cb, ch, on, s.a, s.b, s.cut);
-        if (warp == 1 && unit1 < units) borders<kTileF>(p, unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
-        __syncthreads();
-        float h[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = s.b[warp][lane * V + v];
+        if (first) issue(unit1, buf ^ 1);
+        issue(next, buf);
+        if (warp < CB / 32) bad |= !chain_tile<false>(p, j, cb * CB + tid, tid, s);
+        if (warp == 2 && unit1 < units) borders<kTileF>(p, unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
+            break;
+        }
+        P h = L::load(&s.b[warp][lane * V]);
         if (warp * RUN % kSave == 0 && p.h_save && n > 0) {
-            if (starts & 1) load_state<V>(p.h0, start[0], p.D, ch, on, h);
-            store_state<V>(p.h_save, t / kSave, p.D, ch, on, h);
+            if (starts & 1) h = load_state<T>(p.h0, start[0], p.D, ch);
+            store_state<T>(p.h_save, t / kSave, p.D, ch, h);
         }
         uint32_t *to = word<T>(p.o, t, ch);
-        const int n_out = p.o.p && on && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
+        const int n_out = p.o.p && ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
         auto walk = [&](auto plain) {                      // plain: no borders, all tokens live
+            constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
             for (int k = 0; k < RUN; ++k) {
-                if (!decltype(plain)::value && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = fmaf(a[k * V + v], h[v], b[k * V + v]);
-                if (decltype(plain)::value ? n_out > 0 : k < n_out) *to = Lane<T>::put(h);
+                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                h = L::fma(a[k], h, b[k]);
+                if (PLAIN ? n_out > 0 : k < n_out) *to = L::put(h);
                 to += p.o.st / V;
-                if (!decltype(plain)::value && (ends >> k & 1)) store_state<V>(p.ht, end[k], p.D, ch, on, h);
+                if (!PLAIN && (ends >> k & 1)) store_state<T>(p.ht, end[k], p.D, ch, h);
             }
         };
         if (!(starts | ends) && n == RUN) walk(std::true_type());
@@ -392,214 +344,195 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const Par
         unit = unit1;
         first = false;
     }
-    stage_wait<0>();
+    drain(s.full, busy, parity);
 }
 
 // ---- backward ------------------------------------------------------------
 // As the forward, over the tiles from last to first; a tile's rows stay staged until its gradients are out, and sigmoids are
 // formed again for them (registers).  The states inside the tile come from the one saved before it.
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const Params p) {
-    constexpr int V = Lane<T>::V, CB = Lane<T>::CB, RUN = kRun, N = RUN * V, THREADS = 32 * kWarpsB, BYTES = kTileB * 128;
+__global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
+    using L = Lane<T>;
+    using P = typename L::P;
+    constexpr int V = L::V, CB = L::CB, RUN = kRun, BYTES = kTileB * 128;
     static_assert(kTileB == kSave, "one saved state a tile");
     __shared__ Shared<CB, kWarpsB> s;
     __shared__ float s_h[kWarpsB][CB], s_d[kWarpsB][CB];
     __shared__ int s_cuth[kWarpsB];
-    extern __shared__ __align__(16) uint8_t s_rows[];      // [2][r, x, d_o, i][kTileB][128]
+    extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, d_o, i][kTileB][128]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, narr = p.i.p ? 4 : 3;
     launch_dependents();                                   // (the sum of the rates' gradients waits for this grid's end)
+    if (tid == kIssuer) {
+        tc::mbar_init(&s.full[0], 1);
+        tc::mbar_init(&s.full[1], 1);
+        tc::fence_barrier_init();
+        s.err = 0;
+    }
     grid_dependency_wait();
     if (p.head->blocked) return;
     const int64_t live = p.head->live, n_live = (live + kTileB - 1) / kTileB;
     const uint32_t units = (uint32_t)(n_live * p.n_cb);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 4 : 3;
-    auto stage = [&](uint32_t unit, int buf) {
-        if (unit < units) {
-            const uint32_t seq = unit / p.n_cb;
-            const int64_t t0 = (n_live - 1 - seq) * kTileB;
-            const int cb = unit - seq * p.n_cb, n = live - t0 < kTileB ? (int)(live - t0) : kTileB;
-            uint8_t *dst = s_rows + buf * narr * BYTES;
-            stage_rows<T, kTileB, THREADS>(p, p.r, t0, n, cb, dst);
-            stage_rows<T, kTileB, THREADS>(p, p.x, t0, n, cb, dst + BYTES);
-            stage_rows<T, kTileB, THREADS>(p, p.d_o, t0, n, cb, dst + 2 * BYTES);
-            if (narr == 4) stage_rows<T, kTileB, THREADS>(p, p.i, t0, n, cb, dst + 3 * BYTES);
-        }
-        stage_commit();
+    uint32_t busy = 0, parity = 0;
+    auto issue = [&](uint32_t unit, int buf) {
+        if (unit >= units) return;
+        busy |= 1u << buf;
+        if (tid != kIssuer) return;
+        const uint32_t seq = unit / p.n_cb;
+        tc::mbar_arrive_expect_tx(&s.full[buf], narr * BYTES);
+        for (int k = 0; k < narr; ++k)
+            tc::tma_load_2d(s_rows + (buf * narr + k) * BYTES, &maps.m[k], (unit - seq * p.n_cb) * CB, (int)(n_live - 1 - seq) * kTileB, &s.full[buf]);
     };
-    if (threadIdx.x == 0) s.ticket[0] = atomicAdd(&p.head->ticket, 1u);
+    if (tid == kIssuer) s.ticket[2] = atomicAdd(&p.head->ticket, 1u);
     __syncthreads();
-    uint32_t unit = s.ticket[0];
+    uint32_t unit = s.ticket[2];
     if (unit >= units) return;
-    stage(unit, 0);
-    if (warp == 1) borders<kTileB>(p, n_live - 1 - unit / p.n_cb, s.start[0], s.end[0]);
+    issue(unit, 0);
+    if (warp == 2) borders<kTileB>(p, n_live - 1 - unit / p.n_cb, s.start[0], s.end[0]);
+    __syncthreads();
     for (int buf = 0; unit < units; buf ^= 1) {
-        stage_wait<0>();
-        __syncthreads();
-        uint32_t taken = 0;
-        if (threadIdx.x == 32) taken = atomicAdd(&p.head->ticket, 1u);
         const uint32_t seq = unit / p.n_cb;
         const int64_t j = n_live - 1 - seq, t = j * kTileB + warp * RUN;
         const int cb = unit - seq * p.n_cb, ch = cb * CB + lane * V;
         const int n = live - t < RUN ? (int)(live - t) : RUN;            // live tokens of the warp (none: <= 0)
-        const bool on = ch < p.D;
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
-        auto row = [&](int arr, int k, float *v) { Lane<T>::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128), v); };
-        float rate[V], a[N], m[N], before[V];
-        load_state<V>(p.kind.rate, 0, p.D, ch, on && p.kind.decay == GCL_DECAY_POWER, rate);
-        if (warp == 1) load_state<V>(p.h_save, j, p.D, ch, on, before);
-        {
-            float r[N];
+        auto row = [&](int arr, int k) { return L::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128)); };
+        const P rate = load_state<T>(p.kind.decay == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, p.D, ch);
+        const bool near = __all_sync(0xffffffffu, L::every(rate, [](float v) { return v >= 0.f && v <= kNear; }));
+        P before = L::all(0.f);
+        if (warp == 3) before = load_state<T>(p.h_save, j, p.D, ch);
+        bool bad = !tc::mbar_wait(&s.full[buf], parity >> buf & 1, &s.err, GCL_DEV_WAIT_TIMEOUT);
+        busy &= ~(1u << buf);
+        parity ^= 1u << buf;
+        uint32_t taken = 0;
+        if (tid == kIssuer) taken = atomicAdd(&p.head->ticket, 1u);
+        P a[RUN], m[RUN], prev[RUN];                       // prev: b = m u, later the state before each token
 #pragma unroll
-            for (int k = 0; k < RUN; ++k) row(0, k, r + k * V);
-            decays<T, N>(p.kind, rate, r, a, m);
-            mixes<T, N>(p.kind, a, m);
-        }
+        for (int k = 0; k < RUN; ++k) m[k] = row(0, k);
+        decays<T, RUN>(p.kind, rate, near, a, m);
         if (n < RUN)
 #pragma unroll
             for (int k = 0; k < RUN; ++k)
-                if (k >= n)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) { a[k * V + v] = 1.f; m[k * V + v] = 0.f; }
+                if (k >= n) { a[k] = L::all(1.f); m[k] = L::all(0.f); }
         const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
         const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && start[lane % RUN] >= 0);
         const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && end[lane % RUN] >= 0);
-        float prev[N];                                     // b = m u, then the state before each token
+        const bool edge = (starts | ends) || n < RUN;
         {
-            float A[V], h[V], c[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) { A[v] = 1.f; h[v] = c[v] = 0.f; }
+            P A = L::all(1.f), h = L::all(0.f), c = L::all(0.f);
             auto walk = [&](auto cut) {
+                constexpr bool CUT = decltype(cut)::value;
 #pragma unroll
                 for (int k = 0; k < RUN; ++k) {
-                    float x[V], g[V];
-                    row(1, k, x);
-                    if (narr == 4) row(3, k, g);
-                    if (decltype(cut)::value && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        prev[k * V + v] = m[k * V + v] * (narr == 4 ? x[v] * sigmoid<T>(g[v]) : x[v]);
-                        h[v] = fmaf(a[k * V + v], h[v], prev[k * V + v]);
-                        A[v] *= a[k * V + v];
-                    }
+                    if (CUT && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                    prev[k] = L::mul(m[k], row(1, k));
+                    if (narr == 4) prev[k] = L::mul(prev[k], sigmoid<T>(row(3, k)));
+                    if (CUT && k >= n) prev[k] = L::all(0.f);
+                    h = L::fma(a[k], h, prev[k]);
+                    A = L::mul(A, a[k]);
                 }
 #pragma unroll
                 for (int k = RUN - 1; k >= 0; --k) {
-                    float go[V];
-                    row(2, k, go);
-                    if (decltype(cut)::value && (ends >> k & 1)) load_state<V>(p.dht, end[k], p.D, ch, on, c);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) c[v] = a[k * V + v] * (go[v] + c[v]);
+                    if (CUT && (ends >> k & 1)) c = load_state<T>(p.dht, end[k], p.D, ch);
+                    c = L::mul(a[k], L::add(CUT && k >= n ? L::all(0.f) : row(2, k), c));
                 }
             };
-            if (starts | ends) walk(std::true_type());
+            if (edge) walk(std::true_type());
             else walk(std::false_type());
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s.a[warp][lane * V + v] = A[v];
-                s.b[warp][lane * V + v] = c[v];
-                s_h[warp][lane * V + v] = h[v];
-            }
+            L::store(&s.a[warp][lane * V], A);
+            L::store(&s.b[warp][lane * V], c);
+            L::store(&s_h[warp][lane * V], h);
             if (lane == 0) { s.cut[warp] = ends != 0; s_cuth[warp] = starts != 0; }
         }
-        if (threadIdx.x == 32) s.ticket[0] = taken;
+        if (tid == kIssuer) s.ticket[0] = taken;
         __syncthreads();
         const uint32_t unit1 = s.ticket[0];
-        stage(unit1, buf ^ 1);
-        if (warp == 0) {
-            chain_tile<V, kWarpsB, CB, true>(p, seq, cb, ch, on, s.a, s.b, s.cut);
-        } else if (warp == 1) {                            // the states that enter the warps' tokens
+        issue(unit1, buf ^ 1);
+        if (warp < CB / 32) {
+            bad |= !chain_tile<true>(p, seq, cb * CB + tid, tid, s);
+        } else if (warp == 3) {                            // the states that enter the warps' tokens
 #pragma unroll
-            for (int w = 0; w < kWarpsB; ++w)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float b = s_h[w][lane * V + v], A = s.a[w][lane * V + v];
-                    s_h[w][lane * V + v] = before[v];
-                    before[v] = s_cuth[w] ? b : fmaf(A, before[v], b);
-                }
-            if (unit1 < units) borders<kTileB>(p, n_live - 1 - unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
+            for (int w = 0; w < kWarpsB; ++w) {
+                const P b = L::load(&s_h[w][lane * V]), A = L::load(&s.a[w][lane * V]);
+                L::store(&s_h[w][lane * V], before);
+                before = s_cuth[w] ? b : L::fma(A, before, b);
+            }
+        } else if (warp == 2 && unit1 < units) {
+            borders<kTileB>(p, n_live - 1 - unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
         }
-        __syncthreads();
-        float h[V], c[V], dsum[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) { h[v] = s_h[warp][lane * V + v]; c[v] = s.b[warp][lane * V + v]; dsum[v] = 0.f; }
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
+            break;
+        }
+        P h = L::load(&s_h[warp][lane * V]), c = L::load(&s.b[warp][lane * V]), dsum = L::all(0.f);
         const int64_t last = t + RUN - 1;
         uint32_t *to_x = word<T>(p.dx, last, ch), *to_r = word<T>(p.dr, last, ch), *to_i = word<T>(p.di, last, ch);
-        const int n_out = on && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
+        const int n_out = ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
         auto walk = [&](auto plain) {                      // plain: no borders, all tokens live
             constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
             for (int k = 0; k < RUN; ++k) {
-                if (!PLAIN && (starts >> k & 1)) load_state<V>(p.h0, start[k], p.D, ch, on, h);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float b = prev[k * V + v];
-                    prev[k * V + v] = h[v];
-                    h[v] = fmaf(a[k * V + v], h[v], b);
-                }
+                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                const P b = prev[k];
+                prev[k] = h;
+                h = L::fma(a[k], h, b);
             }
 #pragma unroll
             for (int k = RUN - 1; k >= 0; --k) {
-                if (!PLAIN && (ends >> k & 1)) load_state<V>(p.dht, end[k], p.D, ch, on, c);
-                float dx[V], dr[V], di[V], x[V], g[V], go[V], r[V];
-                row(0, k, r);
-                row(1, k, x);
-                row(2, k, go);
-                if (narr == 4) row(3, k, g);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int e = k * V + v;
-                    const float G = go[v] + c[v];
-                    c[v] = a[e] * G;
-                    float sg = 1.f, ng = 0.f;
-                    if (narr == 4) sigmoids<T>(g[v], sg, ng);
-                    const float u = x[v] * sg;
-                    dx[v] = G * m[e] * sg;
-                    di[v] = dx[v] * x[v] * ng;
-                    float dl = c[v] * prev[e];
-                    if (p.kind.mix == GCL_MIX_COMPLEMENT) dl = fmaf(-c[v], u, dl);
-                    else if (p.kind.mix == GCL_MIX_ROOT) dl = fmaf(m[e] > 0.f ? -a[e] * frcp<T>(m[e]) * c[v] : 0.f, u, dl);
-                    if (p.kind.decay != GCL_DECAY_LOG) {
-                        float sr, nr;
-                        sigmoids<T>(r[v], sr, nr);
-                        if (p.kind.decay == GCL_DECAY_SIGMOID) {
-                            dl *= nr;
-                        } else {
-                            if (PLAIN || k < n) dsum[v] = fmaf(-dl, sr, dsum[v]);
-                            dl *= -rate[v] * sr * nr;
-                        }
+                if (!PLAIN && (ends >> k & 1)) c = load_state<T>(p.dht, end[k], p.D, ch);
+                const P x = row(1, k), G = L::add(row(2, k), c), Gm = L::mul(G, m[k]);
+                c = L::mul(a[k], !PLAIN && k >= n ? c : G);
+                P dx = Gm, di = L::all(0.f), u = x, sg, ng;
+                if (narr == 4) {
+                    sigmoids<T>(row(3, k), sg, ng);
+                    dx = L::mul(Gm, sg);
+                    di = L::mul(L::mul(dx, x), ng);
+                    u = L::mul(x, sg);
+                }
+                P dl = L::mul(c, prev[k]);
+                if (p.kind.mix == GCL_MIX_COMPLEMENT) {
+                    dl = L::fma(L::mul(c, L::all(-1.f)), u, dl);
+                } else if (p.kind.mix == GCL_MIX_ROOT) {   // c (prev - u a / m), the second term 0 where m is
+                    const P q = L::map(L::mul(a[k], L::all(-1.f)), m[k], [](float a, float m) { return m > 0.f ? a * frcp<T>(m) : 0.f; });
+                    dl = L::mul(c, L::fma(q, u, prev[k]));
+                }
+                P dr = dl;
+                if (p.kind.decay != GCL_DECAY_LOG) {
+                    P sr, nr;
+                    sigmoids<T>(row(0, k), sr, nr);
+                    if (p.kind.decay == GCL_DECAY_SIGMOID) {
+                        dr = L::mul(dl, nr);
+                    } else {
+                        const P part = L::mul(L::mul(dl, L::all(-1.f)), sr);
+                        if (PLAIN || k < n) dsum = L::add(dsum, part);
+                        dr = L::mul(L::mul(part, rate), nr);
                     }
-                    dr[v] = dl;
                 }
                 if (PLAIN ? n_out > 0 : k < n_out) {
-                    *to_x = Lane<T>::put(dx);
-                    *to_r = Lane<T>::put(dr);
-                    if (narr == 4) *to_i = Lane<T>::put(di);
+                    *to_x = L::put(dx);
+                    *to_r = L::put(dr);
+                    if (narr == 4) *to_i = L::put(di);
                 }
                 to_x -= p.dx.st / V;
                 to_r -= p.dr.st / V;
                 to_i -= p.di.st / V;
-                if (!PLAIN && (starts >> k & 1)) store_state<V>(p.dh0, start[k], p.D, ch, on, c);
+                if (!PLAIN && (starts >> k & 1)) store_state<T>(p.dh0, start[k], p.D, ch, c);
             }
         };
-        if (!(starts | ends) && n == RUN) walk(std::true_type());
+        if (!edge) walk(std::true_type());
         else walk(std::false_type());
         if (p.drate_part) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) s_d[warp][lane * V + v] = dsum[v];
+            L::store(&s_d[warp][lane * V], dsum);
             __syncthreads();
-            if (warp == 2) {
+            if (warp == 4) {
+                P sum = L::all(0.f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kWarpsB; ++w) sum += s_d[w][lane * V + v];
-                    dsum[v] = sum;
-                }
-                store_state<V>(p.drate_part, j, p.D, ch, on, dsum);
+                for (int w = 0; w < kWarpsB; ++w) sum = L::add(sum, L::load(&s_d[w][lane * V]));
+                store_state<T>(p.drate_part, j, p.D, ch, sum);
             }
         }
         unit = unit1;
     }
-    stage_wait<0>();
+    drain(s.full, busy, parity);
 }
 
 // drate from the tiles' sums, in a fixed order: 32 channels a block, 32 rows of threads over the tiles, eight loads of
@@ -651,12 +584,8 @@ size_t layout(const gcl_glr_args *a, bool backward, Params *p) {
     const int64_t tiles = backward ? tb : tf;
     const size_t row = sizeof(float) * (size_t)a->D;
     set(o.head, sizeof(Header));
-    const int64_t n_cb = (a->D * (a->dtype == GCL_F32 ? 4 : 2) + 127) / 128;
     set(o.first, sizeof(int32_t) * (size_t)tiles);
-    set(o.chain.flag, sizeof(int32_t) * (size_t)(tiles * n_cb));
-    set(o.chain.a, row * tiles);
-    set(o.chain.own, row * tiles);
-    set(o.chain.out, row * tiles);
+    set(o.chain, sizeof(Packet) * (size_t)a->D * tiles);
     if (backward) {
         if (a->drate) set(o.drate_part, row * tiles);
         if (!a->h_save) set(o.h_save, row * tb);
@@ -664,28 +593,46 @@ size_t layout(const gcl_glr_args *a, bool backward, Params *p) {
     return at;
 }
 
+// Tensor map of rows [t_max, D]: a tile by a warp's width of channels.
+template <typename T>
+bool rows_map(CUtensorMap *m, const Params &p, const Rows &r, int tile) {
+    const cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.t_max}, strides[1] = {(cuuint64_t)r.st * sizeof(T)};
+    const cuuint32_t box[2] = {(cuuint32_t)Lane<T>::CB, (cuuint32_t)tile};
+    const CUtensorMapDataType dt = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return make_tensor_map(m, r.p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, dt);
+}
+
 // Launches the set-up and, as its dependent, `kernel` with at most `ctas` blocks an SM.
-template <typename K>
-cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float *out_state, int tile, int threads, int ctas, size_t smem,
-                         cudaStream_t s) {
+template <typename T, typename K>
+cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float *out_state, int tile, int threads, int ctas, cudaStream_t s) {
+    Maps maps;
+    const Rows *rows[4] = {&p.r, &p.x, &p.d_o, &p.i};
+    int n = 0;
+    for (int k = 0; k < 4; ++k)
+        if (rows[k]->p) {
+            if (!rows_map<T>(&maps.m[k], p, *rows[k], tile)) return cudaErrorInvalidValue;
+            ++n;
+        }
+    const size_t smem = (size_t)2 * n * tile * 128;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t units = p.tiles * p.n_cb, most = (int64_t)ctas * num_sms();
-    int64_t setup = (units + 4095) / 4096;
+    int64_t setup = (p.tiles * p.D + 4095) / 4096;
     if (out_state && setup < (p.n_max + 7) / 8) setup = (p.n_max + 7) / 8;
     if (setup > num_sms()) setup = num_sms();
     glr_setup_kernel<<<(unsigned)setup, 1024, 0, s>>>(p, in_state, out_state, tile);
-    return launch_dependent(kernel, dim3((unsigned)(units < most ? units : most)), dim3(threads), smem, s, p);
+    return launch_dependent(kernel, dim3((unsigned)(units < most ? units : most)), dim3(threads), smem, s, maps, p);
 }
 
 template <typename T>
 cudaError_t launch_fwd(const Params &p, cudaStream_t s) {
-    return launch_tiles(glr_fwd_kernel<T>, p, p.h0, p.ht, kTileF, 32 * kWarpsF, kCtasF, (size_t)2 * (p.i.p ? 3 : 2) * kTileF * 128, s);
+    return launch_tiles<T>(glr_fwd_kernel<T>, p, p.h0, p.ht, kTileF, 32 * kWarpsF, kCtasF, s);
 }
 
 template <typename T>
 cudaError_t launch_bwd(const Params &p, cudaStream_t s) {
-    const cudaError_t e = launch_tiles(glr_bwd_kernel<T>, p, p.dht, p.dh0, kTileB, 32 * kWarpsB, kCtasB, (size_t)2 * (p.i.p ? 4 : 3) * kTileB * 128, s);
+    const cudaError_t e = launch_tiles<T>(glr_bwd_kernel<T>, p, p.dht, p.dh0, kTileB, 32 * kWarpsB, kCtasB, s);
     if (e != cudaSuccess || !p.drate) return e;
     return launch_dependent(glr_drate_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, p, kTileB);
 }
@@ -699,7 +646,7 @@ cudaError_t launch(const gcl_glr_args *a, Params p, bool backward, cudaStream_t 
         layout(a, true, &f);
         f.tiles = (p.t_max + kTileF - 1) / kTileF;
         f.ht = nullptr;
-        f.o.p = nullptr;
+        f.o.p = f.d_o.p = nullptr;
         const cudaError_t e = launch_fwd<T>(f, s);
         if (e != cudaSuccess) return e;
     }

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "dla.cuh"
+#include "f32x2.cuh"
 
 namespace gcl {
 namespace glr {
@@ -15,41 +16,14 @@ struct Kind {                      // which a, m and u
     int32_t decay, mix;
 };
 
-// A lane's consecutive channels of a row: four bytes, so that a warp takes 128.
-template <typename T>
-struct Lane {
-    static constexpr int V = 4 / sizeof(T);
-    static constexpr int CB = 32 * V;                  // channels of a warp
-    static __device__ __forceinline__ void get(uint32_t w, float *v) {
-        if constexpr (V == 1) {
-            v[0] = __uint_as_float(w);
-        } else {
-            const T *h = reinterpret_cast<const T *>(&w);
-            v[0] = (float)h[0];
-            v[1] = (float)h[1];
-        }
-    }
-    static __device__ __forceinline__ uint32_t put(const float *v) {
-        if constexpr (V == 1) {
-            return __float_as_uint(v[0]);
-        } else {
-            uint32_t w;
-            T *h = reinterpret_cast<T *>(&w);
-            h[0] = (T)v[0];
-            h[1] = (T)v[1];
-            return w;
-        }
-    }
-};
-
-// exp, 1 / x and the square root: the accurate ones for fp32 rows; for 16-bit rows, whose own rounding is 2^13 ulp, the
+// exp and 1 / x: the accurate ones for fp32 rows; for 16-bit rows, whose own rounding is 2^13 ulp, the
 // special-function unit's, off by a few ulp.  (Flushing subnormals: without it each takes three instructions more, 40 of
 // the forward's 108 a value.)
 template <typename T>
-__device__ __forceinline__ float fexp(float x) {
+__device__ __forceinline__ float fexp2(float x) {          // 2^x; fp32 rows: e^x
     if (sizeof(T) == 4) return expf(x);
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 template <typename T>
@@ -60,77 +34,183 @@ __device__ __forceinline__ float frcp(float x) {
     return y;
 }
 template <typename T>
-__device__ __forceinline__ float root(float x) {
-    x = fmaxf(x, 0.f);
+__device__ __forceinline__ float froot(float x) {
     if (sizeof(T) == 4) return sqrtf(x);
     float y;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// sigmoid(x) and sigmoid(-x), neither by a difference.
+// A lane's channels of a row, four bytes: two values of 16 bits, held as a pair whose arithmetic is one instruction,
+// or one of fp32.  A warp takes 128 bytes of the row.
 template <typename T>
-__device__ __forceinline__ void sigmoids(float x, float &s, float &c) {
-    const float e = fexp<T>(-fabsf(x)), hi = frcp<T>(1.f + e), lo = e * hi;
-    s = x >= 0.f ? hi : lo;
-    c = x >= 0.f ? lo : hi;
-}
-
-// sigmoid(x) alone.  (exp(-x) = infinity gives 0.)
-template <typename T>
-__device__ __forceinline__ float sigmoid(float x) { return frcp<T>(1.f + fexp<T>(-x)); }
-
-// a = exp(l) and q = 1 - a.  Near l = 0 the difference loses q's digits and the fast exp's error, some units of
-// 2^-24 with one sign, would add up over all the tokens that a close to 1 remembers: for 0 <= y = -l < 0.7 q is
-// y P(y), P the polynomial of degree 5 that meets (1 - exp(-y)) / y at the Chebyshev points of [0, 0.7] (off by 1.2e-8 of
-// its value), and a = 1 - q, rounded once.
-template <typename T>
-__device__ __forceinline__ void exps(float l, float &a, float &q) {
-    a = fexp<T>(l);
-    if (sizeof(T) == 4) {
-        q = -expm1f(l);
-        return;
+struct Lane {
+    static constexpr int V = 2;
+    static constexpr int CB = 64;                          // channels of a warp
+    using P = uint64_t;
+    static __device__ __forceinline__ P get(uint32_t w) {
+        const T *h = reinterpret_cast<const T *>(&w);
+        return pair((float)h[0], (float)h[1]);
     }
-    const float y = -l;
-    float s = fmaf(y, -1.0332434e-3f, 8.0679525e-3f);
-    s = fmaf(y, s, -4.1572765e-2f);
-    s = fmaf(y, s, 1.6665146e-1f);
-    s = fmaf(y, s, -4.9999911e-1f);
-    s = fmaf(y, s, 1.f);
-    const bool near = __float_as_uint(y) < __float_as_uint(0.7f);          // (y < 0 and NaN have larger bits)
-    q = near ? y * s : 1.f - a;
-    a = near ? 1.f - q : a;
+    static __device__ __forceinline__ uint32_t put(P x) {
+        const float2 f = unpair(x);
+        uint32_t w;
+        T *h = reinterpret_cast<T *>(&w);
+        h[0] = (T)f.x;
+        h[1] = (T)f.y;
+        return w;
+    }
+    static __device__ __forceinline__ P all(float x) { return pair(x, x); }
+    static __device__ __forceinline__ P load(const float *p) {
+        const float2 f = *reinterpret_cast<const float2 *>(p);
+        return pair(f.x, f.y);
+    }
+    static __device__ __forceinline__ void store(float *p, P x) { *reinterpret_cast<float2 *>(p) = unpair(x); }
+    static __device__ __forceinline__ P mul(P a, P b) { return mul2(a, b); }
+    static __device__ __forceinline__ P add(P a, P b) { return add2(a, b); }
+    static __device__ __forceinline__ P fma(P a, P b, P c) { return fma2(a, b, c); }
+    template <typename F>
+    static __device__ __forceinline__ P map(P x, F f) {
+        const float2 v = unpair(x);
+        return pair(f(v.x), f(v.y));
+    }
+    template <typename F>
+    static __device__ __forceinline__ P map(P x, P y, F f) {
+        const float2 v = unpair(x), w = unpair(y);
+        return pair(f(v.x, w.x), f(v.y, w.y));
+    }
+    template <typename F>
+    static __device__ __forceinline__ P map(P x, P y, P z, F f) {
+        const float2 u = unpair(x), v = unpair(y), w = unpair(z);
+        return pair(f(u.x, v.x, w.x), f(u.y, v.y, w.y));
+    }
+    template <typename F>
+    static __device__ __forceinline__ bool every(P x, F f) {
+        const float2 v = unpair(x);
+        return f(v.x) && f(v.y);
+    }
+};
+template <>
+struct Lane<float> {
+    static constexpr int V = 1;
+    static constexpr int CB = 32;
+    using P = float;
+    static __device__ __forceinline__ P get(uint32_t w) { return __uint_as_float(w); }
+    static __device__ __forceinline__ uint32_t put(P x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ P all(float x) { return x; }
+    static __device__ __forceinline__ P load(const float *p) { return *p; }
+    static __device__ __forceinline__ void store(float *p, P x) { *p = x; }
+    static __device__ __forceinline__ P mul(P a, P b) { return a * b; }
+    static __device__ __forceinline__ P add(P a, P b) { return a + b; }
+    static __device__ __forceinline__ P fma(P a, P b, P c) { return fmaf(a, b, c); }
+    template <typename F>
+    static __device__ __forceinline__ P map(P x, F f) { return f(x); }
+    template <typename F>
+    static __device__ __forceinline__ P map(P x, P y, F f) { return f(x, y); }
+    template <typename F>
+    static __device__ __forceinline__ P map(P x, P y, P z, F f) { return f(x, y, z); }
+    template <typename F>
+    static __device__ __forceinline__ bool every(P x, F f) { return f(x); }
+};
+
+// e^x of each value.
+template <typename T>
+__device__ __forceinline__ typename Lane<T>::P exps(typename Lane<T>::P x) {
+    if (sizeof(T) == 2) x = Lane<T>::mul(x, Lane<T>::all(1.4426950408889634f));
+    return Lane<T>::map(x, [](float v) { return fexp2<T>(v); });
+}
+// sigmoid(x).  (exp(-x) = infinity gives 0.)
+template <typename T>
+__device__ __forceinline__ typename Lane<T>::P sigmoid(typename Lane<T>::P x) {
+    using L = Lane<T>;
+    if (sizeof(T) == 2) x = L::map(L::mul(x, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(v); });
+    else x = L::map(x, [](float v) { return fexp2<T>(-v); });
+    return L::map(L::add(x, L::all(1.f)), [](float v) { return frcp<T>(v); });
+}
+// sigmoid(x) and sigmoid(-x) = exp(-x) sigmoid(x), neither by a difference.
+template <typename T>
+__device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>::P &s, typename Lane<T>::P &c) {
+    using L = Lane<T>;
+    typename L::P e;
+    if (sizeof(T) == 2) e = L::map(L::mul(x, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(fminf(v, 126.f)); });
+    else e = L::map(x, [](float v) { return fexp2<T>(fminf(-v, 87.f)); });
+    s = L::map(L::add(e, L::all(1.f)), [](float v) { return frcp<T>(v); });
+    c = L::mul(e, s);
 }
 
-// a and q = 1 - a of N values of r (N / V tokens of the lane's V channels); the kind is the same for the grid.
+// q = 1 - exp(-y) for 0 <= y <= kNear: y P(y), P the polynomial of degree 6 that meets (1 - exp(-y)) / y at the Chebyshev points
+// of [0, 0.9] (off by 5e-9 of its value).
+constexpr float kNear = 0.9f;
+template <typename T>
+__device__ __forceinline__ typename Lane<T>::P one_minus_exp(typename Lane<T>::P y) {
+    using L = Lane<T>;
+    typename L::P s = L::fma(y, L::all(1.3465580e-4f), L::all(-1.3153803e-3f));
+    s = L::fma(y, s, L::all(8.2897432e-3f));
+    s = L::fma(y, s, L::all(-4.1653194e-2f));
+    s = L::fma(y, s, L::all(1.6666466e-1f));
+    s = L::fma(y, s, L::all(-4.9999988e-1f));
+    s = L::fma(y, s, L::all(1.f));
+    return L::mul(y, s);
+}
+
+// a = exp(-y) and q = 1 - a of N values y.  16-bit rows: the difference loses q's digits near y = 0, and the fast exp's error,
+// some units of 2^-24 with one sign, would add up over all the tokens that a close to 1 remembers: there a = 1 - q from the
+// polynomial, rounded once.  NEAR: all y lie in [0, kNear].
+template <typename T, bool NEAR, int N>
+__device__ __forceinline__ void decay_of(typename Lane<T>::P *a, typename Lane<T>::P *q) {
+    using L = Lane<T>;
+    using P = typename L::P;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const P y = q[e];
+        if (sizeof(T) == 4) {
+            a[e] = L::map(y, [](float v) { return expf(-v); });
+            q[e] = L::map(y, [](float v) { return -expm1f(-v); });
+        } else if (NEAR) {
+            q[e] = one_minus_exp<T>(y);
+            a[e] = L::fma(q[e], L::all(-1.f), L::all(1.f));
+        } else {
+            const P far = L::map(L::mul(y, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(v); });
+            auto pick = [](float v, float n, float f) {    // (y < 0 and NaN have larger bits)
+                return __float_as_uint(v) <= __float_as_uint(kNear) ? n : f;
+            };
+            q[e] = L::map(y, one_minus_exp<T>(y), L::fma(far, L::all(-1.f), L::all(1.f)), pick);
+            a[e] = L::map(y, L::fma(q[e], L::all(-1.f), L::all(1.f)), far, pick);
+        }
+    }
+}
+
+// a and m(a) of N tokens' gates r, which are in m; the kind is the same for the grid.  rate: of the lane's channels;
+// near: all the warp's rates lie in [0, kNear].
 template <typename T, int N>
-__device__ __forceinline__ void decays(const Kind &k, const float *rate, const float *r, float *a, float *q) {
-    constexpr int V = Lane<T>::V;
+__device__ __forceinline__ void decays(const Kind &k, typename Lane<T>::P rate, bool near, typename Lane<T>::P *a, typename Lane<T>::P *m) {
+    using L = Lane<T>;
     if (k.decay == GCL_DECAY_SIGMOID) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) sigmoids<T>(r[e], a[e], q[e]);
+        for (int e = 0; e < N; ++e) {
+            typename L::P s;
+            sigmoids<T>(m[e], s, m[e]);
+            a[e] = s;
+        }
     } else if (k.decay == GCL_DECAY_POWER) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            exps<T>(-rate[e % V] * sigmoid<T>(r[e]), a[e], q[e]);
-        }
+        for (int e = 0; e < N; ++e) m[e] = L::mul(rate, sigmoid<T>(m[e]));
+        if (sizeof(T) == 2 && near) decay_of<T, true, N>(a, m);
+        else decay_of<T, false, N>(a, m);
     } else {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            exps<T>(r[e], a[e], q[e]);
-        }
+        for (int e = 0; e < N; ++e) m[e] = L::mul(m[e], L::all(-1.f));
+        decay_of<T, false, N>(a, m);
     }
-}
-
-// m(a) in place of q = 1 - a.
-template <typename T, int N>
-__device__ __forceinline__ void mixes(const Kind &k, const float *a, float *q) {
     if (k.mix == GCL_MIX_ONE) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) q[e] = 1.f;
-    } else if (k.mix == GCL_MIX_ROOT) {                // 1 - a^2 = (1 - a) (1 + a)
+        for (int e = 0; e < N; ++e) m[e] = L::all(1.f);
+    } else if (k.mix == GCL_MIX_ROOT) {                    // 1 - a^2 = (1 - a) (1 + a); a > 1 counts as 1
+        if (k.decay == GCL_DECAY_LOG)
 #pragma unroll
-        for (int e = 0; e < N; ++e) q[e] = root<T>(q[e] * (1.f + a[e]));
+            for (int e = 0; e < N; ++e) m[e] = L::map(m[e], [](float v) { return fmaxf(v, 0.f); });
+#pragma unroll
+        for (int e = 0; e < N; ++e) m[e] = L::map(L::fma(m[e], a[e], m[e]), [](float v) { return froot<T>(v); });
     }
 }
 
@@ -142,13 +222,13 @@ struct Header {
     int32_t pad;
 };
 
-// The states between tiles, by tile in the order of the recurrence and block of channels.
-struct Chain {
-    int32_t *flag;                 // [n_cb, tiles]: 0, kOwn (a and own are there), kDone (out is there)
-    float *a, *own;                // [tiles, D]: product of the tile's decays, its state from zero
-    float *out;                    // [tiles, D]: the state that leaves the tile
+// What tiles leave each other, a packet a channel of 16 bytes that is written and read as one: the product of the tile's decays
+// and its state from zero (tag kOwn), and the state that leaves it (tag kDone).
+struct __align__(16) Packet {
+    float a, own, out;
+    uint32_t tag;
 };
-constexpr int32_t kOwn = 1, kDone = 2;
+constexpr uint32_t kOwn = 1, kDone = 2;
 
 struct Params {
     Rows x, r, i, o, d_o, dx, dr, di;
@@ -159,7 +239,7 @@ struct Params {
     int32_t *status;
     Header *head;
     int32_t *first;                // [tiles]: the first sequence that starts at or behind the tile's first token
-    Chain chain;
+    Packet *chain;                 // [tiles, D], in the order of the recurrence
     float *drate_part;             // [tiles, D]
     int64_t t_max, tiles;
     int32_t n_max, D, n_cb;        // n_cb: blocks of channels

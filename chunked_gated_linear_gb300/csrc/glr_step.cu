@@ -43,22 +43,32 @@ __global__ void __launch_bounds__(kStepThreads) glr_step_kernel(const StepParams
     }
     if (!GCL_RANGE_IN_BOUNDS(slot * p.D + ch, slot * p.D + ch + 7, (int64_t)p.n_slots * p.D, p.status)) return;
     float *st = p.state + slot * p.D + ch;
-    float h[8], x[8], r[8], g[8], rate[8], a[8], m[8];
-    dla::load8f(st, h);
-    dla::load8f(dla::row_ptr<const T>(p.x, b, 0) + ch, x);
-    dla::load8f(dla::row_ptr<const T>(p.r, b, 0) + ch, r);
-    if (p.i.p) dla::load8f(dla::row_ptr<const T>(p.i, b, 0) + ch, g);
-    if (p.kind.decay == GCL_DECAY_POWER) dla::load8f(p.kind.rate + ch, rate);
+    using L = Lane<T>;
+    constexpr int N = 8 / V;                               // words of eight channels
+    __align__(8) float h[8];
+    typename L::P x[N], m[N], g[N], rate[N], a[N];
+    auto load = [&](const Rows &r, typename L::P *v) {
+        const T *q = dla::row_ptr<const T>(r, b, 0) + ch;
+        uint4 w[sizeof(T) / 2];
 #pragma unroll
-    for (int k = 0; k < 8; k += V) {
-        decays<T, V>(p.kind, rate + k, r + k, a + k, m + k);
-        mixes<T, V>(p.kind, a + k, m + k);
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = reinterpret_cast<const uint4 *>(q)[k];
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = L::get(reinterpret_cast<const uint32_t *>(w)[k]);
+    };
+    dla::load8f(st, h);
+    load(p.x, x);
+    load(p.r, m);
+    if (p.i.p) load(p.i, g);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        rate[k] = L::all(0.f);
+        if (p.kind.decay == GCL_DECAY_POWER) rate[k] = L::load(p.kind.rate + ch + k * V);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float s = 1.f, c;
-        if (p.i.p) sigmoids<T>(g[k], s, c);
-        h[k] = fmaf(a[k], h[k], m[k] * (x[k] * s));
+    for (int k = 0; k < N; ++k) {
+        decays<T, 1>(p.kind, rate[k], false, a + k, m + k);
+        if (p.i.p) x[k] = L::mul(x[k], sigmoid<T>(g[k]));
+        L::store(h + k * V, L::fma(a[k], L::load(h + k * V), L::mul(m[k], x[k])));
     }
     dla::store4f(st, h);
     dla::store4f(st + 4, h + 4);
