@@ -1,15 +1,15 @@
 // glr.cu -- gated linear recurrence over packed sequences: forward and backward.
 //
-// A tile is kTile tokens of the packed axis by the 128 bytes of a warp's width of channels; each of its warps walks kRun
-// tokens.  The sequences need no plan of their own: a token that starts one takes its state from h0, whatever
-// was before.  One pass: blocks take tiles in the order of the recurrence (a counter), form a tile's product of decays and its
-// state from zero, publish both, and take the state that enters from the tile before, or from an earlier one and the products and
-// own states between; the sum is folded from the oldest on, so the result is the same whichever tile had its state
-// ready.  A block waits for tiles with lower tickets alone, whose blocks run already, so the first of them
-// never waits: the launch ends whatever else runs on the GPU.  (Three launches -- own states, their scan, outputs -- read
-// x, r and i twice: 65,536 tokens of 2,048 channels 1,424 us.)
-// The wait for the state before is what a tile spends longest on, so the tiles meet in packets of 16 bytes, values and tag in one
-// access (flags with a fence before and loads behind them: 514 us at that size).
+// The packed axis is cut into tiles of some tokens by the 128 bytes of a warp's width of channels; each warp of a block walks
+// kRun tokens of a tile.  The sequences need no plan of their own: a token that starts one takes its state from h0,
+// whatever was before.  One pass: a cluster of kRanks blocks takes kRanks consecutive tiles of the same channels (a span), in the
+// order of the recurrence (a counter).  Its blocks form their tiles' products of decays and states from zero, exchange them
+// through shared memory, and take the state that enters the span from the span before, or from an earlier one and the products and
+// own states between; the sum is folded from the oldest on, so the result is the same whichever span had its state ready.
+// A cluster waits for spans with lower numbers alone, whose clusters run already, so the first of them never waits: the
+// launch ends whatever else runs on the GPU.
+// The wait for the state before is what a tile spends longest on: spans meet in packets of 16 bytes, values and tag in one access
+// (XCHAIN).
 // Backwards from the states before each 64 tokens (saved by the forward, or formed again): with c_t = a_t G_t the gradient that
 // token t passes on,
 //   G_t = d_o_t + c_{t+1},   c_t = a_t G_t,
@@ -23,13 +23,15 @@ namespace gcl {
 namespace glr {
 namespace {
 
-// Forward: 128 tokens, 16 warps of 8.  Backward: 64 tokens, 8 warps of 8.
-constexpr int kRun = 8;
-constexpr int kWarpsF = 16, kWarpsB = 8, kTileF = kWarpsF * kRun, kTileB = kWarpsB * kRun;
+constexpr int kRun = 8;                                // tokens of a warp
+constexpr int kRanks = 4;                              // blocks of a cluster
+constexpr int kWarpsF = 16, kWarpsB = 8;               // warps of a block; a tile has kRun tokens for each
+constexpr int kTileF = kWarpsF * kRun, kTileB = kWarpsB * kRun;
 constexpr int kCtasF = 2, kCtasB = 3;                  // resident blocks an SM
+static_assert(kWarpsB * kRun == kSave && kWarpsF * kRun % kSave == 0, "saved states lie at tiles' starts");
 
 // ---- set-up: checks cu_seqlens, finds each tile's first sequence, passes states of empty sequences through, clears the
-// packets of the tiles that will be taken ----
+// packets of the spans that will be taken ----
 __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const float *in_state, float *out_state, int tile) {
     launch_dependents();
     const int tid = threadIdx.x;
@@ -48,8 +50,8 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const f
     }
     if (blocked || bad) return;
     const int64_t at = blockIdx.x * (int64_t)blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
-    const int64_t packets = ((int64_t)p.cu[p.n_max] + tile - 1) / tile * p.D;
-    for (int64_t e = at; e < packets; e += step) reinterpret_cast<uint4 *>(p.chain)[e] = make_uint4(0, 0, 0, 0);
+    const int64_t spans = (p.cu[p.n_max] + (int64_t)kRanks * tile - 1) / (kRanks * tile);
+    for (int64_t e = at; e < spans * p.D; e += step) reinterpret_cast<uint4 *>(p.chain)[e] = make_uint4(0, 0, 0, 0);
     for (int64_t j = at; j < p.tiles; j += step) {
         const int64_t t0 = j * tile;
         int lo = 0, hi = p.n_max;                          // first n with cu[n] >= t0 (n_max if none)
@@ -70,22 +72,72 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const f
     }
 }
 
-// Sequences that start and end within the tile's tokens, by token; -1: none.  One warp.
+// ---- clusters ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void peer_store(void *p, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t peer_load(const void *p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// ---- what a block holds of a tile beside its rows ----
 template <int TILE>
-__device__ __forceinline__ void borders(const Params &p, int64_t j, int *s_start, int *s_end) {
+struct Tile {
+    int32_t seq, cb;               // its span's place in the order of the recurrence, its block of channels
+    int32_t t0, n;                 // its first token, its live tokens (0: none)
+    uint32_t starts[TILE / 32], ends[TILE / 32];       // tokens that start and end a sequence, a bit each
+    int32_t start[TILE], end[TILE];                    // which (where the bit is set)
+};
+
+// One warp: the sequences that start and end among the tile's tokens.
+template <int TILE>
+__device__ __forceinline__ void borders(const Params &p, Tile<TILE> &t) {
     const int lane = threadIdx.x & 31;
-    const int64_t t0 = j * TILE;
-    const int f = p.first[j];
+    uint32_t starts[TILE / 32] = {}, ends[TILE / 32] = {};
+    if (t.n > 0) {
+        const int f = p.first[t.t0 / TILE];
+        for (int n = (f > 0 ? f - 1 : 0) + lane; n < p.n_max; n += 32) {
+            const int b = p.cu[n] - t.t0, e = p.cu[n + 1] - t.t0;          // (both lie in [0, 2^31))
+            if (b >= TILE) break;
+            if (e <= b) continue;
 #pragma unroll
-    for (int k = lane; k < TILE; k += 32) s_start[k] = s_end[k] = -1;
-    __syncwarp();
-    for (int n = (f > 0 ? f - 1 : 0) + lane; n < p.n_max; n += 32) {
-        const int64_t b = p.cu[n] - t0, e = p.cu[n + 1] - t0;
-        if (b >= TILE) break;
-        if (e <= b) continue;
-        if (b >= 0) s_start[b] = n;
-        if (e >= 1 && e <= TILE) s_end[e - 1] = n;
+            for (int k = 0; k < TILE / 32; ++k) {
+                if (b >> 5 == k) starts[k] |= 1u << (b & 31);
+                if ((e - 1) >> 5 == k) ends[k] |= 1u << ((e - 1) & 31);
+            }
+            if (b >= 0) t.start[b] = n;
+            if (e >= 1 && e <= TILE) t.end[e - 1] = n;
+        }
     }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < TILE / 32; ++k) {
+        const uint32_t u = __reduce_or_sync(0xffffffffu, starts[k]), v = __reduce_or_sync(0xffffffffu, ends[k]);
+        if (lane == 0) { t.starts[k] = u; t.ends[k] = v; }
+    }
+}
+// The bits of warp w's tokens; whether there are any in the tile.
+__device__ __forceinline__ uint32_t bits_of(const uint32_t *words, int w) { return words[w / 4] >> (w % 4 * 8) & 0xffu; }
+template <int N>
+__device__ __forceinline__ bool any_of(const uint32_t *words) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) a |= words[k];
+    return a != 0;
 }
 
 template <typename T>
@@ -103,7 +155,7 @@ __device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, 
     if (s && ch < D) Lane<T>::store(s + n * D + ch, h);
 }
 
-// ---- what tiles leave each other ----
+// ---- what spans leave each other ----
 __device__ __forceinline__ Packet load_packet(const Packet *p) {
     unsigned __int128 v;
     asm volatile("ld.relaxed.gpu.global.b128 %0, [%1];" : "=q"(v) : "l"(p) : "memory");
@@ -120,11 +172,10 @@ __device__ __forceinline__ void store_packet(Packet *p, float a, float own, floa
     asm volatile("st.relaxed.gpu.global.b128 [%0], %1;" ::"l"(p), "q"(v) : "memory");
 }
 
-// One warp, a channel a lane: the state that enters tile `seq` (its number in the order of the recurrence, > 0): from the nearest
-// tile before it whose state is out for all the warp's channels, and the own states of the tiles between, folded from the oldest on.
-// False: it did not come in time.
+// One warp, a channel a lane: the state that enters span `seq` (> 0): from the nearest span before it whose state is out for all
+// the warp's channels, and the own states of the spans between, folded from the oldest on.  False: it did not come in time.
 __device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch, bool on, float &h) {
-    constexpr int W = 4;                                   // packets in flight
+    constexpr int W = 2;                                   // packets in flight
     const int64_t base = seq - 1;
     int depth = 0;
     uint64_t t0 = 0;
@@ -148,7 +199,7 @@ __device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch
         if (found < W) {
 #pragma unroll
             for (int u = W - 1; u >= 0; --u) h = u == found ? k[u].out : u < found ? fmaf(k[u].a, h, k[u].own) : h;
-            for (int d = depth - 1; d >= 0; d -= W) {      // the tiles nearer than these (a multiple of W)
+            for (int d = depth - 1; d >= 0; d -= W) {      // the spans nearer than these (a multiple of W)
                 Packet n[W];
 #pragma unroll
                 for (int u = 0; u < W; ++u) {
@@ -160,7 +211,7 @@ __device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch
             }
             return true;
         }
-        depth = gap || depth >= 7 * W ? 0 : depth + W;
+        depth = gap || depth >= 15 * W ? 0 : depth + W;
         if (t0 == 0) t0 = tc::globaltimer();
         if (__shfl_sync(0xffffffffu, tc::globaltimer() - t0 > tc::kWaitLimitNs, 0)) return false;
     }
@@ -169,39 +220,70 @@ __device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch
 template <int CB, int WARPS>
 struct Shared {
     float a[WARPS][CB], b[WARPS][CB];
-    int start[2][WARPS * kRun], end[2][WARPS * kRun];
-    int cut[WARPS];
-    uint32_t ticket[3];
+    float tot_a[2][kRanks - 1][CB], tot_b[2][kRanks - 1][CB];      // products and own states of the blocks before, by parity of the tile
+    uint32_t tot_cut[2][kRanks - 1];
+    uint32_t next[2];              // the next span, by parity; next[1] at first: the cluster's first
+    Tile<WARPS * kRun> tile[2];
     int err;
     uint64_t full[2];
 };
 
 // One warp, a channel a lane (column c of s.a, s.b): from the warps' products and own states (in the order of the recurrence: from
-// the first row, REV from the last; s.cut: the row does not depend on the one before), publishes the tile and puts the state
-// that enters each row into s.b.  False: the state before did not come in time.
+// the first row, REV from the last) the block's, exchanged with the cluster's blocks; then the state that enters each row into s.b.
+// `cuts`: a bit a token; a warp with one does not depend on the state before.  wait: false after a wait that ran out (then
+// nothing is waited for any more).  False: the state before did not come in time.
 template <bool REV, int CB, int WARPS>
-__device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch, int c, Shared<CB, WARPS> &s) {
-    const bool on = ch < p.D;
-    Packet *mine = p.chain + seq * p.D + ch;
-    float A = 1.f, h = 0.f, in = 0.f;
-    bool cut = false, ok = true;
+__device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch, int c, uint32_t rank, int par, const uint32_t *cuts,
+                                           Shared<CB, WARPS> &s, bool wait) {
+    const bool on = ch < p.D, cut = any_of<WARPS * kRun / 32>(cuts);
+    float A = 1.f, h = 0.f;
+    if (!cut) {
 #pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-        const int w = REV ? WARPS - 1 - i : i;
-        const bool k = s.cut[w] != 0;
-        cut |= k;
-        h = k ? s.b[w][c] : fmaf(s.a[w][c], h, s.b[w][c]);
-        A *= s.a[w][c];
+        for (int i = 0; i < WARPS; ++i) {
+            const int w = REV ? WARPS - 1 - i : i;
+            const float a = s.a[w][c];
+            h = fmaf(a, h, s.b[w][c]);
+            A *= a;
+        }
+    } else {
+        A = 0.f;
+        for (int i = 0; i < WARPS; ++i) {
+            const int w = REV ? WARPS - 1 - i : i;
+            h = bits_of(cuts, w) ? s.b[w][c] : fmaf(s.a[w][c], h, s.b[w][c]);
+        }
     }
-    if (on) store_packet(mine, A, h, h, cut ? kDone : kOwn);
-    if (seq > 0) ok = chain_enter(p, seq, ch, on, in);     // (the first tile is cut at its first token)
-    if (on && !cut) store_packet(mine, A, h, fmaf(A, in, h), kDone);
+    for (uint32_t r = rank + 1; r < kRanks; ++r) {
+        peer_store(&s.tot_a[par][rank][c], r, __float_as_uint(A));
+        peer_store(&s.tot_b[par][rank][c], r, __float_as_uint(h));
+        if (c % 32 == 0) peer_store(&s.tot_cut[par][rank], r, cut);
+    }
+    cluster_arrive();
+    cluster_wait();
+    Packet *mine = p.chain + seq * p.D + ch;
+    bool ok = true, span_cut = cut;
+    if (rank == kRanks - 1) {                              // the last block speaks for the span
+        float before = 0.f, product = 1.f;
+#pragma unroll
+        for (int r = 0; r < kRanks - 1; ++r) {
+            const bool k = s.tot_cut[par][r] != 0;
+            span_cut |= k;
+            before = k ? s.tot_b[par][r][c] : fmaf(s.tot_a[par][r][c], before, s.tot_b[par][r][c]);
+            product *= s.tot_a[par][r][c];
+        }
+        if (!cut) h = fmaf(A, before, h);
+        A *= product;
+        if (on) store_packet(mine, A, h, h, span_cut ? kDone : kOwn);
+    }
+    float in = 0.f;
+    if (seq > 0 && wait) ok = chain_enter(p, seq, ch, on, in);             // (the first span is cut at its first token)
+    if (rank == kRanks - 1 && on && !span_cut) store_packet(mine, A, h, fmaf(A, in, h), kDone);
+    for (uint32_t r = 0; r < rank; ++r) in = s.tot_cut[par][r] ? s.tot_b[par][r][c] : fmaf(s.tot_a[par][r][c], in, s.tot_b[par][r][c]);
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
         const int w = REV ? WARPS - 1 - i : i;
         const float a = s.a[w][c], b = s.b[w][c];
         s.b[w][c] = in;
-        in = s.cut[w] ? b : fmaf(a, in, b);
+        in = cut && bits_of(cuts, w) ? b : fmaf(a, in, b);
     }
     return ok;
 }
@@ -210,89 +292,168 @@ struct Maps {                      // the staged rows: r, x, d_o (backward), i
     CUtensorMap m[4];
 };
 
-// Waits (with a limit) until the copies into both buffers that are under way have landed; `bits`: buffers with one, and the
-// parity each ends at.
-__device__ __forceinline__ void drain(uint64_t *full, uint32_t busy, uint32_t parity) {
-    const uint64_t t0 = tc::globaltimer();
-    for (int b = 0; b < 2; ++b)
-        if (busy >> b & 1)
-            while (!tc::mbar_try_wait(&full[b], parity >> b & 1) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
-}
+constexpr int kIssuer = 96;        // the thread that takes spans and issues the copies
 
-constexpr int kIssuer = 96;        // the thread that takes tickets and issues the copies
+// A block's walk over its tiles, which both directions share.  Its next tile's rows are staged while one is computed.
+template <bool REV, int CB, int WARPS>
+struct Walk {
+    static constexpr int TILE = WARPS * kRun, BYTES = TILE * 128;
+    const Params &p;
+    Shared<CB, WARPS> &s;
+    const Maps &maps;
+    uint8_t *rows;                 // [2][narr][TILE][128]
+    int narr;
+    int64_t live, tiles;           // live tokens; tiles that have some
+    uint32_t units, rank;
+    uint32_t parity, issued;       // of the copies into the two buffers: the next wait's; the last issued one's, inverted, and
+                                   // whether any was (issuer)
+
+    // The issuer: this block's tile in span `unit`, and its copies.
+    __device__ __forceinline__ void issue(uint32_t unit, int buf) {
+        Tile<TILE> &t = s.tile[buf];
+        t.seq = unit / p.n_cb;
+        t.cb = unit - t.seq * p.n_cb;
+        const int64_t k = (int64_t)t.seq * kRanks + rank, j = REV ? tiles - 1 - k : k;
+        t.n = 0;
+        if (j < 0 || j >= tiles || *reinterpret_cast<volatile int *>(&s.err) != 0) return;
+        t.t0 = (int)(j * TILE);
+        t.n = live - t.t0 < TILE ? (int)(live - t.t0) : TILE;
+        issued = (issued ^ 1u << buf) | 4u << buf;
+        tc::mbar_arrive_expect_tx(&s.full[buf], narr * BYTES);
+        for (int a = 0; a < narr; ++a)
+            tc::tma_load_2d(rows + (buf * narr + a) * BYTES, &maps.m[!REV && a == 2 ? 3 : a], t.cb * CB, t.t0, &s.full[buf]);
+    }
+    // Sets up the barriers and takes the cluster's first span; false: there is none.  Every thread of the cluster.
+    __device__ __forceinline__ bool start() {
+        const int tid = threadIdx.x;
+        if (tid == kIssuer) {
+            tc::mbar_init(&s.full[0], 1);
+            tc::mbar_init(&s.full[1], 1);
+            tc::fence_barrier_init();
+            s.err = 0;
+            if (rank == 0) s.next[1] = atomicAdd(&p.head->ticket, 1u);
+        }
+        cluster_arrive();
+        cluster_wait();
+        const uint32_t unit = peer_load(&s.next[1], 0);
+        if (unit >= units) {
+            cluster_arrive();                              // (the first block stays until all have read)
+            cluster_wait();
+            return false;
+        }
+        if (tid / 32 == kIssuer / 32) {
+            if (tid == kIssuer) issue(unit, 0);
+            __syncwarp();
+            borders(p, s.tile[0]);
+        }
+        __syncthreads();
+        return true;
+    }
+    // The staged rows have landed.
+    __device__ __forceinline__ void landed(int buf) {
+        if (s.tile[buf].n == 0) return;
+        tc::mbar_wait(&s.full[buf], parity >> buf & 1, &s.err, GCL_DEV_WAIT_TIMEOUT);
+        parity ^= 1u << buf;
+    }
+    // Takes the cluster's next span (its number reaches the blocks by the exchange).
+    __device__ __forceinline__ uint32_t take() { return rank == 0 && threadIdx.x == kIssuer ? atomicAdd(&p.head->ticket, 1u) : 0; }
+    // Between a tile's halves: the warps' own states are in s.a, s.b; afterwards the states that enter them in s.b.
+    template <typename Side>
+    __device__ __forceinline__ void exchange(int buf, uint32_t taken, const uint32_t *cuts, Side side) {
+        const int tid = threadIdx.x, warp = tid >> 5;
+        const Tile<TILE> &t = s.tile[buf];
+        if (rank == 0 && tid == kIssuer)
+            for (int r = 0; r < kRanks; ++r) peer_store(&s.next[buf], r, taken);
+        __syncthreads();
+        if (warp < CB / 32) {
+            const bool wait = *reinterpret_cast<volatile int *>(&s.err) == 0;
+            if (!chain_tile<REV>(p, t.seq, t.cb * CB + tid, tid, rank, buf, cuts, s, wait)) atomicCAS(&s.err, 0, GCL_DEV_WAIT_TIMEOUT);
+        } else {
+            cluster_arrive();
+            if (warp == 2) side();
+            cluster_wait();
+            if (warp == kIssuer / 32) {
+                const uint32_t unit = s.next[buf];
+                if (unit < units) {
+                    if (tid == kIssuer) issue(unit, buf ^ 1);
+                    __syncwarp();
+                    borders(p, s.tile[buf ^ 1]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ bool more(int buf) const { return s.next[buf] < units; }
+    // After the last tile: a wait that ran out is reported, and copies still under way are waited for (with a limit).
+    __device__ __forceinline__ void finish() {
+        __syncthreads();
+        if (s.err == 0 || threadIdx.x != kIssuer) return;
+        status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
+        const uint64_t t0 = tc::globaltimer();
+        for (int b = 0; b < 2; ++b)
+            while ((issued >> (2 + b) & 1) && !tc::mbar_try_wait(&s.full[b], (issued >> b & 1) ^ 1) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
+    }
+};
 
 // ---- forward -------------------------------------------------------------
-// Per block: two tiles staged, so that the next one's rows are under way while this one is computed.
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Lane<T>;
     using P = typename L::P;
-    constexpr int V = L::V, CB = L::CB, RUN = kRun, BYTES = kTileF * 128;
+    using W = Walk<false, L::CB, kWarpsF>;
+    constexpr int V = L::V, CB = L::CB, RUN = kRun, BYTES = W::BYTES;
     __shared__ Shared<CB, kWarpsF> s;
-    extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, i][kTileF][128]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, narr = p.i.p ? 3 : 2;
-    if (tid == kIssuer) {
-        tc::mbar_init(&s.full[0], 1);
-        tc::mbar_init(&s.full[1], 1);
-        tc::fence_barrier_init();
-        s.err = 0;
-    }
+    extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, i][tile][128]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 3 : 2;
     grid_dependency_wait();
     if (p.head->blocked) return;
-    const int64_t live = p.head->live;
-    const uint32_t units = (uint32_t)((live + kTileF - 1) / kTileF * p.n_cb);
-    uint32_t busy = 0, parity = 0;                         // buffers with a copy under way, the parity that they end at
-    auto issue = [&](uint32_t unit, int buf) {             // (every thread keeps the two words, the issuer copies)
-        if (unit >= units) return;
-        busy |= 1u << buf;
-        if (tid != kIssuer) return;
-        const uint32_t j = unit / p.n_cb;
-        tc::mbar_arrive_expect_tx(&s.full[buf], narr * BYTES);
-        for (int k = 0; k < narr; ++k)
-            tc::tma_load_2d(s_rows + (buf * narr + k) * BYTES, &maps.m[k < 2 ? k : 3], (unit - j * p.n_cb) * CB, j * kTileF, &s.full[buf]);
-    };
-    if (tid == kIssuer) s.ticket[2] = atomicAdd(&p.head->ticket, 1u);
-    __syncthreads();
-    uint32_t unit = s.ticket[2], next = 0;
-    if (unit >= units) return;
-    issue(unit, 0);
-    if (warp == 2) borders<kTileF>(p, unit / p.n_cb, s.start[0], s.end[0]);
-    __syncthreads();
-    bool first = true;
-    for (int buf = 0; unit < units; buf ^= 1) {
-        const uint32_t j = unit / p.n_cb;
-        const int64_t t = (int64_t)j * kTileF + warp * RUN;
-        const int cb = unit - j * p.n_cb, ch = cb * CB + lane * V;
-        const int n = live - t < RUN ? (int)(live - t) : RUN;            // live tokens of the warp (none: <= 0)
+    const int64_t live = p.head->live, tiles = (live + W::TILE - 1) / W::TILE;
+    W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0};
+    if (!walk.start()) return;
+    for (int buf = 0;; buf ^= 1) {
+        const Tile<W::TILE> &tile = s.tile[buf];
+        const int64_t t = tile.t0 + warp * RUN;
+        const int ch = tile.cb * CB + lane * V, n = tile.n - warp * RUN;          // n: live tokens from the warp's first on
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
         auto row = [&](int arr, int k) { return L::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128)); };
         const P rate = load_state<T>(p.kind.decay == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, p.D, ch);
         const bool near = __all_sync(0xffffffffu, L::every(rate, [](float v) { return v >= 0.f && v <= kNear; }));
-        bool bad = !tc::mbar_wait(&s.full[buf], parity >> buf & 1, &s.err, GCL_DEV_WAIT_TIMEOUT);
-        busy &= ~(1u << buf);
-        parity ^= 1u << buf;
-        // (a second tile is taken only when the first has arrived, so that few tiles spread over all blocks)
-        uint32_t taken = 0;
-        if (tid == kIssuer) taken = atomicAdd(&p.head->ticket, first ? 2u : 1u);
+        walk.landed(buf);
+        // (the next span is taken only when this one's rows are here: few spans go to all clusters, and none is held back for long)
+        const uint32_t taken = walk.take();
         P a[RUN], b[RUN];
+        if (sizeof(T) == 2 && p.kind.decay == GCL_DECAY_POWER && narr == 3) {
+            constexpr int H = RUN / 2;                     // (four tokens at a time: registers)
 #pragma unroll
-        for (int k = 0; k < RUN; ++k) b[k] = row(0, k);
-        decays<T, RUN>(p.kind, rate, near, a, b);
+            for (int k0 = 0; k0 < RUN; k0 += H) {
+                P g[H];
 #pragma unroll
-        for (int k = 0; k < RUN; ++k) b[k] = L::mul(b[k], row(1, k));
-        if (narr == 3)
+                for (int k = 0; k < H; ++k) two_sigmoids<T>(row(0, k0 + k), row(2, k0 + k), b[k0 + k], g[k]);
 #pragma unroll
-            for (int k = 0; k < RUN; ++k) b[k] = L::mul(b[k], sigmoid<T>(row(2, k)));
+                for (int k = 0; k < H; ++k) g[k] = L::mul(g[k], row(1, k0 + k));
+                decays<T, H>(p.kind, rate, near, a + k0, b + k0, true);
+#pragma unroll
+                for (int k = 0; k < H; ++k) b[k0 + k] = L::mul(b[k0 + k], g[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) b[k] = row(0, k);
+            decays<T, RUN>(p.kind, rate, near, a, b);
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) b[k] = L::mul(b[k], row(1, k));
+            if (narr == 3)
+#pragma unroll
+                for (int k = 0; k < RUN; ++k) b[k] = L::mul(b[k], sigmoid<T>(row(2, k)));
+        }
         if (n < RUN)
 #pragma unroll
             for (int k = 0; k < RUN; ++k)
                 if (k >= n) { a[k] = L::all(1.f); b[k] = L::all(0.f); }
-        const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
-        const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && start[lane % RUN] >= 0);
-        const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && end[lane % RUN] >= 0);
+        const int32_t *start = tile.start + warp * RUN, *end = tile.end + warp * RUN;
+        const uint32_t starts = bits_of(tile.starts, warp), ends = bits_of(tile.ends, warp);
         {
             P A = L::all(1.f), h = L::all(0.f);
-            auto walk = [&](auto cut) {
+            auto run = [&](auto cut) {
 #pragma unroll
                 for (int k = 0; k < RUN; ++k) {
                     if (decltype(cut)::value && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
@@ -300,35 +461,20 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const __g
                     A = L::mul(A, a[k]);
                 }
             };
-            if (starts) walk(std::true_type());
-            else walk(std::false_type());
+            if (starts) run(std::true_type());
+            else run(std::false_type());
             L::store(&s.a[warp][lane * V], A);
             L::store(&s.b[warp][lane * V], h);
-            if (lane == 0) s.cut[warp] = starts != 0;
         }
-        if (tid == kIssuer) {
-            s.ticket[0] = first ? taken : next;
-            s.ticket[1] = first ? taken + 1 : taken;
-        }
-        __syncthreads();                                   // the rows are read, the warps' own states there
-        const uint32_t unit1 = s.ticket[0];
-        next = s.ticket[1];
-        if (first) issue(unit1, buf ^ 1);
-        issue(next, buf);
-        if (warp < CB / 32) bad |= !chain_tile<false>(p, j, cb * CB + tid, tid, s);
-        if (warp == 2 && unit1 < units) borders<kTileF>(p, unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
-        if (__syncthreads_or(bad)) {
-            if (tid == 0) status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
-            break;
-        }
+        walk.exchange(buf, taken, tile.starts, [] {});
         P h = L::load(&s.b[warp][lane * V]);
         if (warp * RUN % kSave == 0 && p.h_save && n > 0) {
             if (starts & 1) h = load_state<T>(p.h0, start[0], p.D, ch);
             store_state<T>(p.h_save, t / kSave, p.D, ch, h);
         }
         uint32_t *to = word<T>(p.o, t, ch);
-        const int n_out = p.o.p && ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
-        auto walk = [&](auto plain) {                      // plain: no borders, all tokens live
+        const int n_out = p.o.p && ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + (n < RUN ? n : RUN) - 1, p.t_max, p.status) ? n : 0;
+        auto run = [&](auto plain) {                       // plain: no borders, all tokens live
             constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
             for (int k = 0; k < RUN; ++k) {
@@ -339,12 +485,11 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const __g
                 if (!PLAIN && (ends >> k & 1)) store_state<T>(p.ht, end[k], p.D, ch, h);
             }
         };
-        if (!(starts | ends) && n == RUN) walk(std::true_type());
-        else walk(std::false_type());
-        unit = unit1;
-        first = false;
+        if (!(starts | ends) && n >= RUN) run(std::true_type());
+        else run(std::false_type());
+        if (!walk.more(buf)) break;
     }
-    drain(s.full, busy, parity);
+    walk.finish();
 }
 
 // ---- backward ------------------------------------------------------------
@@ -354,57 +499,30 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Lane<T>;
     using P = typename L::P;
-    constexpr int V = L::V, CB = L::CB, RUN = kRun, BYTES = kTileB * 128;
-    static_assert(kTileB == kSave, "one saved state a tile");
+    using W = Walk<true, L::CB, kWarpsB>;
+    constexpr int V = L::V, CB = L::CB, RUN = kRun, BYTES = W::BYTES;
     __shared__ Shared<CB, kWarpsB> s;
-    __shared__ float s_h[kWarpsB][CB], s_d[kWarpsB][CB];
-    __shared__ int s_cuth[kWarpsB];
-    extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, d_o, i][kTileB][128]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, narr = p.i.p ? 4 : 3;
+    __shared__ float s_h[kWarpsB][CB];
+    extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, d_o, i][tile][128]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, narr = p.i.p ? 4 : 3;
     launch_dependents();                                   // (the sum of the rates' gradients waits for this grid's end)
-    if (tid == kIssuer) {
-        tc::mbar_init(&s.full[0], 1);
-        tc::mbar_init(&s.full[1], 1);
-        tc::fence_barrier_init();
-        s.err = 0;
-    }
     grid_dependency_wait();
     if (p.head->blocked) return;
-    const int64_t live = p.head->live, n_live = (live + kTileB - 1) / kTileB;
-    const uint32_t units = (uint32_t)(n_live * p.n_cb);
-    uint32_t busy = 0, parity = 0;
-    auto issue = [&](uint32_t unit, int buf) {
-        if (unit >= units) return;
-        busy |= 1u << buf;
-        if (tid != kIssuer) return;
-        const uint32_t seq = unit / p.n_cb;
-        tc::mbar_arrive_expect_tx(&s.full[buf], narr * BYTES);
-        for (int k = 0; k < narr; ++k)
-            tc::tma_load_2d(s_rows + (buf * narr + k) * BYTES, &maps.m[k], (unit - seq * p.n_cb) * CB, (int)(n_live - 1 - seq) * kTileB, &s.full[buf]);
-    };
-    if (tid == kIssuer) s.ticket[2] = atomicAdd(&p.head->ticket, 1u);
-    __syncthreads();
-    uint32_t unit = s.ticket[2];
-    if (unit >= units) return;
-    issue(unit, 0);
-    if (warp == 2) borders<kTileB>(p, n_live - 1 - unit / p.n_cb, s.start[0], s.end[0]);
-    __syncthreads();
-    for (int buf = 0; unit < units; buf ^= 1) {
-        const uint32_t seq = unit / p.n_cb;
-        const int64_t j = n_live - 1 - seq, t = j * kTileB + warp * RUN;
-        const int cb = unit - seq * p.n_cb, ch = cb * CB + lane * V;
-        const int n = live - t < RUN ? (int)(live - t) : RUN;            // live tokens of the warp (none: <= 0)
+    const int64_t live = p.head->live, tiles = (live + W::TILE - 1) / W::TILE;
+    W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0};
+    if (!walk.start()) return;
+    for (int buf = 0;; buf ^= 1) {
+        const Tile<W::TILE> &tile = s.tile[buf];
+        const int64_t t = tile.t0 + warp * RUN;
+        const int ch = tile.cb * CB + lane * V, n = tile.n - warp * RUN;
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
         auto row = [&](int arr, int k) { return L::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128)); };
         const P rate = load_state<T>(p.kind.decay == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, p.D, ch);
         const bool near = __all_sync(0xffffffffu, L::every(rate, [](float v) { return v >= 0.f && v <= kNear; }));
         P before = L::all(0.f);
-        if (warp == 3) before = load_state<T>(p.h_save, j, p.D, ch);
-        bool bad = !tc::mbar_wait(&s.full[buf], parity >> buf & 1, &s.err, GCL_DEV_WAIT_TIMEOUT);
-        busy &= ~(1u << buf);
-        parity ^= 1u << buf;
-        uint32_t taken = 0;
-        if (tid == kIssuer) taken = atomicAdd(&p.head->ticket, 1u);
+        if (warp == 2 && tile.n > 0) before = load_state<T>(p.h_save, tile.t0 / kSave, p.D, ch);
+        walk.landed(buf);
+        const uint32_t taken = walk.take();
         P a[RUN], m[RUN], prev[RUN];                       // prev: b = m u, later the state before each token
 #pragma unroll
         for (int k = 0; k < RUN; ++k) m[k] = row(0, k);
@@ -413,13 +531,12 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const __g
 #pragma unroll
             for (int k = 0; k < RUN; ++k)
                 if (k >= n) { a[k] = L::all(1.f); m[k] = L::all(0.f); }
-        const int *start = s.start[buf] + warp * RUN, *end = s.end[buf] + warp * RUN;
-        const uint32_t starts = __ballot_sync(0xffffffffu, lane < RUN && start[lane % RUN] >= 0);
-        const uint32_t ends = __ballot_sync(0xffffffffu, lane < RUN && end[lane % RUN] >= 0);
+        const int32_t *start = tile.start + warp * RUN, *end = tile.end + warp * RUN;
+        const uint32_t starts = bits_of(tile.starts, warp), ends = bits_of(tile.ends, warp);
         const bool edge = (starts | ends) || n < RUN;
         {
             P A = L::all(1.f), h = L::all(0.f), c = L::all(0.f);
-            auto walk = [&](auto cut) {
+            auto run = [&](auto cut) {
                 constexpr bool CUT = decltype(cut)::value;
 #pragma unroll
                 for (int k = 0; k < RUN; ++k) {
@@ -436,38 +553,25 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const __g
                     c = L::mul(a[k], L::add(CUT && k >= n ? L::all(0.f) : row(2, k), c));
                 }
             };
-            if (edge) walk(std::true_type());
-            else walk(std::false_type());
+            if (edge) run(std::true_type());
+            else run(std::false_type());
             L::store(&s.a[warp][lane * V], A);
             L::store(&s.b[warp][lane * V], c);
             L::store(&s_h[warp][lane * V], h);
-            if (lane == 0) { s.cut[warp] = ends != 0; s_cuth[warp] = starts != 0; }
         }
-        if (tid == kIssuer) s.ticket[0] = taken;
-        __syncthreads();
-        const uint32_t unit1 = s.ticket[0];
-        issue(unit1, buf ^ 1);
-        if (warp < CB / 32) {
-            bad |= !chain_tile<true>(p, seq, cb * CB + tid, tid, s);
-        } else if (warp == 3) {                            // the states that enter the warps' tokens
+        walk.exchange(buf, taken, tile.ends, [&] {         // (a warp at leisure: the states that enter the warps' tokens)
 #pragma unroll
             for (int w = 0; w < kWarpsB; ++w) {
                 const P b = L::load(&s_h[w][lane * V]), A = L::load(&s.a[w][lane * V]);
                 L::store(&s_h[w][lane * V], before);
-                before = s_cuth[w] ? b : L::fma(A, before, b);
+                before = bits_of(tile.starts, w) ? b : L::fma(A, before, b);
             }
-        } else if (warp == 2 && unit1 < units) {
-            borders<kTileB>(p, n_live - 1 - unit1 / p.n_cb, s.start[buf ^ 1], s.end[buf ^ 1]);
-        }
-        if (__syncthreads_or(bad)) {
-            if (tid == 0) status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
-            break;
-        }
+        });
         P h = L::load(&s_h[warp][lane * V]), c = L::load(&s.b[warp][lane * V]), dsum = L::all(0.f);
         const int64_t last = t + RUN - 1;
         uint32_t *to_x = word<T>(p.dx, last, ch), *to_r = word<T>(p.dr, last, ch), *to_i = word<T>(p.di, last, ch);
-        const int n_out = ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + n - 1, p.t_max, p.status) ? n : 0;
-        auto walk = [&](auto plain) {                      // plain: no borders, all tokens live
+        const int n_out = ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + (n < RUN ? n : RUN) - 1, p.t_max, p.status) ? n : 0;
+        auto run = [&](auto plain) {                       // plain: no borders, all tokens live
             constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
             for (int k = 0; k < RUN; ++k) {
@@ -518,21 +622,25 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const __g
                 if (!PLAIN && (starts >> k & 1)) store_state<T>(p.dh0, start[k], p.D, ch, c);
             }
         };
-        if (!edge) walk(std::true_type());
-        else walk(std::false_type());
+        if (!edge) run(std::true_type());
+        else run(std::false_type());
         if (p.drate_part) {
+            // (through the staged rows of r, which are read; the copies into them come after the next barrier)
+            float (*s_d)[kRun * 32] = reinterpret_cast<float (*)[kRun * 32]>(s_rows + buf * narr * BYTES);
+            __syncwarp();
             L::store(&s_d[warp][lane * V], dsum);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();
-            if (warp == 4) {
+            if (warp == 4 && tile.n > 0) {
                 P sum = L::all(0.f);
 #pragma unroll
                 for (int w = 0; w < kWarpsB; ++w) sum = L::add(sum, L::load(&s_d[w][lane * V]));
-                store_state<T>(p.drate_part, j, p.D, ch, sum);
+                store_state<T>(p.drate_part, tile.t0 / W::TILE, p.D, ch, sum);
             }
         }
-        unit = unit1;
+        if (!walk.more(buf)) break;
     }
-    drain(s.full, busy, parity);
+    walk.finish();
 }
 
 // drate from the tiles' sums, in a fixed order: 32 channels a block, 32 rows of threads over the tiles, eight loads of
@@ -580,12 +688,11 @@ size_t layout(const gcl_glr_args *a, bool backward, Params *p) {
     auto set = [&](auto *&field, size_t bytes) { field = reinterpret_cast<std::remove_reference_t<decltype(field)>>(take(bytes)); };
     Params dummy{};
     Params &o = p ? *p : dummy;
-    const int64_t tf = (a->t_max + kTileF - 1) / kTileF, tb = (a->t_max + kTileB - 1) / kTileB;
-    const int64_t tiles = backward ? tb : tf;
+    const int64_t tf = (a->t_max + kTileF - 1) / kTileF, tb = (a->t_max + kTileB - 1) / kTileB, tiles = backward ? tb : tf;
     const size_t row = sizeof(float) * (size_t)a->D;
     set(o.head, sizeof(Header));
     set(o.first, sizeof(int32_t) * (size_t)tiles);
-    set(o.chain, sizeof(Packet) * (size_t)a->D * tiles);
+    set(o.chain, sizeof(Packet) * (size_t)a->D * ((tiles + kRanks - 1) / kRanks));
     if (backward) {
         if (a->drate) set(o.drate_part, row * tiles);
         if (!a->h_save) set(o.h_save, row * tb);
@@ -603,9 +710,10 @@ bool rows_map(CUtensorMap *m, const Params &p, const Rows &r, int tile) {
     return make_tensor_map(m, r.p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, dt);
 }
 
-// Launches the set-up and, as its dependent, `kernel` with at most `ctas` blocks an SM.
+// Launches the set-up and, as its dependent, `kernel` in clusters, at most `ctas` blocks an SM.
 template <typename T, typename K>
-cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float *out_state, int tile, int threads, int ctas, cudaStream_t s) {
+cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float *out_state, int warps, int ctas, cudaStream_t s) {
+    const int tile = warps * kRun;
     Maps maps;
     const Rows *rows[4] = {&p.r, &p.x, &p.d_o, &p.i};
     int n = 0;
@@ -617,22 +725,36 @@ cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float
     const size_t smem = (size_t)2 * n * tile * 128;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int64_t units = p.tiles * p.n_cb, most = (int64_t)ctas * num_sms();
-    int64_t setup = (p.tiles * p.D + 4095) / 4096;
+    const int64_t spans = (p.tiles + kRanks - 1) / kRanks, units = spans * p.n_cb, most = (int64_t)ctas * num_sms() / kRanks;
+    int64_t setup = (spans * p.D + 4095) / 4096;
     if (out_state && setup < (p.n_max + 7) / 8) setup = (p.n_max + 7) / 8;
     if (setup > num_sms()) setup = num_sms();
     glr_setup_kernel<<<(unsigned)setup, 1024, 0, s>>>(p, in_state, out_state, tile);
-    return launch_dependent(kernel, dim3((unsigned)(units < most ? units : most)), dim3(threads), smem, s, maps, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((units < most ? units : most) * kRanks));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kRanks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t l = cudaLaunchKernelEx(&cfg, kernel, maps, p);
+    return l != cudaSuccess ? l : cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_fwd(const Params &p, cudaStream_t s) {
-    return launch_tiles<T>(glr_fwd_kernel<T>, p, p.h0, p.ht, kTileF, 32 * kWarpsF, kCtasF, s);
+    return launch_tiles<T>(glr_fwd_kernel<T>, p, p.h0, p.ht, kWarpsF, kCtasF, s);
 }
 
 template <typename T>
 cudaError_t launch_bwd(const Params &p, cudaStream_t s) {
-    const cudaError_t e = launch_tiles<T>(glr_bwd_kernel<T>, p, p.dht, p.dh0, kTileB, 32 * kWarpsB, kCtasB, s);
+    const cudaError_t e = launch_tiles<T>(glr_bwd_kernel<T>, p, p.dht, p.dh0, kWarpsB, kCtasB, s);
     if (e != cudaSuccess || !p.drate) return e;
     return launch_dependent(glr_drate_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, p, kTileB);
 }

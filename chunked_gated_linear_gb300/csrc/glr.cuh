@@ -138,52 +138,75 @@ __device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>
     c = L::mul(e, s);
 }
 
-// q = 1 - exp(-y) for 0 <= y <= kNear: y P(y), P the polynomial of degree 6 that meets (1 - exp(-y)) / y at the Chebyshev points
-// of [0, 0.9] (off by 5e-9 of its value).
-constexpr float kNear = 0.9f;
+// sigmoid(x) and sigmoid(z) of 16-bit rows by one reciprocal, that of (1 + exp(-x)) (1 + exp(-z)): a reciprocal takes the
+// special-function unit as long as two exponentials.  Below 2^-63 (x < -43.6) they stay at 2^-63, so that the product is finite.
 template <typename T>
-__device__ __forceinline__ typename Lane<T>::P one_minus_exp(typename Lane<T>::P y) {
+__device__ __forceinline__ void two_sigmoids(typename Lane<T>::P x, typename Lane<T>::P z, typename Lane<T>::P &sx, typename Lane<T>::P &sz) {
     using L = Lane<T>;
-    typename L::P s = L::fma(y, L::all(1.3465580e-4f), L::all(-1.3153803e-3f));
-    s = L::fma(y, s, L::all(8.2897432e-3f));
-    s = L::fma(y, s, L::all(-4.1653194e-2f));
-    s = L::fma(y, s, L::all(1.6666466e-1f));
-    s = L::fma(y, s, L::all(-4.9999988e-1f));
-    s = L::fma(y, s, L::all(1.f));
-    return L::mul(y, s);
+    auto one_and_exp = [](typename L::P v) {
+        return L::add(L::map(L::mul(v, L::all(-1.4426950408889634f)), [](float u) { return fexp2<T>(fminf(u, 63.f)); }), L::all(1.f));
+    };
+    const typename L::P a = one_and_exp(x), b = one_and_exp(z);
+    const typename L::P r = L::map(L::mul(a, b), [](float u) { return frcp<T>(u); });
+    sx = L::mul(b, r);
+    sz = L::mul(a, r);
 }
 
-// a = exp(-y) and q = 1 - a of N values y.  16-bit rows: the difference loses q's digits near y = 0, and the fast exp's error,
-// some units of 2^-24 with one sign, would add up over all the tokens that a close to 1 remembers: there a = 1 - q from the
+// q = 1 - exp(-y) for 0 <= y <= kNear: y P(y), P the polynomial of degree 6 that meets (1 - exp(-y)) / y at the Chebyshev points
+// of [0, 0.9] (off by 5e-9 of its value).  N values at a time: a pair of constants then serves N instructions.
+constexpr float kNear = 0.9f;
+template <typename T, int N>
+__device__ __forceinline__ void one_minus_exp(const typename Lane<T>::P *y, typename Lane<T>::P *q) {
+    using L = Lane<T>;
+    constexpr float C[7] = {1.3465580e-4f, -1.3153803e-3f, 8.2897432e-3f, -4.1653194e-2f, 1.6666466e-1f, -4.9999988e-1f, 1.f};
+#pragma unroll
+    for (int e = 0; e < N; ++e) q[e] = L::fma(y[e], L::all(C[0]), L::all(C[1]));
+#pragma unroll
+    for (int c = 2; c < 7; ++c)
+#pragma unroll
+        for (int e = 0; e < N; ++e) q[e] = L::fma(y[e], q[e], L::all(C[c]));
+#pragma unroll
+    for (int e = 0; e < N; ++e) q[e] = L::mul(y[e], q[e]);
+}
+
+// a = exp(-y) and q = 1 - a of the N values y in q.  16-bit rows: the difference loses q's digits near y = 0, and the fast exp's
+// error, some units of 2^-24 with one sign, would add up over all the tokens that a close to 1 remembers: there a = 1 - q from the
 // polynomial, rounded once.  NEAR: all y lie in [0, kNear].
 template <typename T, bool NEAR, int N>
 __device__ __forceinline__ void decay_of(typename Lane<T>::P *a, typename Lane<T>::P *q) {
     using L = Lane<T>;
     using P = typename L::P;
+    if (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            a[e] = L::map(q[e], [](float v) { return expf(-v); });
+            q[e] = L::map(q[e], [](float v) { return -expm1f(-v); });
+        }
+        return;
+    }
+    P p[N];
+    one_minus_exp<T, N>(q, p);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const P y = q[e];
-        if (sizeof(T) == 4) {
-            a[e] = L::map(y, [](float v) { return expf(-v); });
-            q[e] = L::map(y, [](float v) { return -expm1f(-v); });
-        } else if (NEAR) {
-            q[e] = one_minus_exp<T>(y);
-            a[e] = L::fma(q[e], L::all(-1.f), L::all(1.f));
+        if (NEAR) {
+            q[e] = p[e];
+            a[e] = L::fma(p[e], L::all(-1.f), L::all(1.f));
         } else {
-            const P far = L::map(L::mul(y, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(v); });
+            const P y = q[e], far = L::map(L::mul(y, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(v); });
             auto pick = [](float v, float n, float f) {    // (y < 0 and NaN have larger bits)
                 return __float_as_uint(v) <= __float_as_uint(kNear) ? n : f;
             };
-            q[e] = L::map(y, one_minus_exp<T>(y), L::fma(far, L::all(-1.f), L::all(1.f)), pick);
-            a[e] = L::map(y, L::fma(q[e], L::all(-1.f), L::all(1.f)), far, pick);
+            q[e] = L::map(y, p[e], L::fma(far, L::all(-1.f), L::all(1.f)), pick);
+            a[e] = L::map(y, L::fma(p[e], L::all(-1.f), L::all(1.f)), far, pick);
         }
     }
 }
 
 // a and m(a) of N tokens' gates r, which are in m; the kind is the same for the grid.  rate: of the lane's channels;
-// near: all the warp's rates lie in [0, kNear].
+// near: all the warp's rates lie in [0, kNear].  done: m holds sigmoid(r) already (GCL_DECAY_POWER).
 template <typename T, int N>
-__device__ __forceinline__ void decays(const Kind &k, typename Lane<T>::P rate, bool near, typename Lane<T>::P *a, typename Lane<T>::P *m) {
+__device__ __forceinline__ void decays(const Kind &k, typename Lane<T>::P rate, bool near, typename Lane<T>::P *a, typename Lane<T>::P *m,
+                                       bool done = false) {
     using L = Lane<T>;
     if (k.decay == GCL_DECAY_SIGMOID) {
 #pragma unroll
@@ -194,7 +217,7 @@ __device__ __forceinline__ void decays(const Kind &k, typename Lane<T>::P rate, 
         }
     } else if (k.decay == GCL_DECAY_POWER) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) m[e] = L::mul(rate, sigmoid<T>(m[e]));
+        for (int e = 0; e < N; ++e) m[e] = L::mul(rate, done ? m[e] : sigmoid<T>(m[e]));
         if (sizeof(T) == 2 && near) decay_of<T, true, N>(a, m);
         else decay_of<T, false, N>(a, m);
     } else {
@@ -218,11 +241,11 @@ __device__ __forceinline__ void decays(const Kind &k, typename Lane<T>::P rate, 
 struct Header {
     int32_t blocked;               // the call does nothing (status word set, or cu_seqlens invalid)
     int32_t live;                  // cu_seqlens[n_max]
-    uint32_t ticket;               // tiles taken
+    uint32_t ticket;               // spans taken
     int32_t pad;
 };
 
-// What tiles leave each other, a packet a channel of 16 bytes that is written and read as one: the product of the tile's decays
+// What spans of tiles leave each other, a packet a channel of 16 bytes that is written and read as one: the product of the span's decays
 // and its state from zero (tag kOwn), and the state that leaves it (tag kDone).
 struct __align__(16) Packet {
     float a, own, out;
@@ -239,7 +262,7 @@ struct Params {
     int32_t *status;
     Header *head;
     int32_t *first;                // [tiles]: the first sequence that starts at or behind the tile's first token
-    Packet *chain;                 // [tiles, D], in the order of the recurrence
+    Packet *chain;                 // [spans, D], in the order of the recurrence
     float *drate_part;             // [tiles, D]
     int64_t t_max, tiles;
     int32_t n_max, D, n_cb;        // n_cb: blocks of channels
