@@ -83,8 +83,16 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ void peer_store(void *p, uint32_t rank, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
+// Stores that count their bytes on the peer's barrier when they have landed there.
+__device__ __forceinline__ void peer_send(void *p, uint64_t *bar, uint32_t rank, uint32_t v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(peer_addr(p, rank)), "r"(v),
+                 "r"(peer_addr(bar, rank))
+                 : "memory");
+}
+__device__ __forceinline__ void peer_send(void *p, uint64_t *bar, uint32_t rank, uint32_t v, uint32_t w) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.u32 [%0], {%1, %2}, [%3];" ::"r"(peer_addr(p, rank)), "r"(v),
+                 "r"(w), "r"(peer_addr(bar, rank))
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t peer_load(const void *p, uint32_t rank) {
     uint32_t v;
@@ -92,6 +100,8 @@ __device__ __forceinline__ uint32_t peer_load(const void *p, uint32_t rank) {
     return v;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// (orders no memory: a release waits for the outputs' stores of the tile before)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // ---- what a block holds of a tile beside its rows ----
@@ -220,9 +230,10 @@ __device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch
 template <int CB, int WARPS>
 struct Shared {
     float a[WARPS][CB], b[WARPS][CB];
-    float tot_a[2][kRanks - 1][CB], tot_b[2][kRanks - 1][CB];      // products and own states of the blocks before, by parity of the tile
+    float2 tot[2][kRanks - 1][CB]; // products and own states of the blocks before, by parity of the tile
     uint32_t tot_cut[2][kRanks - 1];
     uint32_t next[2];              // the next span, by parity; next[1] at first: the cluster's first
+    uint64_t sent[2];              // these have come
     Tile<WARPS * kRun> tile[2];
     int err;
     uint64_t full[2];
@@ -230,11 +241,11 @@ struct Shared {
 
 // One warp, a channel a lane (column c of s.a, s.b): from the warps' products and own states (in the order of the recurrence: from
 // the first row, REV from the last) the block's, exchanged with the cluster's blocks; then the state that enters each row into s.b.
-// `cuts`: a bit a token; a warp with one does not depend on the state before.  wait: false after a wait that ran out (then
-// nothing is waited for any more).  False: the state before did not come in time.
+// `cuts`: a bit a token; a warp with one does not depend on the state before.  False: the state before did not
+// come in time (s.err is set; then nothing is waited for any more).
 template <bool REV, int CB, int WARPS>
 __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch, int c, uint32_t rank, int par, const uint32_t *cuts,
-                                           Shared<CB, WARPS> &s, bool wait) {
+                                           Shared<CB, WARPS> &s, uint32_t phase) {
     const bool on = ch < p.D, cut = any_of<WARPS * kRun / 32>(cuts);
     float A = 1.f, h = 0.f;
     if (!cut) {
@@ -253,12 +264,11 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
         }
     }
     for (uint32_t r = rank + 1; r < kRanks; ++r) {
-        peer_store(&s.tot_a[par][rank][c], r, __float_as_uint(A));
-        peer_store(&s.tot_b[par][rank][c], r, __float_as_uint(h));
-        if (c % 32 == 0) peer_store(&s.tot_cut[par][rank], r, cut);
+        peer_send(&s.tot[par][rank][c], &s.sent[par], r, __float_as_uint(A), __float_as_uint(h));
+        if (c == 0) peer_send(&s.tot_cut[par][rank], &s.sent[par], r, cut);
     }
-    cluster_arrive();
-    cluster_wait();
+    tc::mbar_wait(&s.sent[par], phase, &s.err, GCL_DEV_WAIT_TIMEOUT);
+    const bool wait = *reinterpret_cast<volatile int *>(&s.err) == 0;
     Packet *mine = p.chain + seq * p.D + ch;
     bool ok = true, span_cut = cut;
     if (rank == kRanks - 1) {                              // the last block speaks for the span
@@ -267,8 +277,9 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
         for (int r = 0; r < kRanks - 1; ++r) {
             const bool k = s.tot_cut[par][r] != 0;
             span_cut |= k;
-            before = k ? s.tot_b[par][r][c] : fmaf(s.tot_a[par][r][c], before, s.tot_b[par][r][c]);
-            product *= s.tot_a[par][r][c];
+            const float2 t = s.tot[par][r][c];
+            before = k ? t.y : fmaf(t.x, before, t.y);
+            product *= t.x;
         }
         if (!cut) h = fmaf(A, before, h);
         A *= product;
@@ -277,7 +288,10 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
     float in = 0.f;
     if (seq > 0 && wait) ok = chain_enter(p, seq, ch, on, in);             // (the first span is cut at its first token)
     if (rank == kRanks - 1 && on && !span_cut) store_packet(mine, A, h, fmaf(A, in, h), kDone);
-    for (uint32_t r = 0; r < rank; ++r) in = s.tot_cut[par][r] ? s.tot_b[par][r][c] : fmaf(s.tot_a[par][r][c], in, s.tot_b[par][r][c]);
+    for (uint32_t r = 0; r < rank; ++r) {
+        const float2 t = s.tot[par][r][c];
+        in = s.tot_cut[par][r] ? t.y : fmaf(t.x, in, t.y);
+    }
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
         const int w = REV ? WARPS - 1 - i : i;
@@ -305,6 +319,7 @@ struct Walk {
     int narr;
     int64_t live, tiles;           // live tokens; tiles that have some
     uint32_t units, rank;
+    uint32_t phase;                // parity of the barriers of what the peers send: bit by buffer
     uint32_t parity, issued;       // of the copies into the two buffers: the next wait's; the last issued one's, inverted, and
                                    // whether any was (issuer)
 
@@ -329,6 +344,8 @@ struct Walk {
         if (tid == kIssuer) {
             tc::mbar_init(&s.full[0], 1);
             tc::mbar_init(&s.full[1], 1);
+            tc::mbar_init(&s.sent[0], 1);
+            tc::mbar_init(&s.sent[1], 1);
             tc::fence_barrier_init();
             s.err = 0;
             if (rank == 0) s.next[1] = atomicAdd(&p.head->ticket, 1u);
@@ -346,6 +363,7 @@ struct Walk {
             __syncwarp();
             borders(p, s.tile[0]);
         }
+        cluster_arrive_relaxed();
         __syncthreads();
         return true;
     }
@@ -358,35 +376,43 @@ struct Walk {
     // Takes the cluster's next span (its number reaches the blocks by the exchange).
     __device__ __forceinline__ uint32_t take() { return rank == 0 && threadIdx.x == kIssuer ? atomicAdd(&p.head->ticket, 1u) : 0; }
     // Between a tile's halves: the warps' own states are in s.a, s.b; afterwards the states that enter them in s.b.
+    // What a block receives at parity `buf` it has used when it arrives on the cluster's barrier, and the peers send there again
+    // two tiles later, after they have waited on that barrier.
     template <typename Side>
     __device__ __forceinline__ void exchange(int buf, uint32_t taken, const uint32_t *cuts, Side side) {
         const int tid = threadIdx.x, warp = tid >> 5;
         const Tile<TILE> &t = s.tile[buf];
-        if (rank == 0 && tid == kIssuer)
-            for (int r = 0; r < kRanks; ++r) peer_store(&s.next[buf], r, taken);
+        const uint32_t ph = phase >> buf & 1;
+        phase ^= 1u << buf;
+        cluster_wait();
+        if (tid == kIssuer) {
+            tc::mbar_arrive_expect_tx(&s.sent[buf], 4 + rank * (CB * 8 + 4));
+            if (rank == 0)
+                for (int r = 0; r < kRanks; ++r) peer_send(&s.next[buf], &s.sent[buf], r, taken);
+        }
         __syncthreads();
         if (warp < CB / 32) {
-            const bool wait = *reinterpret_cast<volatile int *>(&s.err) == 0;
-            if (!chain_tile<REV>(p, t.seq, t.cb * CB + tid, tid, rank, buf, cuts, s, wait)) atomicCAS(&s.err, 0, GCL_DEV_WAIT_TIMEOUT);
-        } else {
-            cluster_arrive();
-            if (warp == 2) side();
-            cluster_wait();
-            if (warp == kIssuer / 32) {
-                const uint32_t unit = s.next[buf];
-                if (unit < units) {
-                    if (tid == kIssuer) issue(unit, buf ^ 1);
-                    __syncwarp();
-                    borders(p, s.tile[buf ^ 1]);
-                }
+            if (!chain_tile<REV>(p, t.seq, t.cb * CB + tid, tid, rank, buf, cuts, s, ph)) atomicCAS(&s.err, 0, GCL_DEV_WAIT_TIMEOUT);
+        } else if (warp == 2) {
+            side();
+        } else if (warp == kIssuer / 32) {
+            tc::mbar_wait(&s.sent[buf], ph, &s.err, GCL_DEV_WAIT_TIMEOUT);
+            const uint32_t unit = s.next[buf];
+            if (unit < units) {
+                if (tid == kIssuer) issue(unit, buf ^ 1);
+                __syncwarp();
+                borders(p, s.tile[buf ^ 1]);
             }
         }
         __syncthreads();
+        cluster_arrive_relaxed();
     }
     __device__ __forceinline__ bool more(int buf) const { return s.next[buf] < units; }
     // After the last tile: a wait that ran out is reported, and copies still under way are waited for (with a limit).
     __device__ __forceinline__ void finish() {
-        __syncthreads();
+        cluster_wait();
+        cluster_arrive();                                  // (no block leaves while another may send to it)
+        cluster_wait();
         if (s.err == 0 || threadIdx.x != kIssuer) return;
         status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
         const uint64_t t0 = tc::globaltimer();
@@ -408,7 +434,7 @@ __global__ void __launch_bounds__(32 * kWarpsF, kCtasF) glr_fwd_kernel(const __g
     grid_dependency_wait();
     if (p.head->blocked) return;
     const int64_t live = p.head->live, tiles = (live + W::TILE - 1) / W::TILE;
-    W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0};
+    W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0, 0};
     if (!walk.start()) return;
     for (int buf = 0;; buf ^= 1) {
         const Tile<W::TILE> &tile = s.tile[buf];
@@ -509,7 +535,7 @@ __global__ void __launch_bounds__(32 * kWarpsB, kCtasB) glr_bwd_kernel(const __g
     grid_dependency_wait();
     if (p.head->blocked) return;
     const int64_t live = p.head->live, tiles = (live + W::TILE - 1) / W::TILE;
-    W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0};
+    W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0, 0};
     if (!walk.start()) return;
     for (int buf = 0;; buf ^= 1) {
         const Tile<W::TILE> &tile = s.tile[buf];
