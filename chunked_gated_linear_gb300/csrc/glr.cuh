@@ -1,6 +1,8 @@
 // glr.cuh -- gated linear recurrence h_t = a_t h_{t-1} + m(a_t) u_t: what its kernels share.
 #pragma once
 
+#include <type_traits>
+
 #include "dla.cuh"
 #include "f32x2.cuh"
 
@@ -119,14 +121,6 @@ __device__ __forceinline__ typename Lane<T>::P exps(typename Lane<T>::P x) {
     if (sizeof(T) == 2) x = Lane<T>::mul(x, Lane<T>::all(1.4426950408889634f));
     return Lane<T>::map(x, [](float v) { return fexp2<T>(v); });
 }
-// sigmoid(x).  (exp(-x) = infinity gives 0.)
-template <typename T>
-__device__ __forceinline__ typename Lane<T>::P sigmoid(typename Lane<T>::P x) {
-    using L = Lane<T>;
-    if (sizeof(T) == 2) x = L::map(L::mul(x, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(v); });
-    else x = L::map(x, [](float v) { return fexp2<T>(-v); });
-    return L::map(L::add(x, L::all(1.f)), [](float v) { return frcp<T>(v); });
-}
 // sigmoid(x) and sigmoid(-x) = exp(-x) sigmoid(x), neither by a difference.
 template <typename T>
 __device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>::P &s, typename Lane<T>::P &c) {
@@ -137,19 +131,24 @@ __device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>
     s = L::map(L::add(e, L::all(1.f)), [](float v) { return frcp<T>(v); });
     c = L::mul(e, s);
 }
-
-// sigmoid(x) and sigmoid(z) of 16-bit rows by one reciprocal, that of (1 + exp(-x)) (1 + exp(-z)): a reciprocal takes the
+// The same of x and z.  16-bit rows: by one reciprocal, that of (1 + exp(-x)) (1 + exp(-z)), since a reciprocal takes the
 // special-function unit as long as two exponentials.  Below 2^-63 (x < -43.6) they stay at 2^-63, so that the product is finite.
 template <typename T>
-__device__ __forceinline__ void two_sigmoids(typename Lane<T>::P x, typename Lane<T>::P z, typename Lane<T>::P &sx, typename Lane<T>::P &sz) {
+__device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>::P z, typename Lane<T>::P &sx, typename Lane<T>::P &cx,
+                                         typename Lane<T>::P &sz, typename Lane<T>::P &cz) {
     using L = Lane<T>;
-    auto one_and_exp = [](typename L::P v) {
-        return L::add(L::map(L::mul(v, L::all(-1.4426950408889634f)), [](float u) { return fexp2<T>(fminf(u, 63.f)); }), L::all(1.f));
-    };
-    const typename L::P a = one_and_exp(x), b = one_and_exp(z);
+    if (sizeof(T) == 4) {
+        sigmoids<T>(x, sx, cx);
+        sigmoids<T>(z, sz, cz);
+        return;
+    }
+    auto ex = [](typename L::P v) { return L::map(L::mul(v, L::all(-1.4426950408889634f)), [](float u) { return fexp2<T>(fminf(u, 63.f)); }); };
+    const typename L::P e = ex(x), f = ex(z), a = L::add(e, L::all(1.f)), b = L::add(f, L::all(1.f));
     const typename L::P r = L::map(L::mul(a, b), [](float u) { return frcp<T>(u); });
     sx = L::mul(b, r);
     sz = L::mul(a, r);
+    cx = L::mul(e, sx);
+    cz = L::mul(f, sz);
 }
 
 // q = 1 - exp(-y) for 0 <= y <= kNear: y P(y), P the polynomial of degree 6 that meets (1 - exp(-y)) / y at the Chebyshev points
@@ -202,39 +201,53 @@ __device__ __forceinline__ void decay_of(typename Lane<T>::P *a, typename Lane<T
     }
 }
 
-// a and m(a) of N tokens' gates r, which are in m; the kind is the same for the grid.  rate: of the lane's channels;
-// near: all the warp's rates lie in [0, kNear].  done: m holds sigmoid(r) already (GCL_DECAY_POWER).
-template <typename T, int N>
-__device__ __forceinline__ void decays(const Kind &k, typename Lane<T>::P rate, bool near, typename Lane<T>::P *a, typename Lane<T>::P *m,
-                                       bool done = false) {
+// The gates of N tokens: a, m(a) and the input gate's sigmoid from r and g (g is not read without gate: GATE false, sg = 1).
+// rate: of the lane's channels; near: all the warp's rates lie in [0, kNear].
+template <typename T, int DECAY, int MIX, bool GATE, int N>
+__device__ __forceinline__ void gates(typename Lane<T>::P rate, bool near, const typename Lane<T>::P *r, const typename Lane<T>::P *g,
+                                      typename Lane<T>::P *a, typename Lane<T>::P *m, typename Lane<T>::P *sg) {
     using L = Lane<T>;
-    if (k.decay == GCL_DECAY_SIGMOID) {
+    using P = typename L::P;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            typename L::P s;
-            sigmoids<T>(m[e], s, m[e]);
+    for (int e = 0; e < N; ++e) {
+        P s = L::all(0.f), c = L::all(0.f), cg;
+        if (DECAY == GCL_DECAY_LOG) {
+            if (GATE) sigmoids<T>(g[e], sg[e], cg);
+            m[e] = L::mul(r[e], L::all(-1.f));
+        } else {
+            if (GATE) sigmoids<T>(r[e], g[e], s, c, sg[e], cg);
+            else sigmoids<T>(r[e], s, c);
             a[e] = s;
+            m[e] = DECAY == GCL_DECAY_SIGMOID ? c : L::mul(rate, s);
         }
-    } else if (k.decay == GCL_DECAY_POWER) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) m[e] = L::mul(rate, done ? m[e] : sigmoid<T>(m[e]));
-        if (sizeof(T) == 2 && near) decay_of<T, true, N>(a, m);
+        if (!GATE) sg[e] = L::all(1.f);
+    }
+    if (DECAY != GCL_DECAY_SIGMOID) {                      // from y = -log a in m
+        if (DECAY == GCL_DECAY_POWER && sizeof(T) == 2 && near) decay_of<T, true, N>(a, m);
         else decay_of<T, false, N>(a, m);
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) m[e] = L::mul(m[e], L::all(-1.f));
-        decay_of<T, false, N>(a, m);
     }
-    if (k.mix == GCL_MIX_ONE) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) m[e] = L::all(1.f);
-    } else if (k.mix == GCL_MIX_ROOT) {                    // 1 - a^2 = (1 - a) (1 + a); a > 1 counts as 1
-        if (k.decay == GCL_DECAY_LOG)
-#pragma unroll
-            for (int e = 0; e < N; ++e) m[e] = L::map(m[e], [](float v) { return fmaxf(v, 0.f); });
-#pragma unroll
-        for (int e = 0; e < N; ++e) m[e] = L::map(L::fma(m[e], a[e], m[e]), [](float v) { return froot<T>(v); });
+    for (int e = 0; e < N; ++e) {
+        if (MIX == GCL_MIX_ONE) m[e] = L::all(1.f);
+        if (MIX == GCL_MIX_ROOT) {                         // 1 - a^2 = (1 - a) (1 + a); a > 1 counts as 1
+            if (DECAY == GCL_DECAY_LOG) m[e] = L::map(m[e], [](float v) { return fmaxf(v, 0.f); });
+            m[e] = L::map(L::fma(m[e], a[e], m[e]), [](float v) { return froot<T>(v); });
+        }
     }
+}
+
+// Calls f(integral_constant decay, integral_constant mix, integral_constant gate) for the kind.
+template <typename F>
+inline auto for_kind(int decay, int mix, bool gate, F f) {
+    auto with_mix = [&](auto d) {
+        auto with_gate = [&](auto m) { return gate ? f(d, m, std::true_type()) : f(d, m, std::false_type()); };
+        if (mix == GCL_MIX_ONE) return with_gate(std::integral_constant<int, GCL_MIX_ONE>());
+        if (mix == GCL_MIX_COMPLEMENT) return with_gate(std::integral_constant<int, GCL_MIX_COMPLEMENT>());
+        return with_gate(std::integral_constant<int, GCL_MIX_ROOT>());
+    };
+    if (decay == GCL_DECAY_LOG) return with_mix(std::integral_constant<int, GCL_DECAY_LOG>());
+    if (decay == GCL_DECAY_SIGMOID) return with_mix(std::integral_constant<int, GCL_DECAY_SIGMOID>());
+    return with_mix(std::integral_constant<int, GCL_DECAY_POWER>());
 }
 
 // What the launches of a call leave each other at the front of the workspace.
@@ -267,6 +280,17 @@ struct Params {
     int64_t t_max, tiles;
     int32_t n_max, D, n_cb;        // n_cb: blocks of channels
 };
+
+// Launchers, one pair for each type of the rows.
+template <typename T>
+cudaError_t launch_fwd(const Params &p, cudaStream_t s);
+template <typename T>
+cudaError_t launch_bwd(const Params &p, cudaStream_t s);
+
+void launch_setup(const Params &p, const float *in_state, float *out_state, int tile, int blocks, cudaStream_t s);
+
+constexpr int kTileF = 128, kTileB = 64;               // tokens of a tile, forward and backward
+constexpr int kRanks = 4;                              // tiles of a span
 
 }  // namespace glr
 }  // namespace gcl

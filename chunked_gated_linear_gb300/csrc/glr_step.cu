@@ -23,7 +23,7 @@ struct StepParams {
     int32_t batch, n_slots, D;
 };
 
-template <typename T>
+template <typename T, int DECAY, int MIX, bool GATE>
 __global__ void __launch_bounds__(kStepThreads) glr_step_kernel(const StepParams p) {
     constexpr int V = Lane<T>::V;
     if (dla::call_blocked(p.status, p.slots ? p.batch : 0, [&](int64_t i) { return p.slots[i] >= p.n_slots; })) return;
@@ -58,18 +58,17 @@ __global__ void __launch_bounds__(kStepThreads) glr_step_kernel(const StepParams
     dla::load8f(st, h);
     load(p.x, x);
     load(p.r, m);
-    if (p.i.p) load(p.i, g);
+    if (GATE) load(p.i, g);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         rate[k] = L::all(0.f);
-        if (p.kind.decay == GCL_DECAY_POWER) rate[k] = L::load(p.kind.rate + ch + k * V);
+        if (DECAY == GCL_DECAY_POWER) rate[k] = L::load(p.kind.rate + ch + k * V);
     }
+    typename L::P sg[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        decays<T, 1>(p.kind, rate[k], false, a + k, m + k);
-        if (p.i.p) x[k] = L::mul(x[k], sigmoid<T>(g[k]));
-        L::store(h + k * V, L::fma(a[k], L::load(h + k * V), L::mul(m[k], x[k])));
-    }
+    for (int k = 0; k < N; ++k) gates<T, DECAY, MIX, GATE, 1>(rate[k], false, m + k, g + k, a + k, m + k, sg + k);
+#pragma unroll
+    for (int k = 0; k < N; ++k) L::store(h + k * V, L::fma(a[k], L::load(h + k * V), L::mul(m[k], GATE ? L::mul(x[k], sg[k]) : x[k])));
     dla::store4f(st, h);
     dla::store4f(st + 4, h + 4);
     dla::store4f(o, h);
@@ -79,7 +78,10 @@ __global__ void __launch_bounds__(kStepThreads) glr_step_kernel(const StepParams
 template <typename T>
 cudaError_t launch_step(const StepParams &p, cudaStream_t s) {
     const int64_t n = (int64_t)p.batch * (p.D / 8);
-    glr_step_kernel<T><<<(unsigned)((n + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(p);
+    for_kind(p.kind.decay, p.kind.mix, p.i.p != nullptr, [&](auto d, auto m, auto g) {
+        glr_step_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>
+            <<<(unsigned)((n + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(p);
+    });
     return cudaGetLastError();
 }
 
