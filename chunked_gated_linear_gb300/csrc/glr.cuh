@@ -290,7 +290,8 @@ cudaError_t launch_bwd(const Params &p, cudaStream_t s);
 void launch_setup(const Params &p, const float *in_state, float *out_state, int tile, int blocks, cudaStream_t s);
 
 constexpr int kTileF = 128, kTileB = 64;               // tokens of a tile, forward and backward
-constexpr int kRanks = 4;                              // tiles of a span
+constexpr int kRanks = 2;                              // tiles of a span (65,536 tokens of 2,048 channels: 246 us; four 251, eight 297;
+                                                       // of 1,024 channels, twice the tokens, 282 and 268)
 
 }  // namespace glr
 }  // namespace gcl

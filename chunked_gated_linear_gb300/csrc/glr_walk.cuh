@@ -42,9 +42,9 @@ __device__ __forceinline__ void peer_send(void *p, uint64_t *bar, uint32_t rank,
                  "r"(peer_addr(bar, rank))
                  : "memory");
 }
-__device__ __forceinline__ void peer_send(void *p, uint64_t *bar, uint32_t rank, uint32_t v, uint32_t w) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.u32 [%0], {%1, %2}, [%3];" ::"r"(peer_addr(p, rank)), "r"(v),
-                 "r"(w), "r"(peer_addr(bar, rank))
+__device__ __forceinline__ void peer_send(void *p, uint64_t *bar, uint32_t rank, float a, float b, uint32_t c) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %3}, [%4];" ::"r"(peer_addr(p, rank)),
+                 "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(c), "r"(peer_addr(bar, rank))
                  : "memory");
 }
 __device__ __forceinline__ uint32_t peer_load(const void *p, uint32_t rank) {
@@ -185,8 +185,7 @@ __device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch
 template <int CB, int RUN>
 struct Shared {
     float a[kWarps][CB], b[kWarps][CB];
-    float2 tot[2][kRanks - 1][CB]; // products and own states of the blocks before, by parity of the tile
-    uint32_t tot_cut[2][kRanks - 1];
+    float4 sent_own[2][kRanks - 1][CB];    // product and own state of the blocks before (z: whether one is cut), by parity of the tile
     uint32_t next[2];              // the next span, by parity; next[1] at first: the cluster's first
     uint64_t sent[2];              // these have come
     Tile<kWarps * RUN> tile[2];
@@ -220,37 +219,32 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) h = bits_of<RUN>(cuts, REV ? kWarps - 1 - i : i) ? b[i] : fmaf(a[i], h, b[i]);
     }
-    for (uint32_t r = rank + 1; r < kRanks; ++r) {
-        peer_send(&s.tot[par][rank][c], &s.sent[par], r, __float_as_uint(A), __float_as_uint(h));
-        if (c == 0) peer_send(&s.tot_cut[par][rank], &s.sent[par], r, cut);
-    }
+    for (uint32_t r = rank + 1; r < kRanks; ++r) peer_send(&s.sent_own[par][rank][c], &s.sent[par], r, A, h, cut);
     Packet k[kWindow];
     if (seq > 0) load_window(p, seq, 0, ch, on, k);        // (under way while the peers' states come)
     tc::mbar_wait(&s.sent[par], phase, &s.err, GCL_DEV_WAIT_TIMEOUT);
     const bool wait = *reinterpret_cast<volatile int *>(&s.err) == 0;
     Packet *mine = p.chain + seq * p.D + ch;
-    bool ok = true, span_cut = cut;
-    if (rank == kRanks - 1) {                              // the last block speaks for the span
-        float before = 0.f, product = 1.f;
+    // the blocks before this one, composed
+    float A0 = 1.f, h0 = 0.f;
+    bool ok = true, cut0 = false;
 #pragma unroll
-        for (int r = 0; r < kRanks - 1; ++r) {
-            const bool q = s.tot_cut[par][r] != 0;
-            const float2 t = s.tot[par][r][c];
-            span_cut |= q;
-            before = q ? t.y : fmaf(t.x, before, t.y);
-            product *= t.x;
+    for (int r = 0; r < kRanks - 1; ++r)
+        if (r < rank) {
+            const float4 t = s.sent_own[par][r][c];
+            const bool q = __float_as_uint(t.z) != 0;
+            cut0 |= q;
+            h0 = q ? t.y : fmaf(t.x, h0, t.y);
+            A0 *= t.x;
         }
-        if (!cut) h = fmaf(A, before, h);
-        A *= product;
-        if (on) store_packet(mine, A, h, h, span_cut ? kDone : kOwn);
-    }
+    const bool speaks = rank == kRanks - 1 && on, span_cut = cut || cut0;  // (the last block speaks for the span)
+    if (!cut) h = fmaf(A, h0, h);
+    A *= A0;
+    if (speaks) store_packet(mine, A, h, h, span_cut ? kDone : kOwn);
     float in = 0.f;
     if (seq > 0 && wait) ok = chain_enter(p, seq, ch, on, k, in);          // (the first span is cut at its first token)
-    if (rank == kRanks - 1 && on && !span_cut) store_packet(mine, A, h, fmaf(A, in, h), kDone);
-    for (uint32_t r = 0; r < rank; ++r) {
-        const float2 t = s.tot[par][r][c];
-        in = s.tot_cut[par][r] ? t.y : fmaf(t.x, in, t.y);
-    }
+    if (speaks && !span_cut) store_packet(mine, A, h, fmaf(A, in, h), kDone);
+    in = cut0 ? h0 : fmaf(A0, in, h0);
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
         const int w = REV ? kWarps - 1 - i : i;
@@ -344,7 +338,7 @@ struct Walk {
         phase ^= 1u << buf;
         cluster_wait();
         if (tid == kIssuer) {
-            tc::mbar_arrive_expect_tx(&s.sent[buf], 4 + rank * (CB * 8 + 4));
+            tc::mbar_arrive_expect_tx(&s.sent[buf], 4 + rank * CB * 16);
             if (rank == 0)
                 for (int r = 0; r < kRanks; ++r) peer_send(&s.next[buf], &s.sent[buf], r, taken);
         }
