@@ -90,15 +90,15 @@ gcl_status_t run(const char *fn, const gcl_block_args *a, bool backward, cudaStr
     for (const void *w : {a->post_weight, a->pre_weight, (const void *)a->workspace})
         if (!dla::aligned(w, 16)) return fail(GCL_ERR_INVALID_ARG, "%s: weights and the workspace must be 16-byte aligned", fn);
     Params p{};
-    p.y = dla::rows(a->y); p.gate = dla::rows(a->gate); p.x = dla::rows(a->x);
+    p.y = Rows(a->y); p.gate = Rows(a->gate); p.x = Rows(a->x);
     if (!backward) {
-        p.xo = dla::rows(a->xo);
-        p.z = dla::rows(a->z);
+        p.xo = Rows(a->xo);
+        p.z = Rows(a->z);
     } else {
         if ((a->dpost_weight && !a->post_weight) || (a->dpre_weight && (!a->pre_weight || !a->dz.ptr)))
             return fail(GCL_ERR_INVALID_ARG, "%s: a weight's gradient needs the weight (and dpre_weight dz)", fn);
-        p.dxo = dla::rows(a->dxo); p.dz = dla::rows(a->dz);
-        p.dy = dla::rows(a->dy); p.dgate = dla::rows(a->dgate); p.dx = dla::rows(a->dx);
+        p.dxo = Rows(a->dxo); p.dz = Rows(a->dz);
+        p.dy = Rows(a->dy); p.dgate = Rows(a->dgate); p.dx = Rows(a->dx);
         if (a->dpost_weight || a->dpre_weight) {
             const size_t bytes = bwd_workspace(a);
             if (!a->workspace || a->workspace_bytes < bytes)

@@ -5,8 +5,12 @@
 //   d = dxo + r (u - xo r^2 M / D),   dy = r_y (d v / n - n P / D),   P = sum(d v)
 // P is linear in d, so its three parts sum(dxo v), sum(u v), sum(xo v) cross the row's threads together with S and M: a row
 // has two reductions (y's own length first, on which xo depends).
-// HBM-bound: rows are read and written once.  A row is held by TPR threads, VPT vectors of eight values each, as loaded.
+// Rows are read and written once; a row is held by TPR threads, VPT vectors of eight values each, as loaded.  Bound by HBM and
+// issue together, so arithmetic goes by fp32 pairs, choices are made for a vector and not for a value, and weights stay in
+// registers over a block's rows.  XFIG
 #pragma once
+
+#include <atomic>
 
 #include "dla.cuh"
 #include "dla_simt.cuh"
@@ -14,8 +18,17 @@
 namespace gcl {
 namespace blk {
 
-using dla::Rows;
-using dla::row_ptr;
+// A gcl_rows, and how far (in bytes) a thread moves from one of its rows to the next: by d, and by w more where the head index
+// wraps.  (Here, not in registers: two for each of eight arrays.)
+struct Rows : dla::Rows {
+    int64_t d, w;
+    Rows() = default;
+    Rows(const gcl_rows &r) : dla::Rows(dla::rows(r)), d(0), w(0) {}
+    void step(int64_t rows, int H, int esize) {
+        d = (rows / H * st + rows % H * sh) * esize;
+        w = (st - H * sh) * esize;
+    }
+};
 
 struct Params {
     Rows y, gate, x, xo, z, dxo, dz, dy, dgate, dx;
@@ -30,6 +43,7 @@ struct Params {
     float scale, eps;
     int32_t cut;                   // dropout: half-words below are dropped (0: none)
     int32_t post, pre, act;
+    int32_t dh;                    // heads from a thread's row to its next, modulo H
 };
 
 // Philox4x32-10 of a 64-bit counter half, offset and key.
@@ -49,34 +63,78 @@ __device__ __forceinline__ uint4 philox(uint64_t at, uint64_t offset, uint64_t s
     return make_uint4(c0, c1, c2, c3);
 }
 
-// The mask of a vector's eight values, bit e set where value e is kept.
-__device__ __forceinline__ uint32_t kept(int32_t cut, int64_t vec, uint64_t seed, uint64_t offset) {
-    if (!cut) return 0xFFu;
+using P = float2;                  // two fp32 values
+constexpr int kPairs = 4;          // of a vector
+
+__device__ __forceinline__ P mul2(P a, P b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ P add2(P a, P b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ P fma2(P a, P b, P c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ P both(float x) { return make_float2(x, x); }
+template <typename F>
+__device__ __forceinline__ P map(P x, F f) { return make_float2(f(x.x), f(x.y)); }
+
+// The mask of a vector's eight values, bit e set where value e is kept: half-word e of its block is at least `cut`.
+// (cut16: cut in the upper half; an upper half-word is compared with the lower one still below it.)
+__device__ __forceinline__ uint32_t kept(uint32_t cut16, int64_t vec, uint64_t seed, uint64_t offset) {
     const uint4 w = philox((uint64_t)vec, offset, seed);
     const uint32_t word[4] = {w.x, w.y, w.z, w.w};
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t half = e & 1 ? word[e / 2] >> 16 : word[e / 2] & 0xFFFFu;
-        m |= (half >= (uint32_t)cut ? 1u : 0u) << e;
-    }
+    for (int e = 0; e < 8; ++e) m |= ((e & 1 ? word[e / 2] : word[e / 2] << 16) >= cut16 ? 1u : 0u) << e;
     return m;
 }
+__device__ __forceinline__ P masked(P x, uint32_t mask, int k) {
+    return make_float2(mask >> 2 * k & 1 ? x.x : 0.f, mask >> (2 * k + 1) & 1 ? x.y : 0.f);
+}
 
-// act(g) and its derivative.
+// exp(-x) and 1 / x: the accurate ones for fp32 rows, the special-function unit's (subnormals flushed) for 16-bit rows.
 template <typename T>
-__device__ __forceinline__ void activation(int act, float g, float &a, float &da) {
+__device__ __forceinline__ float exp_minus(float x) {
+    if (sizeof(T) == 4) return expf(-x);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * -1.4426950408889634f));
+    return y;
+}
+template <typename T>
+__device__ __forceinline__ float reciprocal(float x) {
+    if (sizeof(T) == 4) return 1.f / x;
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// act(g) of a vector, and with SLOPE its derivative.
+template <typename T, bool SLOPE>
+__device__ __forceinline__ void activation(int act, const P *g, P *a, P *da) {
     if (act == GCL_ACT_NONE) {
-        a = g;
-        da = 1.f;
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            a[k] = g[k];
+            if (SLOPE) da[k] = both(1.f);
+        }
         return;
     }
-    // sigmoid(g) and sigmoid(-g), neither by a difference
-    const float e = sizeof(T) == 4 ? expf(-fabsf(g)) : __expf(-fabsf(g));
-    const float hi = sizeof(T) == 4 ? 1.f / (1.f + e) : __fdividef(1.f, 1.f + e), lo = e * hi;
-    const float s = g >= 0.f ? hi : lo, c = g >= 0.f ? lo : hi;
-    a = act == GCL_ACT_SILU ? g * s : s;
-    da = act == GCL_ACT_SILU ? s * fmaf(g, c, 1.f) : s * c;
+    P s[kPairs], c[kPairs];                                // sigmoid(g) and sigmoid(-g) = exp(-g) sigmoid(g), neither by a difference
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        // (the largest exponent leaves 1 + exp(-g) finite, so that its product with the reciprocal is)
+        const P e = map(g[k], [](float v) { return exp_minus<T>(fmaxf(v, -87.f)); });
+        s[k] = map(add2(e, both(1.f)), [](float v) { return reciprocal<T>(v); });
+        if (SLOPE) c[k] = mul2(e, s[k]);
+    }
+    if (act == GCL_ACT_SILU) {
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            a[k] = mul2(g[k], s[k]);
+            if (SLOPE) da[k] = mul2(s[k], fma2(g[k], c[k], both(1.f)));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            a[k] = s[k];
+            if (SLOPE) da[k] = mul2(s[k], c[k]);
+        }
+    }
 }
 
 // Eight consecutive values of a row as loaded.
@@ -87,47 +145,89 @@ struct Vec {
 #pragma unroll
         for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = on ? reinterpret_cast<const uint4 *>(p)[e] : make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void get(float *f) const { dla::load8f(reinterpret_cast<const T *>(v), f); }
-    static __device__ __forceinline__ void store(T *p, const float *f) {
+    __device__ __forceinline__ void get(P *f) const {
+        float x[8];
+        dla::load8f(reinterpret_cast<const T *>(v), x);
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) f[k] = make_float2(x[2 * k], x[2 * k + 1]);
+    }
+    static __device__ __forceinline__ void store(T *p, const P *f) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            x[2 * k] = f[k].x;
+            x[2 * k + 1] = f[k].y;
+        }
         Vec o;
-        dla::store4f(reinterpret_cast<T *>(o.v), f);
-        dla::store4f(reinterpret_cast<T *>(o.v) + 4, f + 4);
+        dla::store4f(reinterpret_cast<T *>(o.v), x);
+        dla::store4f(reinterpret_cast<T *>(o.v) + 4, x + 4);
 #pragma unroll
         for (int e = 0; e < (int)sizeof(T) / 2; ++e) reinterpret_cast<uint4 *>(p)[e] = o.v[e];
     }
 };
 
-constexpr int threads_of(int tpr) { return tpr > 256 ? tpr : 256; }
+constexpr int threads_of(int tpr) { return tpr > 128 ? tpr : 128; }
 
 // Sums over a row's threads.  Rows of several warps pass through shared memory; `turn` alternates two buffers, so that
-// one barrier a reduction is enough.
+// one barrier a reduction is enough.  Of five sums four cross a warp together: lanes first part the sums among them (6 shuffles
+// instead of 20), and the warps' sums are added by lanes side by side.
 template <int TPR, int NS>
 struct RowSum {
     static constexpr int W = TPR / 32 > 0 ? TPR / 32 : 1;          // warps of a row
     static constexpr int R = threads_of(TPR) / TPR;                // rows of a block
-    float (*buf)[R][W][NS];
+    float (*buf)[R][NS][W];
     int turn;
+    static __device__ __forceinline__ float across(float x, int most) {
+#pragma unroll
+        for (int d = most / 2; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        return x;
+    }
     template <int N>
     __device__ __forceinline__ void operator()(float *s) {
+        if (TPR <= 32) {
 #pragma unroll
-        for (int d = (TPR < 32 ? TPR : 32) / 2; d; d >>= 1)
+            for (int i = 0; i < N; ++i) s[i] = across(s[i], TPR);
+            return;
+        }
+        const int row = threadIdx.x / TPR, warp = threadIdx.x % TPR / 32, lane = threadIdx.x & 31;
+        float (*b)[W] = buf[turn][row];
+        if (N == 5) {
+            const bool hi = lane & 16, mid = lane & 8;
+            float u = hi ? s[2] : s[0], v = hi ? s[3] : s[1];
+            u += __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[2], 16);
+            v += __shfl_xor_sync(0xffffffffu, hi ? s[1] : s[3], 16);
+            float c = mid ? v : u;
+            c += __shfl_xor_sync(0xffffffffu, mid ? u : v, 8);
+            c = across(c, 8);
+            const float last = across(s[4], 32);
+            if (lane % 8 == 0) b[lane / 8][warp] = c;      // (8 hi + mid: the sum's number)
+            if (lane == 0) b[4][warp] = last;
+        } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-        if (TPR <= 32) return;
-        const int row = threadIdx.x / TPR, warp = threadIdx.x % TPR / 32;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int i = 0; i < N; ++i) buf[turn][row][warp][i] = s[i];
+            for (int i = 0; i < N; ++i) {
+                const float c = across(s[i], 32);
+                if (lane == 0) b[i][warp] = c;
+            }
+        }
         __syncthreads();
+        constexpr int G = 32 / W;                          // sums that a warp adds up side by side
+        if (N == 1) {
+            s[0] = across(b[0][lane % W], W);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            s[i] = 0.f;
+            for (int i0 = 0; i0 < N; i0 += G) {
+                const int i = i0 + lane / W;
+                const float c = across(i < N ? b[i][lane % W] : 0.f, W);
 #pragma unroll
-            for (int w = 0; w < W; ++w) s[i] += buf[turn][row][w][i];
+                for (int j = i0; j < N && j < i0 + G; ++j) s[j] = __shfl_sync(0xffffffffu, c, (j - i0) * W);
+            }
         }
         turn ^= 1;
     }
 };
+__device__ __forceinline__ float sum_of(P x) {
+    return x.x + x.y;
+}
 
 __device__ __forceinline__ float inverse_length(int norm, float ss, float inv_d, float eps) {
     return norm == GCL_NORM_NONE ? 1.f : rsqrtf((norm == GCL_NORM_RMS ? ss * inv_d : ss) + eps);
@@ -148,23 +248,60 @@ __device__ __forceinline__ bool live_rows(const Params &p, int64_t &rows) {
     return true;
 }
 
-// A vector of a weight as floats; ones without weight.
+// A thread's place in an array: its first vector of row t, h.
 template <typename T>
-__device__ __forceinline__ void weight(const void *w, int at, bool on, float *f) {
-    if (w) {
-        Vec<T> r;
-        r.load(static_cast<const T *>(w) + at * 8, on);
-        r.get(f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 1.f;
-    }
+__device__ __forceinline__ char *place(const Rows &r, int64_t t, int h, int l) {
+    return static_cast<char *>(r.p) + (t * r.st + h * r.sh + l * 8) * (int)sizeof(T);
 }
+__device__ __forceinline__ void advance(char *&at, const Rows &r, bool wrap) {
+    at += r.d;
+    if (wrap) at += r.w;
+}
+template <typename T>
+__device__ __forceinline__ T *vec_at(char *at, int v, int tpr) { return reinterpret_cast<T *>(at) + v * tpr * 8; }
+
+// Vectors of eight values in shared memory, each thread's own: copied there a row ahead (asynchronously), read when needed.
+// Rows too wide for that (STAGED false) are read from memory each time.
+template <typename T, bool STAGED, int THREADS>
+__device__ __forceinline__ void stage_copy(uint4 *at, int chunk, const T *src, bool on) {
+    if (!STAGED) return;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(at + (chunk + i) * THREADS))),
+                     "l"(reinterpret_cast<const uint4 *>(src) + i), "r"(on ? 16 : 0)
+                     : "memory");
+}
+template <typename T, bool STAGED, int THREADS>
+__device__ __forceinline__ void stage_get(const uint4 *at, int chunk, const T *src, bool on, P *f) {
+    Vec<T> r;
+    if (STAGED) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = at[(chunk + i) * THREADS];
+    } else {
+        r.load(src, on);
+    }
+    r.get(f);
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void stage_wait_prev() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// 16-byte chunks of a thread's row: y, the gate, x; backwards dxo and dz too.
+template <typename T, typename S, int VPT, bool BWD>
+struct Chunks {
+    static constexpr int t = sizeof(T) / 2, s = sizeof(S) / 2;
+    static constexpr int y = 0, g = VPT * t, x = 2 * VPT * t, dxo = x + VPT * s, dz = dxo + VPT * s;
+    static constexpr int all = BWD ? dz + VPT * t : dxo;
+    static constexpr bool staged(int threads) { return 2 * all * threads * 16 <= 160 * 1024; }
+};
+
+constexpr int fwd_blocks(int tpr, int vpt) { return vpt > 2 ? 1 : 512 / threads_of(tpr); }
+constexpr int bwd_blocks(int tpr, int vpt) { return vpt > 2 ? 1 : tpr > 256 ? 1 : tpr > 128 ? 2 : 3; }
 
 template <typename T, typename S, int TPR, int VPT>
-__global__ void __launch_bounds__(threads_of(TPR)) block_fwd_kernel(const Params p) {
+__global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_fwd_kernel(const Params p) {
     constexpr int R = threads_of(TPR) / TPR;
-    __shared__ float s_sum[2][R][TPR / 32 > 0 ? TPR / 32 : 1][1];
+    __shared__ float s_sum[2][R][1][TPR / 32 > 0 ? TPR / 32 : 1];
     int64_t rows;
     if (!live_rows(p, rows)) return;
     RowSum<TPR, 1> sum{s_sum, 0};
@@ -173,302 +310,428 @@ __global__ void __launch_bounds__(threads_of(TPR)) block_fwd_kernel(const Params
     uint64_t seed = 0, offset = 0;
     if (p.cut) { seed = (uint64_t)p.rng[0]; offset = (uint64_t)p.rng[1]; }
     const float keep = p.cut ? p.scale * (65536.f / (65536 - p.cut)) : p.scale;
-    for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < rows; row0 += (int64_t)gridDim.x * R) {
-        const int64_t row = row0 + threadIdx.x / TPR, t = p.H == 1 ? row : row / p.H;
-        const int h = p.H == 1 ? 0 : (int)(row - t * p.H);
-        const bool live = row < rows;
-        Vec<T> y[VPT], g[VPT];
-        Vec<S> x[VPT];
+    Vec<T> w1[VPT], w2[VPT];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int at = l + v * TPR;
-            const bool on = live && at < nv && GCL_IN_BOUNDS(t, p.t_max, p.status);
-            y[v].load(row_ptr<const T>(p.y, t, h) + at * 8, on);
-            if (p.gate.p) g[v].load(row_ptr<const T>(p.gate, t, h) + at * 8, on);
-            if (p.x.p) x[v].load(row_ptr<const S>(p.x, t, h) + at * 8, on);
-        }
-        float ry = 1.f;
-        if (p.post != GCL_NORM_NONE) {
-            float ss = 0.f;
+    for (int v = 0; v < VPT; ++v) {
+        const bool on = l + v * TPR < nv;
+        if (p.w_post) w1[v].load(static_cast<const T *>(p.w_post) + (l + v * TPR) * 8, on);
+        if (p.w_pre) w2[v].load(static_cast<const T *>(p.w_pre) + (l + v * TPR) * 8, on);
+    }
+    using C = Chunks<T, S, VPT, false>;
+    constexpr int TH = threads_of(TPR);
+    constexpr bool ST = C::staged(TH);
+    extern __shared__ __align__(16) uint4 s_rows[];        // [2][chunks][TH]
+    const int64_t step = (int64_t)gridDim.x * R;
+    int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / TPR;
+    int64_t t = p.H == 1 ? row : row / p.H;
+    int h = p.H == 1 ? 0 : (int)(row - t * p.H);
+    char *cy = place<T>(p.y, t, h, l), *cg = place<T>(p.gate, t, h, l), *cx = place<S>(p.x, t, h, l);
+    char *co = place<S>(p.xo, t, h, l), *cz = place<T>(p.z, t, h, l);
+    auto stage = [&](int64_t r, int buf) {                 // row r, at the cursors; moves them on
+        uint4 *to = s_rows + buf * C::all * TH + threadIdx.x;
+        if (r - threadIdx.x / TPR < rows) {                // (the same for the block)
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                float f[8];
-                y[v].get(f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+                const bool on = r < rows && l + v * TPR < nv;
+                const T *none = static_cast<const T *>(p.y.p);
+                stage_copy<T, ST, TH>(to, C::y + v * C::t, on ? vec_at<const T>(cy, v, TPR) : none, on);
+                if (p.gate.p) stage_copy<T, ST, TH>(to, C::g + v * C::t, on ? vec_at<const T>(cg, v, TPR) : none, on);
+                if (p.x.p) stage_copy<S, ST, TH>(to, C::x + v * C::s, on ? vec_at<const S>(cx, v, TPR) : reinterpret_cast<const S *>(none), on);
             }
-            sum.template operator()<1>(&ss);
-            ry = inverse_length(p.post, ss, inv_d, p.eps);
         }
-        float xo[VPT][8], ss = 0.f;
+        stage_commit();
+    };
+    stage(row, 0);
+    int buf = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < rows; row0 += step, buf ^= 1) {
+        const bool live = row < rows;
+        const bool wrap = (h += p.dh) >= p.H;
+        if (wrap) h -= p.H;
+        char *here_cy = cy, *here_cg = cg, *here_cx = cx;  // (of this row, where it is read from memory)
+        advance(cy, p.y, wrap);
+        advance(cg, p.gate, wrap);
+        advance(cx, p.x, wrap);
+        stage(row + step, buf ^ 1);
+        stage_wait_prev();
+        const uint4 *in = s_rows + buf * C::all * TH + threadIdx.x;
+        float scale = keep;
+        if (p.post != GCL_NORM_NONE) {
+            P q = both(0.f);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                P f[kPairs];
+                stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, f);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) q = fma2(f[k], f[k], q);
+            }
+            float ss = sum_of(q);
+            sum.template operator()<1>(&ss);
+            scale *= inverse_length(p.post, ss, inv_d, p.eps);
+        }
+        P xo[VPT][kPairs], q = both(0.f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int at = l + v * TPR;
-            const bool on = live && at < nv;
-            float w[8];
-            y[v].get(xo[v]);
-            const uint32_t mask = kept(p.cut, row * nv + at, seed, offset);
-            weight<T>(p.w_post, at, on, w);
+            const bool on = live && l + v * TPR < nv;
+            P w[kPairs];
+            stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, xo[v]);
+            if (p.w_post) {
+                w1[v].get(w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xo[v][e] *= ry * (mask >> e & 1 ? keep : 0.f) * w[e];
+                for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], w[k]);
+            }
             if (p.gate.p) {
-                g[v].get(w);
+                P a[kPairs];
+                stage_get<T, ST, TH>(in, C::g + v * C::t, vec_at<const T>(here_cg, v, TPR), live && l + v * TPR < nv, w);
+                activation<T, false>(p.act, w, a, nullptr);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float a, da;
-                    activation<T>(p.act, w[e], a, da);
-                    xo[v][e] *= a;
-                }
+                for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], a[k]);
+            }
+            if (p.cut) {
+                const uint32_t mask = kept((uint32_t)p.cut << 16, row * nv + l + v * TPR, seed, offset);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) xo[v][k] = masked(xo[v][k], mask, k);
             }
             if (p.x.p) {
-                x[v].get(w);
+                stage_get<S, ST, TH>(in, C::x + v * C::s, vec_at<const S>(here_cx, v, TPR), live && l + v * TPR < nv && p.x.p, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) xo[v][e] += w[e];
+                for (int k = 0; k < kPairs; ++k) xo[v][k] = fma2(xo[v][k], both(scale), w[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], both(scale));
             }
-            if (on && p.xo.p) Vec<S>::store(row_ptr<S>(p.xo, t, h) + at * 8, xo[v]);
+            if (on && p.xo.p) Vec<S>::store(vec_at<S>(co, v, TPR), xo[v]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(xo[v][e], xo[v][e], ss);
+            for (int k = 0; k < kPairs; ++k) q = fma2(xo[v][k], xo[v][k], q);
         }
-        if (!p.z.p) continue;
         float r = 1.f;
-        if (p.pre != GCL_NORM_NONE) {
+        if (p.z.p && p.pre != GCL_NORM_NONE) {
+            float ss = sum_of(q);
             sum.template operator()<1>(&ss);
             r = inverse_length(p.pre, ss, inv_d, p.eps);
         }
+        if (p.z.p)
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int at = l + v * TPR;
-            const bool on = live && at < nv;
-            float w[8];
-            weight<T>(p.w_pre, at, on, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xo[v][e] *= r * w[e];
-            if (on) Vec<T>::store(row_ptr<T>(p.z, t, h) + at * 8, xo[v]);
+            for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], both(r));
+            if (p.w_pre) {
+                P w[kPairs];
+                w2[v].get(w);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], w[k]);
+            }
+            if (live && l + v * TPR < nv) Vec<T>::store(vec_at<T>(cz, v, TPR), xo[v]);
         }
+        advance(co, p.xo, wrap);
+        advance(cz, p.z, wrap);
+        row += step;
     }
 }
 
-// Wide rows keep the sums of the weights' gradients in shared memory (each thread its own values), others in registers.
-constexpr bool sums_in_smem(int vpt) { return vpt > 1; }
+// The widest rows keep the sums of the weights' gradients in shared memory (each thread its own values), others in registers.
+constexpr bool sums_in_smem(int vpt) { return vpt > 2; }
 
 template <typename T, typename S, int TPR, int VPT>
-__global__ void __launch_bounds__(threads_of(TPR)) block_bwd_kernel(const Params p) {
+__global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_bwd_kernel(const Params p) {
     constexpr int R = threads_of(TPR) / TPR;
     constexpr bool SM = sums_in_smem(VPT);
-    __shared__ float s_sum[2][R][TPR / 32 > 0 ? TPR / 32 : 1][5];
-    __shared__ float s_dw[R > 1 ? R : 1][R > 1 ? TPR * 8 : 1];
-    extern __shared__ __align__(16) float s_wide[];        // [2][VPT][8][TPR]
+    __shared__ float s_sum[2][R][5][TPR / 32 > 0 ? TPR / 32 : 1];
+    __shared__ P s_dw[R > 1 ? R : 1][R > 1 ? TPR * VPT * kPairs : 1];
+    using C = Chunks<T, S, VPT, true>;
+    constexpr int TH = threads_of(TPR);
+    constexpr bool ST = C::staged(TH);
+    extern __shared__ __align__(16) uint4 s_rows[];        // [2][chunks][TH]
+    P *s_wide = reinterpret_cast<P *>(s_rows + (ST ? 2 * C::all * TH : 0));           // [2][VPT][kPairs][TPR]
     launch_dependents();                                   // (the weights' sums wait for this grid's end)
     int64_t rows;
     if (!live_rows(p, rows)) return;
     RowSum<TPR, 5> sum{s_sum, 0};
     const int l = threadIdx.x % TPR, nv = p.D / 8;
     const float inv_d = 1.f / p.D;
-    const float post_d = p.post == GCL_NORM_RMS ? inv_d : 1.f, pre_d = p.pre == GCL_NORM_RMS ? inv_d : 1.f;
     uint64_t seed = 0, offset = 0;
     if (p.cut) { seed = (uint64_t)p.rng[0]; offset = (uint64_t)p.rng[1]; }
     const float keep = p.cut ? p.scale * (65536.f / (65536 - p.cut)) : p.scale;
-    float dw[2][SM ? 1 : VPT][8];
+    Vec<T> w1[VPT], w2[VPT];
+    P dw[2][SM ? 1 : VPT][kPairs];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int v = 0; v < VPT; ++v) {
+        const bool on = l + v * TPR < nv;
+        if (p.w_post) w1[v].load(static_cast<const T *>(p.w_post) + (l + v * TPR) * 8, on);
+        if (p.w_pre) w2[v].load(static_cast<const T *>(p.w_pre) + (l + v * TPR) * 8, on);
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (SM) s_wide[((k * VPT + v) * 8 + e) * TPR + l] = 0.f;
-                else dw[k][SM ? 0 : v][e] = 0.f;
+            for (int k = 0; k < kPairs; ++k) {
+                if (SM) s_wide[((i * VPT + v) * kPairs + k) * TPR + l] = both(0.f);
+                else dw[i][SM ? 0 : v][k] = both(0.f);
             }
-    auto add = [&](int k, int v, int e, float a) {
-        if (SM) s_wide[((k * VPT + v) * 8 + e) * TPR + l] += a;
-        else dw[k][SM ? 0 : v][e] += a;
-    };
-    for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < rows; row0 += (int64_t)gridDim.x * R) {
-        const int64_t row = row0 + threadIdx.x / TPR, t = p.H == 1 ? row : row / p.H;
-        const int h = p.H == 1 ? 0 : (int)(row - t * p.H);
-        const bool live = row < rows;
-        Vec<T> y[VPT], g[VPT], dz[VPT];
-        Vec<S> x[VPT], dxo[VPT];
-        uint32_t mask[VPT];
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int at = l + v * TPR;
-            const bool on = live && at < nv && GCL_IN_BOUNDS(t, p.t_max, p.status);
-            y[v].load(row_ptr<const T>(p.y, t, h) + at * 8, on);
-            if (p.gate.p) g[v].load(row_ptr<const T>(p.gate, t, h) + at * 8, on);
-            dxo[v].load(row_ptr<const S>(p.dxo, t, h) + at * 8, on && p.dxo.p);
-            if (p.dz.p) {
-                dz[v].load(row_ptr<const T>(p.dz, t, h) + at * 8, on);
-                x[v].load(row_ptr<const S>(p.x, t, h) + at * 8, on && p.x.p);
-            }
+    }
+    auto add = [&](int i, int v, int k, P a, P b) {        // += a b
+        if (SM) {
+            P &d = s_wide[((i * VPT + v) * kPairs + k) * TPR + l];
+            d = fma2(a, b, d);
+        } else {
+            dw[i][SM ? 0 : v][k] = fma2(a, b, dw[i][SM ? 0 : v][k]);
         }
-        float ry = 1.f;
-        if (p.post != GCL_NORM_NONE) {
-            float ss = 0.f;
+    };
+    const int64_t step = (int64_t)gridDim.x * R;
+    int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / TPR;
+    int64_t t = p.H == 1 ? row : row / p.H;
+    int h = p.H == 1 ? 0 : (int)(row - t * p.H);
+    char *cy = place<T>(p.y, t, h, l), *cg = place<T>(p.gate, t, h, l), *cx = place<S>(p.x, t, h, l);
+    char *cdo = place<S>(p.dxo, t, h, l), *cdz = place<T>(p.dz, t, h, l);
+    char *cdy = place<T>(p.dy, t, h, l), *cdg = place<T>(p.dgate, t, h, l), *cdx = place<S>(p.dx, t, h, l);
+    auto stage = [&](int64_t r, int buf) {                 // row r, at the cursors
+        uint4 *to = s_rows + buf * C::all * TH + threadIdx.x;
+        if (r - threadIdx.x / TPR < rows) {                // (the same for the block)
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                float f[8];
-                y[v].get(f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-            }
-            sum.template operator()<1>(&ss);
-            ry = inverse_length(p.post, ss, inv_d, p.eps);
-        }
-        // n = y ry, w_post, act and its slope of a vector (formed again for the outputs: registers)
-        auto branch = [&](int v, float *n, float *w, float *a, float *da) {
-            const int at = l + v * TPR;
-            y[v].get(n);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) { n[e] *= ry; a[e] = 1.f; da[e] = 0.f; }
-            weight<T>(p.w_post, at, live && at < nv, w);
-            if (p.gate.p) {
-                float q[8];
-                g[v].get(q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) activation<T>(p.act, q[e], a[e], da[e]);
-            }
-        };
-        float s5[5] = {0.f, 0.f, 0.f, 0.f, 0.f};           // sums of dxo v, xo^2, u xo, u v, xo v
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            float n[8], w[8], a[8], da[8], q[8], u[8];
-            mask[v] = kept(p.cut, row * nv + l + v * TPR, seed, offset);
-            branch(v, n, w, a, da);
-            dxo[v].get(q);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                n[e] *= w[e] * (mask[v] >> e & 1 ? keep : 0.f) * a[e];          // v
-                s5[0] = fmaf(q[e], n[e], s5[0]);
-            }
-            if (p.dz.p) {
-                dz[v].get(u);
-                weight<T>(p.w_pre, l + v * TPR, live && l + v * TPR < nv, w);
-                if (p.x.p) x[v].get(q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float xo = p.x.p ? q[e] + n[e] : n[e];
-                    u[e] *= w[e];
-                    s5[1] = fmaf(xo, xo, s5[1]);
-                    s5[2] = fmaf(u[e], xo, s5[2]);
-                    s5[3] = fmaf(u[e], n[e], s5[3]);
-                    s5[4] = fmaf(xo, n[e], s5[4]);
+                const bool on = r < rows && l + v * TPR < nv;
+                const T *none = static_cast<const T *>(p.y.p);
+                const S *none_s = reinterpret_cast<const S *>(none);
+                stage_copy<T, ST, TH>(to, C::y + v * C::t, on ? vec_at<const T>(cy, v, TPR) : none, on);
+                if (p.gate.p) stage_copy<T, ST, TH>(to, C::g + v * C::t, on ? vec_at<const T>(cg, v, TPR) : none, on);
+                stage_copy<S, ST, TH>(to, C::dxo + v * C::s, on && p.dxo.p ? vec_at<const S>(cdo, v, TPR) : none_s, on && p.dxo.p);
+                if (p.dz.p) {
+                    stage_copy<T, ST, TH>(to, C::dz + v * C::t, on ? vec_at<const T>(cdz, v, TPR) : none, on);
+                    stage_copy<S, ST, TH>(to, C::x + v * C::s, on && p.x.p ? vec_at<const S>(cx, v, TPR) : none_s, on && p.x.p);
                 }
             }
         }
-        float r = 1.f, m = 0.f, P = 0.f;                   // r, r^3 M / D, P / D
+        stage_commit();
+    };
+    stage(row, 0);
+    int buf = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < rows; row0 += step, buf ^= 1) {
+        const bool live = row < rows;
+        const bool wrap = (h += p.dh) >= p.H;
+        if (wrap) h -= p.H;
+        char *here_cy = cy, *here_cg = cg, *here_cx = cx, *here_cdo = cdo, *here_cdz = cdz;        // (of this row, where it is read from memory)
+        advance(cy, p.y, wrap);
+        advance(cg, p.gate, wrap);
+        advance(cx, p.x, wrap);
+        advance(cdo, p.dxo, wrap);
+        advance(cdz, p.dz, wrap);
+        stage(row + step, buf ^ 1);
+        stage_wait_prev();
+        const uint4 *in = s_rows + buf * C::all * TH + threadIdx.x;
+        uint32_t mask[VPT];
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) mask[v] = p.cut ? kept((uint32_t)p.cut << 16, row * nv + l + v * TPR, seed, offset) : 0xffu;
+        float ry = 1.f;
+        if (p.post != GCL_NORM_NONE) {
+            P q = both(0.f);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                P f[kPairs];
+                stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, f);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) q = fma2(f[k], f[k], q);
+            }
+            float ss = sum_of(q);
+            sum.template operator()<1>(&ss);
+            ry = inverse_length(p.post, ss, inv_d, p.eps);
+        }
+        // per vector: act and its slope; then xo (v without dz), which the outputs use again
+        P a[VPT][kPairs], da[VPT][kPairs], xo[VPT][kPairs];
+        P s0 = both(0.f), s1 = s0, s2 = s0, s3 = s0, s4 = s0;          // sums of dxo v, xo^2, u xo, u v, xo v
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            P f[kPairs], w[kPairs];
+            stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, f);
+            if (p.w_post) {
+                w1[v].get(w);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) f[k] = mul2(f[k], w[k]);
+            }
+            if (p.gate.p) {
+                stage_get<T, ST, TH>(in, C::g + v * C::t, vec_at<const T>(here_cg, v, TPR), live && l + v * TPR < nv, w);
+                activation<T, true>(p.act, w, a[v], da[v]);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) f[k] = mul2(f[k], a[v][k]);
+            }
+            stage_get<S, ST, TH>(in, C::dxo + v * C::s, vec_at<const S>(here_cdo, v, TPR), live && l + v * TPR < nv && p.dxo.p, w);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                f[k] = mul2(f[k], both(ry * keep));        // v
+                if (p.cut) f[k] = masked(f[k], mask[v], k);
+                s0 = fma2(w[k], f[k], s0);
+            }
+            if (p.dz.p) {
+                P u[kPairs];
+                stage_get<T, ST, TH>(in, C::dz + v * C::t, vec_at<const T>(here_cdz, v, TPR), live && l + v * TPR < nv, u);
+                if (p.w_pre) {
+                    w2[v].get(w);
+#pragma unroll
+                    for (int k = 0; k < kPairs; ++k) u[k] = mul2(u[k], w[k]);
+                }
+                stage_get<S, ST, TH>(in, C::x + v * C::s, vec_at<const S>(here_cx, v, TPR), live && l + v * TPR < nv && p.x.p, w);                               // (zeros without x)
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) {
+                    const P o = add2(w[k], f[k]);
+                    xo[v][k] = o;
+                    s1 = fma2(o, o, s1);
+                    s2 = fma2(u[k], o, s2);
+                    s3 = fma2(u[k], f[k], s3);
+                    s4 = fma2(o, f[k], s4);
+                }
+            }
+        }
+        float s5[5] = {sum_of(s0), sum_of(s1), sum_of(s2), sum_of(s3), sum_of(s4)};
+        float r = 1.f, m = 0.f, mean = 0.f;                // r, r^3 M / D, P / D
         if (p.dz.p) {
             sum.template operator()<5>(s5);
             if (p.pre != GCL_NORM_NONE) {
                 r = inverse_length(p.pre, s5[1], inv_d, p.eps);
-                m = r * r * r * s5[2] * pre_d;
+                m = r * r * r * s5[2] * (p.pre == GCL_NORM_RMS ? inv_d : 1.f);
             }
-            P = s5[0] + r * s5[3] - m * s5[4];
+            mean = s5[0] + r * s5[3] - m * s5[4];
         } else if (p.post != GCL_NORM_NONE) {
             sum.template operator()<1>(s5);
-            P = s5[0];
+            mean = s5[0];
         }
-        P = p.post != GCL_NORM_NONE ? P * post_d : 0.f;
+        mean = p.post == GCL_NORM_NONE ? 0.f : p.post == GCL_NORM_RMS ? mean * inv_d : mean;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int at = l + v * TPR;
-            const bool on = live && at < nv;
-            float n[8], w[8], a[8], da[8], d[8], q[8];
-            branch(v, n, w, a, da);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float f = mask[v] >> e & 1 ? keep : 0.f;
-                a[e] *= f;
-                da[e] *= f;
-            }
-            dxo[v].get(d);
+            const bool on = live && l + v * TPR < nv;
+            P d[kPairs], w[kPairs], q[kPairs], n[kPairs];
+            stage_get<S, ST, TH>(in, C::dxo + v * C::s, vec_at<const S>(here_cdo, v, TPR), live && l + v * TPR < nv && p.dxo.p, d);
             if (p.dz.p) {
-                float u[8], w2[8];
-                if (p.x.p) x[v].get(q);
-                dz[v].get(u);
-                weight<T>(p.w_pre, at, on, w2);
+                stage_get<T, ST, TH>(in, C::dz + v * C::t, vec_at<const T>(here_cdz, v, TPR), live && l + v * TPR < nv, q);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float xo = fmaf(n[e] * w[e], a[e], p.x.p ? q[e] : 0.f);
-                    add(1, v, e, u[e] * xo * r);
-                    d[e] += u[e] * w2[e] * r - xo * m;
+                for (int k = 0; k < kPairs; ++k) {
+                    q[k] = mul2(q[k], both(r));
+                    add(1, v, k, q[k], xo[v][k]);
+                    d[k] = fma2(xo[v][k], both(-m), d[k]);
                 }
+                if (p.w_pre) {
+                    w2[v].get(w);
+#pragma unroll
+                    for (int k = 0; k < kPairs; ++k) q[k] = mul2(q[k], w[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) d[k] = add2(d[k], q[k]);
             }
-            if (on && p.dx.p) Vec<S>::store(row_ptr<S>(p.dx, t, h) + at * 8, d);
+            if (on && p.dx.p) Vec<S>::store(vec_at<S>(cdx, v, TPR), d);
+            stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, n);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                n[k] = mul2(n[k], both(ry));
+                d[k] = mul2(d[k], both(keep));
+                if (p.cut) d[k] = masked(d[k], mask[v], k);
+            }
             if (p.gate.p) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q[e] = d[e] * n[e] * w[e] * da[e];
-                if (on) Vec<T>::store(row_ptr<T>(p.dgate, t, h) + at * 8, q);
+                for (int k = 0; k < kPairs; ++k) q[k] = mul2(mul2(d[k], da[v][k]), n[k]);
+                if (p.w_post) {
+                    w1[v].get(w);
+#pragma unroll
+                    for (int k = 0; k < kPairs; ++k) q[k] = mul2(q[k], w[k]);
+                }
+                if (on) Vec<T>::store(vec_at<T>(cdg, v, TPR), q);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) d[k] = mul2(d[k], a[v][k]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float dn = d[e] * a[e];
-                add(0, v, e, dn * n[e]);
-                q[e] = ry * (dn * w[e] - n[e] * P);
+            for (int k = 0; k < kPairs; ++k) add(0, v, k, d[k], n[k]);
+            if (p.w_post) {
+                w1[v].get(w);
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) d[k] = mul2(d[k], w[k]);
             }
-            if (on) Vec<T>::store(row_ptr<T>(p.dy, t, h) + at * 8, q);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) q[k] = mul2(fma2(n[k], both(-mean), d[k]), both(ry));
+            if (on) Vec<T>::store(vec_at<T>(cdy, v, TPR), q);
         }
+        advance(cdy, p.dy, wrap);
+        advance(cdg, p.dgate, wrap);
+        advance(cdx, p.dx, wrap);
+        row += step;
     }
     // the block's sums of the weights' gradients, its rows side by side first
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float *part = k ? p.part_pre : p.part_post;
+    for (int i = 0; i < 2; ++i) {
+        float *part = i ? p.part_pre : p.part_post;
         if (!part) continue;
+        part += (int64_t)blockIdx.x * p.D;
         if (R > 1) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s_dw[R > 1 ? threadIdx.x / TPR : 0][R > 1 ? l * 8 + e : 0] = dw[k][0][e];
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) s_dw[R > 1 ? threadIdx.x / TPR : 0][R > 1 ? (l + v * TPR) * kPairs + k : 0] = dw[i][SM ? 0 : v][k];
             __syncthreads();
-            for (int c = threadIdx.x; c < p.D; c += threads_of(TPR)) {
-                float s = 0.f;
-                for (int i = 0; i < R; ++i) s += s_dw[i][R > 1 ? c : 0];
-                part[(int64_t)blockIdx.x * p.D + c] = s;
+            for (int c = threadIdx.x; c < p.D / 2; c += threads_of(TPR)) {
+                P s = both(0.f);
+                for (int j = 0; j < R; ++j) s = add2(s, s_dw[j][R > 1 ? c : 0]);
+                reinterpret_cast<P *>(part)[c] = s;
             }
         } else {
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
                 if (l + v * TPR < nv)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        part[(int64_t)blockIdx.x * p.D + (l + v * TPR) * 8 + e] =
-                            SM ? s_wide[((k * VPT + v) * 8 + e) * TPR + l] : dw[k][SM ? 0 : v][e];
+                    for (int k = 0; k < kPairs; ++k)
+                        reinterpret_cast<P *>(part)[(l + v * TPR) * kPairs + k] =
+                            SM ? s_wide[((i * VPT + v) * kPairs + k) * TPR + l] : dw[i][SM ? 0 : v][k];
         }
     }
 }
 
-constexpr int kMaxBlocks = 8;      // resident blocks an SM at most (256 threads of the SM's 2,048)
+constexpr int kMaxBlocks = 8;      // blocks an SM at most
 
-// Resident blocks on the current device (each then walks rows); 0: an error.
+// Resident blocks on the current device (each then walks rows); 0: an error.  Looked up once a kernel and device, in `cache`.
 template <typename K>
-inline int resident(K kernel, int threads, size_t smem) {
-    int n = 0;
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) return 0;
-    return (n < kMaxBlocks ? n : kMaxBlocks) * num_sms();
+inline int resident(K kernel, int threads, size_t smem, std::atomic<int> *cache) {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if ((n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess)
+        return 0;
+    n = (n < kMaxBlocks ? n : kMaxBlocks) * num_sms();
+    cache[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 template <typename T, typename S, int TPR, int VPT, bool BWD>
-cudaError_t launch_kernel(const Params &p, int *blocks, cudaStream_t s) {
+cudaError_t launch_kernel(Params p, int *blocks, cudaStream_t s) {
     constexpr int R = threads_of(TPR) / TPR;
-    const auto kernel = BWD ? block_bwd_kernel<T, S, TPR, VPT> : block_fwd_kernel<T, S, TPR, VPT>;
-    const size_t smem = BWD && sums_in_smem(VPT) ? sizeof(float) * 2 * VPT * 8 * TPR : 0;
-    const int most = resident(kernel, threads_of(TPR), smem);
-    if (most < 1) return cudaErrorInvalidConfiguration;
-    const int64_t need = (p.t_max * p.H + R - 1) / R;
-    *blocks = (int)(need < most ? need : most);
-    kernel<<<*blocks, threads_of(TPR), smem, s>>>(p);
-    return cudaGetLastError();
+    using C = Chunks<T, S, VPT, BWD>;
+    const size_t smem = (C::staged(threads_of(TPR)) ? sizeof(uint4) * 2 * C::all * threads_of(TPR) : 0) +
+                        (BWD && sums_in_smem(VPT) ? sizeof(P) * 2 * VPT * kPairs * TPR : 0);
+    static std::atomic<int> cache[64];                     // zero-initialised (static storage)
+    auto launch = [&](auto kernel) {
+        const int most = resident(kernel, threads_of(TPR), smem, cache);
+        if (most < 1) return cudaErrorInvalidConfiguration;
+        const int64_t need = (p.t_max * p.H + R - 1) / R;
+        *blocks = (int)(need < most ? need : most);
+        const int64_t step = (int64_t)*blocks * R;
+        for (Rows *r : {&p.y, &p.gate, &p.z, &p.dz, &p.dy, &p.dgate}) r->step(step, p.H, sizeof(T));
+        for (Rows *r : {&p.x, &p.xo, &p.dxo, &p.dx}) r->step(step, p.H, sizeof(S));
+        p.dh = (int32_t)(step % p.H);
+        kernel<<<*blocks, threads_of(TPR), smem, s>>>(p);
+        return cudaGetLastError();
+    };
+    if constexpr (BWD) return launch(block_bwd_kernel<T, S, TPR, VPT>);
+    else return launch(block_fwd_kernel<T, S, TPR, VPT>);
 }
 
-// Threads of a row by its width: at most two vectors a thread up to 8,192 values, four beyond.
+// Threads of a row by its width: forwards two vectors a thread (one 195 us against 158), backwards and for fp32 rows one
+// (two spill: 386 us against 338), more where 512
+// threads do not hold the row so.
 template <typename T, typename S, bool BWD>
 cudaError_t launch_ts(const Params &p, int *blocks, cudaStream_t s) {
-    if (p.D <= 64) return launch_kernel<T, S, 8, 1, BWD>(p, blocks, s);
-    if (p.D <= 128) return launch_kernel<T, S, 16, 1, BWD>(p, blocks, s);
-    if (p.D <= 256) return launch_kernel<T, S, 32, 1, BWD>(p, blocks, s);
-    if (p.D <= 1024) return launch_kernel<T, S, 128, 1, BWD>(p, blocks, s);
-    if (p.D <= 2048) return launch_kernel<T, S, 256, 1, BWD>(p, blocks, s);
-    if (p.D <= 4096) return launch_kernel<T, S, 256, 2, BWD>(p, blocks, s);
-    if (p.D <= 8192) return launch_kernel<T, S, 512, 2, BWD>(p, blocks, s);
+    constexpr int V = sizeof(T) == 4 || BWD ? 1 : 2;
+    if (p.D <= 32 * V) return launch_kernel<T, S, 4, V, BWD>(p, blocks, s);
+    if (p.D <= 64 * V) return launch_kernel<T, S, 8, V, BWD>(p, blocks, s);
+    if (p.D <= 128 * V) return launch_kernel<T, S, 16, V, BWD>(p, blocks, s);
+    if (p.D <= 256 * V) return launch_kernel<T, S, 32, V, BWD>(p, blocks, s);
+    if (p.D <= 512 * V) return launch_kernel<T, S, 64, V, BWD>(p, blocks, s);
+    if (p.D <= 1024 * V) return launch_kernel<T, S, 128, V, BWD>(p, blocks, s);
+    if (p.D <= 2048 * V) return launch_kernel<T, S, 256, V, BWD>(p, blocks, s);
+    if (p.D <= 4096 * V) return launch_kernel<T, S, 512, V, BWD>(p, blocks, s);
+    if (V == 1 && p.D <= 8192) return launch_kernel<T, S, 512, 2, BWD>(p, blocks, s);
     return launch_kernel<T, S, 512, 4, BWD>(p, blocks, s);
 }
 

@@ -4,7 +4,6 @@
 #include <type_traits>
 
 #include "dla.cuh"
-#include "f32x2.cuh"
 
 namespace gcl {
 namespace glr {
@@ -49,47 +48,41 @@ template <typename T>
 struct Lane {
     static constexpr int V = 2;
     static constexpr int CB = 64;                          // channels of a warp
-    using P = uint64_t;
+    using P = float2;
     static __device__ __forceinline__ P get(uint32_t w) {
         const T *h = reinterpret_cast<const T *>(&w);
-        return pair((float)h[0], (float)h[1]);
+        return make_float2((float)h[0], (float)h[1]);
     }
     static __device__ __forceinline__ uint32_t put(P x) {
-        const float2 f = unpair(x);
         uint32_t w;
         T *h = reinterpret_cast<T *>(&w);
-        h[0] = (T)f.x;
-        h[1] = (T)f.y;
+        h[0] = (T)x.x;
+        h[1] = (T)x.y;
         return w;
     }
-    static __device__ __forceinline__ P all(float x) { return pair(x, x); }
+    static __device__ __forceinline__ P all(float x) { return make_float2(x, x); }
     static __device__ __forceinline__ P load(const float *p) {
-        const float2 f = *reinterpret_cast<const float2 *>(p);
-        return pair(f.x, f.y);
+        return *reinterpret_cast<const float2 *>(p);
     }
-    static __device__ __forceinline__ void store(float *p, P x) { *reinterpret_cast<float2 *>(p) = unpair(x); }
-    static __device__ __forceinline__ P mul(P a, P b) { return mul2(a, b); }
-    static __device__ __forceinline__ P add(P a, P b) { return add2(a, b); }
-    static __device__ __forceinline__ P fma(P a, P b, P c) { return fma2(a, b, c); }
+    static __device__ __forceinline__ void store(float *p, P x) { *reinterpret_cast<float2 *>(p) = x; }
+    static __device__ __forceinline__ P mul(P a, P b) { return __fmul2_rn(a, b); }
+    static __device__ __forceinline__ P add(P a, P b) { return __fadd2_rn(a, b); }
+    static __device__ __forceinline__ P fma(P a, P b, P c) { return __ffma2_rn(a, b, c); }
     template <typename F>
     static __device__ __forceinline__ P map(P x, F f) {
-        const float2 v = unpair(x);
-        return pair(f(v.x), f(v.y));
+        return make_float2(f(x.x), f(x.y));
     }
     template <typename F>
     static __device__ __forceinline__ P map(P x, P y, F f) {
-        const float2 v = unpair(x), w = unpair(y);
-        return pair(f(v.x, w.x), f(v.y, w.y));
+        return make_float2(f(x.x, y.x), f(x.y, y.y));
     }
     template <typename F>
     static __device__ __forceinline__ P map(P x, P y, P z, F f) {
-        const float2 u = unpair(x), v = unpair(y), w = unpair(z);
-        return pair(f(u.x, v.x, w.x), f(u.y, v.y, w.y));
+        return make_float2(f(x.x, y.x, z.x), f(x.y, y.y, z.y));
     }
     template <typename F>
     static __device__ __forceinline__ bool every(P x, F f) {
-        const float2 v = unpair(x);
-        return f(v.x) && f(v.y);
+        return f(x.x) && f(x.y);
     }
 };
 template <>
