@@ -73,18 +73,15 @@ __device__ __forceinline__ P both(float x) { return make_float2(x, x); }
 template <typename F>
 __device__ __forceinline__ P map(P x, F f) { return make_float2(f(x.x), f(x.y)); }
 
-// The mask of a vector's eight values, bit e set where value e is kept: half-word e of its block is at least `cut`.
+// Zeros in place of a vector's dropped values: value e is kept where half-word e of its block is at least `cut`.
 // (cut16: cut in the upper half; an upper half-word is compared with the lower one still below it.)
-__device__ __forceinline__ uint32_t kept(uint32_t cut16, int64_t vec, uint64_t seed, uint64_t offset) {
-    const uint4 w = philox((uint64_t)vec, offset, seed);
-    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-    uint32_t m = 0;
+__device__ __forceinline__ void drop(const uint4 &w, uint32_t cut16, P *x) {
+    const uint32_t word[kPairs] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m |= ((e & 1 ? word[e / 2] : word[e / 2] << 16) >= cut16 ? 1u : 0u) << e;
-    return m;
-}
-__device__ __forceinline__ P masked(P x, uint32_t mask, int k) {
-    return make_float2(mask >> 2 * k & 1 ? x.x : 0.f, mask >> (2 * k + 1) & 1 ? x.y : 0.f);
+    for (int k = 0; k < kPairs; ++k) {
+        if (word[k] << 16 < cut16) x[k].x = 0.f;
+        if (word[k] < cut16) x[k].y = 0.f;
+    }
 }
 
 // exp(-x) and 1 / x: the accurate ones for fp32 rows, the special-function unit's (subnormals flushed) for 16-bit rows.
@@ -292,10 +289,37 @@ struct Chunks {
     static constexpr int t = sizeof(T) / 2, s = sizeof(S) / 2;
     static constexpr int y = 0, g = VPT * t, x = 2 * VPT * t, dxo = x + VPT * s, dz = dxo + VPT * s;
     static constexpr int all = BWD ? dz + VPT * t : dxo;
-    static constexpr bool staged(int threads) { return 2 * all * threads * 16 <= 160 * 1024; }
+    static constexpr int weights = 2 * VPT * t;
+    static constexpr bool staged(int threads) { return (weights + 2 * all) * threads * 16 <= 224 * 1024; }
 };
 
-constexpr int fwd_blocks(int tpr, int vpt) { return vpt > 2 ? 1 : 512 / threads_of(tpr); }
+// A thread's vectors of the weights, in slots of its own (registers would be 16 to 32 a thread).
+template <typename T, int TPR, int VPT, int THREADS>
+__device__ __forceinline__ void keep_weights(const Params &p, int l, uint4 *at) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const T *w = static_cast<const T *>(i ? p.w_pre : p.w_post);
+            Vec<T> r;
+            r.load(w + (l + v * TPR) * 8, w && l + v * TPR < p.D / 8);
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(T) / 2; ++k) at[((i * VPT + v) * (int)sizeof(T) / 2 + k) * THREADS] = r.v[k];
+        }
+}
+template <typename T, int TPR, bool STAGED, int THREADS>
+__device__ __forceinline__ void weight(const uint4 *at, int v, const void *w, int vec, int nv, P *f) {
+    Vec<T> r;
+    if (STAGED) {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.v[k] = at[(v * (int)sizeof(T) / 2 + k) * THREADS];
+    } else {
+        r.load(static_cast<const T *>(w) + vec * 8, vec < nv);
+    }
+    r.get(f);
+}
+
+constexpr int fwd_blocks(int tpr, int vpt) { return vpt > 2 ? 1 : 640 / threads_of(tpr); }
 constexpr int bwd_blocks(int tpr, int vpt) { return vpt > 2 ? 1 : tpr > 256 ? 1 : tpr > 128 ? 2 : 3; }
 
 template <typename T, typename S, int TPR, int VPT>
@@ -310,17 +334,12 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
     uint64_t seed = 0, offset = 0;
     if (p.cut) { seed = (uint64_t)p.rng[0]; offset = (uint64_t)p.rng[1]; }
     const float keep = p.cut ? p.scale * (65536.f / (65536 - p.cut)) : p.scale;
-    Vec<T> w1[VPT], w2[VPT];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const bool on = l + v * TPR < nv;
-        if (p.w_post) w1[v].load(static_cast<const T *>(p.w_post) + (l + v * TPR) * 8, on);
-        if (p.w_pre) w2[v].load(static_cast<const T *>(p.w_pre) + (l + v * TPR) * 8, on);
-    }
     using C = Chunks<T, S, VPT, false>;
     constexpr int TH = threads_of(TPR);
     constexpr bool ST = C::staged(TH);
-    extern __shared__ __align__(16) uint4 s_rows[];        // [2][chunks][TH]
+    extern __shared__ __align__(16) uint4 s_rows[];        // weights [2 VPT t][TH], rows [2][chunks][TH]
+    uint4 *weights = s_rows + threadIdx.x, *staged = weights + C::weights * TH;
+    if (ST) keep_weights<T, TPR, VPT, TH>(p, l, weights);
     const int64_t step = (int64_t)gridDim.x * R;
     int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / TPR;
     int64_t t = p.H == 1 ? row : row / p.H;
@@ -328,7 +347,7 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
     char *cy = place<T>(p.y, t, h, l), *cg = place<T>(p.gate, t, h, l), *cx = place<S>(p.x, t, h, l);
     char *co = place<S>(p.xo, t, h, l), *cz = place<T>(p.z, t, h, l);
     auto stage = [&](int64_t r, int buf) {                 // row r, at the cursors; moves them on
-        uint4 *to = s_rows + buf * C::all * TH + threadIdx.x;
+        uint4 *to = staged + buf * C::all * TH;
         if (r - threadIdx.x / TPR < rows) {                // (the same for the block)
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
@@ -353,7 +372,7 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
         advance(cx, p.x, wrap);
         stage(row + step, buf ^ 1);
         stage_wait_prev();
-        const uint4 *in = s_rows + buf * C::all * TH + threadIdx.x;
+        const uint4 *in = staged + buf * C::all * TH;
         float scale = keep;
         if (p.post != GCL_NORM_NONE) {
             P q = both(0.f);
@@ -375,7 +394,7 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
             P w[kPairs];
             stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, xo[v]);
             if (p.w_post) {
-                w1[v].get(w);
+                weight<T, TPR, ST, TH>(weights, v, p.w_post, l + v * TPR, nv, w);
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], w[k]);
             }
@@ -386,11 +405,7 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], a[k]);
             }
-            if (p.cut) {
-                const uint32_t mask = kept((uint32_t)p.cut << 16, row * nv + l + v * TPR, seed, offset);
-#pragma unroll
-                for (int k = 0; k < kPairs; ++k) xo[v][k] = masked(xo[v][k], mask, k);
-            }
+            if (p.cut) drop(philox((uint64_t)(row * nv + l + v * TPR), offset, seed), (uint32_t)p.cut << 16, xo[v]);
             if (p.x.p) {
                 stage_get<S, ST, TH>(in, C::x + v * C::s, vec_at<const S>(here_cx, v, TPR), live && l + v * TPR < nv && p.x.p, w);
 #pragma unroll
@@ -416,7 +431,7 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
             for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], both(r));
             if (p.w_pre) {
                 P w[kPairs];
-                w2[v].get(w);
+                weight<T, TPR, ST, TH>(weights, VPT + v, p.w_pre, l + v * TPR, nv, w);
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) xo[v][k] = mul2(xo[v][k], w[k]);
             }
@@ -440,8 +455,9 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
     using C = Chunks<T, S, VPT, true>;
     constexpr int TH = threads_of(TPR);
     constexpr bool ST = C::staged(TH);
-    extern __shared__ __align__(16) uint4 s_rows[];        // [2][chunks][TH]
-    P *s_wide = reinterpret_cast<P *>(s_rows + (ST ? 2 * C::all * TH : 0));           // [2][VPT][kPairs][TPR]
+    extern __shared__ __align__(16) uint4 s_rows[];        // weights [2 VPT t][TH], rows [2][chunks][TH]
+    uint4 *weights = s_rows + threadIdx.x, *staged = weights + C::weights * TH;
+    P *s_wide = reinterpret_cast<P *>(s_rows + (ST ? C::weights + 2 * C::all : 0) * TH);           // [2][VPT][kPairs][TPR]
     launch_dependents();                                   // (the weights' sums wait for this grid's end)
     int64_t rows;
     if (!live_rows(p, rows)) return;
@@ -451,13 +467,10 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
     uint64_t seed = 0, offset = 0;
     if (p.cut) { seed = (uint64_t)p.rng[0]; offset = (uint64_t)p.rng[1]; }
     const float keep = p.cut ? p.scale * (65536.f / (65536 - p.cut)) : p.scale;
-    Vec<T> w1[VPT], w2[VPT];
+    if (ST) keep_weights<T, TPR, VPT, TH>(p, l, weights);
     P dw[2][SM ? 1 : VPT][kPairs];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const bool on = l + v * TPR < nv;
-        if (p.w_post) w1[v].load(static_cast<const T *>(p.w_post) + (l + v * TPR) * 8, on);
-        if (p.w_pre) w2[v].load(static_cast<const T *>(p.w_pre) + (l + v * TPR) * 8, on);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
     char *cdo = place<S>(p.dxo, t, h, l), *cdz = place<T>(p.dz, t, h, l);
     char *cdy = place<T>(p.dy, t, h, l), *cdg = place<T>(p.dgate, t, h, l), *cdx = place<S>(p.dx, t, h, l);
     auto stage = [&](int64_t r, int buf) {                 // row r, at the cursors
-        uint4 *to = s_rows + buf * C::all * TH + threadIdx.x;
+        uint4 *to = staged + buf * C::all * TH;
         if (r - threadIdx.x / TPR < rows) {                // (the same for the block)
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
@@ -514,10 +527,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
         advance(cdz, p.dz, wrap);
         stage(row + step, buf ^ 1);
         stage_wait_prev();
-        const uint4 *in = s_rows + buf * C::all * TH + threadIdx.x;
-        uint32_t mask[VPT];
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) mask[v] = p.cut ? kept((uint32_t)p.cut << 16, row * nv + l + v * TPR, seed, offset) : 0xffu;
+        const uint4 *in = staged + buf * C::all * TH;
         float ry = 1.f;
         if (p.post != GCL_NORM_NONE) {
             P q = both(0.f);
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
             sum.template operator()<1>(&ss);
             ry = inverse_length(p.post, ss, inv_d, p.eps);
         }
-        // per vector: act and its slope; then xo (v without dz), which the outputs use again
+        // per vector: act and its slope, times scale and dropout's factor; then xo (v without dz), which the outputs use again
         P a[VPT][kPairs], da[VPT][kPairs], xo[VPT][kPairs];
         P s0 = both(0.f), s1 = s0, s2 = s0, s3 = s0, s4 = s0;          // sums of dxo v, xo^2, u xo, u v, xo v
 #pragma unroll
@@ -540,7 +550,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
             P f[kPairs], w[kPairs];
             stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, f);
             if (p.w_post) {
-                w1[v].get(w);
+                weight<T, TPR, ST, TH>(weights, v, p.w_post, l + v * TPR, nv, w);
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) f[k] = mul2(f[k], w[k]);
             }
@@ -548,20 +558,30 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
                 stage_get<T, ST, TH>(in, C::g + v * C::t, vec_at<const T>(here_cg, v, TPR), live && l + v * TPR < nv, w);
                 activation<T, true>(p.act, w, a[v], da[v]);
 #pragma unroll
-                for (int k = 0; k < kPairs; ++k) f[k] = mul2(f[k], a[v][k]);
+                for (int k = 0; k < kPairs; ++k) {
+                    a[v][k] = mul2(a[v][k], both(keep));
+                    da[v][k] = mul2(da[v][k], both(keep));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) a[v][k] = both(keep);
+            }
+            if (p.cut) {
+                const uint4 words = philox((uint64_t)(row * nv + l + v * TPR), offset, seed);
+                drop(words, (uint32_t)p.cut << 16, a[v]);
+                if (p.gate.p) drop(words, (uint32_t)p.cut << 16, da[v]);
             }
             stage_get<S, ST, TH>(in, C::dxo + v * C::s, vec_at<const S>(here_cdo, v, TPR), live && l + v * TPR < nv && p.dxo.p, w);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
-                f[k] = mul2(f[k], both(ry * keep));        // v
-                if (p.cut) f[k] = masked(f[k], mask[v], k);
+                f[k] = mul2(mul2(f[k], both(ry)), a[v][k]);                    // v
                 s0 = fma2(w[k], f[k], s0);
             }
             if (p.dz.p) {
                 P u[kPairs];
                 stage_get<T, ST, TH>(in, C::dz + v * C::t, vec_at<const T>(here_cdz, v, TPR), live && l + v * TPR < nv, u);
                 if (p.w_pre) {
-                    w2[v].get(w);
+                    weight<T, TPR, ST, TH>(weights, VPT + v, p.w_pre, l + v * TPR, nv, w);
 #pragma unroll
                     for (int k = 0; k < kPairs; ++k) u[k] = mul2(u[k], w[k]);
                 }
@@ -605,7 +625,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
                     d[k] = fma2(xo[v][k], both(-m), d[k]);
                 }
                 if (p.w_pre) {
-                    w2[v].get(w);
+                    weight<T, TPR, ST, TH>(weights, VPT + v, p.w_pre, l + v * TPR, nv, w);
 #pragma unroll
                     for (int k = 0; k < kPairs; ++k) q[k] = mul2(q[k], w[k]);
                 }
@@ -615,27 +635,24 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
             if (on && p.dx.p) Vec<S>::store(vec_at<S>(cdx, v, TPR), d);
             stage_get<T, ST, TH>(in, C::y + v * C::t, vec_at<const T>(here_cy, v, TPR), live && l + v * TPR < nv, n);
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-                n[k] = mul2(n[k], both(ry));
-                d[k] = mul2(d[k], both(keep));
-                if (p.cut) d[k] = masked(d[k], mask[v], k);
-            }
+            for (int k = 0; k < kPairs; ++k) n[k] = mul2(n[k], both(ry));
             if (p.gate.p) {
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) q[k] = mul2(mul2(d[k], da[v][k]), n[k]);
                 if (p.w_post) {
-                    w1[v].get(w);
+                    weight<T, TPR, ST, TH>(weights, v, p.w_post, l + v * TPR, nv, w);
 #pragma unroll
                     for (int k = 0; k < kPairs; ++k) q[k] = mul2(q[k], w[k]);
                 }
                 if (on) Vec<T>::store(vec_at<T>(cdg, v, TPR), q);
-#pragma unroll
-                for (int k = 0; k < kPairs; ++k) d[k] = mul2(d[k], a[v][k]);
             }
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) add(0, v, k, d[k], n[k]);
+            for (int k = 0; k < kPairs; ++k) {
+                d[k] = mul2(d[k], a[v][k]);
+                add(0, v, k, d[k], n[k]);
+            }
             if (p.w_post) {
-                w1[v].get(w);
+                weight<T, TPR, ST, TH>(weights, v, p.w_post, l + v * TPR, nv, w);
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) d[k] = mul2(d[k], w[k]);
             }
@@ -698,7 +715,7 @@ template <typename T, typename S, int TPR, int VPT, bool BWD>
 cudaError_t launch_kernel(Params p, int *blocks, cudaStream_t s) {
     constexpr int R = threads_of(TPR) / TPR;
     using C = Chunks<T, S, VPT, BWD>;
-    const size_t smem = (C::staged(threads_of(TPR)) ? sizeof(uint4) * 2 * C::all * threads_of(TPR) : 0) +
+    const size_t smem = sizeof(uint4) * (C::staged(threads_of(TPR)) ? C::weights + 2 * C::all : 0) * threads_of(TPR) +
                         (BWD && sums_in_smem(VPT) ? sizeof(P) * 2 * VPT * kPairs * TPR : 0);
     static std::atomic<int> cache[64];                     // zero-initialised (static storage)
     auto launch = [&](auto kernel) {
@@ -717,12 +734,11 @@ cudaError_t launch_kernel(Params p, int *blocks, cudaStream_t s) {
     else return launch(block_fwd_kernel<T, S, TPR, VPT>);
 }
 
-// Threads of a row by its width: forwards two vectors a thread (one 195 us against 158), backwards and for fp32 rows one
-// (two spill: 386 us against 338), more where 512
+// Threads of a row by its width: two vectors a thread (fp32 rows one, which takes the same registers), more where 512
 // threads do not hold the row so.
 template <typename T, typename S, bool BWD>
 cudaError_t launch_ts(const Params &p, int *blocks, cudaStream_t s) {
-    constexpr int V = sizeof(T) == 4 || BWD ? 1 : 2;
+    constexpr int V = sizeof(T) == 4 ? 1 : 2;
     if (p.D <= 32 * V) return launch_kernel<T, S, 4, V, BWD>(p, blocks, s);
     if (p.D <= 64 * V) return launch_kernel<T, S, 8, V, BWD>(p, blocks, s);
     if (p.D <= 128 * V) return launch_kernel<T, S, 16, V, BWD>(p, blocks, s);
