@@ -600,6 +600,14 @@ def _on_device(fn, device):
                          f"theirs current (torch.cuda.device)")
 
 
+def _raw_stream(device):
+    """The current stream; after the first call torch's own function."""
+    global _raw_stream
+    import torch
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(device)
+
+
 def _packed_call(fn, packed, stream, device):
     """Calls entry point `fn` of the loaded library with a packed argument struct."""
     if _devices != 1:                    # (with one device there is no other; the look at it takes 0.4 us a call)
@@ -611,8 +619,7 @@ def _packed_call(fn, packed, stream, device):
         entry.restype, entry.argtypes = ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]
         handle.__dict__["_packed_" + fn] = entry
     if stream is None:
-        import torch
-        stream = torch._C._cuda_getCurrentRawStream(device)
+        stream = _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     st = entry(packed, stream)
@@ -826,22 +833,35 @@ _GLR_PACK = struct.Struct("@" + _ROWS_FMT * 8 + "PPPPPPPPPPNqiiiii0q")
 _GLR_STEP_PACK = struct.Struct("@" + _ROWS_FMT * 4 + "PPPPiiiiii0q")
 
 
+# What the calls below look up of torch, kept from the first call on (an import statement in the call takes 0.6 us of it).
+_F32 = _I32 = _I64 = None
+_DTYPE_CODES = {}
+
+
+def _load_torch():
+    global _F32, _I32, _I64
+    import torch
+    _DTYPE_CODES.update({torch.float32: GCL_F32, torch.bfloat16: GCL_BF16, torch.float16: GCL_F16})
+    _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+
+
+def _code_of(fn, name, dtype):
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"{fn}: {name} has dtype {dtype}, expected one of {tuple(_DTYPE_CODES)}")
+    return code
+
+
 def _rows2(fn, name, t, shape, dtype, device):
     """gcl_rows of a tensor [tokens, D] with contiguous D and any token stride."""
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{fn}: {name} must be a CUDA tensor on the call's device (got {t.device})")
-    if t.dtype is not dtype:
-        raise ValueError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor {shape} of {dtype} on the call's device (got {tuple(t.shape)}, "
+                         f"{t.dtype}, {t.device})")
     st, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{fn}: {name} must have contiguous rows (strides {t.stride()})")
-    if shape[0] == 1:                        # the stride of an extent of one is free: one that fits
-        st = shape[1]
-    if st < 0:
-        raise ValueError(f"{fn}: {name} has negative strides {t.stride()}")
-    return t.data_ptr(), st, shape[1]
+    if sd != 1 or st < 0:
+        raise ValueError(f"{fn}: {name} must have contiguous rows and no negative stride (strides {t.stride()})")
+    # (the stride of an extent of one is free: one that fits)
+    return t.data_ptr(), st if shape[0] != 1 else shape[1], shape[1]
 
 
 def _kind(fn, decay, mix):
@@ -877,7 +897,9 @@ def glr_fwd(x, r, cu_seqlens, o, i=None, rate=None, h0=None, ht=None, h_save=Non
     """The gated linear recurrence over packed sequences (include/gcl.h, glr): o [T, D] (None: only the states) and
     ht [N, D] from x, the decay gate r, the input gate i (or None) [T, D] and h0.  x, r, i and o may have strided
     tokens.  h_save [ceil(T / 64), D] fp32 keeps the states that the backward reads."""
-    from torch import float32 as f32, int32 as i32
+    if _F32 is None:
+        _load_torch()
+    f32, i32 = _F32, _I32
     fn = "glr_fwd"
     sx = tuple(x.shape)
     T, D = sx
@@ -890,7 +912,7 @@ def glr_fwd(x, r, cu_seqlens, o, i=None, rate=None, h0=None, ht=None, h_save=Non
         _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "h0", h0, (N, D), f32, dev), _flat(fn, "ht", ht, (N, D), f32, dev),
         0, 0, 0, _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
         _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
-        *_scratch(fn, workspace, dev), T, N, D, kd, km, _dtype_of(x))
+        *_scratch(fn, workspace, dev), T, N, D, kd, km, _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
 
@@ -898,7 +920,9 @@ def glr_bwd(x, r, d_o, cu_seqlens, dx, dr, i=None, di=None, rate=None, drate=Non
             h_save=None, decay="power", mix="root", dev_status=None, workspace=None, stream=None):
     """The backward of glr_fwd: dx, dr, di (with i) of x's dtype, drate [D] and dh0 [N, D] from d_o and dht.  With the
     forward's h_save the states are not formed again."""
-    from torch import float32 as f32, int32 as i32
+    if _F32 is None:
+        _load_torch()
+    f32, i32 = _F32, _I32
     fn = "glr_bwd"
     sx = tuple(x.shape)
     T, D = sx
@@ -915,14 +939,16 @@ def glr_bwd(x, r, d_o, cu_seqlens, dx, dr, i=None, di=None, rate=None, drate=Non
         _flat(fn, "dht", dht, (N, D), f32, dev), _flat(fn, "dh0", dh0, (N, D), f32, dev),
         _flat(fn, "drate", drate, (D,), f32, dev), _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
         _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
-        *_scratch(fn, workspace, dev), T, N, D, kd, km, _dtype_of(x))
+        *_scratch(fn, workspace, dev), T, N, D, kd, km, _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
 
 def glr_step(x, r, state, o, i=None, rate=None, slots=None, decay="power", mix="root", dev_status=None, stream=None):
     """One token of each request: the states [n_slots, D] of the requests' slots are updated in place and
     o [B, D] is written (include/gcl.h, glr_step).  slots int32 [B]; negative: idle."""
-    from torch import float32 as f32, int32 as i32
+    if _F32 is None:
+        _load_torch()
+    f32, i32 = _F32, _I32
     fn = "glr_step"
     sx = tuple(x.shape)
     B, D = sx
@@ -933,7 +959,7 @@ def glr_step(x, r, state, o, i=None, rate=None, slots=None, decay="power", mix="
         *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)), *_rows2(fn, "o", o, sx, dt, dev),
         _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "state", state, (n_slots, D), f32, dev),
         _flat(fn, "slots", slots, (B,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, D, kd, km,
-        _dtype_of(x))
+        _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
 
@@ -943,15 +969,26 @@ _BLOCK_PACK = struct.Struct("@" + _ROWS_FMT * 10 + "PPPPPPPPNqiiifffiiiii0q")
 
 
 def _rows3(fn, name, t, shape, dtype, device):
-    """gcl_rows of a tensor [tokens, heads, D], or [tokens, D] where the call's rows have one head; None: no rows."""
-    if t is None:
-        return _NO_ROWS
-    return (_rows2 if len(shape) == 2 else _rows)(fn, name, t, shape, dtype, device)
+    """gcl_rows of a tensor [tokens, heads, D], or [tokens, D] where the call's rows have one head."""
+    if len(shape) == 2:
+        return _rows2(fn, name, t, shape, dtype, device)
+    if t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor {shape} of {dtype} on the call's device (got {tuple(t.shape)}, "
+                         f"{t.dtype}, {t.device})")
+    T, H, D = shape
+    st, sh, sd = t.stride()
+    if sd != 1 or st < 0 or sh < 0:
+        raise ValueError(f"{fn}: {name} must have contiguous rows and no negative stride (strides {t.stride()})")
+    if H == 1:                               # the stride of an extent of one is free: one that fits
+        sh = D
+    return t.data_ptr(), st if T != 1 else H * sh, sh
 
 
 def _block_call(fn, y, gate, x, xo, z, dxo, dz, dy, dgate, dx, post_weight, pre_weight, dpost_weight, dpre_weight,
                 post_norm, pre_norm, activation, scale, eps, dropout, rng, cu_seqlens, dev_status, workspace, stream):
-    from torch import float32 as f32, int32 as i32, int64 as i64
+    if _F32 is None:
+        _load_torch()
+    f32, i32, i64 = _F32, _I32, _I64
     sy = tuple(y.shape)
     T, H, D = sy if len(sy) == 3 else (sy[0], 1, sy[1])
     dt, dev = y.dtype, y.get_device()
@@ -963,16 +1000,23 @@ def _block_call(fn, y, gate, x, xo, z, dxo, dz, dy, dgate, dx, post_weight, pre_
     if st is not dt and st is not f32:
         raise ValueError(f"{fn}: x, xo and their gradients have dtype {st}, expected {dt} or {f32}")
     n = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    code = _code_of(fn, "y", dt)
+    no = _NO_ROWS
     packed = _BLOCK_PACK.pack(
-        *_rows3(fn, "y", y, sy, dt, dev), *_rows3(fn, "gate", gate, sy, dt, dev), *_rows3(fn, "x", x, sy, st, dev),
-        *_rows3(fn, "xo", xo, sy, st, dev), *_rows3(fn, "z", z, sy, dt, dev), *_rows3(fn, "dxo", dxo, sy, st, dev),
-        *_rows3(fn, "dz", dz, sy, dt, dev), *_rows3(fn, "dy", dy, sy, dt, dev), *_rows3(fn, "dgate", dgate, sy, dt, dev),
-        *_rows3(fn, "dx", dx, sy, st, dev), _flat(fn, "post_weight", post_weight, (D,), dt, dev),
-        _flat(fn, "pre_weight", pre_weight, (D,), dt, dev), _flat(fn, "dpost_weight", dpost_weight, (D,), f32, dev),
-        _flat(fn, "dpre_weight", dpre_weight, (D,), f32, dev), _flat(fn, "rng", rng, (2,), i64, dev),
-        _flat(fn, "cu_seqlens", cu_seqlens, (n + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        *_rows3(fn, "y", y, sy, dt, dev), *(no if gate is None else _rows3(fn, "gate", gate, sy, dt, dev)),
+        *(no if x is None else _rows3(fn, "x", x, sy, st, dev)), *(no if xo is None else _rows3(fn, "xo", xo, sy, st, dev)),
+        *(no if z is None else _rows3(fn, "z", z, sy, dt, dev)), *(no if dxo is None else _rows3(fn, "dxo", dxo, sy, st, dev)),
+        *(no if dz is None else _rows3(fn, "dz", dz, sy, dt, dev)), *(no if dy is None else _rows3(fn, "dy", dy, sy, dt, dev)),
+        *(no if dgate is None else _rows3(fn, "dgate", dgate, sy, dt, dev)), *(no if dx is None else _rows3(fn, "dx", dx, sy, st, dev)),
+        0 if post_weight is None else _flat(fn, "post_weight", post_weight, (D,), dt, dev),
+        0 if pre_weight is None else _flat(fn, "pre_weight", pre_weight, (D,), dt, dev),
+        0 if dpost_weight is None else _flat(fn, "dpost_weight", dpost_weight, (D,), f32, dev),
+        0 if dpre_weight is None else _flat(fn, "dpre_weight", dpre_weight, (D,), f32, dev),
+        0 if rng is None else _flat(fn, "rng", rng, (2,), i64, dev),
+        0 if cu_seqlens is None else _flat(fn, "cu_seqlens", cu_seqlens, (n + 1,), i32, dev),
+        0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev),
         *_scratch(fn, workspace, dev), T, n, H, D, scale, eps, dropout, NORMS[post_norm], NORMS[pre_norm],
-        GATE_ACTIVATIONS[activation], _dtype_of(y), GCL_F32 if st is f32 else _dtype_of(y))
+        GATE_ACTIVATIONS[activation], code, GCL_F32 if st is f32 else code)
     _packed_call(fn, packed, stream, dev)
 
 

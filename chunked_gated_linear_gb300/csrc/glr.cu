@@ -7,7 +7,29 @@ namespace {
 
 // ---- set-up: checks cu_seqlens, finds each tile's first sequence, passes states of empty sequences through, clears the
 // packets of the spans that will be taken ----
-__global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const float *in_state, float *out_state, int tile) {
+__device__ __forceinline__ void set_up(const Params &p, bool stop, int64_t at, int64_t step) {
+    if (at == 0) {
+        p.head->blocked = stop;
+        p.head->live = stop ? 0 : p.cu[p.n_max];
+        p.head->ticket = 0;
+    }
+    if (stop) return;
+    const int64_t spans = (p.cu[p.n_max] + (int64_t)kRanks * p.tile - 1) / (kRanks * p.tile);
+    for (int64_t e = at; e < spans * p.D; e += step) reinterpret_cast<uint4 *>(p.chain)[e] = make_uint4(0, 0, 0, 0);
+    for (int64_t j = at; j < p.tiles; j += step) {
+        const int64_t t0 = j * p.tile;
+        int lo = 0, hi = p.n_max;                          // first n with cu[n] >= t0 (n_max if none)
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.cu[mid] >= t0) hi = mid;
+            else lo = mid + 1;
+        }
+        p.first[j] = lo;
+    }
+}
+
+// before: the walk that forms the states for p's, or one without tiles.
+__global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const Params before, const float *in_state, float *out_state) {
     launch_dependents();
     const int tid = threadIdx.x;
     int bad = 0;
@@ -17,27 +39,11 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const f
     }
     const bool blocked = status_blocks_cta(p.status);
     bad = __syncthreads_or(bad);
-    if (blockIdx.x == 0 && tid == 0) {
-        p.head->blocked = blocked || bad;
-        p.head->live = blocked || bad ? 0 : p.cu[p.n_max];
-        p.head->ticket = 0;
-        if (bad) status_set(p.status, GCL_DEV_BAD_RANGE);
-    }
-    if (blocked || bad) return;
     const int64_t at = blockIdx.x * (int64_t)blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
-    const int64_t spans = (p.cu[p.n_max] + (int64_t)kRanks * tile - 1) / (kRanks * tile);
-    for (int64_t e = at; e < spans * p.D; e += step) reinterpret_cast<uint4 *>(p.chain)[e] = make_uint4(0, 0, 0, 0);
-    for (int64_t j = at; j < p.tiles; j += step) {
-        const int64_t t0 = j * tile;
-        int lo = 0, hi = p.n_max;                          // first n with cu[n] >= t0 (n_max if none)
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (p.cu[mid] >= t0) hi = mid;
-            else lo = mid + 1;
-        }
-        p.first[j] = lo;
-    }
-    if (!out_state) return;
+    if (at == 0 && bad) status_set(p.status, GCL_DEV_BAD_RANGE);
+    set_up(p, blocked || bad, at, step);
+    if (before.tiles > 0) set_up(before, blocked || bad, at, step);
+    if (blocked || bad || !out_state) return;
     for (int n = blockIdx.x; n < p.n_max; n += gridDim.x) {
         if (p.cu[n + 1] != p.cu[n]) continue;
         for (int d = tid; d < p.D; d += blockDim.x) {
@@ -49,8 +55,13 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const f
 
 }  // namespace
 
-void launch_setup(const Params &p, const float *in_state, float *out_state, int tile, int blocks, cudaStream_t s) {
-    glr_setup_kernel<<<blocks, 1024, 0, s>>>(p, in_state, out_state, tile);
+// (a block sets `blocked` by the status word alone where another has set the word in the meantime: both stop the call)
+cudaError_t launch_setup(const Params &p, const Params &before, const float *in_state, float *out_state, cudaStream_t s) {
+    int64_t blocks = ((p.tiles + before.tiles + kRanks - 1) / kRanks * p.D + 4095) / 4096;
+    if (out_state && blocks < (p.n_max + 7) / 8) blocks = (p.n_max + 7) / 8;
+    if (blocks > num_sms()) blocks = num_sms();
+    glr_setup_kernel<<<(unsigned)blocks, 1024, 0, s>>>(p, before, in_state, out_state);
+    return cudaGetLastError();
 }
 
 extern template cudaError_t launch_fwd<float>(const Params &, cudaStream_t);
@@ -70,43 +81,40 @@ bool sizes_ok(const gcl_glr_args *a) {
            a->D <= (1 << 20) && (a->dtype == GCL_F32 || a->dtype == GCL_BF16 || a->dtype == GCL_F16);
 }
 
-// The workspace's parts, in order; `base` may be NULL (for the size alone).
-size_t layout(const gcl_glr_args *a, bool backward, Params *p) {
+// The workspace's parts, in order; its base may be NULL (for the size alone).  before: the walk that forms the states which a
+// backward without h_save needs.
+size_t layout(const gcl_glr_args *a, bool backward, Params *p, Params *before) {
     uint8_t *base = static_cast<uint8_t *>(a->workspace);
     size_t at = 0;
-    auto take = [&](size_t bytes) {
-        uint8_t *q = base ? base + at : nullptr;
-        at += up16(bytes);
-        return q;
-    };
-    auto set = [&](auto *&field, size_t bytes) { field = reinterpret_cast<std::remove_reference_t<decltype(field)>>(take(bytes)); };
-    Params dummy{};
-    Params &o = p ? *p : dummy;
-    const int64_t tf = (a->t_max + kTileF - 1) / kTileF, tb = (a->t_max + kTileB - 1) / kTileB, tiles = backward ? tb : tf;
     const size_t row = sizeof(float) * (size_t)a->D;
-    set(o.head, sizeof(Header));
-    set(o.first, sizeof(int32_t) * (size_t)tiles);
-    set(o.chain, sizeof(Packet) * (size_t)a->D * ((tiles + kRanks - 1) / kRanks));
-    if (backward) {
-        if (a->drate) set(o.drate_part, row * tiles);
-        if (!a->h_save) set(o.h_save, row * tb);
+    auto set = [&](auto *&field, size_t bytes) {
+        field = base ? reinterpret_cast<std::remove_reference_t<decltype(field)>>(base + at) : nullptr;
+        at += up16(bytes);
+    };
+    auto walk = [&](Params &w, int tile) {
+        w.tile = tile;
+        w.tiles = (a->t_max + tile - 1) / tile;
+        set(w.head, sizeof(Header));
+        set(w.first, sizeof(int32_t) * (size_t)w.tiles);
+        set(w.chain, sizeof(Packet) * (size_t)a->D * ((w.tiles + kRanks - 1) / kRanks));
+    };
+    walk(*p, backward ? kTileB : kTileF);
+    p->h_save = a->h_save;
+    if (backward && a->drate) set(p->drate_part, row * p->tiles);
+    if (backward && !a->h_save) {
+        set(p->h_save, row * p->tiles);
+        walk(*before, kTileF);
     }
     return at;
 }
 
 template <typename T>
-cudaError_t launch(const gcl_glr_args *a, Params p, bool backward, cudaStream_t s) {
-    p.n_cb = (p.D + Lane<T>::CB - 1) / Lane<T>::CB;
+cudaError_t launch(Params p, Params before, bool backward, cudaStream_t s) {
+    p.n_cb = before.n_cb = (p.D + Lane<T>::CB - 1) / Lane<T>::CB;
+    cudaError_t e = launch_setup(p, before, backward ? p.dht : p.h0, backward ? p.dh0 : p.ht, s);
+    if (e != cudaSuccess) return e;
     if (!backward) return launch_fwd<T>(p, s);
-    if (!a->h_save) {                                      // the states before each 64 tokens, by the forward without o and ht
-        Params f = p;
-        layout(a, true, &f);
-        f.tiles = (p.t_max + kTileF - 1) / kTileF;
-        f.ht = nullptr;
-        f.o.p = f.d_o.p = nullptr;
-        const cudaError_t e = launch_fwd<T>(f, s);
-        if (e != cudaSuccess) return e;
-    }
+    if (before.tiles > 0 && (e = launch_fwd<T>(before, s)) != cudaSuccess) return e;
     return launch_bwd<T>(p, s);
 }
 
@@ -125,6 +133,11 @@ gcl_status_t check_kind(const char *fn, const float *rate, int32_t D, int32_t de
 }
 
 namespace {
+
+size_t workspace(const gcl_glr_args *a, bool backward) {
+    Params p{}, before{};
+    return sizes_ok(a) ? layout(a, backward, &p, &before) : 0;
+}
 
 gcl_status_t run(const char *fn, const gcl_glr_args *a, bool backward, cudaStream_t s) {
     fail(GCL_OK, "%s", "");                                // clears gcl_last_error()
@@ -162,8 +175,8 @@ gcl_status_t run(const char *fn, const gcl_glr_args *a, bool backward, cudaStrea
         if (i && o && (i < o ? o - i : i - o) < state_bytes)
             return fail(GCL_ERR_INVALID_ARG, "%s: %s must not be %s (their states overlap)", fn, backward ? "dh0" : "ht", x.name);
     }
-    Params p{};
-    const size_t bytes = layout(a, backward, &p);
+    Params p{}, before{};
+    const size_t bytes = layout(a, backward, &p, &before);
     if (!a->workspace || a->workspace_bytes < bytes)
         return fail(GCL_ERR_CAPACITY, "%s: workspace of %zu bytes needed, %zu given", fn, bytes, a->workspace ? a->workspace_bytes : (size_t)0);
     p.x = dla::rows(a->x); p.r = dla::rows(a->r); p.i = dla::rows(a->i);
@@ -174,14 +187,19 @@ gcl_status_t run(const char *fn, const gcl_glr_args *a, bool backward, cudaStrea
         p.o = dla::rows(a->o);
         p.ht = a->ht;
     }
-    if (a->h_save) p.h_save = a->h_save;
     p.kind = Kind{a->rate, a->decay, a->mix};
     p.h0 = a->h0; p.cu = a->cu_seqlens; p.status = a->dev_status;
     p.t_max = a->t_max; p.n_max = a->n_max; p.D = a->D;
-    p.tiles = (a->t_max + (backward ? kTileB : kTileF) - 1) / (backward ? kTileB : kTileF);
-    const cudaError_t e = a->dtype == GCL_BF16 ? launch<__nv_bfloat16>(a, p, backward, s)
-                          : a->dtype == GCL_F16 ? launch<__half>(a, p, backward, s)
-                                                : launch<float>(a, p, backward, s);
+    if (before.tiles > 0) {                                // the states before each 64 tokens, by a forward without o and ht
+        const Params w = before;
+        before = p;
+        before.head = w.head; before.first = w.first; before.chain = w.chain;
+        before.tile = w.tile; before.tiles = w.tiles;
+        before.d_o.p = nullptr;
+    }
+    const cudaError_t e = a->dtype == GCL_BF16 ? launch<__nv_bfloat16>(p, before, backward, s)
+                          : a->dtype == GCL_F16 ? launch<__half>(p, before, backward, s)
+                                                : launch<float>(p, before, backward, s);
     return cuda_check(e, fn);
 }
 
@@ -193,8 +211,8 @@ using namespace gcl;
 
 extern "C" {
 
-size_t gcl_glr_fwd_workspace_bytes(const gcl_glr_args *a) { return glr::sizes_ok(a) ? glr::layout(a, false, nullptr) : 0; }
-size_t gcl_glr_bwd_workspace_bytes(const gcl_glr_args *a) { return glr::sizes_ok(a) ? glr::layout(a, true, nullptr) : 0; }
+size_t gcl_glr_fwd_workspace_bytes(const gcl_glr_args *a) { return glr::workspace(a, false); }
+size_t gcl_glr_bwd_workspace_bytes(const gcl_glr_args *a) { return glr::workspace(a, true); }
 gcl_status_t glr_fwd(const gcl_glr_args *a, gcl_stream_t stream) { return glr::run("glr_fwd", a, false, static_cast<cudaStream_t>(stream)); }
 gcl_status_t glr_bwd(const gcl_glr_args *a, gcl_stream_t stream) { return glr::run("glr_bwd", a, true, static_cast<cudaStream_t>(stream)); }
 

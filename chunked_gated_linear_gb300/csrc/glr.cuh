@@ -271,7 +271,7 @@ struct Params {
     Packet *chain;                 // [spans, D], in the order of the recurrence
     float *drate_part;             // [tiles, D]
     int64_t t_max, tiles;
-    int32_t n_max, D, n_cb;        // n_cb: blocks of channels
+    int32_t n_max, D, n_cb, tile;  // n_cb: blocks of channels; tokens of a tile
 };
 
 // Launchers, one pair for each type of the rows.
@@ -279,8 +279,6 @@ template <typename T>
 cudaError_t launch_fwd(const Params &p, cudaStream_t s);
 template <typename T>
 cudaError_t launch_bwd(const Params &p, cudaStream_t s);
-
-void launch_setup(const Params &p, const float *in_state, float *out_state, int tile, int blocks, cudaStream_t s);
 
 constexpr int kTileF = 128, kTileB = 64;               // tokens of a tile, forward and backward
 constexpr int kRanks = 2;                              // tiles of a span (65,536 tokens of 2,048 channels: 246 us; four 251, eight 297;

@@ -383,9 +383,11 @@ bool rows_map(CUtensorMap *m, const Params &p, const Rows &r, int tile) {
     return make_tensor_map(m, r.p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, dt);
 }
 
-// Launches the set-up and, as its dependent, `kernel` in clusters, at most `ctas` blocks an SM.
+// Launches `kernel` in clusters, at most `ctas` blocks an SM, as the dependent of the launch before (the set-up, or the walk that
+// forms the states).
 template <typename T, typename K>
-cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float *out_state, int tile, int ctas, cudaStream_t s) {
+cudaError_t launch_tiles(K kernel, const Params &p, int ctas, cudaStream_t s) {
+    const int tile = p.tile;
     Maps maps;
     const Rows *rows[4] = {&p.r, &p.x, &p.d_o, &p.i};
     int n = 0;
@@ -398,10 +400,6 @@ cudaError_t launch_tiles(K kernel, const Params &p, const float *in_state, float
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t spans = (p.tiles + kRanks - 1) / kRanks, units = spans * p.n_cb, most = (int64_t)ctas * num_sms() / kRanks;
-    int64_t setup = (spans * p.D + 4095) / 4096;
-    if (out_state && setup < (p.n_max + 7) / 8) setup = (p.n_max + 7) / 8;
-    if (setup > num_sms()) setup = num_sms();
-    launch_setup(p, in_state, out_state, tile, (int)setup, s);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((units < most ? units : most) * kRanks));
     cfg.blockDim = dim3(32 * kWarps);
