@@ -50,7 +50,7 @@ bool sizes_ok(const gcl_block_args *a) {
 
 size_t bwd_workspace(const gcl_block_args *a) {
     if (!sizes_ok(a)) return 0;
-    const int64_t rows = a->t_max * a->H, most = (int64_t)kMaxBlocks * num_sms();
+    const int64_t rows = a->t_max * a->H, most = (int64_t)kBwdBlocks * num_sms();
     return (size_t)(rows < most ? rows : most) * 2 * a->D * sizeof(float);
 }
 

@@ -319,6 +319,8 @@ __device__ __forceinline__ void weight(const uint4 *at, int v, const void *w, in
     r.get(f);
 }
 
+namespace {                        // (of each library its own: the caches of launch_kernel too)
+
 constexpr int fwd_blocks(int tpr, int vpt) { return vpt > 2 ? 1 : 640 / threads_of(tpr); }
 constexpr int bwd_blocks(int tpr, int vpt) { return vpt > 2 ? 1 : tpr > 256 ? 1 : tpr > 128 ? 2 : 3; }
 
@@ -695,18 +697,18 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
     }
 }
 
-constexpr int kMaxBlocks = 8;      // blocks an SM at most
+constexpr int kFwdBlocks = 8, kBwdBlocks = 3;          // blocks an SM at most (the backward's leave sums in the workspace)
 
 // Resident blocks on the current device (each then walks rows); 0: an error.  Looked up once a kernel and device, in `cache`.
 template <typename K>
-inline int resident(K kernel, int threads, size_t smem, std::atomic<int> *cache) {
+inline int resident(K kernel, int threads, size_t smem, int most, std::atomic<int> *cache) {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     if ((n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess)
         return 0;
-    n = (n < kMaxBlocks ? n : kMaxBlocks) * num_sms();
+    n = (n < most ? n : most) * num_sms();
     cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
@@ -719,7 +721,7 @@ cudaError_t launch_kernel(Params p, int *blocks, cudaStream_t s) {
                         (BWD && sums_in_smem(VPT) ? sizeof(P) * 2 * VPT * kPairs * TPR : 0);
     static std::atomic<int> cache[64];                     // zero-initialised (static storage)
     auto launch = [&](auto kernel) {
-        const int most = resident(kernel, threads_of(TPR), smem, cache);
+        const int most = resident(kernel, threads_of(TPR), smem, BWD ? kBwdBlocks : kFwdBlocks, cache);
         if (most < 1) return cudaErrorInvalidConfiguration;
         const int64_t need = (p.t_max * p.H + R - 1) / R;
         *blocks = (int)(need < most ? need : most);
@@ -750,6 +752,8 @@ cudaError_t launch_ts(const Params &p, int *blocks, cudaStream_t s) {
     if (V == 1 && p.D <= 8192) return launch_kernel<T, S, 512, 2, BWD>(p, blocks, s);
     return launch_kernel<T, S, 512, 4, BWD>(p, blocks, s);
 }
+
+}  // namespace
 
 // One pair of these for each type of the rows and of the stream (block_norm_*.cu); *blocks: the backward's blocks.
 template <typename T, typename S>

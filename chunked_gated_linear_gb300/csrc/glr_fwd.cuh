@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
 template <typename T>
 cudaError_t launch_fwd(const Params &p, cudaStream_t s) {
     return for_kind(p.kind.decay, p.kind.mix, p.i.p != nullptr, [&](auto d, auto m, auto g) {
-        return launch_tiles<T>(glr_fwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>, p, kCtas, s);
+        return launch_tiles<T, glr_fwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>>(p, kCtas, s);
     });
 }
 

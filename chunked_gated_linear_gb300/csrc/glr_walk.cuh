@@ -16,6 +16,8 @@
 // the same recurrence with the same decays, cut where a sequence ends, over the tiles from last to first.
 #pragma once
 
+#include <atomic>
+
 #include "glr.cuh"
 #include "tc_ptx.cuh"
 
@@ -385,8 +387,8 @@ bool rows_map(CUtensorMap *m, const Params &p, const Rows &r, int tile) {
 
 // Launches `kernel` in clusters, at most `ctas` blocks an SM, as the dependent of the launch before (the set-up, or the walk that
 // forms the states).
-template <typename T, typename K>
-cudaError_t launch_tiles(K kernel, const Params &p, int ctas, cudaStream_t s) {
+template <typename T, auto kernel>
+cudaError_t launch_tiles(const Params &p, int ctas, cudaStream_t s) {
     const int tile = p.tile;
     Maps maps;
     const Rows *rows[4] = {&p.r, &p.x, &p.d_o, &p.i};
@@ -397,8 +399,14 @@ cudaError_t launch_tiles(K kernel, const Params &p, int ctas, cudaStream_t s) {
             ++n;
         }
     const size_t smem = (size_t)2 * n * tile * 128;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> allowed[64];                  // by device; zero-initialised (static storage)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+    }
     const int64_t spans = (p.tiles + kRanks - 1) / kRanks, units = spans * p.n_cb, most = (int64_t)ctas * num_sms() / kRanks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((units < most ? units : most) * kRanks));
@@ -413,8 +421,8 @@ cudaError_t launch_tiles(K kernel, const Params &p, int ctas, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t l = cudaLaunchKernelEx(&cfg, kernel, maps, p);
-    return l != cudaSuccess ? l : cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, kernel, maps, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

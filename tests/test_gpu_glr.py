@@ -153,6 +153,19 @@ def test_wide_and_many_tiles():
     c.check_bwd(c.bwd(c.save))
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 8), ("bf16", 72), ("f16", 264)])
+def test_borders_anywhere(dtype, D):
+    """Thousands of tokens in sequences of 0 to 400: starts and ends at every place of tiles, spans and warps, many spans in flight
+    of few channels."""
+    r = np.random.default_rng(D)
+    lens = [int(n) for n in r.integers(0, 401, 60)] + [1] * 40 + [0] * 3 + [5000]
+    c = Case(dtype, lens, D, "power", "root", True, seed=D, pad=200)
+    c.fwd()
+    c.check_fwd()
+    c.check_bwd(c.bwd(c.save))
+    c.check_bwd(c.bwd())
+
+
 def test_results_repeat():
     c = Case("bf16", [3000, 77, 4000], 1000, "power", "root", True)
     first = [t.clone() for t in c.fwd()]
