@@ -855,7 +855,7 @@ def _code_of(fn, name, dtype):
 def _rows2(fn, name, t, shape, dtype, device):
     """gcl_rows of a tensor [tokens, D] with contiguous D and any token stride."""
     if t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{fn}: {name} must be a CUDA tensor {shape} of {dtype} on the call's device (got {tuple(t.shape)}, "
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor {tuple(shape)} of {dtype} on the call's device (got {tuple(t.shape)}, "
                          f"{t.dtype}, {t.device})")
     st, sd = t.stride()
     if sd != 1 or st < 0:
@@ -901,7 +901,7 @@ def glr_fwd(x, r, cu_seqlens, o, i=None, rate=None, h0=None, ht=None, h_save=Non
         _load_torch()
     f32, i32 = _F32, _I32
     fn = "glr_fwd"
-    sx = tuple(x.shape)
+    sx = x.shape
     T, D = sx
     N, dt, dev = cu_seqlens.shape[0] - 1, x.dtype, x.get_device()
     kd, km = _kind(fn, decay, mix)
@@ -909,9 +909,9 @@ def glr_fwd(x, r, cu_seqlens, o, i=None, rate=None, h0=None, ht=None, h_save=Non
         *_rows2(fn, "x", x, sx, dt, dev), *_rows2(fn, "r", r, sx, dt, dev),
         *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)),
         *(_NO_ROWS if o is None else _rows2(fn, "o", o, sx, dt, dev)), *_NO_ROWS, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
-        _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "h0", h0, (N, D), f32, dev), _flat(fn, "ht", ht, (N, D), f32, dev),
-        0, 0, 0, _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
-        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev), 0 if h0 is None else _flat(fn, "h0", h0, (N, D), f32, dev), 0 if ht is None else _flat(fn, "ht", ht, (N, D), f32, dev),
+        0, 0, 0, 0 if h_save is None else _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), 0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev),
         *_scratch(fn, workspace, dev), T, N, D, kd, km, _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
@@ -924,7 +924,7 @@ def glr_bwd(x, r, d_o, cu_seqlens, dx, dr, i=None, di=None, rate=None, drate=Non
         _load_torch()
     f32, i32 = _F32, _I32
     fn = "glr_bwd"
-    sx = tuple(x.shape)
+    sx = x.shape
     T, D = sx
     N, dt, dev = cu_seqlens.shape[0] - 1, x.dtype, x.get_device()
     kd, km = _kind(fn, decay, mix)
@@ -935,10 +935,10 @@ def glr_bwd(x, r, d_o, cu_seqlens, dx, dr, i=None, di=None, rate=None, drate=Non
         *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)), *_NO_ROWS, *_rows2(fn, "d_o", d_o, sx, dt, dev),
         *_rows2(fn, "dx", dx, sx, dt, dev), *_rows2(fn, "dr", dr, sx, dt, dev),
         *(_NO_ROWS if di is None else _rows2(fn, "di", di, sx, dt, dev)),
-        _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "h0", h0, (N, D), f32, dev), 0,
-        _flat(fn, "dht", dht, (N, D), f32, dev), _flat(fn, "dh0", dh0, (N, D), f32, dev),
-        _flat(fn, "drate", drate, (D,), f32, dev), _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
-        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev), 0 if h0 is None else _flat(fn, "h0", h0, (N, D), f32, dev), 0,
+        0 if dht is None else _flat(fn, "dht", dht, (N, D), f32, dev), 0 if dh0 is None else _flat(fn, "dh0", dh0, (N, D), f32, dev),
+        0 if drate is None else _flat(fn, "drate", drate, (D,), f32, dev), 0 if h_save is None else _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), 0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev),
         *_scratch(fn, workspace, dev), T, N, D, kd, km, _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
@@ -950,15 +950,15 @@ def glr_step(x, r, state, o, i=None, rate=None, slots=None, decay="power", mix="
         _load_torch()
     f32, i32 = _F32, _I32
     fn = "glr_step"
-    sx = tuple(x.shape)
+    sx = x.shape
     B, D = sx
     dt, dev, n_slots = x.dtype, x.get_device(), state.shape[0]
     kd, km = _kind(fn, decay, mix)
     packed = _GLR_STEP_PACK.pack(
         *_rows2(fn, "x", x, sx, dt, dev), *_rows2(fn, "r", r, sx, dt, dev),
         *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)), *_rows2(fn, "o", o, sx, dt, dev),
-        _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "state", state, (n_slots, D), f32, dev),
-        _flat(fn, "slots", slots, (B,), i32, dev), _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, D, kd, km,
+        0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "state", state, (n_slots, D), f32, dev),
+        0 if slots is None else _flat(fn, "slots", slots, (B,), i32, dev), 0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, D, kd, km,
         _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
@@ -973,7 +973,7 @@ def _rows3(fn, name, t, shape, dtype, device):
     if len(shape) == 2:
         return _rows2(fn, name, t, shape, dtype, device)
     if t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{fn}: {name} must be a CUDA tensor {shape} of {dtype} on the call's device (got {tuple(t.shape)}, "
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor {tuple(shape)} of {dtype} on the call's device (got {tuple(t.shape)}, "
                          f"{t.dtype}, {t.device})")
     T, H, D = shape
     st, sh, sd = t.stride()

@@ -81,6 +81,9 @@ bool sizes_ok(const gcl_glr_args *a) {
            a->D <= (1 << 20) && (a->dtype == GCL_F32 || a->dtype == GCL_BF16 || a->dtype == GCL_F16);
 }
 
+// A call of one span needs no meeting of spans and no launch before it (256 tokens of 512 channels, fp16: XSOLO).
+bool solo(const Params &p) { return p.tiles <= kRanks; }
+
 // The workspace's parts, in order; its base may be NULL (for the size alone).  before: the walk that forms the states which a
 // backward without h_save needs.
 size_t layout(const gcl_glr_args *a, bool backward, Params *p, Params *before) {
@@ -111,11 +114,17 @@ size_t layout(const gcl_glr_args *a, bool backward, Params *p, Params *before) {
 template <typename T>
 cudaError_t launch(Params p, Params before, bool backward, cudaStream_t s) {
     p.n_cb = before.n_cb = (p.D + Lane<T>::CB - 1) / Lane<T>::CB;
-    cudaError_t e = launch_setup(p, before, backward ? p.dht : p.h0, backward ? p.dh0 : p.ht, s);
+    const bool states = before.tiles > 0;
+    for (Params *w : {&p, &before})
+        if (solo(*w)) w->first = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (!solo(p)) {
+        Params none{};
+        e = launch_setup(p, states && !solo(before) ? before : none, backward ? p.dht : p.h0, backward ? p.dh0 : p.ht, s);
+    }
+    if (e == cudaSuccess && states) e = launch_fwd<T>(before, s);
     if (e != cudaSuccess) return e;
-    if (!backward) return launch_fwd<T>(p, s);
-    if (before.tiles > 0 && (e = launch_fwd<T>(before, s)) != cudaSuccess) return e;
-    return launch_bwd<T>(p, s);
+    return backward ? launch_bwd<T>(p, s) : launch_fwd<T>(p, s);
 }
 
 }  // namespace

@@ -267,7 +267,8 @@ struct Params {
     const int32_t *cu;
     int32_t *status;
     Header *head;
-    int32_t *first;                // [tiles]: the first sequence that starts at or behind the tile's first token
+    int32_t *first;                // [tiles]: the first sequence that starts at or behind the tile's first token; NULL: solo, a call of one
+                                   // span, whose launch does the set-up's work itself
     Packet *chain;                 // [spans, D], in the order of the recurrence
     float *drate_part;             // [tiles, D]
     int64_t t_max, tiles;

@@ -74,7 +74,18 @@ __device__ __forceinline__ void borders(const Params &p, Tile<TILE> &t) {
     const int lane = threadIdx.x & 31;
     uint32_t starts[TILE / 32] = {}, ends[TILE / 32] = {};
     if (t.n > 0) {
-        const int f = p.first[t.t0 / TILE];
+        int f;
+        if (p.first) {
+            f = p.first[t.t0 / TILE];
+        } else {                                           // first n with cu[n] >= t0 (n_max if none)
+            int hi = p.n_max;
+            f = 0;
+            while (f < hi) {
+                const int mid = (f + hi) >> 1;
+                if (p.cu[mid] >= t.t0) hi = mid;
+                else f = mid + 1;
+            }
+        }
         for (int n = (f > 0 ? f - 1 : 0) + lane; n < p.n_max; n += 32) {
             const int b = p.cu[n] - t.t0, e = p.cu[n + 1] - t.t0;          // (both lie in [0, 2^31))
             if (b >= TILE) break;
@@ -239,7 +250,7 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
             h0 = q ? t.y : fmaf(t.x, h0, t.y);
             A0 *= t.x;
         }
-    const bool speaks = rank == kRanks - 1 && on, span_cut = cut || cut0;  // (the last block speaks for the span)
+    const bool speaks = rank == kRanks - 1 && on && p.first, span_cut = cut || cut0;  // (the last block speaks for the span)
     if (!cut) h = fmaf(A, h0, h);
     A *= A0;
     if (speaks) store_packet(mine, A, h, h, span_cut ? kDone : kOwn);
@@ -261,6 +272,35 @@ struct Maps {                      // the staged rows: r, x, d_o (backward), i
 };
 
 constexpr int kIssuer = 96;        // the thread that takes spans and issues the copies
+
+// Live tokens, once the set-up is done; -1: the call does nothing.  A solo call's blocks check cu_seqlens themselves and pass
+// the states of empty sequences through, each its channels.  Every thread of the block (block barriers).
+template <typename T>
+__device__ __forceinline__ int64_t live_tokens(const Params &p, const float *in_state, float *out_state) {
+    grid_dependency_wait();
+    if (p.first) return p.head->blocked ? -1 : p.head->live;
+    const bool stop = status_blocks_cta(p.status);
+    int bad = 0;
+    for (int n = threadIdx.x; n < p.n_max; n += blockDim.x) {
+        const int b = p.cu[n], e = p.cu[n + 1];
+        bad |= b < 0 || e < b || e > p.t_max || (n == 0 && b != 0);
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+        if (bad && !stop) status_set(p.status, GCL_DEV_BAD_RANGE);
+        if (blockIdx.x == 0) {                             // (for the sum of the rates' gradients)
+            p.head->blocked = stop || bad;
+            p.head->live = stop || bad ? 0 : p.cu[p.n_max];
+        }
+    }
+    if (stop || bad) return -1;
+    if (out_state) {
+        const int ch = (blockIdx.x / kRanks) * Lane<T>::CB + (threadIdx.x & 31) * Lane<T>::V;
+        for (int n = blockIdx.x % kRanks * kWarps + (threadIdx.x >> 5); n < p.n_max; n += kRanks * kWarps)
+            if (p.cu[n + 1] == p.cu[n]) store_state<T>(out_state, n, p.D, ch, load_state<T>(in_state, n, p.D, ch));
+    }
+    return p.cu[p.n_max];
+}
 
 // A block's walk over its tiles, which both directions share.  Its next tile's rows are staged while one is computed.
 template <bool REV, int CB, int RUN>
@@ -302,7 +342,7 @@ struct Walk {
             tc::mbar_init(&s.sent[1], 1);
             tc::fence_barrier_init();
             s.err = 0;
-            if (rank == 0) s.next[1] = atomicAdd(&p.head->ticket, 1u);
+            if (rank == 0) s.next[1] = p.first ? atomicAdd(&p.head->ticket, 1u) : blockIdx.x / kRanks;
         }
         cluster_arrive();
         cluster_wait();
@@ -328,7 +368,9 @@ struct Walk {
         parity ^= 1u << buf;
     }
     // Takes the cluster's next span (its number reaches the blocks by the exchange).
-    __device__ __forceinline__ uint32_t take() { return rank == 0 && threadIdx.x == kIssuer ? atomicAdd(&p.head->ticket, 1u) : 0; }
+    __device__ __forceinline__ uint32_t take() {
+        return rank != 0 || threadIdx.x != kIssuer ? 0 : p.first ? atomicAdd(&p.head->ticket, 1u) : units;
+    }
     // Between a tile's halves: the warps' own states are in s.a, s.b; afterwards the states that enter them in s.b.
     // What a block receives at parity `buf` it has used when it arrives on the cluster's barrier, and the peers send there again
     // two tiles later, after they have waited on that barrier.
@@ -409,18 +451,18 @@ cudaError_t launch_tiles(const Params &p, int ctas, cudaStream_t s) {
     }
     const int64_t spans = (p.tiles + kRanks - 1) / kRanks, units = spans * p.n_cb, most = (int64_t)ctas * num_sms() / kRanks;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((units < most ? units : most) * kRanks));
+    cfg.gridDim = dim3((unsigned)((units < most || !p.first ? units : most) * kRanks));
     cfg.blockDim = dim3(32 * kWarps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kRanks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kRanks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = p.first ? 2 : 1;                        // (a solo call waits for whatever was before)
     e = cudaLaunchKernelEx(&cfg, kernel, maps, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
