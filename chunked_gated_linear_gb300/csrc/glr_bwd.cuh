@@ -26,11 +26,12 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int narr = GATE ? 4 : 3;
     launch_dependents();                                   // (the sum of the rates' gradients waits for this grid's end)
-    const int64_t live = live_tokens<T>(p, p.dht, p.dh0);
+    bool stop;
+    const int64_t live = live_tokens(p, stop);
     if (live < 0) return;
     const int64_t tiles = (live + W::TILE - 1) / W::TILE;
     W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0, 0};
-    if (!walk.start()) return;
+    if (!walk.template start<T>(stop, p.dht, p.dh0)) return;
     for (int buf = 0;; buf ^= 1) {
         const Tile<W::TILE> &tile = s.tile[buf];
         const int64_t t = tile.t0 + warp * RUN;

@@ -271,35 +271,39 @@ struct Maps {                      // the staged rows: r, x, d_o (backward), i
     CUtensorMap m[4];
 };
 
+constexpr uint32_t kStopped = 0xffffffffu;             // no span: the call does nothing
 constexpr int kIssuer = 96;        // the thread that takes spans and issues the copies
 
-// Live tokens, once the set-up is done; -1: the call does nothing.  A solo call's blocks check cu_seqlens themselves and pass
-// the states of empty sequences through, each its channels.  Every thread of the block (block barriers).
-template <typename T>
-__device__ __forceinline__ int64_t live_tokens(const Params &p, const float *in_state, float *out_state) {
+// Live tokens, once the set-up is done; -1: the call does nothing.  A solo call's blocks check cu_seqlens themselves; the status word
+// is read by each cluster's first block alone (`stop`, in one thread: `start` tells the others), since it may change between two reads
+// and a block that left alone would be sent to.  Every thread of the block (block barriers).
+__device__ __forceinline__ int64_t live_tokens(const Params &p, bool &stop) {
+    stop = false;
     grid_dependency_wait();
     if (p.first) return p.head->blocked ? -1 : p.head->live;
-    const bool stop = status_blocks_cta(p.status);
     int bad = 0;
     for (int n = threadIdx.x; n < p.n_max; n += blockDim.x) {
         const int b = p.cu[n], e = p.cu[n + 1];
         bad |= b < 0 || e < b || e > p.t_max || (n == 0 && b != 0);
     }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kIssuer && cluster_rank() == 0) {
+        stop = p.status && *reinterpret_cast<volatile int32_t *>(p.status) != 0;
         if (bad && !stop) status_set(p.status, GCL_DEV_BAD_RANGE);
         if (blockIdx.x == 0) {                             // (for the sum of the rates' gradients)
             p.head->blocked = stop || bad;
             p.head->live = stop || bad ? 0 : p.cu[p.n_max];
         }
     }
-    if (stop || bad) return -1;
-    if (out_state) {
-        const int ch = (blockIdx.x / kRanks) * Lane<T>::CB + (threadIdx.x & 31) * Lane<T>::V;
-        for (int n = blockIdx.x % kRanks * kWarps + (threadIdx.x >> 5); n < p.n_max; n += kRanks * kWarps)
-            if (p.cu[n + 1] == p.cu[n]) store_state<T>(out_state, n, p.D, ch, load_state<T>(in_state, n, p.D, ch));
-    }
-    return p.cu[p.n_max];
+    return bad ? -1 : p.cu[p.n_max];
+}
+// The states of empty sequences, of the block's channels (a solo call).
+template <typename T>
+__device__ __forceinline__ void pass_empty(const Params &p, const float *in_state, float *out_state) {
+    if (!out_state) return;
+    const int ch = (blockIdx.x / kRanks) * Lane<T>::CB + (threadIdx.x & 31) * Lane<T>::V;
+    for (int n = blockIdx.x % kRanks * kWarps + (threadIdx.x >> 5); n < p.n_max; n += kRanks * kWarps)
+        if (p.cu[n + 1] == p.cu[n]) store_state<T>(out_state, n, p.D, ch, load_state<T>(in_state, n, p.D, ch));
 }
 
 // A block's walk over its tiles, which both directions share.  Its next tile's rows are staged while one is computed.
@@ -332,8 +336,10 @@ struct Walk {
         for (int a = 0; a < narr; ++a)
             tc::tma_load_2d(rows + (buf * narr + a) * BYTES, &maps.m[!REV && a == 2 ? 3 : a], t.cb * CB, t.t0, &s.full[buf]);
     }
-    // Sets up the barriers and takes the cluster's first span; false: there is none.  Every thread of the cluster.
-    __device__ __forceinline__ bool start() {
+    // Sets up the barriers and takes the cluster's first span; false: there is none, or a solo call is to do nothing (`stop`, the first
+    // block's issuer's).  Every thread of the cluster.
+    template <typename T>
+    __device__ __forceinline__ bool start(bool stop, const float *in_state, float *out_state) {
         const int tid = threadIdx.x;
         if (tid == kIssuer) {
             tc::mbar_init(&s.full[0], 1);
@@ -342,11 +348,12 @@ struct Walk {
             tc::mbar_init(&s.sent[1], 1);
             tc::fence_barrier_init();
             s.err = 0;
-            if (rank == 0) s.next[1] = p.first ? atomicAdd(&p.head->ticket, 1u) : blockIdx.x / kRanks;
+            if (rank == 0) s.next[1] = p.first ? atomicAdd(&p.head->ticket, 1u) : stop ? kStopped : blockIdx.x / kRanks;
         }
         cluster_arrive();
         cluster_wait();
         const uint32_t unit = peer_load(&s.next[1], 0);
+        if (!p.first && unit != kStopped) pass_empty<T>(p, in_state, out_state);
         if (unit >= units) {
             cluster_arrive();                              // (the first block stays until all have read)
             cluster_wait();
