@@ -637,7 +637,7 @@ gcl_status_t rope_table_build(float *cos_table, float *sin_table, int64_t n_posi
  *
  * A zero-length sequence passes its state through (ht = h0, dh0 = dht).  a = 0 (r = -inf) and a = 1 are
  * allowed; r > 0 of GCL_DECAY_LOG is computed as given (m(a) = 0 with GCL_MIX_ROOT) as long as the product of a over
- * 128 consecutive tokens is finite.  Rows at or past cu_seqlens[n_max] are neither used nor written.  A value
+ * 256 consecutive tokens is finite.  For 16-bit rows with an input gate, sigmoid(r) and sigmoid(i) are not below 2^-63.  Rows at or past cu_seqlens[n_max] are neither used nor written.  A value
  * that is not finite reaches later tokens of its own sequence and channel alone (a d_o: earlier ones).
  *
  * h_save (forward, optional) receives the state before tokens 0, 64, 128, ... of the packed axis (a
