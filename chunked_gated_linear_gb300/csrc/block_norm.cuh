@@ -261,13 +261,14 @@ __device__ __forceinline__ T *vec_at(char *at, int v, int tpr) { return reinterp
 // Rows too wide for that (STAGED false) are read from memory each time.
 template <typename T, bool STAGED, int THREADS>
 __device__ __forceinline__ void stage_copy(uint4 *at, int chunk, const T *src, bool on) {
-    if (!STAGED) return;
+    if constexpr (STAGED) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         static_cast<uint32_t>(__cvta_generic_to_shared(at + (chunk + i) * THREADS))),
-                     "l"(reinterpret_cast<const uint4 *>(src) + i), "r"(on ? 16 : 0)
-                     : "memory");
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             static_cast<uint32_t>(__cvta_generic_to_shared(at + (chunk + i) * THREADS))),
+                         "l"(reinterpret_cast<const uint4 *>(src) + i), "r"(on ? 16 : 0)
+                         : "memory");
+    }
 }
 template <typename T, bool STAGED, int THREADS>
 __device__ __forceinline__ void stage_get(const uint4 *at, int chunk, const T *src, bool on, P *f) {
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
             }
             float ss = sum_of(q);
             sum.template operator()<1>(&ss);
-            ry = inverse_length(p.post, ss, inv_d, p.eps);
+            ry = live ? inverse_length(p.post, ss, inv_d, p.eps) : 0.f;       // (a row past the last adds 0 to the weights' sums)
         }
         // per vector: act and its slope, times scale and dropout's factor; then xo (v without dz), which the outputs use again
         P a[VPT][kPairs], da[VPT][kPairs], xo[VPT][kPairs];
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
         if (p.dz.p) {
             sum.template operator()<5>(s5);
             if (p.pre != GCL_NORM_NONE) {
-                r = inverse_length(p.pre, s5[1], inv_d, p.eps);
+                r = live ? inverse_length(p.pre, s5[1], inv_d, p.eps) : 0.f;
                 m = r * r * r * s5[2] * (p.pre == GCL_NORM_RMS ? inv_d : 1.f);
             }
             mean = s5[0] + r * s5[3] - m * s5[4];

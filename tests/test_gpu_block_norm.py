@@ -1,5 +1,6 @@
 """The norms around a block on the GPU against their definition in fp64 (tests/glr_ref.py, where the tolerances stand)."""
 import itertools
+import sys
 
 import numpy as np
 import pytest
@@ -276,3 +277,11 @@ def test_captured_calls_read_their_buffers():
             c.check_bwd(out)
     finally:
         OFFSET = was
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_no_eps(norm, monkeypatch):
+    """eps = 0: rows that a block holds no more of add nothing to the weights' gradients (not 0 times infinity)."""
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 0.0)
+    for T, live in ((5, None), (37, 30)):
+        Case(T, 1, 64, "bf16", post=norm, pre=norm, live=live).check()
