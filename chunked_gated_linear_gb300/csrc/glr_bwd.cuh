@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(1024) glr_drate_kernel(const Params p, int til
 template <typename T>
 cudaError_t launch_bwd(const Params &p, cudaStream_t s) {
     const cudaError_t e = for_kind(p.kind.decay, p.kind.mix, p.i.p != nullptr, [&](auto d, auto m, auto g) {
-        return launch_tiles<T, glr_bwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>>(p, kCtas, s);
+        return launch_tiles<T, glr_bwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>>(p, kCtas, 2, s);
     });
     if (e != cudaSuccess || !p.drate) return e;
     return launch_dependent(glr_drate_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, p, kTileB);

@@ -310,6 +310,7 @@ __device__ __forceinline__ void pass_empty(const Params &p, const float *in_stat
 template <bool REV, int CB, int RUN>
 struct Walk {
     static constexpr int TILE = kWarps * RUN, BYTES = TILE * 128;
+    static constexpr int BUFS = REV ? 2 : 1;               // of rows: forwards they are read before the exchange alone
     const Params &p;
     Shared<CB, RUN> &s;
     const Maps &maps;
@@ -334,7 +335,7 @@ struct Walk {
         issued = (issued ^ 1u << buf) | 4u << buf;
         tc::mbar_arrive_expect_tx(&s.full[buf], narr * BYTES);
         for (int a = 0; a < narr; ++a)
-            tc::tma_load_2d(rows + (buf * narr + a) * BYTES, &maps.m[!REV && a == 2 ? 3 : a], t.cb * CB, t.t0, &s.full[buf]);
+            tc::tma_load_2d(rows + (buf * (BUFS - 1) * narr + a) * BYTES, &maps.m[!REV && a == 2 ? 3 : a], t.cb * CB, t.t0, &s.full[buf]);
     }
     // Sets up the barriers and takes the cluster's first span; false: there is none, or a solo call is to do nothing (`stop`, the first
     // block's issuer's).  Every thread of the cluster.
@@ -437,7 +438,7 @@ bool rows_map(CUtensorMap *m, const Params &p, const Rows &r, int tile) {
 // Launches `kernel` in clusters, at most `ctas` blocks an SM, as the dependent of the launch before (the set-up, or the walk that
 // forms the states).
 template <typename T, auto kernel>
-cudaError_t launch_tiles(const Params &p, int ctas, cudaStream_t s) {
+cudaError_t launch_tiles(const Params &p, int ctas, int bufs, cudaStream_t s) {
     const int tile = p.tile;
     Maps maps;
     const Rows *rows[4] = {&p.r, &p.x, &p.d_o, &p.i};
@@ -447,7 +448,7 @@ cudaError_t launch_tiles(const Params &p, int ctas, cudaStream_t s) {
             if (!rows_map<T>(&maps.m[k], p, *rows[k], tile)) return cudaErrorInvalidValue;
             ++n;
         }
-    const size_t smem = (size_t)2 * n * tile * 128;
+    const size_t smem = (size_t)bufs * n * tile * 128;
     static std::atomic<bool> allowed[64];                  // by device; zero-initialised (static storage)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
