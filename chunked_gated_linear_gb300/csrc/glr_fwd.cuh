@@ -12,29 +12,6 @@ namespace {
 constexpr int kCtas = 3;                               // resident blocks an SM
 static_assert(kTileF % kSave == 0, "saved states lie at tiles' starts");
 
-// a and b of a group of tokens, 16 words a lane, through tensor memory: the lane's own words.
-template <typename T>
-struct Group {
-    using L = Lane<T>;
-    static constexpr int N = 8 / L::V;                     // tokens
-    typename L::P a[N], b[N];
-    __device__ __forceinline__ void put(uint32_t at) const {
-        __align__(8) float v[16];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            L::store(v + k * L::V, a[k]);
-            L::store(v + 8 + k * L::V, b[k]);
-        }
-        tc::tmem_st16(at, v);
-    }
-};
-// (the wait takes the words along, so that no use of one moves before it)
-__device__ __forceinline__ void group_wait(float *v) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
-                   "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
-}
-
 template <typename T, int DECAY, int MIX, bool GATE>
 __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Lane<T>;
@@ -44,7 +21,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
     __shared__ Shared<CB, RUN> s;
     __shared__ uint32_t s_tmem;
     extern __shared__ __align__(128) uint8_t s_rows[];     // [r, x, i][tile][128]
-    constexpr int G = Group<T>::N, WORDS = RUN / G * 16, COLS = WORDS * kWarps / 4;        // words of a lane; columns of a block
+    constexpr int G = 8 / V, WORDS = RUN / G * 16, COLS = WORDS * kWarps / 4;        // words of a lane; columns of a block
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int narr = GATE ? 3 : 2;
     bool stop;
@@ -81,30 +58,29 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
             P A = L::all(1.f), h = L::all(0.f);
 #pragma unroll
             for (int k0 = 0; k0 < RUN; k0 += G) {
-                P r[G], g[G], sg[G];
-                Group<T> c;
+                P r[G], g[G], sg[G], a[G], b[G];
 #pragma unroll
                 for (int k = 0; k < G; ++k) {
                     r[k] = row(0, k0 + k);
                     if (GATE) g[k] = row(2, k0 + k);
                 }
-                gates<T, DECAY, MIX, GATE, G>(rate, near, r, g, c.a, c.b, sg);
+                gates<T, DECAY, MIX, GATE, G>(rate, near, r, g, a, b, sg);
 #pragma unroll
                 for (int k = 0; k < G; ++k) {
                     const P x = row(1, k0 + k);
-                    c.b[k] = L::mul(c.b[k], GATE ? L::mul(x, sg[k]) : x);
+                    b[k] = L::mul(b[k], GATE ? L::mul(x, sg[k]) : x);
                 }
                 if (n < k0 + G)
 #pragma unroll
                     for (int k = 0; k < G; ++k)
-                        if (k0 + k >= n) { c.a[k] = L::all(1.f); c.b[k] = L::all(0.f); }
-                c.put(words + k0 / G * 16);
+                        if (k0 + k >= n) { a[k] = L::all(1.f); b[k] = L::all(0.f); }
+                tmem_put<T>(words + k0 / G * 16, a, b);
                 auto run = [&](auto cut) {
 #pragma unroll
                     for (int k = 0; k < G; ++k) {
                         if (decltype(cut)::value && (starts >> (k0 + k) & 1)) h = load_state<T>(p.h0, start[k0 + k], p.D, ch);
-                        h = L::fma(c.a[k], h, c.b[k]);
-                        A = L::mul(A, c.a[k]);
+                        h = L::fma(a[k], h, b[k]);
+                        A = L::mul(A, a[k]);
                     }
                 };
                 if (starts >> k0 & ((1u << G) - 1)) run(std::true_type());
@@ -129,7 +105,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
 #pragma unroll
             for (int k0 = 0; k0 < RUN; k0 += G) {
                 float *c = v[k0 / G % 2];
-                group_wait(c);
+                tmem_wait<16>(c);
                 if (k0 + G < RUN) tc::tmem_ld16(words + (k0 / G + 1) * 16, v[(k0 / G + 1) % 2]);
 #pragma unroll
                 for (int k = 0; k < G; ++k) {

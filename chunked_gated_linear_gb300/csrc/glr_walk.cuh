@@ -135,6 +135,33 @@ __device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, 
     if (s && ch < D) Lane<T>::store(s + n * D + ch, h);
 }
 
+// ---- tensor memory: a lane's own words, eight for the tokens of a group ----
+template <typename T>
+__device__ __forceinline__ void tmem_put(uint32_t at, const typename Lane<T>::P *x, const typename Lane<T>::P *y) {
+    __align__(8) float v[16];
+#pragma unroll
+    for (int k = 0; k < 8; k += Lane<T>::V) {
+        Lane<T>::store(v + k, x[k / Lane<T>::V]);
+        Lane<T>::store(v + 8 + k, y[k / Lane<T>::V]);
+    }
+    tc::tmem_st16(at, v);
+}
+template <typename T>
+__device__ __forceinline__ void tmem_put(uint32_t at, const typename Lane<T>::P *x) {
+    __align__(8) float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; k += Lane<T>::V) Lane<T>::store(v + k, x[k / Lane<T>::V]);
+    tc::tmem_st8_b32(at, reinterpret_cast<const uint32_t *>(v));
+}
+// (the wait takes the words along, so that no use of one moves before it)
+template <int N>
+__device__ __forceinline__ void tmem_wait(float *v) {
+#pragma unroll
+    for (int k = 0; k < N; k += 8)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[k]), "+f"(v[k + 1]), "+f"(v[k + 2]), "+f"(v[k + 3]), "+f"(v[k + 4]), "+f"(v[k + 5]), "+f"(v[k + 6]), "+f"(v[k + 7])::"memory");
+}
+
 // ---- what spans leave each other ----
 __device__ __forceinline__ Packet load_packet(const Packet *p) {
     unsigned __int128 v;
