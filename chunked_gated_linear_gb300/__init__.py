@@ -909,9 +909,12 @@ def glr_fwd(x, r, cu_seqlens, o, i=None, rate=None, h0=None, ht=None, h_save=Non
         *_rows2(fn, "x", x, sx, dt, dev), *_rows2(fn, "r", r, sx, dt, dev),
         *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)),
         *(_NO_ROWS if o is None else _rows2(fn, "o", o, sx, dt, dev)), *_NO_ROWS, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
-        0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev), 0 if h0 is None else _flat(fn, "h0", h0, (N, D), f32, dev), 0 if ht is None else _flat(fn, "ht", ht, (N, D), f32, dev),
+        0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev),
+        0 if h0 is None else _flat(fn, "h0", h0, (N, D), f32, dev),
+        0 if ht is None else _flat(fn, "ht", ht, (N, D), f32, dev),
         0, 0, 0, 0 if h_save is None else _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
-        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), 0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev),
+        0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev),
         *_scratch(fn, workspace, dev), T, N, D, kd, km, _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
@@ -935,10 +938,14 @@ def glr_bwd(x, r, d_o, cu_seqlens, dx, dr, i=None, di=None, rate=None, drate=Non
         *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)), *_NO_ROWS, *_rows2(fn, "d_o", d_o, sx, dt, dev),
         *_rows2(fn, "dx", dx, sx, dt, dev), *_rows2(fn, "dr", dr, sx, dt, dev),
         *(_NO_ROWS if di is None else _rows2(fn, "di", di, sx, dt, dev)),
-        0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev), 0 if h0 is None else _flat(fn, "h0", h0, (N, D), f32, dev), 0,
-        0 if dht is None else _flat(fn, "dht", dht, (N, D), f32, dev), 0 if dh0 is None else _flat(fn, "dh0", dh0, (N, D), f32, dev),
-        0 if drate is None else _flat(fn, "drate", drate, (D,), f32, dev), 0 if h_save is None else _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
-        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev), 0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev),
+        0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev),
+        0 if h0 is None else _flat(fn, "h0", h0, (N, D), f32, dev), 0,
+        0 if dht is None else _flat(fn, "dht", dht, (N, D), f32, dev),
+        0 if dh0 is None else _flat(fn, "dh0", dh0, (N, D), f32, dev),
+        0 if drate is None else _flat(fn, "drate", drate, (D,), f32, dev),
+        0 if h_save is None else _flat(fn, "h_save", h_save, (_save_rows(T), D), f32, dev),
+        _flat(fn, "cu_seqlens", cu_seqlens, (N + 1,), i32, dev),
+        0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev),
         *_scratch(fn, workspace, dev), T, N, D, kd, km, _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 
@@ -958,7 +965,8 @@ def glr_step(x, r, state, o, i=None, rate=None, slots=None, decay="power", mix="
         *_rows2(fn, "x", x, sx, dt, dev), *_rows2(fn, "r", r, sx, dt, dev),
         *(_NO_ROWS if i is None else _rows2(fn, "i", i, sx, dt, dev)), *_rows2(fn, "o", o, sx, dt, dev),
         0 if rate is None else _flat(fn, "rate", rate, (D,), f32, dev), _flat(fn, "state", state, (n_slots, D), f32, dev),
-        0 if slots is None else _flat(fn, "slots", slots, (B,), i32, dev), 0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, D, kd, km,
+        0 if slots is None else _flat(fn, "slots", slots, (B,), i32, dev),
+        0 if dev_status is None else _flat(fn, "dev_status", dev_status, (1,), i32, dev), B, n_slots, D, kd, km,
         _code_of(fn, "x", dt))
     _packed_call(fn, packed, stream, dev)
 

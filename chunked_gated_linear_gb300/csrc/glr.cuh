@@ -195,20 +195,15 @@ __device__ __forceinline__ void decay_of(typename Lane<T>::P *a, typename Lane<T
 }
 
 // The gates of N tokens: a, m(a) and the input gate's sigmoid from r and g (g is not read without gate: GATE false, sg = 1).
-// rate: of the lane's channels; near: all the warp's rates lie in [0, kNear].  keep: for sigmoid(r), sigmoid(-r) and sigmoid(-g).
-template <typename P, int N>
-struct Sigmoids {
-    P r[N], nr[N], ng[N];
-};
+// rate: of the lane's channels; near: all the warp's rates lie in [0, kNear].
 template <typename T, int DECAY, int MIX, bool GATE, int N>
 __device__ __forceinline__ void gates(typename Lane<T>::P rate, bool near, const typename Lane<T>::P *r, const typename Lane<T>::P *g,
-                                      typename Lane<T>::P *a, typename Lane<T>::P *m, typename Lane<T>::P *sg,
-                                      Sigmoids<typename Lane<T>::P, N> *keep = nullptr) {
+                                      typename Lane<T>::P *a, typename Lane<T>::P *m, typename Lane<T>::P *sg) {
     using L = Lane<T>;
     using P = typename L::P;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        P s = L::all(0.f), c = L::all(0.f), cg = L::all(0.f);
+        P s = L::all(0.f), c = L::all(0.f), cg;
         if (DECAY == GCL_DECAY_LOG) {
             if (GATE) sigmoids<T>(g[e], sg[e], cg);
             m[e] = L::mul(r[e], L::all(-1.f));
@@ -219,11 +214,6 @@ __device__ __forceinline__ void gates(typename Lane<T>::P rate, bool near, const
             m[e] = DECAY == GCL_DECAY_SIGMOID ? c : L::mul(rate, s);
         }
         if (!GATE) sg[e] = L::all(1.f);
-        if (keep) {
-            keep->r[e] = s;
-            keep->nr[e] = c;
-            keep->ng[e] = cg;
-        }
     }
     if (DECAY != GCL_DECAY_SIGMOID) {                      // from y = -log a in m
         if (DECAY == GCL_DECAY_POWER && sizeof(T) == 2 && near) decay_of<T, true, N>(a, m);

@@ -1,6 +1,11 @@
 // glr_bwd.cuh -- gated linear recurrence, backward.
 //
-// XBWD
+// Gradients of G_t = d_o_t + c_{t+1}, c_t = a_t G_t, over the tiles from last to first, together with the states again: a tile's come
+// from the one saved before it.  The walk's exchange passes c.  A tile's rows stay staged until its gradients are out, and sigmoids are
+// formed again for them; a, m and b (later the states) of a warp's eight tokens are 48 registers a thread.  Bound by issue (85
+// instructions a value, 49% of slots) and the special-function unit, then by the exchange between spans: 32,768 tokens of 2,048 channels,
+// bf16, with drate 272 us, 51% of copy bandwidth.  Not kept: three blocks an SM (80 registers spill, 374 us); clusters of four (295); a, m,
+// b and the sigmoids in tensor memory (261; the forward says why).
 #pragma once
 
 #include "glr_walk.cuh"
@@ -12,8 +17,6 @@ namespace {
 constexpr int kCtas = 2;                               // resident blocks an SM
 static_assert(kTileB == kSave, "one saved state a tile");
 
-// As the forward, over the tiles from last to first; a tile's rows stay staged until its gradients are out, and sigmoids are
-// formed again for them (registers).  The states inside the tile come from the one saved before it.
 template <typename T, int DECAY, int MIX, bool GATE>
 __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Lane<T>;
@@ -22,8 +25,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
     constexpr int V = L::V, CB = L::CB, RUN = kTileB / kWarps, BYTES = W::BYTES;
     __shared__ Shared<CB, RUN> s;
     __shared__ float s_h[kWarps][CB];
-    __shared__ uint32_t s_tmem;
-    constexpr int G = 8 / V, PER = 56, WORDS = RUN / G * PER, COLS = WORDS * kWarps / 4 > 128 ? 256 : 128;       // words of a group and of a lane; columns
     extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, d_o, i][tile][128]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int narr = GATE ? 4 : 3;
@@ -33,18 +34,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
     if (live < 0) return;
     const int64_t tiles = (live + W::TILE - 1) / W::TILE;
     W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0, 0};
-    if (warp == 0) {
-        tc::tmem_alloc(&s_tmem, COLS);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
-    const bool some = walk.template start<T>(stop, p.dht, p.dh0);
-    tc::tc_fence_after();
-    if (!some) {
-        if (warp == 0) tc::tmem_dealloc(s_tmem, COLS);
-        return;
-    }
-    const uint32_t words = s_tmem + ((warp & 3) << 21) + (warp >> 2) * WORDS;
+    if (!walk.template start<T>(stop, p.dht, p.dh0)) return;
     for (int buf = 0;; buf ^= 1) {
         const Tile<W::TILE> &tile = s.tile[buf];
         const int64_t t = tile.t0 + warp * RUN;
@@ -57,58 +47,51 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
         if (warp == 2 && tile.n > 0) before = load_state<T>(p.h_save, tile.t0 / kSave, p.D, ch);
         walk.landed(buf);
         const uint32_t taken = walk.take();
+        P a[RUN], m[RUN], prev[RUN];                       // prev: b = m u, later the state before each token
+        constexpr int H = 4;                               // tokens at a time (registers)
+#pragma unroll
+        for (int k0 = 0; k0 < RUN; k0 += H) {
+            P r[H], g[H], sg[H];
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                r[k] = row(0, k0 + k);
+                if (GATE) g[k] = row(3, k0 + k);
+            }
+            gates<T, DECAY, MIX, GATE, H>(rate, near, r, g, a + k0, m + k0, sg);
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                const P x = row(1, k0 + k);
+                prev[k0 + k] = L::mul(m[k0 + k], GATE ? L::mul(x, sg[k]) : x);
+            }
+        }
+        if (n < RUN)
+#pragma unroll
+            for (int k = 0; k < RUN; ++k)
+                if (k >= n) { a[k] = L::all(1.f); m[k] = prev[k] = L::all(0.f); }
         const int32_t *start = tile.start + warp * RUN, *end = tile.end + warp * RUN;
         const uint32_t starts = bits_of<RUN>(tile.starts, warp), ends = bits_of<RUN>(tile.ends, warp);
         const bool edge = (starts | ends) || n < RUN;
         {
-            // the state from the first token on; c = sum of (product of a up to a token) d_o, up to the first sequence's end
             P A = L::all(1.f), h = L::all(0.f), c = L::all(0.f);
-            bool open = true;
+            auto run = [&](auto cut) {
+                constexpr bool CUT = decltype(cut)::value;
 #pragma unroll
-            for (int k0 = 0; k0 < RUN; k0 += G) {
-                P r[G], g[G], sg[G], a[G], m[G], b[G];
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    r[k] = row(0, k0 + k);
-                    if (GATE) g[k] = row(3, k0 + k);
+                for (int k = 0; k < RUN; ++k) {
+                    if (CUT && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                    h = L::fma(a[k], h, prev[k]);
+                    A = L::mul(A, a[k]);
                 }
-                Sigmoids<P, G> q;
-                gates<T, DECAY, MIX, GATE, G>(rate, near, r, g, a, m, sg, &q);
 #pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    const P x = row(1, k0 + k);
-                    b[k] = L::mul(m[k], GATE ? L::mul(x, sg[k]) : x);
+                for (int k = RUN - 1; k >= 0; --k) {
+                    if (CUT && (ends >> k & 1)) c = load_state<T>(p.dht, end[k], p.D, ch);
+                    c = L::mul(a[k], L::add(CUT && k >= n ? L::all(0.f) : row(2, k), c));
                 }
-                if (n < k0 + G)
-#pragma unroll
-                    for (int k = 0; k < G; ++k)
-                        if (k0 + k >= n) { a[k] = L::all(1.f); m[k] = b[k] = L::all(0.f); }
-                const uint32_t to = words + k0 / G * PER;  // b, a, m and sigmoid(g), of r, of -r, of -g
-                tmem_put<T>(to, b, a);
-                tmem_put<T>(to + 16, m, sg);
-                if (DECAY != GCL_DECAY_LOG) tmem_put<T>(to + 32, q.r, q.nr);
-                if (GATE) tmem_put<T>(to + 48, q.ng);
-                auto run = [&](auto cut) {
-                    constexpr bool CUT = decltype(cut)::value;
-#pragma unroll
-                    for (int k = 0; k < G; ++k) {
-                        if (CUT && (starts >> (k0 + k) & 1)) h = load_state<T>(p.h0, start[k0 + k], p.D, ch);
-                        h = L::fma(a[k], h, b[k]);
-                        A = L::mul(A, a[k]);
-                        if (!CUT || (open && k0 + k < n)) c = L::fma(A, row(2, k0 + k), c);
-                        if (CUT && open && (ends >> (k0 + k) & 1)) {
-                            c = L::fma(A, load_state<T>(p.dht, end[k0 + k], p.D, ch), c);
-                            open = false;
-                        }
-                    }
-                };
-                if (edge) run(std::true_type());
-                else run(std::false_type());
-            }
+            };
+            if (edge) run(std::true_type());
+            else run(std::false_type());
             L::store(&s.a[warp][lane * V], A);
             L::store(&s.b[warp][lane * V], c);
             L::store(&s_h[warp][lane * V], h);
-            tc::tmem_st_wait();
         }
         walk.exchange(buf, taken, tile.ends, [&] {         // (a warp at leisure: the states that enter the warps' tokens)
 #pragma unroll
@@ -125,49 +108,28 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
         auto run = [&](auto plain) {                       // plain: no borders, all tokens live
             constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-            for (int k0 = 0; k0 < RUN; k0 += G) {
-                __align__(8) float v[16];
-                tc::tmem_ld16(words + k0 / G * PER, v);
-                tmem_wait<16>(v);
-                P prev[G];
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    if (!PLAIN && (starts >> (k0 + k) & 1)) h = load_state<T>(p.h0, start[k0 + k], p.D, ch);
-                    prev[k] = h;
-                    h = L::fma(L::load(v + 8 + k * V), h, L::load(v + k * V));
-                }
-                tmem_put<T>(words + k0 / G * PER, prev);   // (the states before the tokens, over b)
+            for (int k = 0; k < RUN; ++k) {
+                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                const P b = prev[k];
+                prev[k] = h;
+                h = L::fma(a[k], h, b);
             }
-            tc::tmem_st_wait();
-            __align__(8) float v[16], vg[16], vr[16], vn[8];
 #pragma unroll
             for (int k = RUN - 1; k >= 0; --k) {
-                if (k % G == G - 1) {
-                    const uint32_t at = words + k / G * PER;
-                    tc::tmem_ld16(at, v);
-                    tc::tmem_ld16(at + 16, vg);
-                    if (DECAY != GCL_DECAY_LOG) tc::tmem_ld16(at + 32, vr);
-                    if (GATE) tc::tmem_ld8(at + 48, vn);
-                    tmem_wait<16>(v);
-                    tmem_wait<16>(vg);
-                    if (DECAY != GCL_DECAY_LOG) tmem_wait<16>(vr);
-                    if (GATE) tmem_wait<8>(vn);
-                }
-                const int w = k % G * V;
-                const P prev = L::load(v + w), ak = L::load(v + 8 + w), mk = L::load(vg + w);
                 if (!PLAIN && (ends >> k & 1)) c = load_state<T>(p.dht, end[k], p.D, ch);
-                const P x = row(1, k), d = L::add(row(2, k), c), Gm = L::mul(d, mk);
-                c = L::mul(ak, !PLAIN && k >= n ? c : d);
+                const P x = row(1, k), G = L::add(row(2, k), c), Gm = L::mul(G, m[k]);
+                c = L::mul(a[k], !PLAIN && k >= n ? c : G);
                 P sr, nr, sg, ng;
-                if (DECAY != GCL_DECAY_LOG) { sr = L::load(vr + w); nr = L::load(vr + 8 + w); }
-                if (GATE) { sg = L::load(vg + 8 + w); ng = L::load(vn + w); }
+                if (DECAY != GCL_DECAY_LOG && GATE) sigmoids<T>(row(0, k), row(3, k), sr, nr, sg, ng);
+                else if (DECAY != GCL_DECAY_LOG) sigmoids<T>(row(0, k), sr, nr);
+                else if (GATE) sigmoids<T>(row(3, k), sg, ng);
                 const P u = GATE ? L::mul(x, sg) : x, dx = GATE ? L::mul(Gm, sg) : Gm;
                 P dl;
                 if (MIX == GCL_MIX_ROOT) {                 // c (prev - u a / m), the second term 0 where m is
-                    const P q = L::map(L::mul(ak, L::all(-1.f)), mk, [](float a, float m) { return m > 0.f ? a * frcp<T>(m) : 0.f; });
-                    dl = L::mul(c, L::fma(q, u, prev));
+                    const P q = L::map(L::mul(a[k], L::all(-1.f)), m[k], [](float a, float m) { return m > 0.f ? a * frcp<T>(m) : 0.f; });
+                    dl = L::mul(c, L::fma(q, u, prev[k]));
                 } else {
-                    dl = L::mul(c, MIX == GCL_MIX_COMPLEMENT ? L::fma(u, L::all(-1.f), prev) : prev);
+                    dl = L::mul(c, MIX == GCL_MIX_COMPLEMENT ? L::fma(u, L::all(-1.f), prev[k]) : prev[k]);
                 }
                 P dr = dl;
                 if (DECAY == GCL_DECAY_SIGMOID) dr = L::mul(dl, nr);
@@ -206,9 +168,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
         if (!walk.more(buf)) break;
     }
     walk.finish();
-    tc::tc_fence_before();
-    __syncthreads();
-    if (warp == 0) tc::tmem_dealloc(s_tmem, COLS);
 }
 
 // drate from the tiles' sums, in a fixed order: 32 channels a block, 32 rows of threads over the tiles, eight loads of
@@ -241,7 +200,7 @@ __global__ void __launch_bounds__(1024) glr_drate_kernel(const Params p, int til
 template <typename T>
 cudaError_t launch_bwd(const Params &p, cudaStream_t s) {
     const cudaError_t e = for_kind(p.kind.decay, p.kind.mix, p.i.p != nullptr, [&](auto d, auto m, auto g) {
-        return launch_tiles<T, glr_bwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>>(p, kCtas, 2, s);
+        return launch_tiles<T, glr_bwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>>(p, kCtas, s);
     });
     if (e != cudaSuccess || !p.drate) return e;
     return launch_dependent(glr_drate_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, p, kTileB);

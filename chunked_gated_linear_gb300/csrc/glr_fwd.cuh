@@ -1,6 +1,13 @@
 // glr_fwd.cuh -- gated linear recurrence, forward.
 //
-// XFWD
+// A warp's 16 tokens: gates (three special-function results and about 30 other instructions a value), their product of decays and
+// state from zero; the state that enters from the walk's exchange; then the states, rounded, out.  Each row is read once
+// and written once; a and b of the tokens stay in registers (64 of 125 a thread), which leaves two blocks an SM.  Bound by the exchange
+// between spans beside the issue of 35 instructions a value (45% of slots): one sequence of 65,536 tokens of 2,048 channels, bf16, power
+// decay, root mix, input gate 246 us, 64% of copy bandwidth.  Not kept: tiles of 64 tokens 333 to 375; a and b in tensor memory, three
+// blocks an SM, 230 us, because a cluster whose blocks wait for each other's tensor memory can meet another stream's cluster that does the
+// same, each holding what the other waits for; without clusters (16 warps a block) 239 us, but a call of 256 tokens 10.0 us instead of 8.0
+// and short ones 16% longer.
 #pragma once
 
 #include "glr_walk.cuh"
@@ -9,7 +16,7 @@ namespace gcl {
 namespace glr {
 namespace {
 
-constexpr int kCtas = 3;                               // resident blocks an SM
+constexpr int kCtas = 2;                               // resident blocks an SM (a and b of a tile are 64 registers a thread)
 static_assert(kTileF % kSave == 0, "saved states lie at tiles' starts");
 
 template <typename T, int DECAY, int MIX, bool GATE>
@@ -19,9 +26,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
     using W = Walk<false, L::CB, kTileF / kWarps>;
     constexpr int V = L::V, CB = L::CB, RUN = kTileF / kWarps, BYTES = W::BYTES;
     __shared__ Shared<CB, RUN> s;
-    __shared__ uint32_t s_tmem;
-    extern __shared__ __align__(128) uint8_t s_rows[];     // [r, x, i][tile][128]
-    constexpr int G = 8 / V, WORDS = RUN / G * 16, COLS = WORDS * kWarps / 4;        // words of a lane; columns of a block
+    extern __shared__ __align__(128) uint8_t s_rows[];     // [2][r, x, i][tile][128]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int narr = GATE ? 3 : 2;
     bool stop;
@@ -29,66 +34,55 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
     if (live < 0) return;
     const int64_t tiles = (live + W::TILE - 1) / W::TILE;
     W walk{p, s, maps, s_rows, narr, live, tiles, (uint32_t)((tiles + kRanks - 1) / kRanks * p.n_cb), cluster_rank(), 0, 0, 0};
-    if (warp == 0) {
-        tc::tmem_alloc(&s_tmem, COLS);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
-    const bool some = walk.template start<T>(stop, p.h0, p.ht);
-    tc::tc_fence_after();
-    if (!some) {
-        if (warp == 0) tc::tmem_dealloc(s_tmem, COLS);
-        return;
-    }
-    const uint32_t words = s_tmem + ((warp & 3) << 21) + (warp >> 2) * WORDS;
+    if (!walk.template start<T>(stop, p.h0, p.ht)) return;
     for (int buf = 0;; buf ^= 1) {
         const Tile<W::TILE> &tile = s.tile[buf];
         const int64_t t = tile.t0 + warp * RUN;
         const int ch = tile.cb * CB + lane * V, n = tile.n - warp * RUN;          // n: live tokens from the warp's first on
-        const uint8_t *rows = s_rows + warp * RUN * 128 + lane * 4;
+        const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
         auto row = [&](int arr, int k) { return L::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128)); };
         const P rate = load_state<T>(DECAY == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, p.D, ch);
         const bool near = __all_sync(0xffffffffu, L::every(rate, [](float v) { return v >= 0.f && v <= kNear; }));
         walk.landed(buf);
         // (the next span is taken only when this one's rows are here: few spans go to all clusters, and none is held back for long)
         const uint32_t taken = walk.take();
+        P a[RUN], b[RUN];
+        constexpr int H = 4;                               // tokens at a time (registers)
+#pragma unroll
+        for (int k0 = 0; k0 < RUN; k0 += H) {
+            P r[H], g[H], sg[H];
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                r[k] = row(0, k0 + k);
+                if (GATE) g[k] = row(2, k0 + k);
+            }
+            gates<T, DECAY, MIX, GATE, H>(rate, near, r, g, a + k0, b + k0, sg);
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                const P x = row(1, k0 + k);
+                b[k0 + k] = L::mul(b[k0 + k], GATE ? L::mul(x, sg[k]) : x);
+            }
+        }
+        if (n < RUN)
+#pragma unroll
+            for (int k = 0; k < RUN; ++k)
+                if (k >= n) { a[k] = L::all(1.f); b[k] = L::all(0.f); }
         const int32_t *start = tile.start + warp * RUN, *end = tile.end + warp * RUN;
         const uint32_t starts = bits_of<RUN>(tile.starts, warp), ends = bits_of<RUN>(tile.ends, warp);
         {
             P A = L::all(1.f), h = L::all(0.f);
+            auto run = [&](auto cut) {
 #pragma unroll
-            for (int k0 = 0; k0 < RUN; k0 += G) {
-                P r[G], g[G], sg[G], a[G], b[G];
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    r[k] = row(0, k0 + k);
-                    if (GATE) g[k] = row(2, k0 + k);
+                for (int k = 0; k < RUN; ++k) {
+                    if (decltype(cut)::value && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                    h = L::fma(a[k], h, b[k]);
+                    A = L::mul(A, a[k]);
                 }
-                gates<T, DECAY, MIX, GATE, G>(rate, near, r, g, a, b, sg);
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    const P x = row(1, k0 + k);
-                    b[k] = L::mul(b[k], GATE ? L::mul(x, sg[k]) : x);
-                }
-                if (n < k0 + G)
-#pragma unroll
-                    for (int k = 0; k < G; ++k)
-                        if (k0 + k >= n) { a[k] = L::all(1.f); b[k] = L::all(0.f); }
-                tmem_put<T>(words + k0 / G * 16, a, b);
-                auto run = [&](auto cut) {
-#pragma unroll
-                    for (int k = 0; k < G; ++k) {
-                        if (decltype(cut)::value && (starts >> (k0 + k) & 1)) h = load_state<T>(p.h0, start[k0 + k], p.D, ch);
-                        h = L::fma(a[k], h, b[k]);
-                        A = L::mul(A, a[k]);
-                    }
-                };
-                if (starts >> k0 & ((1u << G) - 1)) run(std::true_type());
-                else run(std::false_type());
-            }
+            };
+            if (starts) run(std::true_type());
+            else run(std::false_type());
             L::store(&s.a[warp][lane * V], A);
             L::store(&s.b[warp][lane * V], h);
-            tc::tmem_st_wait();
         }
         walk.exchange(buf, taken, tile.starts, [] {});
         P h = L::load(&s.b[warp][lane * V]);
@@ -98,23 +92,15 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
         }
         uint32_t *to = word<T>(p.o, t, ch);
         const int n_out = p.o.p && ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + (n < RUN ? n : RUN) - 1, p.t_max, p.status) ? n : 0;
-        __align__(8) float v[2][16];
-        tc::tmem_ld16(words, v[0]);
         auto run = [&](auto plain) {                       // plain: no borders, all tokens live
             constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-            for (int k0 = 0; k0 < RUN; k0 += G) {
-                float *c = v[k0 / G % 2];
-                tmem_wait<16>(c);
-                if (k0 + G < RUN) tc::tmem_ld16(words + (k0 / G + 1) * 16, v[(k0 / G + 1) % 2]);
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    if (!PLAIN && (starts >> (k0 + k) & 1)) h = load_state<T>(p.h0, start[k0 + k], p.D, ch);
-                    h = L::fma(L::load(c + k * V), h, L::load(c + 8 + k * V));
-                    if (PLAIN ? n_out > 0 : k0 + k < n_out) *to = L::put(h);
-                    to += p.o.st / V;
-                    if (!PLAIN && (ends >> (k0 + k) & 1)) store_state<T>(p.ht, end[k0 + k], p.D, ch, h);
-                }
+            for (int k = 0; k < RUN; ++k) {
+                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                h = L::fma(a[k], h, b[k]);
+                if (PLAIN ? n_out > 0 : k < n_out) *to = L::put(h);
+                to += p.o.st / V;
+                if (!PLAIN && (ends >> k & 1)) store_state<T>(p.ht, end[k], p.D, ch, h);
             }
         };
         if (!(starts | ends) && n >= RUN) run(std::true_type());
@@ -122,9 +108,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
         if (!walk.more(buf)) break;
     }
     walk.finish();
-    tc::tc_fence_before();
-    __syncthreads();
-    if (warp == 0) tc::tmem_dealloc(s_tmem, COLS);
 }
 
 }  // namespace
@@ -132,7 +115,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
 template <typename T>
 cudaError_t launch_fwd(const Params &p, cudaStream_t s) {
     return for_kind(p.kind.decay, p.kind.mix, p.i.p != nullptr, [&](auto d, auto m, auto g) {
-        return launch_tiles<T, glr_fwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>>(p, kCtas, 1, s);
+        return launch_tiles<T, glr_fwd_kernel<T, decltype(d)::value, decltype(m)::value, decltype(g)::value>>(p, kCtas, s);
     });
 }
 

@@ -1,7 +1,7 @@
 // glr_walk.cuh -- gated linear recurrence over packed sequences: how blocks walk the tiles, and the launch.
 //
 // The packed axis is cut into tiles of some tokens by the 128 bytes of a warp's width of channels; each warp of a block walks
-// kRun tokens of a tile.  The sequences need no plan of their own: a token that starts one takes its state from h0,
+// an eighth of a tile's tokens.  The sequences need no plan of their own: a token that starts one takes its state from h0,
 // whatever was before.  One pass: a cluster of kRanks blocks takes kRanks consecutive tiles of the same channels (a span), in the
 // order of the recurrence (a counter).  Its blocks form their tiles' products of decays and states from zero, exchange them
 // through shared memory, and take the state that enters the span from the span before, or from an earlier one and the products and
@@ -9,7 +9,9 @@
 // A cluster waits for spans with lower numbers alone, whose clusters run already, so the first of them never waits: the
 // launch ends whatever else runs on the GPU.
 // The wait for the state before is what a tile spends longest on: spans meet in packets of 16 bytes, values and tag in one access
-// (XCHAIN).
+// (one sequence of 65,536 tokens of 2,048 channels: three launches, states from zero, their scan and the outputs, 1,424 us; one pass
+// with a flag beside each state 655; packets, TMA copies of the rows and fp32 pairs 396; clusters of four, exchanging by shared memory, 342;
+// sends that count on the receiver's barrier 312; kernels for each kind and 16 tokens a warp 251; clusters of two 246).
 // Backwards from the states before each 64 tokens (saved by the forward, or formed again): with c_t = a_t G_t the gradient that
 // token t passes on,
 //   G_t = d_o_t + c_{t+1},   c_t = a_t G_t,
@@ -25,7 +27,7 @@ namespace gcl {
 namespace glr {
 namespace {
 
-constexpr int kWarps = 8;                              // warps of a block; each walks kRun = tile / kWarps tokens
+constexpr int kWarps = 8;                              // warps of a block; each walks tile / kWarps tokens
 
 // ---- clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -135,33 +137,6 @@ __device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, 
     if (s && ch < D) Lane<T>::store(s + n * D + ch, h);
 }
 
-// ---- tensor memory: a lane's own words, eight for the tokens of a group ----
-template <typename T>
-__device__ __forceinline__ void tmem_put(uint32_t at, const typename Lane<T>::P *x, const typename Lane<T>::P *y) {
-    __align__(8) float v[16];
-#pragma unroll
-    for (int k = 0; k < 8; k += Lane<T>::V) {
-        Lane<T>::store(v + k, x[k / Lane<T>::V]);
-        Lane<T>::store(v + 8 + k, y[k / Lane<T>::V]);
-    }
-    tc::tmem_st16(at, v);
-}
-template <typename T>
-__device__ __forceinline__ void tmem_put(uint32_t at, const typename Lane<T>::P *x) {
-    __align__(8) float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; k += Lane<T>::V) Lane<T>::store(v + k, x[k / Lane<T>::V]);
-    tc::tmem_st8_b32(at, reinterpret_cast<const uint32_t *>(v));
-}
-// (the wait takes the words along, so that no use of one moves before it)
-template <int N>
-__device__ __forceinline__ void tmem_wait(float *v) {
-#pragma unroll
-    for (int k = 0; k < N; k += 8)
-        asm volatile("tcgen05.wait::ld.sync.aligned;"
-                     : "+f"(v[k]), "+f"(v[k + 1]), "+f"(v[k + 2]), "+f"(v[k + 3]), "+f"(v[k + 4]), "+f"(v[k + 5]), "+f"(v[k + 6]), "+f"(v[k + 7])::"memory");
-}
-
 // ---- what spans leave each other ----
 __device__ __forceinline__ Packet load_packet(const Packet *p) {
     unsigned __int128 v;
@@ -180,7 +155,7 @@ __device__ __forceinline__ void store_packet(Packet *p, float a, float own, floa
 }
 
 // One warp, a channel a lane: packets of the spans before span `seq`, `depth` and depth + 1 back.
-constexpr int kWindow = 2;
+constexpr int kWindow = 2;                             // (65,536 tokens of 2,048 channels: 246 us; one 250, three 248, four 283)
 __device__ __forceinline__ void load_window(const Params &p, int64_t seq, int depth, int ch, bool on, Packet *k) {
 #pragma unroll
     for (int u = 0; u < kWindow; ++u) {
@@ -337,7 +312,6 @@ __device__ __forceinline__ void pass_empty(const Params &p, const float *in_stat
 template <bool REV, int CB, int RUN>
 struct Walk {
     static constexpr int TILE = kWarps * RUN, BYTES = TILE * 128;
-    static constexpr int BUFS = REV ? 2 : 1;               // of rows: forwards they are read before the exchange alone
     const Params &p;
     Shared<CB, RUN> &s;
     const Maps &maps;
@@ -362,7 +336,7 @@ struct Walk {
         issued = (issued ^ 1u << buf) | 4u << buf;
         tc::mbar_arrive_expect_tx(&s.full[buf], narr * BYTES);
         for (int a = 0; a < narr; ++a)
-            tc::tma_load_2d(rows + (buf * (BUFS - 1) * narr + a) * BYTES, &maps.m[!REV && a == 2 ? 3 : a], t.cb * CB, t.t0, &s.full[buf]);
+            tc::tma_load_2d(rows + (buf * narr + a) * BYTES, &maps.m[!REV && a == 2 ? 3 : a], t.cb * CB, t.t0, &s.full[buf]);
     }
     // Sets up the barriers and takes the cluster's first span; false: there is none, or a solo call is to do nothing (`stop`, the first
     // block's issuer's).  Every thread of the cluster.
@@ -465,7 +439,7 @@ bool rows_map(CUtensorMap *m, const Params &p, const Rows &r, int tile) {
 // Launches `kernel` in clusters, at most `ctas` blocks an SM, as the dependent of the launch before (the set-up, or the walk that
 // forms the states).
 template <typename T, auto kernel>
-cudaError_t launch_tiles(const Params &p, int ctas, int bufs, cudaStream_t s) {
+cudaError_t launch_tiles(const Params &p, int ctas, cudaStream_t s) {
     const int tile = p.tile;
     Maps maps;
     const Rows *rows[4] = {&p.r, &p.x, &p.d_o, &p.i};
@@ -475,7 +449,7 @@ cudaError_t launch_tiles(const Params &p, int ctas, int bufs, cudaStream_t s) {
             if (!rows_map<T>(&maps.m[k], p, *rows[k], tile)) return cudaErrorInvalidValue;
             ++n;
         }
-    const size_t smem = (size_t)bufs * n * tile * 128;
+    const size_t smem = (size_t)2 * n * tile * 128;
     static std::atomic<bool> allowed[64];                  // by device; zero-initialised (static storage)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
