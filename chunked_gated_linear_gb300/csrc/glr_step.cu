@@ -2,7 +2,7 @@
 // request, on a pool of fp32 states updated in place.
 //
 // A lane takes eight channels: a 16-byte load of each row (fp32: two), two of the state, all before the first use.  Bound by the latency of
-// one pass of loads: one request of 512 channels takes 2.0 us in a captured graph; a call from Python
+// one pass of loads: one request of 512 channels takes 2.0 to 2.4 us in a captured graph; a call from Python
 // 8, as 256 requests of 2,048 channels do (8 MB moved, floor 1.2).
 #include "dla_simt.cuh"
 #include "glr.cuh"
