@@ -42,6 +42,13 @@ __device__ __forceinline__ float froot(float x) {
     return y;
 }
 
+// The smaller of x and a bound, NaN where x is (fminf would answer with the bound: a gate that is not a number would count as closed).
+__device__ __forceinline__ float at_most(float x, float bound) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(bound));
+    return y;
+}
+
 // A lane's channels of a row, four bytes: two values of 16 bits, held as a pair whose arithmetic is one instruction,
 // or one of fp32.  A warp takes 128 bytes of the row.
 template <typename T>
@@ -119,14 +126,15 @@ template <typename T>
 __device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>::P &s, typename Lane<T>::P &c) {
     using L = Lane<T>;
     typename L::P e;
-    if (sizeof(T) == 2) e = L::map(L::mul(x, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(fminf(v, 126.f)); });
-    else e = L::map(x, [](float v) { return fexp2<T>(fminf(-v, 87.f)); });
+    if (sizeof(T) == 2) e = L::map(L::mul(x, L::all(-1.4426950408889634f)), [](float v) { return fexp2<T>(at_most(v, 126.f)); });
+    else e = L::map(x, [](float v) { return fexp2<T>(at_most(-v, 87.f)); });
     s = L::map(L::add(e, L::all(1.f)), [](float v) { return frcp<T>(v); });
     c = L::mul(e, s);
 }
 // The same of x and z.  16-bit rows: by one reciprocal, that of (1 + exp(-x)) (1 + exp(-z)), since a reciprocal takes the
-// special-function unit as long as two exponentials.  Below 2^-63 (x < -43.6) they stay at 2^-63, so that the product is finite.
-template <typename T>
+// special-function unit as long as two exponentials.  Below 2^-63 (x < -43.6) they stay at 2^-63, so that the product is finite.  A NaN
+// of either makes all four NaN; with APART one of z leaves x's alone.
+template <typename T, bool APART = false>
 __device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>::P z, typename Lane<T>::P &sx, typename Lane<T>::P &cx,
                                          typename Lane<T>::P &sz, typename Lane<T>::P &cz) {
     using L = Lane<T>;
@@ -135,11 +143,12 @@ __device__ __forceinline__ void sigmoids(typename Lane<T>::P x, typename Lane<T>
         sigmoids<T>(z, sz, cz);
         return;
     }
-    auto ex = [](typename L::P v) { return L::map(L::mul(v, L::all(-1.4426950408889634f)), [](float u) { return fexp2<T>(fminf(u, 63.f)); }); };
-    const typename L::P e = ex(x), f = ex(z), a = L::add(e, L::all(1.f)), b = L::add(f, L::all(1.f));
+    auto ex = [](typename L::P v) { return L::map(L::mul(v, L::all(-1.4426950408889634f)), [](float u) { return fexp2<T>(at_most(u, 63.f)); }); };
+    const typename L::P e = ex(x), f = ex(z), a = L::add(e, L::all(1.f));
+    const typename L::P b = L::add(APART ? L::map(f, [](float u) { return fminf(u, 0x1p63f); }) : f, L::all(1.f));
     const typename L::P r = L::map(L::mul(a, b), [](float u) { return frcp<T>(u); });
     sx = L::mul(b, r);
-    sz = L::mul(a, r);
+    sz = L::mul(APART ? L::fma(f, L::all(0.f), a) : a, r);
     cx = L::mul(e, sx);
     cz = L::mul(f, sz);
 }
@@ -195,8 +204,9 @@ __device__ __forceinline__ void decay_of(typename Lane<T>::P *a, typename Lane<T
 }
 
 // The gates of N tokens: a, m(a) and the input gate's sigmoid from r and g (g is not read without gate: GATE false, sg = 1).
-// rate: of the lane's channels; near: all the warp's rates lie in [0, kNear].
-template <typename T, int DECAY, int MIX, bool GATE, int N>
+// rate: of the lane's channels; near: all the warp's rates lie in [0, kNear].  APART: a and m do not take a NaN from g (forwards the
+// state is NaN by either; the gradient that a token passes on does not depend on g).
+template <typename T, int DECAY, int MIX, bool GATE, int N, bool APART = false>
 __device__ __forceinline__ void gates(typename Lane<T>::P rate, bool near, const typename Lane<T>::P *r, const typename Lane<T>::P *g,
                                       typename Lane<T>::P *a, typename Lane<T>::P *m, typename Lane<T>::P *sg) {
     using L = Lane<T>;
@@ -208,7 +218,7 @@ __device__ __forceinline__ void gates(typename Lane<T>::P rate, bool near, const
             if (GATE) sigmoids<T>(g[e], sg[e], cg);
             m[e] = L::mul(r[e], L::all(-1.f));
         } else {
-            if (GATE) sigmoids<T>(r[e], g[e], s, c, sg[e], cg);
+            if (GATE) sigmoids<T, APART>(r[e], g[e], s, c, sg[e], cg);
             else sigmoids<T>(r[e], s, c);
             a[e] = s;
             m[e] = DECAY == GCL_DECAY_SIGMOID ? c : L::mul(rate, s);

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
                 r[k] = row(0, k0 + k);
                 if (GATE) g[k] = row(3, k0 + k);
             }
-            gates<T, DECAY, MIX, GATE, H>(rate, near, r, g, a + k0, m + k0, sg);
+            gates<T, DECAY, MIX, GATE, H, true>(rate, near, r, g, a + k0, m + k0, sg);
 #pragma unroll
             for (int k = 0; k < H; ++k) {
                 const P x = row(1, k0 + k);
@@ -120,7 +120,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
                 const P x = row(1, k), G = L::add(row(2, k), c), Gm = L::mul(G, m[k]);
                 c = L::mul(a[k], !PLAIN && k >= n ? c : G);
                 P sr, nr, sg, ng;
-                if (DECAY != GCL_DECAY_LOG && GATE) sigmoids<T>(row(0, k), row(3, k), sr, nr, sg, ng);
+                if (DECAY != GCL_DECAY_LOG && GATE && MIX == GCL_MIX_ONE) {           // (here dx does not depend on r's)
+                    sigmoids<T>(row(0, k), sr, nr);
+                    sigmoids<T>(row(3, k), sg, ng);
+                } else if (DECAY != GCL_DECAY_LOG && GATE) sigmoids<T>(row(0, k), row(3, k), sr, nr, sg, ng);
                 else if (DECAY != GCL_DECAY_LOG) sigmoids<T>(row(0, k), sr, nr);
                 else if (GATE) sigmoids<T>(row(3, k), sg, ng);
                 const P u = GATE ? L::mul(x, sg) : x, dx = GATE ? L::mul(Gm, sg) : Gm;

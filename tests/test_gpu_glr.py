@@ -402,3 +402,52 @@ def test_two_streams_at_once():
     for c in cs:
         c.check_fwd()
         c.check_bwd(c.out)
+
+
+# ---------------------------------------------------------------- gates that are not numbers
+@pytest.mark.parametrize("lens", [[50, 100, 200], [20, 40]])
+@pytest.mark.parametrize("decay,mix,gate", KINDS + [("power", "one", True)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_gates_that_are_not_numbers_are_passed_on(dtype, decay, mix, gate, lens):
+    """NaN in r and in i: NaN wherever the definition has it, numbers everywhere else (in other channels the same bits)."""
+    c, at = Case(dtype, lens, 72, decay, mix, gate), lens[0] + 10
+    e = c.e32()
+    clean, grads = [t.clone() for t in c.fwd()], c.bwd(c.save)
+    c.r[at, 5] = float("nan")
+    if gate:
+        c.i[at + 8, 9] = float("nan")
+    got, out = c.fwd(), c.bwd(c.save)
+    torch.cuda.synchronize()
+    x, r, i, rate, h0 = c.ref_args()
+    with np.errstate(invalid="ignore"):
+        h, prev, ht = ref.fwd(x, r, i, rate, h0, c.cu.tolist(), decay, mix)
+        dx, dr, di, drate, dh0, _ = ref.bwd(x, r, i, rate, h0, np64(c.d_o), np64(c.dht), c.cu.tolist(), decay, mix)
+    if gate and mix == "one":
+        dr[at + 8, 9] = np64(grads["dr"])[at + 8, 9]       # (m is a constant: the input has no part in its decay's gradient)
+    L, n = c.live, -(-c.live // 64)
+    rows = [("o", got[0][:L], clean[0][:L], h[:L], dtype), ("ht", got[1], clean[1], ht, "f32"), ("h_save", got[2][:n], clean[2][:n], prev[:L:64], "f32")]
+    rows += [(k, out[k][:L], grads[k][:L], v[:L], dtype) for k, v in (("dx", dx), ("dr", dr), ("di", di)) if out[k] is not None]
+    rows += [("dh0", out["dh0"], grads["dh0"], dh0, "f32")] + ([("drate", out["drate"], grads["drate"], drate, "f32")] if decay == "power" else [])
+    for name, a, b, want, dt in rows:
+        bad = np.isnan(want)
+        assert np.isnan(np64(a)[bad]).all(), name
+        same = [k for k in range(72) if k not in (5, 9)]
+        assert torch.equal(a[..., same], b[..., same]), name
+        if name != "drate":
+            ref.check(name, np64(a)[~bad], want[~bad], dt, 4 * e, max(np.abs(want[~bad]).max(), 1.0))
+
+
+@pytest.mark.parametrize("decay,mix,gate", KINDS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_step_passes_on_gates_that_are_not_numbers(dtype, decay, mix, gate):
+    c = Case(dtype, [4], 200, decay, mix, gate, pad=0)
+    states = [torch.ones(4, 200, device=DEV) for _ in range(2)]
+    outs = [c.full(4, 200, dtype=DT[dtype]) for _ in range(2)]
+    gcl.glr_step(c.x, c.r, states[0], outs[0], **c.kw)
+    bad = torch.zeros(4, 200, dtype=torch.bool, device=DEV)
+    c.r[1, 3], bad[1, 3] = float("nan"), True
+    if gate:
+        c.i[2, 150], bad[2, 150] = float("nan"), True
+    gcl.glr_step(c.x, c.r, states[1], outs[1], **c.kw)
+    for a, b in ((states[1], states[0]), (outs[1], outs[0])):
+        assert a[bad].isnan().all() and torch.equal(a[~bad], b[~bad])
