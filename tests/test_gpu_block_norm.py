@@ -285,3 +285,21 @@ def test_no_eps(norm, monkeypatch):
     monkeypatch.setattr(sys.modules[__name__], "EPS", 0.0)
     for T, live in ((5, None), (37, 30)):
         Case(T, 1, 64, "bf16", post=norm, pre=norm, live=live).check()
+
+
+@pytest.mark.parametrize("gate", ["plain", "silu", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_gates_that_are_not_numbers_are_passed_on(dtype, gate):
+    """A NaN of the gate: NaN in its value of xo, in its row of z and in its row of every gradient; other rows as without."""
+    for D, H in ((128, 4), (2048, 1)):
+        c = Case(12, H, D, dtype, gate=gate)
+        clean, grads = [t.clone() for t in c.fwd()], c.bwd()
+        c.gate[9, 0, 1] = float("nan")
+        (xo, z), out = c.fwd(), c.bwd()
+        bad = torch.zeros(12, H, D, dtype=torch.bool, device=DEV)
+        bad[9, 0, 1] = True
+        assert xo[bad].isnan().all() and torch.equal(xo[~bad], clean[0][~bad])
+        bad[9, 0] = True
+        for a, b in ((z, clean[1]), *((out[n], grads[n]) for n in ("dy", "dgate", "dx"))):
+            assert a[bad].isnan().all() and torch.equal(a[~bad], b[~bad])
+        assert out["dpost_weight"].isnan().all() and out["dpre_weight"].isnan().all()
