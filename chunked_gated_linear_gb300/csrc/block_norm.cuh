@@ -104,13 +104,6 @@ __device__ __forceinline__ float reciprocal(float x) {
     return y;
 }
 
-// The larger of x and a bound, NaN where x is (fmaxf would answer with the bound: a gate that is not a number would count as closed).
-__device__ __forceinline__ float at_least(float x, float bound) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(bound));
-    return y;
-}
-
 // act(g) of a vector, and with SLOPE its derivative.
 template <typename T, bool SLOPE>
 __device__ __forceinline__ void activation(int act, const P *g, P *a, P *da) {
@@ -125,10 +118,14 @@ __device__ __forceinline__ void activation(int act, const P *g, P *a, P *da) {
     P s[kPairs], c[kPairs];                                // sigmoid(g) and sigmoid(-g) = exp(-g) sigmoid(g), neither by a difference
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
-        // (the largest exponent leaves 1 + exp(-g) finite, so that its product with the reciprocal is)
-        const P e = map(g[k], [](float v) { return exp_minus<T>(at_least(v, -87.f)); });
+        // (exp(-g) may be infinite: then s = 0, and c is 1 from where it rounds to that; a NaN passes)
+        const P e = map(g[k], [](float v) { return exp_minus<T>(v); });
         s[k] = map(add2(e, both(1.f)), [](float v) { return reciprocal<T>(v); });
-        if (SLOPE) c[k] = mul2(e, s[k]);
+        if (SLOPE) {
+            c[k] = mul2(e, s[k]);
+            if (e.x > 0x1p26f) c[k].x = 1.f;
+            if (e.y > 0x1p26f) c[k].y = 1.f;
+        }
     }
     if (act == GCL_ACT_SILU) {
 #pragma unroll

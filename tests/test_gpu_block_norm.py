@@ -303,3 +303,13 @@ def test_gates_that_are_not_numbers_are_passed_on(dtype, gate):
         for a, b in ((z, clean[1]), *((out[n], grads[n]) for n in ("dy", "dgate", "dx"))):
             assert a[bad].isnan().all() and torch.equal(a[~bad], b[~bad])
         assert out["dpost_weight"].isnan().all() and out["dpre_weight"].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_far_gates(dtype):
+    """Gates whose exponential overflows: SiLU, the sigmoid and their slopes are 0 there, not the gate times the least sigmoid."""
+    top = float(torch.finfo(DT[dtype]).max)
+    for gate in ("silu", "sigmoid"):
+        c = Case(3, 1, 72, dtype, gate=gate)
+        c.gate[1, 0, :11] = torch.tensor([-top, -top / 1e3, -1e4, -150.0, -100.0, -90.0, -88.0, -87.0, -60.0, 100.0, 60.0])
+        c.check()
