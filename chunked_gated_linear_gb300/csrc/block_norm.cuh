@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
             sum.template operator()<5>(s5);
             if (p.pre != GCL_NORM_NONE) {
                 r = live ? inverse_length(p.pre, s5[1], inv_d, p.eps) : 0.f;
-                m = r * r * r * s5[2] * (p.pre == GCL_NORM_RMS ? inv_d : 1.f);
+                m = r * (r * (r * s5[2])) * (p.pre == GCL_NORM_RMS ? inv_d : 1.f);      // (r^3 alone leaves fp32's range)
             }
             mean = s5[0] + r * s5[3] - m * s5[4];
         } else if (p.post != GCL_NORM_NONE) {

@@ -313,3 +313,18 @@ def test_far_gates(dtype):
         c = Case(3, 1, 72, dtype, gate=gate)
         c.gate[1, 0, :11] = torch.tensor([-top, -top / 1e3, -1e4, -150.0, -100.0, -90.0, -88.0, -87.0, -60.0, 100.0, 60.0])
         c.check()
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("size", [1e-16, 1e-13, 1e14, 1e17])
+def test_rows_of_extreme_length(norm, size, monkeypatch):
+    """Rows whose inverse length has a cube outside fp32's range: the gradients themselves are inside it."""
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 0.0)
+    for D in (64, 1024):
+        c = Case(7, 1, D, "f32", post=norm, pre=norm, scale=size)
+        c.x.mul_(size)
+        c.fwd()
+        c.check_fwd()
+        c.check_bwd(c.bwd(dxo=False), dxo=False)
+        if size < 1:
+            c.check_bwd(c.bwd())
