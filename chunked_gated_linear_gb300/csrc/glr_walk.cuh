@@ -28,6 +28,7 @@ namespace glr {
 namespace {
 
 constexpr int kWarps = 8;                              // warps of a block; each walks tile / kWarps tokens
+constexpr int kEnd = -1;
 
 // ---- clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -39,6 +40,9 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
     return a;
+}
+__device__ __forceinline__ void peer_store(void *p, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
 }
 // Stores that count their bytes on the peer's barrier when they have landed there.
 __device__ __forceinline__ void peer_send(void *p, uint64_t *bar, uint32_t rank, uint32_t v) {
@@ -59,12 +63,13 @@ __device__ __forceinline__ uint32_t peer_load(const void *p, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 // (orders no memory: a release waits for the outputs' stores of the tile before)
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // ---- what a block holds of a tile beside its rows ----
 template <int TILE>
 struct Tile {
-    int32_t seq, cb;               // its span's place in the order of the recurrence, its block of channels
+    int32_t seq, cb;               // its span's place in the order of the recurrence, its block of channels (kEnd: no tile, the walk is over)
     int32_t t0, n;                 // its first token, its live tokens (0: none)
     uint32_t starts[TILE / 32], ends[TILE / 32];       // tokens that start and end a sequence, a bit each
     int32_t start[TILE], end[TILE];                    // which (where the bit is set)
@@ -166,8 +171,9 @@ __device__ __forceinline__ void load_window(const Params &p, int64_t seq, int de
     }
 }
 // The state that enters span `seq` (> 0): from the nearest span before it whose state is out for all the warp's channels, and the
-// own states of the spans between, folded from the oldest on.  k: the first window.  False: it did not come in time.
-__device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch, bool on, Packet *k, float &h) {
+// own states of the spans between, folded from the oldest on.  k: the first window.  False: it did not come in time, or another wait of
+// the block's had run out (*err).
+__device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch, bool on, Packet *k, float &h, const int *err) {
     constexpr int W = kWindow;
     int depth = 0;
     uint64_t t0 = 0;
@@ -192,7 +198,8 @@ __device__ __forceinline__ bool chain_enter(const Params &p, int64_t seq, int ch
         }
         depth = gap || depth >= 15 * W ? 0 : depth + W;
         if (t0 == 0) t0 = tc::globaltimer();
-        if (__shfl_sync(0xffffffffu, tc::globaltimer() - t0 > tc::kWaitLimitNs, 0)) return false;
+        // (lane 0's answer for all: they may see the error at different times)
+        if (__shfl_sync(0xffffffffu, tc::globaltimer() - t0 > tc::kWaitLimitNs || *reinterpret_cast<const volatile int *>(err) != 0, 0)) return false;
         load_window(p, seq, depth, ch, on, k);
     }
 }
@@ -201,8 +208,9 @@ template <int CB, int RUN>
 struct Shared {
     float a[kWarps][CB], b[kWarps][CB];
     float4 sent_own[2][kRanks - 1][CB];    // product and own state of the blocks before (z: whether one is cut), by parity of the tile
-    uint32_t next[2];              // the next span, by parity; next[1] at first: the cluster's first
+    uint32_t next[2];              // the next span, by parity, from the first block; next[1] at first: the cluster's first
     uint64_t sent[2];              // these have come
+    int lost;                      // exchanges since (and with) the one that the next span's number did not come in time for; 0: none
     Tile<kWarps * RUN> tile[2];
     int err;
     uint64_t full[2];
@@ -238,7 +246,6 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
     Packet k[kWindow];
     if (seq > 0) load_window(p, seq, 0, ch, on, k);        // (under way while the peers' states come)
     tc::mbar_wait(&s.sent[par], phase, &s.err, GCL_DEV_WAIT_TIMEOUT);
-    const bool wait = *reinterpret_cast<volatile int *>(&s.err) == 0;
     Packet *mine = p.chain + seq * p.D + ch;
     // the blocks before this one, composed
     float A0 = 1.f, h0 = 0.f;
@@ -257,7 +264,7 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
     A *= A0;
     if (speaks) store_packet(mine, A, h, h, span_cut ? kDone : kOwn);
     float in = 0.f;
-    if (seq > 0 && wait) ok = chain_enter(p, seq, ch, on, k, in);          // (the first span is cut at its first token)
+    if (seq > 0) ok = chain_enter(p, seq, ch, on, k, in, &s.err);          // (the first span is cut at its first token)
     if (speaks && !span_cut) store_packet(mine, A, h, fmaf(A, in, h), kDone);
     in = cut0 ? h0 : fmaf(A0, in, h0);
 #pragma unroll
@@ -273,7 +280,8 @@ struct Maps {                      // the staged rows: r, x, d_o (backward), i
     CUtensorMap m[4];
 };
 
-constexpr uint32_t kStopped = 0xffffffffu;             // no span: the call does nothing
+constexpr uint32_t kStopped = 0xffffffffu;             // no span: the call does nothing, or the end
+constexpr int kLeave = 3;                              // exchanges after which a block that lost the number leaves
 constexpr int kIssuer = 96;        // the thread that takes spans and issues the copies
 
 // Live tokens, once the set-up is done; -1: the call does nothing.  A solo call's blocks check cu_seqlens themselves; the status word
@@ -349,7 +357,7 @@ struct Walk {
             tc::mbar_init(&s.sent[0], 1);
             tc::mbar_init(&s.sent[1], 1);
             tc::fence_barrier_init();
-            s.err = 0;
+            s.err = s.lost = 0;
             if (rank == 0) s.next[1] = p.first ? atomicAdd(&p.head->ticket, 1u) : stop ? kStopped : blockIdx.x / kRanks;
         }
         cluster_arrive();
@@ -376,24 +384,31 @@ struct Walk {
         tc::mbar_wait(&s.full[buf], parity >> buf & 1, &s.err, GCL_DEV_WAIT_TIMEOUT);
         parity ^= 1u << buf;
     }
-    // Takes the cluster's next span (its number reaches the blocks by the exchange).
+    // The first block takes the cluster's next span (its number reaches the others by the exchange); none after an error.
     __device__ __forceinline__ uint32_t take() {
-        return rank != 0 || threadIdx.x != kIssuer ? 0 : p.first ? atomicAdd(&p.head->ticket, 1u) : units;
+        if (rank != 0 || threadIdx.x != kIssuer) return 0;
+        return p.first && *reinterpret_cast<volatile int *>(&s.err) == 0 ? atomicAdd(&p.head->ticket, 1u) : units;
     }
     // Between a tile's halves: the warps' own states are in s.a, s.b; afterwards the states that enter them in s.b.
     // What a block receives at parity `buf` it has used when it arrives on the cluster's barrier, and the peers send there again
     // two tiles later, after they have waited on that barrier.
+    // A block that the next span's number does not reach in time cannot know whether the first block goes on.  It sets that block's error,
+    // before it arrives on the barrier behind which the exchange after this one lies, and takes part in two more with empty tiles, so that it
+    // is still there to be sent to: the first block sees the error when it takes a span after the first of them, and ends with the
+    // second (or did before).
     template <typename Side>
     __device__ __forceinline__ void exchange(int buf, uint32_t taken, const uint32_t *cuts, Side side) {
+        static_assert(kRanks == 2, "a block that lost the number sends to no other");
         const int tid = threadIdx.x, warp = tid >> 5;
         const Tile<TILE> &t = s.tile[buf];
         const uint32_t ph = phase >> buf & 1;
         phase ^= 1u << buf;
         cluster_wait();
         if (tid == kIssuer) {
-            tc::mbar_arrive_expect_tx(&s.sent[buf], 4 + rank * CB * 16);
+            if (rank == 0) s.next[buf] = taken;
+            tc::mbar_arrive_expect_tx(&s.sent[buf], rank == 0 ? 0 : 4 + rank * CB * 16);
             if (rank == 0)
-                for (int r = 0; r < kRanks; ++r) peer_send(&s.next[buf], &s.sent[buf], r, taken);
+                for (int r = 1; r < kRanks; ++r) peer_send(&s.next[buf], &s.sent[buf], r, taken);
         }
         __syncthreads();
         if (warp < CB / 32) {
@@ -401,19 +416,38 @@ struct Walk {
         } else if (warp == 2) {
             side();
         } else if (warp == kIssuer / 32) {
-            tc::mbar_wait(&s.sent[buf], ph, &s.err, GCL_DEV_WAIT_TIMEOUT);
-            const uint32_t unit = s.next[buf];
-            if (unit < units) {
-                if (tid == kIssuer) issue(unit, buf ^ 1);
+            const int before = *reinterpret_cast<volatile int *>(&s.lost);
+            __syncwarp();
+            // (by its own limit: an error elsewhere in the block does not cut it short)
+            const bool come = __all_sync(0xffffffffu, tc::mbar_wait(&s.sent[buf], ph, &s.lost, 1)) && before == 0;
+            if (!come || s.next[buf] < units) {
+                if (tid == kIssuer) {
+                    if (come) issue(s.next[buf], buf ^ 1);
+                    else lose(before + 1, buf ^ 1);
+                }
                 __syncwarp();
                 borders(p, s.tile[buf ^ 1]);
+            } else if (tid == kIssuer) {
+                s.tile[buf ^ 1].cb = kEnd;
             }
         }
         __syncthreads();
         cluster_arrive_relaxed();
     }
-    __device__ __forceinline__ bool more(int buf) const { return s.next[buf] < units; }
-    // After the last tile: a wait that ran out is reported, and copies still under way are waited for (with a limit).
+    // The issuer of a block that the number did not reach; exchanges: since then.
+    __device__ __forceinline__ void lose(int exchanges, int buf) {
+        atomicCAS(&s.err, 0, GCL_DEV_WAIT_TIMEOUT);
+        s.lost = exchanges;
+        if (exchanges == 1) {                              // (later the first block may have left)
+            peer_store(&s.err, 0, GCL_DEV_WAIT_TIMEOUT);
+            cluster_fence();                               // (the barrier is arrived on without one)
+        }
+        Tile<TILE> &t = s.tile[buf];
+        t.seq = t.t0 = t.n = 0;
+        t.cb = exchanges < kLeave ? p.n_cb : kEnd;         // (past the channels: nothing is read, written or waited for)
+    }
+    __device__ __forceinline__ bool more(int buf) const { return s.tile[buf ^ 1].cb != kEnd; }
+    // After the last tile: a wait that ran out is reported; copies and what the peers sent are waited for (with a limit).
     __device__ __forceinline__ void finish() {
         cluster_wait();
         cluster_arrive();                                  // (no block leaves while another may send to it)
@@ -421,8 +455,10 @@ struct Walk {
         if (s.err == 0 || threadIdx.x != kIssuer) return;
         status_set(p.status, GCL_DEV_WAIT_TIMEOUT);
         const uint64_t t0 = tc::globaltimer();
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b) {
             while ((issued >> (2 + b) & 1) && !tc::mbar_try_wait(&s.full[b], (issued >> b & 1) ^ 1) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
+            while (!tc::mbar_try_wait(&s.sent[b], (phase >> b & 1) ^ 1) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
+        }
     }
 };
 
