@@ -116,12 +116,11 @@ template <typename T>
 cudaError_t launch(Params p, Params before, bool backward, cudaStream_t s) {
     p.n_cb = before.n_cb = (p.D + Lane<T>::CB - 1) / Lane<T>::CB;
     const bool states = before.tiles > 0;
-    for (Params *w : {&p, &before})
-        if (solo(*w)) w->first = nullptr;
     cudaError_t e = cudaSuccess;
-    if (!solo(p)) {
-        Params none{};
-        e = launch_setup(p, states && !solo(before) ? before : none, backward ? p.dht : p.h0, backward ? p.dh0 : p.ht, s);
+    if (solo(p)) {
+        p.first = before.first = nullptr;
+    } else {                                               // (then the states' walk goes by the set-up's look at the status word too)
+        e = launch_setup(p, before, backward ? p.dht : p.h0, backward ? p.dh0 : p.ht, s);
     }
     if (e == cudaSuccess && states) e = launch_fwd<T>(before, s);
     if (e != cudaSuccess) return e;
