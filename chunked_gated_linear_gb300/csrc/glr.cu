@@ -7,13 +7,13 @@ namespace {
 
 // ---- set-up: checks cu_seqlens, finds each tile's first sequence, passes states of empty sequences through, clears the
 // packets of the spans that will be taken ----
-__device__ __forceinline__ void set_up(const Params &p, bool stop, int64_t at, int64_t step) {
-    if (at == 0) {
-        p.head->blocked = stop;
-        p.head->live = stop ? 0 : p.cu[p.n_max];
+__device__ __forceinline__ void set_up(const Params &p, bool blocked, bool bad, int64_t at, int64_t step) {
+    if (at == 0) {                                         // (this thread's block decides for the call)
+        p.head->blocked = blocked || bad;
+        p.head->live = blocked || bad ? 0 : p.cu[p.n_max];
         p.head->ticket = 0;
     }
-    if (stop) return;
+    if (bad) return;
     const int64_t spans = (p.cu[p.n_max] + (int64_t)kRanks * p.tile - 1) / (kRanks * p.tile);
     for (int64_t e = at; e < spans * p.D; e += step) reinterpret_cast<uint4 *>(p.chain)[e] = make_uint4(0, 0, 0, 0);
     for (int64_t j = at; j < p.tiles; j += step) {
@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const P
     bad = __syncthreads_or(bad);
     const int64_t at = blockIdx.x * (int64_t)blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
     if (at == 0 && bad) status_set(p.status, GCL_DEV_BAD_RANGE);
-    set_up(p, blocked || bad, at, step);
-    if (before.tiles > 0) set_up(before, blocked || bad, at, step);
+    set_up(p, blocked, bad, at, step);
+    if (before.tiles > 0) set_up(before, blocked, bad, at, step);
     if (blocked || bad || !out_state) return;
     for (int n = blockIdx.x; n < p.n_max; n += gridDim.x) {
         if (p.cu[n + 1] != p.cu[n]) continue;
@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(1024) glr_setup_kernel(const Params p, const P
 
 }  // namespace
 
-// (a block sets `blocked` by the status word alone where another has set the word in the meantime: both stop the call)
+// (The blocks' looks at the status word may differ, where another call sets it in the meantime: the first block's decides, and what the walks
+// read is set up by every block whatever it saw; a block that saw the word set leaves its empty sequences' states unwritten.)
 cudaError_t launch_setup(const Params &p, const Params &before, const float *in_state, float *out_state, cudaStream_t s) {
     int64_t blocks = ((p.tiles + before.tiles + kRanks - 1) / kRanks * p.D + 4095) / 4096;
     if (out_state && blocks < (p.n_max + 7) / 8) blocks = (p.n_max + 7) / 8;

@@ -20,20 +20,24 @@ class Word:
         return self.value
 
 
-def backward(rng, word, blocks=4, states_decide=False):
+def backward(rng, word, blocks=4, states_decide=False, setup_skips=False):
     """A backward of several spans that forms the states itself: set-up, the walk that forms the states, the walk of the gradients.
-    states_decide: the states' walk, of one span, looks at the word for itself."""
+    states_decide: the states' walk, of one span, looks at the word for itself.  setup_skips: a block of the set-up that sees the word set
+    leaves its share of the packets and borders as they were."""
     looks = {b: word.look() for b in rng.sample(range(blocks), blocks)}
     stopped = looks[0]                                     # what the set-up leaves the walks
+    if stopped:
+        return []
     formed = not (word.look() if states_decide else stopped)
-    return [] if stopped or formed else ["states"]
+    return ["packets"] * (setup_skips and any(looks.values())) + ["states"] * (not formed)
 
 
 @pytest.mark.parametrize("at", range(8))
-def test_the_states_walk_goes_by_the_set_ups_look(at):
+def test_the_call_goes_by_one_look(at):
     for seed in range(50):
         assert backward(random.Random(seed), Word(at)) == []
 
 
-def test_model_sees_a_walk_that_looks_for_itself():
-    assert any(backward(random.Random(s), Word(at), states_decide=True) for s in range(50) for at in range(8))
+@pytest.mark.parametrize("form,read", [("states_decide", "states"), ("setup_skips", "packets")])
+def test_model_sees_looks_that_differ(form, read):
+    assert any(read in backward(random.Random(s), Word(at), **{form: True}) for s in range(50) for at in range(8))
