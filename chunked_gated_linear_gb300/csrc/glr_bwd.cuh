@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
 __global__ void __launch_bounds__(1024) glr_drate_kernel(const Params p, int tile) {
     __shared__ float s[32][33];
     grid_dependency_wait();
-    if (p.head->blocked) return;
+    // (the clusters of a call of one span look at the status word each for itself: one that stopped leaves no sums)
+    if (p.head->blocked || (!p.first && status_blocks_cta(p.status))) return;
     const int64_t n = (p.head->live + tile - 1) / tile;
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
     float sum = 0.f;

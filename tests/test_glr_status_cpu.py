@@ -32,6 +32,24 @@ def backward(rng, word, blocks=4, states_decide=False, setup_skips=False):
     return ["packets"] * (setup_skips and any(looks.values())) + ["states"] * (not formed)
 
 
+def one_span(rng, word, clusters=4, sum_by_the_first=False):
+    """A backward of one span with the gradient of the rates: each cluster looks at the word and leaves the sums of its channels, a last
+    launch adds them up.  sum_by_the_first: it goes by the first cluster's look alone."""
+    looks = {c: word.look() for c in rng.sample(range(clusters), clusters)}
+    stopped = looks[0] or not sum_by_the_first and word.look()
+    return [] if stopped or not any(looks.values()) else ["sums"]
+
+
+@pytest.mark.parametrize("at", range(8))
+def test_sums_are_of_what_was_formed(at):
+    for seed in range(50):
+        assert one_span(random.Random(seed), Word(at)) == []
+
+
+def test_model_sees_sums_of_what_was_not_formed():
+    assert any(one_span(random.Random(s), Word(at), sum_by_the_first=True) for s in range(50) for at in range(8))
+
+
 @pytest.mark.parametrize("at", range(8))
 def test_the_call_goes_by_one_look(at):
     for seed in range(50):
