@@ -451,3 +451,33 @@ def test_step_passes_on_gates_that_are_not_numbers(dtype, decay, mix, gate):
     gcl.glr_step(c.x, c.r, states[1], outs[1], **c.kw)
     for a, b in ((states[1], states[0]), (outs[1], outs[0])):
         assert a[bad].isnan().all() and torch.equal(a[~bad], b[~bad])
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_sigmoid_decay_near_one(dtype, gate):
+    """The decay itself: with x = 0 and a state of 1 the state after a token is a, unrounded (a 1 + 0).  Where a >= 1/2 it is 1 - c with
+    c = sigmoid(-r): one rounding of at most 2^-25, and c's own error.  c's (a's where a < 1/2) is relative: the exponent's product and
+    its constant are off by 2^-24 of it each, 2 |r| in all, and exponential, sum, reciprocal and product by at most 10 more."""
+    n = 4096
+    c = Case(dtype, [1], n, "sigmoid", "complement", gate, pad=0)
+    c.r.copy_(torch.linspace(-12, 12, n, device=DEV).view(1, n))
+    c.x.zero_()
+    state, o = torch.ones(1, n, device=DEV), c.full(1, n, dtype=DT[dtype])
+    gcl.glr_step(c.x, c.r, state, o, **c.kw)
+    r = np64(c.r)[0]
+    a, small = ref.sigmoid(r), ref.sigmoid(-np.abs(r))
+    bound = np.where(r > 0, 2.0 ** -25, 0) + (2 * np.abs(r) + 10) * ref.E32 * small
+    err = np.abs(np64(state)[0] - a)
+    assert (err <= bound).all(), (float(r[(err - bound).argmax()]), float((err / bound).max()))
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_memory(dtype, gate):
+    """Sigmoid decays of 0.998 to 0.9999 over thousands of tokens."""
+    c = Case(dtype, [3001, 500], 72, "sigmoid", "complement", gate)
+    c.r.copy_(6.2 + 3 * torch.rand(c.T, 72, device=DEV))
+    c.fwd()
+    c.check_fwd()
+    c.check_bwd(c.bwd(c.save))
