@@ -221,7 +221,7 @@ __device__ __forceinline__ void gates(typename Lane<T>::P rate, bool near, const
             if (GATE) sigmoids<T, APART>(r[e], g[e], s, c, sg[e], cg);
             else sigmoids<T>(r[e], s, c);
             // a >= 1/2 from c: one rounding, where s carries those of its sum, its reciprocal and their product (r of 6 to 10: 3e-8
-            // instead of up to 2e-7, which 1 / (1 - a) tokens add up)
+            // instead of up to 1.6e-7, which 1 / (1 - a) tokens add up)
             a[e] = s;
             if (DECAY == GCL_DECAY_SIGMOID)
                 a[e] = L::map(c, s, L::fma(c, L::all(-1.f), L::all(1.f)), [](float u, float v, float w) { return u <= 0.5f ? w : v; });

@@ -481,3 +481,25 @@ def test_long_memory(dtype, gate):
     c.fwd()
     c.check_fwd()
     c.check_bwd(c.bwd(c.save))
+
+
+@pytest.mark.parametrize("mix,gate", [("root", True), ("complement", False), ("one", True)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rates_on_both_sides_of_the_near_range(dtype, mix, gate):
+    """Rates of 0.01 to 8 in every warp's channels, and of one warp's channels alone: the exponential beside the polynomial."""
+    for lens, D in (([70, 0, 200, 1], 200), ([100], 72), ([900, 2100], 136)):
+        c = Case(dtype, lens, D, "power", mix, gate, seed=D)
+        c.rate.copy_(torch.logspace(-2, 0.9, D, device=DEV)[torch.randperm(D, device=DEV)])
+        if D == 136:
+            c.rate[64:].mul_(0.1)
+        c.fwd()
+        c.check_fwd()
+        c.check_bwd(c.bwd(c.save))
+        c.check_bwd(c.bwd())
+        state, o = torch.ones(c.T, D, device=DEV), c.full(c.T, D, dtype=DT[dtype])
+        gcl.glr_step(c.x, c.r, state, o, **c.kw)
+        x, r, i, rate, _ = c.ref_args()
+        _, a, m, _ = ref.gates(r, rate, "power", mix)
+        h = a + m * (x if i is None else x * ref.sigmoid(i))
+        ref.check("state", np64(state), h, "f32", 10 * ref.E32)
+        ref.check("o", np64(o), h, dtype, 10 * ref.E32)
