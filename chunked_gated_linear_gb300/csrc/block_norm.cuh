@@ -262,6 +262,13 @@ __device__ __forceinline__ void advance(char *&at, const Rows &r, bool wrap) {
     at += r.d;
     if (wrap) at += r.w;
 }
+// (debug build) Whether the row of a thread's cursor lies in its array.
+template <typename T>
+__device__ __forceinline__ bool row_in(const Params &p, const Rows &r, const char *at, int l) {
+    return !r.p || GCL_RANGE_IN_BOUNDS(at - static_cast<const char *>(r.p) - l * 8 * (int)sizeof(T),
+                                       at - static_cast<const char *>(r.p) + (p.D - l * 8) * (int)sizeof(T) - 1,
+                                       ((p.t_max - 1) * r.st + (p.H - 1) * r.sh + p.D) * (int)sizeof(T), p.status);
+}
 template <typename T>
 __device__ __forceinline__ T *vec_at(char *at, int v, int tpr) { return reinterpret_cast<T *>(at) + v * tpr * 8; }
 
@@ -360,9 +367,10 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
     auto stage = [&](int64_t r, int buf) {                 // row r, at the cursors; moves them on
         uint4 *to = staged + buf * C::all * TH;
         if (r - threadIdx.x / TPR < rows) {                // (the same for the block)
+            const bool live = r < rows && row_in<T>(p, p.y, cy, l) && row_in<T>(p, p.gate, cg, l) && row_in<S>(p, p.x, cx, l);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const bool on = r < rows && l + v * TPR < nv;
+                const bool on = live && l + v * TPR < nv;
                 const T *none = static_cast<const T *>(p.y.p);
                 stage_copy<T, ST, TH>(to, C::y + v * C::t, on ? vec_at<const T>(cy, v, TPR) : none, on);
                 if (p.gate.p) stage_copy<T, ST, TH>(to, C::g + v * C::t, on ? vec_at<const T>(cg, v, TPR) : none, on);
@@ -374,7 +382,8 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_blocks(TPR, VPT)) block_f
     stage(row, 0);
     int buf = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < rows; row0 += step, buf ^= 1) {
-        const bool live = row < rows;
+        const bool live = row < rows && row_in<T>(p, p.y, cy, l) && row_in<T>(p, p.gate, cg, l) && row_in<S>(p, p.x, cx, l) &&
+                          row_in<S>(p, p.xo, co, l) && row_in<T>(p, p.z, cz, l);
         const bool wrap = (h += p.dh) >= p.H;
         if (wrap) h -= p.H;
         char *here_cy = cy, *here_cg = cg, *here_cx = cx;  // (of this row, where it is read from memory)
@@ -508,9 +517,11 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
     auto stage = [&](int64_t r, int buf) {                 // row r, at the cursors
         uint4 *to = staged + buf * C::all * TH;
         if (r - threadIdx.x / TPR < rows) {                // (the same for the block)
+            const bool live = r < rows && row_in<T>(p, p.y, cy, l) && row_in<T>(p, p.gate, cg, l) && row_in<S>(p, p.x, cx, l) &&
+                              row_in<S>(p, p.dxo, cdo, l) && row_in<T>(p, p.dz, cdz, l);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const bool on = r < rows && l + v * TPR < nv;
+                const bool on = live && l + v * TPR < nv;
                 const T *none = static_cast<const T *>(p.y.p);
                 const S *none_s = reinterpret_cast<const S *>(none);
                 stage_copy<T, ST, TH>(to, C::y + v * C::t, on ? vec_at<const T>(cy, v, TPR) : none, on);
@@ -527,7 +538,9 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_blocks(TPR, VPT)) block_b
     stage(row, 0);
     int buf = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < rows; row0 += step, buf ^= 1) {
-        const bool live = row < rows;
+        const bool live = row < rows && row_in<T>(p, p.y, cy, l) && row_in<T>(p, p.gate, cg, l) && row_in<S>(p, p.x, cx, l) &&
+                          row_in<S>(p, p.dxo, cdo, l) && row_in<T>(p, p.dz, cdz, l) && row_in<T>(p, p.dy, cdy, l) &&
+                          row_in<T>(p, p.dgate, cdg, l) && row_in<S>(p, p.dx, cdx, l);
         const bool wrap = (h += p.dh) >= p.H;
         if (wrap) h -= p.H;
         char *here_cy = cy, *here_cg = cg, *here_cx = cx, *here_cdo = cdo, *here_cdz = cdz;        // (of this row, where it is read from memory)

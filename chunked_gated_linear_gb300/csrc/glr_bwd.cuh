@@ -41,10 +41,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
         const int ch = tile.cb * CB + lane * V, n = tile.n - warp * RUN;
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
         auto row = [&](int arr, int k) { return L::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128)); };
-        const P rate = load_state<T>(DECAY == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, p.D, ch);
+        const P rate = load_state<T>(p, DECAY == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, 1, ch);
         const bool near = __all_sync(0xffffffffu, L::every(rate, [](float v) { return v >= 0.f && v <= kNear; }));
         P before = L::all(0.f);
-        if (warp == 2 && tile.n > 0) before = load_state<T>(p.h_save, tile.t0 / kSave, p.D, ch);
+        if (warp == 2 && tile.n > 0) before = load_state<T>(p, p.h_save, tile.t0 / kSave, save_rows(p), ch);
         walk.landed(buf);
         const uint32_t taken = walk.take();
         P a[RUN], m[RUN], prev[RUN];                       // prev: b = m u, later the state before each token
@@ -77,13 +77,13 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
                 constexpr bool CUT = decltype(cut)::value;
 #pragma unroll
                 for (int k = 0; k < RUN; ++k) {
-                    if (CUT && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                    if (CUT && (starts >> k & 1)) h = load_state<T>(p, p.h0, start[k], p.n_max, ch);
                     h = L::fma(a[k], h, prev[k]);
                     A = L::mul(A, a[k]);
                 }
 #pragma unroll
                 for (int k = RUN - 1; k >= 0; --k) {
-                    if (CUT && (ends >> k & 1)) c = load_state<T>(p.dht, end[k], p.D, ch);
+                    if (CUT && (ends >> k & 1)) c = load_state<T>(p, p.dht, end[k], p.n_max, ch);
                     c = L::mul(a[k], L::add(CUT && k >= n ? L::all(0.f) : row(2, k), c));
                 }
             };
@@ -109,14 +109,14 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
             constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
             for (int k = 0; k < RUN; ++k) {
-                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p, p.h0, start[k], p.n_max, ch);
                 const P b = prev[k];
                 prev[k] = h;
                 h = L::fma(a[k], h, b);
             }
 #pragma unroll
             for (int k = RUN - 1; k >= 0; --k) {
-                if (!PLAIN && (ends >> k & 1)) c = load_state<T>(p.dht, end[k], p.D, ch);
+                if (!PLAIN && (ends >> k & 1)) c = load_state<T>(p, p.dht, end[k], p.n_max, ch);
                 const P x = row(1, k), G = L::add(row(2, k), c), Gm = L::mul(G, m[k]);
                 c = L::mul(a[k], !PLAIN && k >= n ? c : G);
                 P sr, nr, sg, ng;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
                 to_x -= p.dx.st / V;
                 to_r -= p.dr.st / V;
                 to_i -= p.di.st / V;
-                if (!PLAIN && (starts >> k & 1)) store_state<T>(p.dh0, start[k], p.D, ch, c);
+                if (!PLAIN && (starts >> k & 1)) store_state<T>(p, p.dh0, start[k], p.n_max, ch, c);
             }
         };
         if (!edge) run(std::true_type());
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_bwd_kernel(const __gri
                 P sum = L::all(0.f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) sum = L::add(sum, L::load(&s_d[w][lane * V]));
-                store_state<T>(p.drate_part, tile.t0 / W::TILE, p.D, ch, sum);
+                store_state<T>(p, p.drate_part, tile.t0 / W::TILE, p.tiles, ch, sum);
             }
         }
         if (!walk.more(buf)) break;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(1024) glr_drate_kernel(const Params p, int til
         for (int64_t j0 = r; j0 < n; j0 += 8 * 32) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = j0 + i * 32 < n ? p.drate_part[(j0 + i * 32) * p.D + d] : 0.f;
+            for (int i = 0; i < 8; ++i) v[i] = j0 + i * 32 < n && GCL_IN_BOUNDS(j0 + i * 32, p.tiles, p.status) ? p.drate_part[(j0 + i * 32) * p.D + d] : 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += v[i];
         }

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
         const int ch = tile.cb * CB + lane * V, n = tile.n - warp * RUN;          // n: live tokens from the warp's first on
         const uint8_t *rows = s_rows + buf * narr * BYTES + warp * RUN * 128 + lane * 4;
         auto row = [&](int arr, int k) { return L::get(*reinterpret_cast<const uint32_t *>(rows + arr * BYTES + k * 128)); };
-        const P rate = load_state<T>(DECAY == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, p.D, ch);
+        const P rate = load_state<T>(p, DECAY == GCL_DECAY_POWER ? p.kind.rate : nullptr, 0, 1, ch);
         const bool near = __all_sync(0xffffffffu, L::every(rate, [](float v) { return v >= 0.f && v <= kNear; }));
         walk.landed(buf);
         // (the next span is taken only when this one's rows are here: few spans go to all clusters, and none is held back for long)
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
             auto run = [&](auto cut) {
 #pragma unroll
                 for (int k = 0; k < RUN; ++k) {
-                    if (decltype(cut)::value && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                    if (decltype(cut)::value && (starts >> k & 1)) h = load_state<T>(p, p.h0, start[k], p.n_max, ch);
                     h = L::fma(a[k], h, b[k]);
                     A = L::mul(A, a[k]);
                 }
@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
         walk.exchange(buf, taken, tile.starts, [] {});
         P h = L::load(&s.b[warp][lane * V]);
         if (warp * RUN % kSave == 0 && p.h_save && n > 0) {
-            if (starts & 1) h = load_state<T>(p.h0, start[0], p.D, ch);
-            store_state<T>(p.h_save, t / kSave, p.D, ch, h);
+            if (starts & 1) h = load_state<T>(p, p.h0, start[0], p.n_max, ch);
+            store_state<T>(p, p.h_save, t / kSave, save_rows(p), ch, h);
         }
         uint32_t *to = word<T>(p.o, t, ch);
         const int n_out = p.o.p && ch < p.D && n > 0 && GCL_RANGE_IN_BOUNDS(t, t + (n < RUN ? n : RUN) - 1, p.t_max, p.status) ? n : 0;
@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) glr_fwd_kernel(const __gri
             constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
             for (int k = 0; k < RUN; ++k) {
-                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p.h0, start[k], p.D, ch);
+                if (!PLAIN && (starts >> k & 1)) h = load_state<T>(p, p.h0, start[k], p.n_max, ch);
                 h = L::fma(a[k], h, b[k]);
                 if (PLAIN ? n_out > 0 : k < n_out) *to = L::put(h);
                 to += p.o.st / V;
-                if (!PLAIN && (ends >> k & 1)) store_state<T>(p.ht, end[k], p.D, ch, h);
+                if (!PLAIN && (ends >> k & 1)) store_state<T>(p, p.ht, end[k], p.n_max, ch, h);
             }
         };
         if (!(starts | ends) && n >= RUN) run(std::true_type());

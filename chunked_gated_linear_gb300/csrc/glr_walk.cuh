@@ -83,7 +83,7 @@ __device__ __forceinline__ void borders(const Params &p, Tile<TILE> &t) {
     if (t.n > 0) {
         int f;
         if (p.first) {
-            f = p.first[t.t0 / TILE];
+            f = GCL_IN_BOUNDS(t.t0 / TILE, p.tiles, p.status) ? p.first[t.t0 / TILE] : 0;
         } else {                                           // first n with cu[n] >= t0 (n_max if none)
             int hi = p.n_max;
             f = 0;
@@ -132,15 +132,16 @@ __device__ __forceinline__ uint32_t *word(const Rows &r, int64_t t, int ch) {
     return reinterpret_cast<uint32_t *>(static_cast<T *>(r.p) + t * r.st + ch);
 }
 
-// A lane's values of row n of [n, D]; zeros without the array or past the channels.
+// A lane's values of row n of [rows, D]; zeros without the array or past the channels.
 template <typename T>
-__device__ __forceinline__ typename Lane<T>::P load_state(const float *s, int64_t n, int D, int ch) {
-    return s && ch < D ? Lane<T>::load(s + n * D + ch) : Lane<T>::all(0.f);
+__device__ __forceinline__ typename Lane<T>::P load_state(const Params &p, const float *s, int64_t n, int64_t rows, int ch) {
+    return s && ch < p.D && GCL_IN_BOUNDS(n, rows, p.status) ? Lane<T>::load(s + n * p.D + ch) : Lane<T>::all(0.f);
 }
 template <typename T>
-__device__ __forceinline__ void store_state(float *s, int64_t n, int D, int ch, typename Lane<T>::P h) {
-    if (s && ch < D) Lane<T>::store(s + n * D + ch, h);
+__device__ __forceinline__ void store_state(const Params &p, float *s, int64_t n, int64_t rows, int ch, typename Lane<T>::P h) {
+    if (s && ch < p.D && GCL_IN_BOUNDS(n, rows, p.status)) Lane<T>::store(s + n * p.D + ch, h);
 }
+__device__ __forceinline__ int64_t save_rows(const Params &p) { return (p.t_max + kSave - 1) / kSave; }
 
 // ---- what spans leave each other ----
 __device__ __forceinline__ Packet load_packet(const Packet *p) {
@@ -167,7 +168,7 @@ __device__ __forceinline__ void load_window(const Params &p, int64_t seq, int de
         const int64_t at = seq - 1 - depth - u;
         k[u].a = k[u].own = k[u].out = 0.f;
         k[u].tag = on ? 0 : kDone;
-        if (on && at >= 0) k[u] = load_packet(p.chain + at * p.D + ch);
+        if (on && at >= 0 && GCL_IN_BOUNDS(at, (p.tiles + kRanks - 1) / kRanks, p.status)) k[u] = load_packet(p.chain + at * p.D + ch);
     }
 }
 // The state that enters span `seq` (> 0): from the nearest span before it whose state is out for all the warp's channels, and the
@@ -259,7 +260,8 @@ __device__ __forceinline__ bool chain_tile(const Params &p, int64_t seq, int ch,
             h0 = q ? t.y : fmaf(t.x, h0, t.y);
             A0 *= t.x;
         }
-    const bool speaks = rank == kRanks - 1 && on && p.first, span_cut = cut || cut0;  // (the last block speaks for the span)
+    const bool speaks = rank == kRanks - 1 && on && p.first && GCL_IN_BOUNDS(seq, (p.tiles + kRanks - 1) / kRanks, p.status);
+    const bool span_cut = cut || cut0;                     // (the last block speaks for the span)
     if (!cut) h = fmaf(A, h0, h);
     A *= A0;
     if (speaks) store_packet(mine, A, h, h, span_cut ? kDone : kOwn);
@@ -313,7 +315,7 @@ __device__ __forceinline__ void pass_empty(const Params &p, const float *in_stat
     if (!out_state) return;
     const int ch = (blockIdx.x / kRanks) * Lane<T>::CB + (threadIdx.x & 31) * Lane<T>::V;
     for (int n = blockIdx.x % kRanks * kWarps + (threadIdx.x >> 5); n < p.n_max; n += kRanks * kWarps)
-        if (p.cu[n + 1] == p.cu[n]) store_state<T>(out_state, n, p.D, ch, load_state<T>(in_state, n, p.D, ch));
+        if (p.cu[n + 1] == p.cu[n]) store_state<T>(p, out_state, n, p.n_max, ch, load_state<T>(p, in_state, n, p.n_max, ch));
 }
 
 // A block's walk over its tiles, which both directions share.  Its next tile's rows are staged while one is computed.
