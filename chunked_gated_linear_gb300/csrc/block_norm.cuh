@@ -7,10 +7,11 @@
 // has two reductions (y's own length first, on which xo depends).
 // Rows are read and written once.  A row is held by TPR threads, VPT vectors of eight values each; a block's next row comes into shared
 // memory by asynchronous copies while one is worked on (each thread its own vectors, so that no barrier belongs to it).  Bound by HBM and
-// issue together (47 instructions a value forwards, 85 backwards; a third are conversions, Philox and the sums), so
+// issue together forwards (46 instructions a value, 62% of slots; a third are conversions, Philox and the sums), so
 // arithmetic goes by fp32 pairs, choices are made for a vector and not for a value, and weights stay in shared memory over a
-// block's rows.  bf16, both norms, gate and dropout: 32,768 tokens of 2,048 130 us, 76% of copy bandwidth; backward 262 us, 60%; gated
-// norms of heads (no x, no z) 71 us, 84%.  On the way: rows loaded when needed 190 and 440; copied a row ahead, pairs, sums
+// block's rows.  Backwards by latency: 86 instructions a value take 55% of the slots and rows 42% of HBM's peak, with 12 warps an SM and two
+// reductions a row one after the other.  bf16, both norms, gate and dropout: 32,768 tokens of 2,048 129 us, 77% of copy bandwidth;
+// backward 262 us, 60%; gated norms of heads (no x, no z) 72 us, 83%.  On the way: rows loaded when needed 190 and 440; copied a row ahead, pairs, sums
 // side by side 136 and 279.  Not kept: one vector a thread (195, backward 279 to 304); more blocks of fewer registers (spills, 291 to 399).
 #pragma once
 

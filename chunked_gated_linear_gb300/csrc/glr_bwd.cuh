@@ -2,9 +2,9 @@
 //
 // Gradients of G_t = d_o_t + c_{t+1}, c_t = a_t G_t, over the tiles from last to first, together with the states again: a tile's come
 // from the one saved before it.  The walk's exchange passes c.  A tile's rows stay staged until its gradients are out, and sigmoids are
-// formed again for them; a, m and b (later the states) of a warp's eight tokens are 48 registers a thread.  Bound by issue (85
-// instructions a value, 49% of slots) and the special-function unit, then by the exchange between spans: 32,768 tokens of 2,048 channels,
-// bf16, with drate 272 us, 51% of copy bandwidth.  Not kept: three blocks an SM (80 registers spill, 374 us); clusters of four (295); a, m,
+// formed again for them; a, m and b (later the states) of a warp's eight tokens are 48 registers a thread.  Bound by issue (87
+// instructions a value, 48% of slots) and the special-function unit, then by the exchange between spans: 32,768 tokens of 2,048 channels,
+// bf16, with drate 277 us, 50% of copy bandwidth; fp32, 16,384 tokens, 348 us, 40%.  Not kept (beside 272 at that time): three blocks an SM (80 registers spill, 374 us); clusters of four (295); a, m,
 // b and the sigmoids in tensor memory (261; the forward says why).
 #pragma once
 

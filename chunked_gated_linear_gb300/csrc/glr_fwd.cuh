@@ -2,9 +2,9 @@
 //
 // A warp's 16 tokens: gates (three special-function results and about 30 other instructions a value), their product of decays and
 // state from zero; the state that enters from the walk's exchange; then the states, rounded, out.  Each row is read once
-// and written once; a and b of the tokens stay in registers (64 of 125 a thread), which leaves two blocks an SM.  Bound by the exchange
+// and written once; a and b of the tokens stay in registers (64 of 128 a thread), which leaves two blocks an SM.  Bound by the exchange
 // between spans beside the issue of 35 instructions a value (45% of slots): one sequence of 65,536 tokens of 2,048 channels, bf16, power
-// decay, root mix, input gate 246 us, 64% of copy bandwidth.  Not kept: tiles of 64 tokens 333 to 375; a and b in tensor memory, three
+// decay, root mix, input gate 247 us, 64% of copy bandwidth; fp32, 32,768 tokens, 348 us, 45%.  Not kept: tiles of 64 tokens 333 to 375; a and b in tensor memory, three
 // blocks an SM, 230 us, because a cluster whose blocks wait for each other's tensor memory can meet another stream's cluster that does the
 // same, each holding what the other waits for; without clusters (16 warps a block) 239 us, but a call of 256 tokens 10.0 us instead of 8.0
 // and short ones 16% longer.

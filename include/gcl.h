@@ -637,8 +637,9 @@ gcl_status_t rope_table_build(float *cos_table, float *sin_table, int64_t n_posi
  *
  * A zero-length sequence passes its state through (ht = h0, dh0 = dht).  a = 0 (r = -inf) and a = 1 are
  * allowed; r > 0 of GCL_DECAY_LOG is computed as given (m(a) = 0 with GCL_MIX_ROOT) as long as the product of a over
- * 256 consecutive tokens is finite.  For 16-bit rows with an input gate, sigmoid(r) and sigmoid(i) are not below 2^-63.  Rows at or past cu_seqlens[n_max] are neither used nor written.  A value
- * that is not finite reaches later tokens of its own sequence and channel alone (a d_o: earlier ones).
+ * 256 consecutive tokens is finite.  Of 16-bit rows with an input gate sigmoid(r) and sigmoid(i) are not below 2^-63, of others not below
+ * 2^-126 (fp32: e^-87).  Rows at or past cu_seqlens[n_max] are neither used nor written.  A value that is not finite, NaN in a gate among
+ * them, reaches later tokens of its own sequence and channel alone; a d_o, and in the backward an r, earlier ones too.
  *
  * h_save (forward, optional) receives the state before tokens 0, 64, 128, ... of the packed axis (a
  * sequence's first token: h0); a backward that gets it does not form the states again.
@@ -724,6 +725,8 @@ gcl_status_t glr_step(const gcl_glr_step_args *args, gcl_stream_t stream);
  * inputs, and gives dy, dgate, dx (may be NULL) and the weights' gradients (fp32, summed over the tokens and heads in a fixed
  * order), with d = dxo + back(dz w_pre; xo), back(u; a) = (u - n_a mean(u n_a)) / |a|, n_a = a / |a| (mean: the sum for GCL_NORM_L2):
  *   dx = d,  dgate = scale drop(d n w_post) act'(gate),  dy = back(scale drop(d act) w_post; y).
+ *
+ * A value that is not finite stays in its row (and in the weights' gradients); in the backward it does so where dropout removed it too.
  *
  * Rows y, gate, z and theirs have dtype; x, xo and theirs stream_dtype: the same, or GCL_F32.  With cu_seqlens rows
  * at or past cu_seqlens[n_max] are neither used nor written; without, every row is live.  Arithmetic is fp32; each output is
